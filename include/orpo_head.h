@@ -70,8 +70,9 @@ enum {
   ORPO_STATUS_EMPTY_SEQ = 1 << 6,  /* a sequence has no mask = 1 row (its mean is undefined) */
   ORPO_STATUS_NONFINITE = 1 << 7,  /* a non-finite lse, loss, log-odds or gradient */
   ORPO_STATUS_TIMEOUT = 1 << 8,    /* a bounded on-chip wait gave up (the kernel returned early) */
-  ORPO_STATUS_BOUNDS = 1 << 9      /* bounds-checked build only (ORPO_DEBUG_BOUNDS): a computed index fell
+  ORPO_STATUS_BOUNDS = 1 << 9,     /* bounds-checked build only (ORPO_DEBUG_BOUNDS): a computed index fell
                                       outside its buffer; the access was skipped */
+  ORPO_STATUS_PARENT = 1 << 10     /* orpo_beam_reorder: a parent or a length out of range */
 };
 
 /* Largest number of pairs orpo_loss accepts. */
@@ -352,7 +353,8 @@ int orpo_debug_wait_timeout(int32_t* status, int64_t limit_ns, void* stream);
  * kernel the library launches is bracketed by two CUDA events on its stream.
  * orpo_profile_stop() waits for those events and writes, for kernel kinds
  * 0 .. nkinds-1 (names from orpo_profile_kind_name: fwd_logits, fwd_merge,
- * orpo_loss, bwd_recompute, bwd_grad_gemm, debug_gemm), the summed milliseconds
+ * orpo_loss, bwd_recompute, bwd_grad_gemm, debug_gemm, dequant, bwd_skip_plan,
+ * logits_q, beam_select, beam_reorder), the summed milliseconds
  * into ms[] and the launch count into count[] (host arrays).  Events are
  * host-side objects pooled inside the library; no device memory is used.
  */

@@ -24,3 +24,9 @@ from .orpo_oracle import (  # noqa: F401
     dequant_affine,
     OracleError,
 )
+from .decode_oracle import (  # noqa: F401
+    beam_reorder,
+    beam_select,
+    head_logits,
+    logits_error_bound,
+)

@@ -21,12 +21,15 @@ __all__ = [
     "orpo_head_bwd", "orpo_status_string", "orpo_debug_gemm", "OrpoHead", "STATUS_BITS",
     "orpo_profile_start", "orpo_profile_stop", "orpo_head_fwd_static", "orpo_debug_wait_timeout",
     "orpo_pref_loss", "PREF_KINDS", "orpo_head_q_workspace_bytes", "orpo_head_fwd_q", "orpo_head_bwd_q",
-    "use_bounds_checked_library",
+    "use_bounds_checked_library", "orpo_head_logits_q", "orpo_beam_select", "orpo_beam_select_workspace_bytes",
+    "orpo_beam_reorder", "BeamDecoder",
 ]
 
 STATUS_BITS = {"target": 1 << 4, "seqid": 1 << 5, "empty": 1 << 6, "nonfinite": 1 << 7, "timeout": 1 << 8,
-               "bounds": 1 << 9}
+               "bounds": 1 << 9, "parent": 1 << 10}
 MAX_PAIRS = 2048
+MAX_BEAMS = 64
+MAX_SELECT = 64
 
 _lib = None
 
@@ -104,6 +107,16 @@ def load():
     L.orpo_head_bwd_q_skip.argtypes = [vp, vp, vp, vp, ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, f32, i64, i64,
                                        i64, f32, vp, vp, ctypes.c_int, vp, sz, vp, vp]
     L.orpo_head_bwd_q_skip.restype = ctypes.c_int
+    L.orpo_head_logits_q.argtypes = [vp, i64, vp, vp, vp, ctypes.c_int, ctypes.c_int, i64, i64, i64, f32, vp, i64,
+                                     ctypes.c_int, vp, vp]
+    L.orpo_head_logits_q.restype = ctypes.c_int
+    L.orpo_beam_select_workspace_bytes.argtypes = [i64, ctypes.c_int, i64, ctypes.c_int]
+    L.orpo_beam_select_workspace_bytes.restype = sz
+    L.orpo_beam_select.argtypes = [vp, i64, ctypes.c_int, vp, vp, i32, i64, ctypes.c_int, i64, ctypes.c_int, vp, vp,
+                                   vp, vp, vp, sz, vp, vp]
+    L.orpo_beam_select.restype = ctypes.c_int
+    L.orpo_beam_reorder.argtypes = [vp, vp, i64, vp, i64, i64, ctypes.c_int, i64, i64, i64, vp, vp]
+    L.orpo_beam_reorder.restype = ctypes.c_int
     L.orpo_profile_start.argtypes = []
     L.orpo_profile_start.restype = ctypes.c_int
     L.orpo_profile_stop.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64), ctypes.c_int]
@@ -381,6 +394,94 @@ def orpo_head_bwd_q_skip(h, wq, scales, biases, bits, group, targets, mask, lse,
            "orpo_head_bwd_q_skip")
 
 
+def _rows(t, name, dtypes, cols=None, rows=None):
+    """A 2-D CUDA tensor whose rows are contiguous; returns its row pitch in elements."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         f"({'rows' if rows is None else rows}, {'columns' if cols is None else cols})")
+    pitch = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if (t.shape[1] > 1 and t.stride(1) != 1) or pitch < t.shape[1]:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return pitch
+
+
+LOGITS = (torch.float32, torch.bfloat16)
+
+
+def orpo_head_logits_q(h, wq, scales, biases, bits, group, softcap, logits, status, stream=None):
+    """Logits [M, V] (fp32 or bf16) of the rows of h [M, d] under the affine group-quantised head.
+
+    h and logits may have any row pitch, e.g. hidden[:, -1] of [M, T, d] hidden states."""
+    ld_h = _rows(h, "h", BF16)
+    M, d = h.shape
+    V = wq.shape[0]
+    _quant_args(wq, scales, biases, V, d, bits, group)
+    ld_logits = _rows(logits, "logits", LOGITS, cols=V, rows=M)
+    _dev(status, "status", (torch.int32,))
+    _check(load().orpo_head_logits_q(_ptr(h), ld_h, _ptr(wq), _ptr(scales), _ptr(biases), int(bits), int(group), M, V,
+                                     d, float(softcap), _ptr(logits), ld_logits,
+                                     1 if logits.dtype == torch.bfloat16 else 0, _ptr(status), _stream(stream)),
+           "orpo_head_logits_q")
+
+
+def orpo_beam_select_workspace_bytes(batch: int, beams: int, V: int, n: int) -> int:
+    return int(load().orpo_beam_select_workspace_bytes(batch, beams, V, n))
+
+
+def orpo_beam_select(logits, score, finished, eos, beams, out_score, out_parent, out_token, out_finished, workspace,
+                     status, stream=None):
+    """The n best continuations (out_* are [batch, n]) over beams x vocabulary of logits [batch * beams, V].
+
+    finished and out_finished may be None; eos is -1 when no token ends a response."""
+    V = logits.shape[1]
+    batch, n = out_score.shape
+    rows = batch * beams
+    ld_logits = _rows(logits, "logits", LOGITS, rows=rows)
+    _dev(score, "score", (torch.float32,))
+    if score.numel() != rows:
+        raise ValueError(f"score has {score.numel()} elements, expected batch * beams = {rows}")
+    if finished is not None:
+        _dev(finished, "finished", (torch.uint8, torch.bool))
+        if finished.numel() != rows:
+            raise ValueError(f"finished has {finished.numel()} elements, expected batch * beams = {rows}")
+    _dev(out_score, "out_score", (torch.float32,))
+    _dev(out_parent, "out_parent", (torch.int32,), (batch, n))
+    _dev(out_token, "out_token", (torch.int32,), (batch, n))
+    if out_finished is not None:
+        _dev(out_finished, "out_finished", (torch.uint8, torch.bool), (batch, n))
+    _dev(workspace, "workspace", (torch.uint8,))
+    _dev(status, "status", (torch.int32,))
+    _check(load().orpo_beam_select(_ptr(logits), ld_logits, 1 if logits.dtype == torch.bfloat16 else 0, _ptr(score),
+                                   _ptr(finished), int(eos), batch, int(beams), V, n, _ptr(out_score),
+                                   _ptr(out_parent), _ptr(out_token), _ptr(out_finished), _ptr(workspace),
+                                   workspace.numel(), _ptr(status), _stream(stream)), "orpo_beam_select")
+
+
+def orpo_beam_reorder(state, parent, length, status, stream=None):
+    """state [outer, batch * beams, rows, capacity, unit] (any dtype) follows parent [batch, beams] in place.
+
+    Only positions t < length[b] (int32 [batch]; None: all) of the capacity dimension move."""
+    if state is None or not state.is_cuda or not state.is_contiguous() or state.dim() != 5:
+        raise ValueError("state must be a contiguous CUDA tensor [outer, batch * beams, rows, capacity, unit]")
+    ld_parent = _rows(parent, "parent", (torch.int32,))
+    batch, beams = parent.shape
+    if state.shape[1] != batch * beams:
+        raise ValueError(f"state has {state.shape[1]} beams, expected batch * beams = {batch * beams}")
+    if length is not None:
+        _dev(length, "length", (torch.int32,), (batch,))
+    _dev(status, "status", (torch.int32,))
+    outer, _, rows, capacity, unit = state.shape
+    _check(load().orpo_beam_reorder(_ptr(state), _ptr(parent), ld_parent, _ptr(length), outer, batch, beams, rows,
+                                    capacity, unit * state.element_size(), _ptr(status), _stream(stream)),
+           "orpo_beam_reorder")
+
+
 def orpo_debug_gemm(A, B, C, M, N, K, a_mn_major, b_mn_major, status, stream=None):
     _dev(A, "A", BF16)
     _dev(B, "B", BF16)
@@ -394,7 +495,7 @@ def orpo_debug_wait_timeout(status, limit_ns, stream=None):
     _check(load().orpo_debug_wait_timeout(_ptr(status), int(limit_ns), _stream(stream)), "orpo_debug_wait_timeout")
 
 
-PROFILE_KINDS = 8
+PROFILE_KINDS = 11
 
 
 def orpo_profile_start():
@@ -467,3 +568,49 @@ class OrpoHead:
         with torch.cuda.graph(graph):
             self.step(*args)
         return graph
+
+
+class BeamDecoder:
+    """Owns the buffers of beam search on the quantised head and runs one decode step.
+
+    A step is the three C entry points of orpo_decode.h in order on the current stream: logits of the
+    beams' last hidden rows, selection of each batch entry's `beams` best continuations, and the states
+    following their parents.  score, finished, parent and token stay on the device; nothing waits on
+    the host, so a step can be recorded in a CUDA graph."""
+
+    def __init__(self, batch: int, beams: int, V: int, d: int, bits: int = 4, group: int = 64, softcap: float = 0.0,
+                 eos: int = -1, logits_dtype=torch.float32, device="cuda"):
+        self.batch, self.beams, self.V, self.d = batch, beams, V, d
+        self.bits, self.group, self.softcap, self.eos = bits, group, float(softcap), int(eos)
+        dev = torch.device(device)
+        ws = orpo_beam_select_workspace_bytes(batch, beams, V, beams)
+        if ws == 0:
+            raise ValueError(f"batch {batch}, beams {beams}, V {V} are out of orpo_beam_select's range")
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.logits = torch.empty((batch * beams, V), dtype=logits_dtype, device=dev)
+        self.score = torch.empty((batch, beams), dtype=torch.float32, device=dev)
+        self.finished = torch.empty((batch, beams), dtype=torch.uint8, device=dev) if self.eos >= 0 else None
+        self.parent = torch.empty((batch, beams), dtype=torch.int32, device=dev)
+        self.token = torch.empty((batch, beams), dtype=torch.int32, device=dev)
+        self.reset()
+
+    def reset(self):
+        """Start new responses: all beams of an entry hold the same prompt, so only beam 0 may propose."""
+        self.score.fill_(float("-inf"))
+        self.score[:, 0] = 0.0
+        if self.finished is not None:
+            self.finished.zero_()
+
+    def step(self, h, wq, scales, biases, states=(), length=None, stream=None):
+        """One step from the hidden rows h [batch * beams, d]; returns (parent, token) [batch, beams].
+
+        states: tensors [outer, batch * beams, rows, capacity, unit] that follow their parents, up to
+        position length[b] of each entry."""
+        orpo_head_logits_q(h, wq, scales, biases, self.bits, self.group, self.softcap, self.logits, self.status,
+                           stream)
+        orpo_beam_select(self.logits, self.score, self.finished, self.eos, self.beams, self.score, self.parent,
+                         self.token, self.finished, self.workspace, self.status, stream)
+        for state in states:
+            orpo_beam_reorder(state, self.parent, length, self.status, stream)
+        return self.parent, self.token

@@ -17,10 +17,6 @@ size_t loss_smem_bytes(int P);
 
 namespace {
 
-// Largest M, V (and debug-GEMM extent): row and column indices, tile counts rounded up to whole tiles,
-// and per-thread row chunks of the loss stay inside int32 with room to spare.
-constexpr int64_t kMaxRows = (1ll << 31) - (1ll << 16);
-
 // ---------------------------------------------------------------- driver entry point
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
@@ -41,6 +37,8 @@ struct DevInfo {
 };
 DevInfo g_dev[64];
 std::mutex g_dev_mu;
+
+}  // namespace
 
 int device_check(int* sms) {
   int dev = 0;
@@ -64,8 +62,7 @@ int device_check(int* sms) {
   return ORPO_OK;
 }
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+namespace {
 
 // ---------------------------------------------------------------- blocking
 struct BwdBlocks {
@@ -281,15 +278,7 @@ using namespace orpo;
 
 // ---------------------------------------------------------------- forward / backward implementations
 
-// Source of an affine group-quantised head (nullptr: W is bf16).
-struct QuantW {
-  const uint8_t* wq;
-  const void* scales;
-  const void* biases;
-  int bits, group;
-};
-
-int check_quant(const QuantW* q, int64_t d) {
+int orpo::check_quant(const QuantW* q, int64_t d) {
   if (!q) return ORPO_OK;
   if (!q->wq || !q->scales || !q->biases) return ORPO_ERR_NULL;
   if ((q->bits != 4 && q->bits != 8) || q->group < 8 || q->group % 8 != 0 || d % q->group != 0)
@@ -816,7 +805,8 @@ const char* orpo_status_string(int code) {
               {ORPO_STATUS_EMPTY_SEQ, "empty sequence"},
               {ORPO_STATUS_NONFINITE, "non-finite value"},
               {ORPO_STATUS_TIMEOUT, "on-chip wait timed out"},
-              {ORPO_STATUS_BOUNDS, "index out of bounds (bounds-checked build)"}};
+              {ORPO_STATUS_BOUNDS, "index out of bounds (bounds-checked build)"},
+              {ORPO_STATUS_PARENT, "beam parent or length out of range"}};
   for (const auto& b : bits) {
     if (code & b.bit) {
       if (buf[0]) strncat(buf, "; ", sizeof(buf) - strlen(buf) - 1);

@@ -1,0 +1,141 @@
+// decode_logits.cu — logits of a few rows under the quantised head (orpo_head_logits_q).
+//
+//   z[m, v] = sum_j h[m, j] W[v, j],  W[v, j] = bf16(scale q + bias),  logits = softcap(z)
+//
+// Every weight is used for M rows only, so the call is bound by reading the quantised weights once.
+//
+// Generic kernel: a warp owns one vocabulary row and a tile of 8 rows of h.  Lane l takes the
+// 8-weight slices l, l + 32, ... of the row (one 4- or 8-byte word of q, one scale and bias: a group
+// is a multiple of 8 columns), so any d that is a multiple of 8 works; the lanes' fp32 sums are
+// added in a fixed shuffle order.
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/orpo_decode.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace orpo {
+namespace {
+
+constexpr int kRowsTile = 8;
+
+struct LogitsArgs {
+  const uint16_t* h;
+  int64_t ld_h;
+  const uint8_t* wq;
+  const uint16_t* scales;
+  const uint16_t* biases;
+  int group;
+  int M, V, d;
+  float softcap;
+  void* out;
+  int64_t ld_out;
+  int out_bf16;
+  int32_t* status;
+};
+
+__device__ __forceinline__ float softcap_of(float z, float cap) {
+  if (cap <= 0.f) return z;
+  const float u = z / cap;
+  float q;
+  return cap * (fabsf(u) < kTanhSmall ? tanh_small(u) : tanh_exp(u, &q));
+}
+
+__device__ __forceinline__ void store_logit(const LogitsArgs& a, int m, int v, float z) {
+  const float x = softcap_of(z, a.softcap);
+  const int64_t at = (int64_t)m * a.ld_out + v;
+  if (a.out_bf16)
+    static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
+  else
+    static_cast<float*>(a.out)[at] = x;
+}
+
+template <int kBits>
+__global__ void __launch_bounds__(256) logits_generic_kernel(LogitsArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t v = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int m0 = blockIdx.y * kRowsTile;
+  if (v >= a.V) return;
+  const uint8_t* row = a.wq + v * ((int64_t)a.d * kBits / 8);
+  const int64_t g0 = v * (a.d / a.group);
+  float acc[kRowsTile] = {};
+  for (int c = lane; c < a.d / 8; c += 32) {
+    uint2 raw = make_uint2(0u, 0u);
+    if constexpr (kBits == 4)
+      raw.x = __ldg(reinterpret_cast<const uint32_t*>(row) + c);
+    else
+      raw = __ldg(reinterpret_cast<const uint2*>(row) + c);
+    const int64_t gi = g0 + (8 * c) / a.group;
+    const float sc = dq_bf16_to_float(__ldg(a.scales + gi)), bi = dq_bf16_to_float(__ldg(a.biases + gi));
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t q = kBits == 4 ? (raw.x >> (4 * e)) & 15u : ((e < 4 ? raw.x : raw.y) >> (8 * (e & 3))) & 255u;
+      w[e] = __uint_as_float(dq_pack2(0.f, fmaf(sc, (float)q, bi)) & 0xffff0000u);
+    }
+#pragma unroll
+    for (int m = 0; m < kRowsTile; ++m) {
+      if (m0 + m < a.M) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.h + (int64_t)(m0 + m) * a.ld_h) + c);
+        const uint32_t p[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[m] = fmaf(__uint_as_float(p[e] << 16), w[2 * e], acc[m]);
+          acc[m] = fmaf(__uint_as_float(p[e] & 0xffff0000u), w[2 * e + 1], acc[m]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < kRowsTile; ++m) {
+    float s = acc[m];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == m && m0 + m < a.M) store_logit(a, m0 + m, (int)v, s);
+  }
+}
+
+}  // namespace
+}  // namespace orpo
+
+using namespace orpo;
+
+extern "C" int orpo_head_logits_q(const void* h, int64_t ld_h, const uint8_t* wq, const void* scales,
+                                  const void* biases, int bits, int group, int64_t M, int64_t V, int64_t d,
+                                  float softcap, void* logits, int64_t ld_logits, int logits_bf16, int32_t* status,
+                                  void* stream) {
+  if (M < 0 || M > kMaxRows || V < 1 || V > kMaxRows || d < 8 || d >= (1 << 20)) return ORPO_ERR_SHAPE;
+  if (M == 0) return ORPO_OK;
+  if (ld_h < d || ld_logits < V || ld_h > (1ll << 40) || ld_logits > (1ll << 40)) return ORPO_ERR_SHAPE;
+  if (!h || !logits || !status) return ORPO_ERR_NULL;
+  const QuantW q{wq, scales, biases, bits, group};
+  if (int e = check_quant(&q, d)) return e;
+  const uintptr_t out_align = logits_bf16 ? 1 : 3;
+  if (d % 8 != 0 || ld_h % 8 != 0 || !aligned16(h) || (reinterpret_cast<uintptr_t>(logits) & out_align))
+    return ORPO_ERR_ALIGN;
+  if (!isfinite(softcap)) return ORPO_ERR_ARG;
+  int sms = 0;
+  if (int e = device_check(&sms)) return e;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  LogitsArgs a{static_cast<const uint16_t*>(h), ld_h, wq, static_cast<const uint16_t*>(scales),
+               static_cast<const uint16_t*>(biases), group, (int)M, (int)V, (int)d, softcap > 0.f ? softcap : 0.f,
+               logits, ld_logits, logits_bf16 != 0, status};
+  // rows of h in launches of at most 65535 tiles
+  const int64_t chunk = 65535ll * kRowsTile;
+  for (int64_t m = 0; m < M; m += chunk) {
+    a.h = static_cast<const uint16_t*>(h) + m * ld_h;
+    a.out = static_cast<uint8_t*>(logits) + m * ld_logits * (logits_bf16 ? 2 : 4);
+    a.M = (int)std::min(chunk, M - m);
+    const dim3 grid((unsigned)cdiv(V, 8), (unsigned)cdiv(a.M, kRowsTile));
+    prof_begin(K_LOGITS, st);
+    if (bits == 4)
+      logits_generic_kernel<4><<<grid, 256, 0, st>>>(a);
+    else
+      logits_generic_kernel<8><<<grid, 256, 0, st>>>(a);
+    prof_end(K_LOGITS, st);
+    if (cudaGetLastError() != cudaSuccess) return ORPO_ERR_CUDA;
+  }
+  return ORPO_OK;
+}

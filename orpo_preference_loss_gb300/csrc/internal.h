@@ -24,8 +24,26 @@ inline cudaError_t opt_in_smem(Kernel kernel, int bytes, std::atomic<int> (&done
   return e;
 }
 
+// ---- host-side checks shared by the entry points
+// Largest M, V (and debug-GEMM extent): row and column indices, tile counts rounded up to whole tiles,
+// and per-thread row chunks of the loss stay inside int32 with room to spare.
+constexpr int64_t kMaxRows = (1ll << 31) - (1ll << 16);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int device_check(int* sms);  // ORPO_OK on a compute-capability 10.3 device (its SM count in *sms)
+
+// Source of an affine group-quantised head (nullptr: W is bf16).
+struct QuantW {
+  const uint8_t* wq;
+  const void* scales;
+  const void* biases;
+  int bits, group;
+};
+int check_quant(const QuantW* q, int64_t d);
+
 // ---- launch timing (profile.cu); no-ops unless orpo_profile_start() was called
-enum KernelKind { K_FWD = 0, K_MERGE, K_LOSS, K_REC, K_GEMM, K_DEBUG, K_DEQUANT, K_SKIP, K_NKINDS };
+enum KernelKind { K_FWD = 0, K_MERGE, K_LOSS, K_REC, K_GEMM, K_DEBUG, K_DEQUANT, K_SKIP, K_LOGITS, K_BEAM, K_REORDER,
+                  K_NKINDS };
 void prof_begin(int kind, cudaStream_t st);
 void prof_end(int kind, cudaStream_t st);
 

@@ -33,8 +33,9 @@ cudaEvent_t take_event() {
   return e;
 }
 
-const char* kNames[K_NKINDS] = {"fwd_logits",    "fwd_merge",  "orpo_loss", "bwd_recompute",
-                                "bwd_grad_gemm", "debug_gemm", "dequant",   "bwd_skip_plan"};
+const char* kNames[K_NKINDS] = {"fwd_logits",    "fwd_merge",    "orpo_loss",   "bwd_recompute",
+                                "bwd_grad_gemm", "debug_gemm",   "dequant",     "bwd_skip_plan",
+                                "logits_q",      "beam_select",  "beam_reorder"};
 
 }  // namespace
 
