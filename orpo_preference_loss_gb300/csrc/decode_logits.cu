@@ -9,10 +9,12 @@
 // is a multiple of 8 columns), so any d that is a multiple of 8 works; the lanes' fp32 sums are
 // added in a fixed shuffle order.
 #include <math.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
 #include "../../include/orpo_decode.h"
+#include "decode_logits.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -20,37 +22,6 @@ namespace orpo {
 namespace {
 
 constexpr int kRowsTile = 8;
-
-struct LogitsArgs {
-  const uint16_t* h;
-  int64_t ld_h;
-  const uint8_t* wq;
-  const uint16_t* scales;
-  const uint16_t* biases;
-  int group;
-  int M, V, d;
-  float softcap;
-  void* out;
-  int64_t ld_out;
-  int out_bf16;
-  int32_t* status;
-};
-
-__device__ __forceinline__ float softcap_of(float z, float cap) {
-  if (cap <= 0.f) return z;
-  const float u = z / cap;
-  float q;
-  return cap * (fabsf(u) < kTanhSmall ? tanh_small(u) : tanh_exp(u, &q));
-}
-
-__device__ __forceinline__ void store_logit(const LogitsArgs& a, int m, int v, float z) {
-  const float x = softcap_of(z, a.softcap);
-  const int64_t at = (int64_t)m * a.ld_out + v;
-  if (a.out_bf16)
-    static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
-  else
-    static_cast<float*>(a.out)[at] = x;
-}
 
 // ---------------------------------------------------------------- streaming kernel
 //
@@ -88,37 +59,6 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
-}
-
-__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) { return (x & mask) | bits; }
-
-constexpr uint32_t kOne2 = 0x3F803F80u;     // (1, 1) in bf16
-constexpr uint32_t kMinus128 = 0xC300C300u;  // (-128, -128)
-
-// Eight 4-bit values -> bf16(s q + b) as the pairs (0,4), (1,5), (2,6), (3,7).  0x4300 | q is the
-// bf16 value 128 + q, and subtracting 128 is exact; the product and sum round once.
-__device__ __forceinline__ void dequant4(uint32_t w, uint32_t s, uint32_t b, uint32_t (&p)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p[i] = bf16x2_fma(bf16x2_fma(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u), kOne2, kMinus128), s, b);
-}
-
-// Four 8-bit values -> bf16(s q + b) as the pairs (0,2), (1,3).  The low seven bits make 128 + low as
-// above; the high bit, shifted into bit 14, is the bf16 value 2 or 0 and adds 64 times itself.
-__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t b, uint32_t (&p)[2]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t x = w >> (8 * i);
-    const uint32_t low = bf16x2_fma(and_or(x, 0x007F007Fu, 0x43004300u), kOne2, kMinus128);
-    const uint32_t q = bf16x2_fma((x << 7) & 0x40004000u, 0x42804280u, low);  // 64 * (2 or 0) + low
-    p[i] = bf16x2_fma(q, s, b);
-  }
 }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -391,6 +331,7 @@ extern "C" int orpo_head_logits_q(const void* h, int64_t ld_h, const uint8_t* wq
   // The streaming kernel wants 16-byte pieces of a row that lie in one group.
   const int per_thread = bits == 4 ? 32 : 16;
   const bool streamed = d % per_thread == 0 && group % per_thread == 0 && aligned16(wq);
+  const bool tensor = streamed && group % 32 == 0 && getenv("ORPO_LOGITS_STREAM") == nullptr;
   // rows of h in launches of at most 65535 tiles
   const int64_t chunk = 65535ll * kRowsTile;
   for (int64_t m = 0; m < M; m += chunk) {
@@ -398,7 +339,8 @@ extern "C" int orpo_head_logits_q(const void* h, int64_t ld_h, const uint8_t* wq
     a.out = static_cast<uint8_t*>(logits) + m * ld_logits * (logits_bf16 ? 2 : 4);
     a.M = (int)std::min(chunk, M - m);
     prof_begin(K_LOGITS, st);
-    const cudaError_t e = streamed ? (bits == 4 ? launch_stream_rows<4>(a, sms, st) : launch_stream_rows<8>(a, sms, st))
+    const cudaError_t e = tensor     ? launch_logits_tc(a, bits, sms, st)
+                          : streamed ? (bits == 4 ? launch_stream_rows<4>(a, sms, st) : launch_stream_rows<8>(a, sms, st))
                                    : launch_generic(a, bits, st);
     prof_end(K_LOGITS, st);
     if (e != cudaSuccess) return ORPO_ERR_CUDA;

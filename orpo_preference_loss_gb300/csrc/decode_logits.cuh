@@ -1,0 +1,87 @@
+// decode_logits.cuh — what the kernels of orpo_head_logits_q share: arguments, the softcap and store of
+// one logit, and the dequantisation of packed weights into bf16 pairs.
+#pragma once
+
+#include <stdint.h>
+
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace orpo {
+
+struct LogitsArgs {
+  const uint16_t* h;
+  int64_t ld_h;
+  const uint8_t* wq;
+  const uint16_t* scales;
+  const uint16_t* biases;
+  int group;
+  int M, V, d;
+  float softcap;
+  void* out;
+  int64_t ld_out;
+  int out_bf16;
+  int32_t* status;
+};
+
+__device__ __forceinline__ float softcap_of(float z, float cap) {
+  if (cap <= 0.f) return z;
+  const float u = z / cap;
+  float q;
+  return cap * (fabsf(u) < kTanhSmall ? tanh_small(u) : tanh_exp(u, &q));
+}
+
+__device__ __forceinline__ void store_logit(const LogitsArgs& a, int m, int v, float z) {
+  const float x = softcap_of(z, a.softcap);
+  const int64_t at = (int64_t)m * a.ld_out + v;
+  if (a.out_bf16)
+    static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
+  else
+    static_cast<float*>(a.out)[at] = x;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// (x & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+  return r;
+}
+
+constexpr uint32_t k128x2 = 0x43004300u;  // (128, 128) in bf16
+
+// Eight 4-bit values -> bf16(s q + b) as the pairs (0,4), (1,5), (2,6), (3,7).  0x4300 | q is the
+// bf16 value 128 + q, and subtracting 128 is exact; the product and sum round once.
+__device__ __forceinline__ void dequant4(uint32_t w, uint32_t s, uint32_t b, uint32_t (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    p[i] = bf16x2_fma(bf16x2_sub(and_or(w >> (4 * i), 0x000F000Fu, k128x2), k128x2), s, b);
+}
+
+// Four 8-bit values -> bf16(s q + b) as the pairs (0,2), (1,3).  The low seven bits make 128 + low as
+// above; the high bit, shifted into bit 14, is the bf16 value 2 or 0 and adds 64 times itself.
+__device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t b, uint32_t (&p)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = w >> (8 * i);
+    const uint32_t low = bf16x2_sub(and_or(x, 0x007F007Fu, k128x2), k128x2);
+    const uint32_t q = bf16x2_fma((x << 7) & 0x40004000u, 0x42804280u, low);  // 64 * (2 or 0) + low
+    p[i] = bf16x2_fma(q, s, b);
+  }
+}
+
+// Tensor-core kernel (decode_logits_tc.cu); cudaErrorNotSupported when a tensor map cannot be made.
+cudaError_t launch_logits_tc(const LogitsArgs& a, int bits, int sms, cudaStream_t st);
+
+}  // namespace orpo

@@ -1,0 +1,612 @@
+// decode_logits_tc.cu — logits of up to 64 rows of h per pass over the quantised head, on tcgen05.
+//
+//   D[v, m] = sum_k W[v, k] h[m, k],  W[v, k] = bf16(scale q + bias)
+//
+// A CTA takes tiles of 128 vocabulary rows.  The weights are the A operand (128 rows of the tile, in
+// tensor memory) and h the B operand (N = 16, 32 or 64 columns, in shared memory), so the tensor core
+// does as little more than the 2 M V d useful flop as its least N allows, and the dequantised weights
+// never cross shared memory (at 40 weights a clock per SM, writing them there and reading them back
+// would take 160 B/clk of its 128).  What a call costs beside reading the weights once is turning q
+// into bf16: 15 instructions per 8 weights (dequant4), about 65% of the issue slots at the rate the
+// weights arrive.
+//
+// Roles (warps):
+//   0       TMA: 128-byte segments of the tile's 128 rows of q (16 KiB boxes, 128-byte swizzle) into a
+//           ring, and h, either all of it once (resident) or per 128 columns (streamed)
+//   1, 2    MMA issue: the even and the odd units of 128 columns, each into accumulators of its own
+//   4..7    scales and biases, a thread per vocabulary row: 16 groups at a time from global memory, then
+//           a (scale, bias) word per 32 columns beside each segment of q in the ring
+//   8..11   h into the dequantised order (below), then sums and output of the accumulators
+//   12..    dequantisation, 4 warps per group, a thread per vocabulary row; group i takes units of 128
+//           columns i, i + kGroups, ...
+//
+// Order of k: dequant4 yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights (dequant8
+// (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes in place.
+// Accuracy: the tensor core truncates as it accumulates (measured: 1e-9 of the result per product, one
+// sign), so an accumulator spans 512 columns and those sums are added in registers, rounding.
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/orpo_decode.h"
+#include "decode_logits.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace orpo {
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr int kSegBytes = 128;                        // bytes of a row per segment
+constexpr int kStageBytes = kTileRows * kSegBytes;    // 16 KiB
+constexpr int kUnitK = 128;                           // columns per A buffer (64 tensor-memory columns)
+constexpr int kAccUnits = 4;                          // units per accumulator: 512 columns
+constexpr int kScaleBytes = kSegBytes / 16 * kTileRows * 4;  // words of a segment: 4 KiB (8-bit: half used)
+constexpr int kScaleGroups = 16;                      // groups per fetch of a row's scales
+constexpr int kScratchBytes = kTileRows * kScaleGroups * 4;  // and their (scale, bias) words
+constexpr int kMaxStages = 8;
+constexpr int kMaxH = 8;  // streamed h: units in the ring
+constexpr int kMaxABufs = 7;
+constexpr int kMma = 2;  // warps that issue
+constexpr int kScaleWarp = 4, kSumWarp = 8;
+constexpr uint64_t kLimitNs = 4000000000ull;          // far above any legitimate wait
+constexpr int kSmemLimit = 232448 - 1024;             // less the slack that aligns the base
+
+struct TcCtl {
+  uint64_t w_full[kMaxStages], w_empty[kMaxStages];
+  uint64_t a_full[kMaxABufs], a_empty[kMaxABufs];
+  uint64_t d_full[2 * kMma], d_empty[2 * kMma];  // [MMA warp][set]
+  uint64_t h_raw[kMaxH], h_full[kMaxH], h_empty[kMaxH];
+  uint64_t drain[kMma];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+};
+constexpr int kCtlBytes = 1024;
+static_assert(sizeof(TcCtl) <= kCtlBytes, "control block");
+
+struct TcArgs {
+  LogitsArgs a;
+  int tiles, segs;        // tiles of 128 rows, segments per row
+  int units;              // 128-column units per row: segs * units per segment
+  int ngroups;            // groups per row
+  int spb;                // segments per 16 groups
+  uint32_t gmul;          // ceil(2^31 / (group / 32))
+  int stages;             // weight ring
+  int hslots;             // streamed h: ring slots; 0: h is resident
+  int wide_scales;        // rows of scales and biases are 16-byte aligned
+};
+
+// One wait of up to kPollNs in the barrier unit: the polls of eight waiting warps at the default
+// interval took as many issue slots as the dequantisation.
+constexpr uint32_t kPollNs = 20000;
+__device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded wait: false on a timeout (reported) or when another role gave up.
+__device__ __forceinline__ bool wait_bar(TcCtl* ctl, uint64_t* bar, uint32_t parity, int32_t* status) {
+  if (poll_bar(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!poll_bar(bar, parity)) {
+    if (ctl->abort_flag) return false;
+    if (globaltimer_ns() - t0 > kLimitNs) {
+      atomicOr(status, ORPO_STATUS_TIMEOUT);
+      ctl->abort_flag = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+// The same for a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool wait_warp(TcCtl* ctl, uint64_t* bar, uint32_t parity, int32_t* status) {
+  return __all_sync(0xffffffffu, wait_bar(ctl, bar, parity, status));
+}
+
+__device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > 200000000ull) return;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, bf16 in, fp32 accumulate
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+#define ORPO_IN32(r)                                                                                          \
+  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),   \
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),            \
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),            \
+      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+
+// 32 columns of this thread's lane (warp's quadrant)
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      ORPO_IN32(r)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Warps that sum: four per 32 columns of the accumulator at most
+constexpr int sum_groups(int np) { return np > 32 ? np / 32 : 1; }
+constexpr int first_dequant_warp(int np) { return kSumWarp + 4 * sum_groups(np); }
+constexpr int tc_threads(int np, int groups) { return 32 * (first_dequant_warp(np) + 4 * groups); }
+
+template <int kBits, int NP, int kGroups>
+__global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
+    logits_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
+                     const __grid_constant__ TcArgs p) {
+  constexpr int kUnits = kBits == 4 ? 2 : 1;        // units per segment
+  constexpr int kSegK = kUnits * kUnitK;            // columns per segment
+  constexpr uint32_t kHUnit = NP * kUnitK * 2;      // bytes of a unit of h: two blocks of 64 columns
+  constexpr int kChunkUnits = kAccUnits * kMma;              // units per set of accumulators
+  constexpr uint32_t kABufs = (512 - 2 * kMma * NP) / 64;   // units of A in tensor memory, beside two sets
+  constexpr uint32_t kTmemA = 512 - 64 * kABufs;            // first column of A; the sets start at 0
+  constexpr int kSums = sum_groups(NP), kCols = NP / kSums, kFirstDequantWarp = first_dequant_warp(NP);
+  static_assert(2 * kMma * NP <= kTmemA && kABufs <= kMaxABufs && kGroups <= kABufs, "tensor memory");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const LogitsArgs& a = p.a;
+  uint8_t* const ring = smem;
+  uint8_t* const hbuf = ring + p.stages * kStageBytes;
+  uint8_t* const sring = hbuf + (p.hslots ? p.hslots : p.units) * kHUnit;  // scale words, by ring stage
+  uint8_t* const scratch = sring + p.stages * kScaleBytes;
+  TcCtl* const ctl = reinterpret_cast<TcCtl*>(scratch + kScratchBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m0 = blockIdx.y * NP;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 4), mbar_init(&ctl->w_empty[i], 4 * kUnits);
+    for (int i = 0; i < kMaxABufs; ++i) mbar_init(&ctl->a_full[i], 4), mbar_init(&ctl->a_empty[i], 1);
+    for (int i = 0; i < 2 * kMma; ++i) mbar_init(&ctl->d_full[i], 1), mbar_init(&ctl->d_empty[i], 4 * kSums);
+    for (int i = 0; i < kMaxH; ++i)
+      mbar_init(&ctl->h_raw[i], 1), mbar_init(&ctl->h_full[i], 4 * kSums), mbar_init(&ctl->h_empty[i], 1);
+    for (int i = 0; i < kMma; ++i) mbar_init(&ctl->drain[i], 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<1>(&ctl->tmem_base, 512);
+    tmem_relinquish<1>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const int my_tiles = (p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const bool resident = p.hslots == 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- TMA
+      const int64_t total = (int64_t)my_tiles * p.segs;
+      uint32_t hu = 0;  // streamed h units issued
+      bool ok = true;
+      auto load_h = [&](uint64_t* bar, uint8_t* dst, int unit) {
+        tma_load_2d(&map_h, smem_u32(bar), dst, unit * kUnitK, m0);
+        tma_load_2d(&map_h, smem_u32(bar), dst + kHUnit / 2, unit * kUnitK + 64, m0);
+      };
+      int tile = blockIdx.x, seg = 0;
+      uint32_t it = 0;
+      if (resident) {
+        mbar_arrive_expect_tx(&ctl->h_raw[0], p.units * kHUnit);
+        for (int u = 0; u < p.units; ++u) load_h(&ctl->h_raw[0], hbuf + u * kHUnit, u);
+        hu = 1;
+      }
+      for (; (int64_t)it < total; ++it) {
+        const uint32_t s = it % p.stages, ph = (it / p.stages) & 1u;
+        if (!wait_bar(ctl, &ctl->w_empty[s], ph ^ 1u, a.status)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&ctl->w_full[s], kStageBytes);
+        tma_load_2d(&map_w, smem_u32(&ctl->w_full[s]), ring + s * kStageBytes, seg * kSegBytes, tile * kTileRows);
+        if (!resident) {
+          for (int j = 0; ok && j < kUnits; ++j, ++hu) {
+            const uint32_t hs = hu % p.hslots, hp = (hu / p.hslots) & 1u;
+            if (!wait_bar(ctl, &ctl->h_empty[hs], hp ^ 1u, a.status)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&ctl->h_raw[hs], kHUnit);
+            load_h(&ctl->h_raw[hs], hbuf + hs * kHUnit, seg * kUnits + j);
+          }
+          if (!ok) {
+            ++it;
+            break;
+          }
+        }
+        if (++seg == p.segs) seg = 0, tile += gridDim.x;
+      }
+      if (!ok) {  // let the loads in flight land before the CTA can exit
+        const uint32_t w0 = it > (uint32_t)p.stages ? it - p.stages : 0;
+        for (uint32_t k = w0; k < it; ++k) drain_bar(&ctl->w_full[k % p.stages], (k / p.stages) & 1u);
+        if (resident) {
+          if (hu) drain_bar(&ctl->h_raw[0], 0);
+        } else {
+          const uint32_t h0 = hu > (uint32_t)p.hslots ? hu - p.hslots : 0;
+          for (uint32_t k = h0; k < hu; ++k) drain_bar(&ctl->h_raw[k % p.hslots], (k / p.hslots) & 1u);
+        }
+      }
+    }
+  } else if (warp <= kMma) {
+    // ---- MMA: units me, me + kMma, ... of every tile.  The whole warp walks the loop, so that addresses
+    // and descriptors stay in uniform registers, and one elected lane issues: with a single thread in
+    // the loop a product took 109 clocks to issue.
+    const int me = warp - 1;
+    const bool leader = elect_one();
+    const uint32_t idesc = make_idesc_bf16(kTileRows, NP, 0, 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(hbuf), 16, 1024);
+    uint32_t buf = me, ap = 0;  // A buffer and parity
+    uint32_t db = 0, dp = 1;    // set of accumulators, parity of its release
+    uint32_t hs = me, hp = 0;   // streamed h: ring slot and parity
+    bool ok = !resident || wait_warp(ctl, &ctl->h_full[0], 0, a.status);
+    int first = me;             // my first unit of the tile
+    for (int i = 0; ok && i < my_tiles; ++i) {
+      int j = 0, ku = first;    // units in the accumulator, unit of the tile
+      for (; ku < p.units; ku += kMma) {
+        if (j == 0) ok = wait_warp(ctl, &ctl->d_empty[2 * me + db], dp, a.status);
+        ok = ok && wait_warp(ctl, &ctl->a_full[buf], ap, a.status);
+        if (!resident) ok = ok && wait_warp(ctl, &ctl->h_full[hs], hp, a.status);
+        if (!ok) break;
+        tc_fence_after();
+        const bool last = j == kAccUnits - 1 || ku + kMma >= p.units;
+        if (leader) {
+          const uint64_t desc = desc0 + (uint64_t)((resident ? (uint32_t)ku : hs) * (kHUnit >> 4));
+          const uint32_t at = tm + kTmemA + buf * 64, dt = tm + (2 * me + db) * NP;
+#pragma unroll
+          for (int kk = 0; kk < kUnitK / 16; ++kk)
+            umma_bf16_ta(dt, at + kk * 8, desc + ((kk >> 2) * (kHUnit / 2) + (kk & 3) * 32) / 16, idesc,
+                         (kk | j) != 0 ? 1u : 0u);
+          umma_commit(&ctl->a_empty[buf]);
+          if (!resident) umma_commit(&ctl->h_empty[hs]);
+          if (last) umma_commit(&ctl->d_full[2 * me + db]);
+        }
+        __syncwarp();
+        ++j;
+        if (last) {
+          j = 0;
+          db ^= 1u;
+          dp ^= db ^ 1u;  // after both sets
+        }
+        buf += kMma;
+        if (buf >= kABufs) buf -= kABufs, ap ^= 1u;
+        if (!resident) {
+          hs += kMma;
+          if (hs >= (uint32_t)p.hslots) hs -= p.hslots, hp ^= 1u;
+        }
+      }
+      first = ku - p.units;  // units alternate across tiles too
+    }
+    if (leader) {  // every issued MMA has finished before tensor memory is released
+      umma_commit(&ctl->drain[me]);
+      drain_bar(&ctl->drain[me], 0);
+    }
+  } else if (warp < kScaleWarp) {
+    // spare
+  } else if (warp < kSumWarp) {
+    // ---- scales and biases of row (warp - kScaleWarp) * 32 + lane of the tile
+    const int row = (warp - kScaleWarp) * 32 + lane;
+    uint32_t cur[16], nxt[16];  // 16 groups: 8 words of scales, 8 of biases
+    auto fetch = [&](uint32_t (&r)[16], int tile, int g0) {
+      const int64_t v = (int64_t)tile * kTileRows + row;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[i] = 0;
+      if (v >= a.V) return;
+      const uint16_t* src[2] = {a.scales + v * p.ngroups + g0, a.biases + v * p.ngroups + g0};
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (p.wide_scales) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (g0 + 8 * i < p.ngroups) {
+              const uint4 x = __ldg(reinterpret_cast<const uint4*>(src[w]) + i);
+              r[8 * w + 4 * i] = x.x, r[8 * w + 4 * i + 1] = x.y, r[8 * w + 4 * i + 2] = x.z, r[8 * w + 4 * i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (g0 + i < p.ngroups) r[8 * w + i / 2] |= (uint32_t)__ldg(src[w] + i) << (16 * (i & 1));
+        }
+      }
+    };
+    const uint32_t mine = smem_u32(scratch) + row * 4;  // written and read by this thread only
+    const uint32_t out = smem_u32(sring) + row * 4;
+    uint32_t stage = 0, ph = 0;
+    bool ok = true;
+    fetch(nxt, blockIdx.x, 0);
+    for (int i = 0; ok && i < my_tiles; ++i) {
+      const int tile = blockIdx.x + i * (int)gridDim.x;
+      for (int seg = 0, in = 0; seg < p.segs; ++seg) {
+        if (in == 0) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) cur[j] = nxt[j];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sts32(mine + (2 * j) * (kTileRows * 4), __byte_perm(cur[j], cur[8 + j], 0x5410));
+            sts32(mine + (2 * j + 1) * (kTileRows * 4), __byte_perm(cur[j], cur[8 + j], 0x7632));
+          }
+          const int g1 = (seg / p.spb + 1) * kScaleGroups;  // the next 16, of this tile or the next
+          if (g1 < p.ngroups)
+            fetch(nxt, tile, g1);
+          else if (i + 1 < my_tiles)
+            fetch(nxt, tile + (int)gridDim.x, 0);
+        }
+        ok = wait_warp(ctl, &ctl->w_empty[stage], ph ^ 1u, a.status);
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < kSegK / 32; ++j) {
+          const uint32_t gi = (uint32_t)(((uint64_t)(uint32_t)(in * (kSegK / 32) + j) * p.gmul) >> 31);
+          sts32(out + stage * kScaleBytes + j * (kTileRows * 4), lds32(mine + gi * (kTileRows * 4)));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->w_full[stage]);
+        if (++stage == (uint32_t)p.stages) stage = 0, ph ^= 1u;
+        if (++in == p.spb) in = 0;
+      }
+    }
+  } else if (warp < kFirstDequantWarp) {
+    // ---- h into the dequantised order, sums and output
+    const int q = warp & 3, n0 = (warp - kSumWarp) / 4 * kCols, tid = threadIdx.x - 32 * kSumWarp;
+    const int live = min(NP, a.M - m0);           // rows of h; the others are zero
+    auto reorder_h = [&](uint8_t* base, int n) {  // n blocks of [NP rows, 64 columns], in place
+      const uint32_t b = smem_u32(base);
+      for (int j = tid; j < n * live * 8; j += 128 * kSums) {
+        const int blk = j / (live * 8), i = blk * (NP * 8) + j - blk * (live * 8);  // 16-byte piece
+        const uint4 x = lds128(b + i * 16);
+        if constexpr (kBits == 4)
+          st_shared_v4(b + i * 16, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+        else
+          st_shared_v4(b + i * 16, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
+                       __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    bool ok = true;
+    if (resident) {
+      ok = wait_warp(ctl, &ctl->h_raw[0], 0, a.status);
+      if (ok) {
+        reorder_h(hbuf, p.units * 2);
+        if (lane == 0) mbar_arrive(&ctl->h_full[0]);
+      }
+    }
+    float acc[kCols];  // columns n0 on
+    uint32_t hu = 0;
+    const int chunks = (p.units + kChunkUnits - 1) / kChunkUnits;
+    const int64_t total = (int64_t)my_tiles * chunks;
+    // streamed h runs one set of accumulators ahead of the one that is read
+    int64_t fed = 0;
+    auto feed = [&]() {
+      const int n = min(kChunkUnits, p.units - (int)(fed % chunks) * kChunkUnits);
+      for (int j = 0; ok && j < n; ++j, ++hu) {
+        const uint32_t hs = hu % p.hslots;
+        ok = wait_warp(ctl, &ctl->h_raw[hs], (hu / p.hslots) & 1u, a.status);
+        if (!ok) break;
+        reorder_h(hbuf + hs * kHUnit, 2);
+        if (lane == 0) mbar_arrive(&ctl->h_full[hs]);
+      }
+      ++fed;
+    };
+    uint32_t db[kMma] = {}, dp[kMma] = {};  // per MMA warp: set and parity
+    int first[kMma];                        // and its first unit of the tile
+#pragma unroll
+    for (int w = 0; w < kMma; ++w) first[w] = w;
+    for (int i = 0; ok && i < my_tiles; ++i) {
+#pragma unroll
+      for (int n = 0; n < kCols; ++n) acc[n] = 0.f;
+      for (int c = 0; ok && c < chunks; ++c) {
+        if (!resident)
+          while (ok && fed < total && fed <= (int64_t)i * chunks + c + 1) feed();
+#pragma unroll
+        for (int w = 0; w < kMma; ++w) {
+          if (!ok || first[w] + c * kChunkUnits >= p.units) continue;  // no unit of this warp's here
+          ok = wait_warp(ctl, &ctl->d_full[2 * w + db[w]], dp[w], a.status);
+          if (!ok) continue;
+          tc_fence_after();
+#pragma unroll
+          for (int n = 0; n < kCols; n += 16) {
+            uint32_t r[16];
+            tmem_ld16(tmem + (2 * w + db[w]) * NP + n0 + n + ((uint32_t)(32 * q) << 16), r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[n + e] += __uint_as_float(r[e]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->d_empty[2 * w + db[w]]);
+          db[w] ^= 1u;
+          dp[w] ^= db[w] ^ 1u;
+        }
+      }
+      if (!ok) break;
+      const int64_t v = (int64_t)(blockIdx.x + i * gridDim.x) * kTileRows + 32 * q + lane;
+      if (v < a.V) {
+#pragma unroll
+        for (int n = 0; n < kCols; ++n)
+          if (m0 + n0 + n < a.M) store_logit(a, m0 + n0 + n, (int)v, acc[n]);
+      }
+#pragma unroll
+      for (int w = 0; w < kMma; ++w) {  // the warp's units go on alternating in the next tile
+        const int over = (p.units - first[w] + kMma - 1) / kMma * kMma + first[w] - p.units;
+        first[w] = first[w] < p.units ? over : first[w] - p.units;
+      }
+    }
+  } else {
+    // ---- dequantisation
+    const int wg = (warp - kFirstDequantWarp) >> 2, q = warp & 3, row = 32 * q + lane;
+    // unit u: half u % kUnits of segment u / kUnits; the group goes on by kGroups units at a time
+    constexpr uint32_t kStep = kGroups / kUnits;
+    static_assert(kGroups % kUnits == 0, "a group keeps to one half of the segments");
+    const uint32_t half = wg % kUnits, swz = (uint32_t)(row & 7) << 4;
+    const uint32_t wrow = smem_u32(ring) + row * kSegBytes;
+    const uint32_t srow = smem_u32(sring) + row * 4 + half * (4 * kTileRows * 4);
+    const uint32_t trow = tmem + kTmemA + ((uint32_t)(32 * q) << 16);
+    uint32_t stage = wg / kUnits, wph = 0;  // weight ring (kStep <= stages)
+    uint32_t buf = wg, aph = 0;             // A buffer (kGroups <= kABufs)
+    bool ok = true;
+    for (int64_t left = (int64_t)my_tiles * p.segs - wg / kUnits; left > 0; left -= kStep) {
+      ok = wait_warp(ctl, &ctl->w_full[stage], wph, a.status);
+      if (!ok) break;
+      const uint32_t wst = wrow + stage * kStageBytes, sst = srow + stage * kScaleBytes;
+#pragma unroll 1  // one copy of the body: more would not stay in the instruction cache
+      for (int part = 0; part < 2; ++part) {  // 64 columns: 32 words of tensor memory
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // 32 columns: one group
+          const uint32_t sw = lds32(sst + (part * 2 + i) * (kTileRows * 4));
+          const uint32_t s2 = __byte_perm(sw, 0, 0x1010), b2 = __byte_perm(sw, 0, 0x3232);
+          const uint32_t piece = half * 4 + part * 2 + i;
+          if constexpr (kBits == 4) {
+            const uint4 w = lds128(wst + ((piece << 4) ^ swz));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t x[4];
+              dequant4(ww[e], s2, b2, x);
+#pragma unroll
+              for (int f = 0; f < 4; ++f) r[16 * i + 4 * e + f] = x[f];
+            }
+          } else {
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const uint4 w = lds128(wst + (((2 * piece + o) << 4) ^ swz));
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t x[2];
+                dequant8(ww[e], s2, b2, x);
+                r[16 * i + 8 * o + 2 * e] = x[0], r[16 * i + 8 * o + 2 * e + 1] = x[1];
+              }
+            }
+          }
+        }
+        if (part == 0) {
+          ok = wait_warp(ctl, &ctl->a_empty[buf], aph ^ 1u, a.status);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st32(trow + buf * 64 + part * 32, r);
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->w_empty[stage]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->a_full[buf]);
+      buf += kGroups;
+      if (buf >= kABufs) buf -= kABufs, aph ^= 1u;
+      stage += kStep;
+      if (stage >= (uint32_t)p.stages) stage -= p.stages, wph ^= 1u;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, 512);
+  }
+}
+
+template <int kBits, int NP, int kGroups>
+cudaError_t launch_np(const LogitsArgs& a, int sms, cudaStream_t st) {
+  constexpr int kUnits = kBits == 4 ? 2 : 1;
+  constexpr int kHUnit = NP * kUnitK * 2;
+  static std::atomic<int> done[64];
+  auto kernel = logits_tc_kernel<kBits, NP, kGroups>;
+  if (cudaError_t e = opt_in_smem(kernel, kSmemLimit + 1024, done)) return e;
+  TcArgs p;
+  p.a = a;
+  const int64_t row_bytes = (int64_t)a.d * kBits / 8;
+  p.tiles = (int)cdiv(a.V, kTileRows);
+  p.segs = (int)cdiv(row_bytes, kSegBytes);
+  p.units = p.segs * kUnits;
+  p.ngroups = a.d / a.group;
+  p.spb = kScaleGroups * a.group / (kUnits * kUnitK);
+  const uint32_t per = (uint32_t)(a.group / 32);
+  p.gmul = (uint32_t)(((1ull << 31) + per - 1) / per);
+  p.wide_scales = p.ngroups % 8 == 0 && aligned16(a.scales) && aligned16(a.biases);
+  // h resident where at least four weight stages fit beside it, else streamed through up to 8 units
+  const int fixed = kScratchBytes + kCtlBytes, stage = kStageBytes + kScaleBytes;
+  const int64_t all_h = (int64_t)p.units * kHUnit;
+  if (all_h <= kSmemLimit - fixed - 4 * stage) {
+    p.hslots = 0;
+    p.stages = (int)std::min<int64_t>(kMaxStages, (kSmemLimit - fixed - all_h) / stage);
+  } else {
+    p.hslots = std::min(kMaxH, (64 << 10) / kHUnit);
+    p.stages = std::min(kMaxStages, (kSmemLimit - fixed - p.hslots * kHUnit) / stage);
+  }
+  const int smem = p.stages * stage + (p.hslots ? p.hslots * kHUnit : (int)all_h) + fixed + 1024;
+  CUtensorMap mw, mh;
+  if (!encode_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq, row_bytes, a.V, row_bytes, kSegBytes, kTileRows) ||
+      !encode_map_2d(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.h, a.d, a.M, a.ld_h * 2, 64, NP))
+    return cudaErrorNotSupported;
+  const dim3 grid((unsigned)std::min(p.tiles, sms), (unsigned)cdiv(a.M, NP));
+  kernel<<<grid, tc_threads(NP, kGroups), smem, st>>>(mw, mh, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_logits_tc(const LogitsArgs& a, int bits, int sms, cudaStream_t st) {
+  if (a.M <= 16) return bits == 4 ? launch_np<4, 16, 4>(a, sms, st) : launch_np<8, 16, 4>(a, sms, st);
+  if (a.M <= 32) return bits == 4 ? launch_np<4, 32, 4>(a, sms, st) : launch_np<8, 32, 4>(a, sms, st);
+  return bits == 4 ? launch_np<4, 64, 2>(a, sms, st) : launch_np<8, 64, 2>(a, sms, st);
+}
+
+}  // namespace orpo
