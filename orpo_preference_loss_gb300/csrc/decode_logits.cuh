@@ -52,6 +52,12 @@ __device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // (x & mask) | bits in one instruction
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
   uint32_t r;
@@ -79,6 +85,23 @@ __device__ __forceinline__ void dequant8(uint32_t w, uint32_t s, uint32_t b, uin
     const uint32_t q = bf16x2_fma((x << 7) & 0x40004000u, 0x42804280u, low);  // 64 * (2 or 0) + low
     p[i] = bf16x2_fma(q, s, b);
   }
+}
+
+// The same results in 9 instructions per 8 4-bit weights instead of 15 (5 instead of 13 per 4 8-bit
+// weights).  The bf16 with the bit pattern q, 0 <= q < 256, is q 2^-133 exactly: subnormals and the first
+// normal binade are one linear scale.  So the masked bits are an operand as they stand, with the scale
+// multiplied by 2^133 (exact while |s| < 2^-5, s133), or by 2^129 for a nibble left in bits 4..7
+// (s129); bf16 fma takes subnormal operands at full rate, and product and sum still round once.
+__device__ __forceinline__ void dequant4_scaled(uint32_t w, uint32_t s133, uint32_t s129, uint32_t b, uint32_t (&p)[4]) {
+  const uint32_t v = w >> 8;
+  p[0] = bf16x2_fma(w & 0x000F000Fu, s133, b);
+  p[1] = bf16x2_fma(w & 0x00F000F0u, s129, b);
+  p[2] = bf16x2_fma(v & 0x000F000Fu, s133, b);
+  p[3] = bf16x2_fma(v & 0x00F000F0u, s129, b);
+}
+__device__ __forceinline__ void dequant8_scaled(uint32_t w, uint32_t s133, uint32_t b, uint32_t (&p)[2]) {
+  p[0] = bf16x2_fma(w & 0x00FF00FFu, s133, b);
+  p[1] = bf16x2_fma((w >> 8) & 0x00FF00FFu, s133, b);
 }
 
 // Tensor-core kernel (decode_logits_tc.cu); cudaErrorNotSupported when a tensor map cannot be made.

@@ -7,21 +7,21 @@
 // does as little more than the 2 M V d useful flop as its least N allows, and the dequantised weights
 // never cross shared memory (at 40 weights a clock per SM, writing them there and reading them back
 // would take 160 B/clk of its 128).  What a call costs beside reading the weights once is turning q
-// into bf16: 15 instructions per 8 weights (dequant4), about 65% of the issue slots at the rate the
-// weights arrive.
+// into bf16: 9 instructions per 8 weights where the scales allow it (dequant4_scaled), 15 where not.
 //
 // Roles (warps):
-//   0       TMA: 128-byte segments of the tile's 128 rows of q (16 KiB boxes, 128-byte swizzle) into a
-//           ring, and h, either all of it once (resident) or per 128 columns (streamed)
+//   0       TMA of q: 128-byte segments of the tile's 128 rows (16 KiB boxes, 128-byte swizzle) into a ring
 //   1, 2    MMA issue: the even and the odd units of 128 columns, each into accumulators of its own
-//   4..7    scales and biases, a thread per vocabulary row: 16 groups at a time from global memory, then
-//           a (scale, bias) word per 32 columns beside each segment of q in the ring
+//   3       TMA of h, either all of it once (resident) or per 128 columns (streamed)
+//   4..7    scales and biases, every second segment and half of the rows each: (scale, bias) words beside
+//           the segment of q in the ring; scales multiplied by 2^133 where those of 32 rows are all small
+//           enough, which a flag of the stage says
 //   8..11   h into the dequantised order (below), then sums and output of the accumulators
 //   12..    dequantisation, 4 warps per group, a thread per vocabulary row; group i takes units of 128
 //           columns i, i + kGroups, ...
 //
-// Order of k: dequant4 yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights (dequant8
-// (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes in place.
+// Order of k: 4-bit dequantisation yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights
+// (8-bit: (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes in place.
 // Accuracy: the tensor core truncates as it accumulates (measured: 1e-9 of the result per product, one
 // sign), so an accumulator spans 512 columns and those sums are added in registers, rounding.
 #include <math.h>
@@ -42,13 +42,11 @@ constexpr int kStageBytes = kTileRows * kSegBytes;    // 16 KiB
 constexpr int kUnitK = 128;                           // columns per A buffer (64 tensor-memory columns)
 constexpr int kAccUnits = 4;                          // units per accumulator: 512 columns
 constexpr int kScaleBytes = kSegBytes / 16 * kTileRows * 4;  // words of a segment: 4 KiB (8-bit: half used)
-constexpr int kScaleGroups = 16;                      // groups per fetch of a row's scales
-constexpr int kScratchBytes = kTileRows * kScaleGroups * 4;  // and their (scale, bias) words
 constexpr int kMaxStages = 8;
 constexpr int kMaxH = 8;  // streamed h: units in the ring
-constexpr int kMaxABufs = 7;
+constexpr int kMaxABufs = 4;
 constexpr int kMma = 2;  // warps that issue
-constexpr int kScaleWarp = 4, kSumWarp = 8;
+constexpr int kHWarp = 3, kScaleWarp = 4, kSumWarp = 8;
 constexpr uint64_t kLimitNs = 4000000000ull;          // far above any legitimate wait
 constexpr int kSmemLimit = 232448 - 1024;             // less the slack that aligns the base
 
@@ -60,6 +58,7 @@ struct TcCtl {
   uint64_t drain[kMma];
   uint32_t tmem_base;
   volatile int abort_flag;
+  uint32_t plain[kMaxStages][4];  // per stage and warp of rows: scales as they are, not times 2^133
 };
 constexpr int kCtlBytes = 1024;
 static_assert(sizeof(TcCtl) <= kCtlBytes, "control block");
@@ -69,11 +68,11 @@ struct TcArgs {
   int tiles, segs;        // tiles of 128 rows, segments per row
   int units;              // 128-column units per row: segs * units per segment
   int ngroups;            // groups per row
-  int spb;                // segments per 16 groups
-  uint32_t gmul;          // ceil(2^31 / (group / 32))
+  int seg_words, shift;   // scale words per segment: one per 2^shift times 32 columns
+  uint32_t gmul;          // group of word j of a row: j if 0, else umulhi(j, gmul)
   int stages;             // weight ring
   int hslots;             // streamed h: ring slots; 0: h is resident
-  int wide_scales;        // rows of scales and biases are 16-byte aligned
+  int wide_scales;        // a segment's scales and biases are one aligned word of up to 16 bytes
 };
 
 // One wait of up to kPollNs in the barrier unit: the polls of eight waiting warps at the default
@@ -89,6 +88,10 @@ __device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
       : "memory");
   return ok != 0;
+}
+
+__device__ __forceinline__ uint32_t group_of(const TcArgs& p, uint32_t word) {
+  return p.gmul ? __umulhi(word, p.gmul) : word;
 }
 
 // Bounded wait: false on a timeout (reported) or when another role gave up.
@@ -170,6 +173,16 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
   return r;
 }
+// Bring `bytes` (a multiple of 16) from a 16-byte aligned address to L2.
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// f(0..3, word) over a vector's words
+template <class F>
+__device__ __forceinline__ void unpack(const uint4& v, F f) {
+  f(0, v.x), f(1, v.y), f(2, v.z), f(3, v.w);
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t r;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(addr));
@@ -179,40 +192,149 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// One of the four warps that bring scales and biases beside the segments of q: segments turn, turn + 2, ...,
+// rows row0 + lane and + 32 of the tile.
+template <int kSegK>
+struct ScaleRole {
+  const TcArgs& p;
+  TcCtl* ctl;
+  uint32_t sring;
+  int my_tiles, turn, row0, lane;
+
+  // W: words per segment, their groups' scales and biases aligned vectors; 0: any number, element by element
+  template <int W>
+  __device__ __forceinline__ void run() const {
+    constexpr int kPairs = W ? W / 2 : kSegK / 64;
+    const LogitsArgs& a = p.a;
+    const int64_t total = (int64_t)my_tiles * p.segs;
+    uint32_t sc[2][kPairs], bi[2][kPairs];  // per row the groups of the segment, in pairs
+    int seg = turn;                         // of the next fetch
+    int64_t row = (int64_t)blockIdx.x * kTileRows + row0 + lane;
+    auto fetch = [&]() {
+      const int g0 = W ? seg * W : (int)group_of(p, (uint32_t)(seg * p.seg_words));
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int64_t v = row + 32 * r;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) sc[r][i] = bi[r][i] = 0;
+        if (v >= a.V) continue;
+        const uint16_t* s = a.scales + v * p.ngroups + g0;
+        const uint16_t* b = a.biases + v * p.ngroups + g0;
+        if constexpr (W == 8) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(s)), y = __ldg(reinterpret_cast<const uint4*>(b));
+          sc[r][0] = x.x, sc[r][1] = x.y, sc[r][2] = x.z, sc[r][3] = x.w;
+          bi[r][0] = y.x, bi[r][1] = y.y, bi[r][2] = y.z, bi[r][3] = y.w;
+        } else if constexpr (W == 4) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(s)), y = __ldg(reinterpret_cast<const uint2*>(b));
+          sc[r][0] = x.x, sc[r][1] = x.y, bi[r][0] = y.x, bi[r][1] = y.y;
+        } else if constexpr (W == 2) {
+          sc[r][0] = __ldg(reinterpret_cast<const uint32_t*>(s)), bi[r][0] = __ldg(reinterpret_cast<const uint32_t*>(b));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2 * kPairs; ++i) {
+            const int gi = (int)group_of(p, (uint32_t)(seg * p.seg_words + i)) - g0;
+            if (i < p.seg_words && g0 + gi < p.ngroups) {
+              sc[r][i / 2] |= (uint32_t)__ldg(s + gi) << (16 * (i & 1));
+              bi[r][i / 2] |= (uint32_t)__ldg(b + gi) << (16 * (i & 1));
+            }
+          }
+        }
+      }
+    };
+    // A segment's scales are fetched two segments ahead, which covers the way from L2 and
+    // not from memory: the rows' scales of the next tile, contiguous, are brought to L2 a tile ahead.
+    const uint32_t tile_bytes = (uint32_t)(kTileRows * 2) * p.ngroups;
+    int64_t ahead = (int64_t)blockIdx.x + gridDim.x;
+    auto prefetch = [&]() {
+      if (W && turn == 0 && row0 == 0 && lane < 2 && (ahead + 1) * kTileRows <= a.V)
+        l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + ahead * tile_bytes, tile_bytes);
+      ahead += gridDim.x;
+    };
+    auto wrap = [&]() {
+      while (seg >= p.segs) {
+        seg -= p.segs, row += (int64_t)gridDim.x * kTileRows;
+        prefetch();
+      }
+    };
+    prefetch();
+    wrap();
+    if (turn < total) fetch();
+    uint32_t stage = turn, ph = 0;
+    for (int64_t left = total - turn; left > 0; left -= 2) {
+      if (!wait_warp(ctl, &ctl->w_empty[stage], ph ^ 1u, a.status)) break;
+      const uint32_t out = sring + stage * kScaleBytes + (row0 + lane) * 4;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t big[kPairs], odd = 0;  // times 2^133; odd: NaN where one is infinite or NaN, else 0
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          big[i] = bf16x2_mul(bf16x2_mul(sc[r][i], 0x7F007F00u), 0x42804280u);  // 2^127, 2^6
+          odd = bf16x2_fma(big[i], 0u, odd);
+        }
+        const bool plain = __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0);
+        if (plain) {
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) big[i] = sc[r][i];
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          if (W || 2 * i < p.seg_words)
+            sts32(out + r * 128 + 2 * i * (kTileRows * 4), __byte_perm(big[i], bi[r][i], 0x5410));
+          if (W || 2 * i + 1 < p.seg_words)
+            sts32(out + r * 128 + (2 * i + 1) * (kTileRows * 4), __byte_perm(big[i], bi[r][i], 0x7632));
+        }
+        if (lane == 0) ctl->plain[stage][row0 / 32 + r] = plain ? 1u : 0u;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->w_full[stage]);
+      seg += 2;
+      wrap();
+      if (left > 2) fetch();
+      stage += 2;
+      if (stage >= (uint32_t)p.stages) stage -= p.stages, ph ^= 1u;
+    }
+  }
+};
+
 // Warps that sum: four per 32 columns of the accumulator at most
 constexpr int sum_groups(int np) { return np > 32 ? np / 32 : 1; }
 constexpr int first_dequant_warp(int np) { return kSumWarp + 4 * sum_groups(np); }
+// Segments between a group's turns, and the least common multiple of that and the two scale turns: weight
+// stages are a multiple of it.
+constexpr int seg_step(int bits, int groups) { return groups / (bits == 4 ? 2 : 1); }
+constexpr int ring_multiple(int bits, int groups) { return seg_step(bits, groups) < 2 ? 2 : seg_step(bits, groups); }
 constexpr int tc_threads(int np, int groups) { return 32 * (first_dequant_warp(np) + 4 * groups); }
 
-template <int kBits, int NP, int kGroups>
+template <int kBits, int NP, int kGroups, bool resident>
 __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     logits_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
                      const __grid_constant__ TcArgs p) {
   constexpr int kUnits = kBits == 4 ? 2 : 1;        // units per segment
-  constexpr int kSegK = kUnits * kUnitK;            // columns per segment
   constexpr uint32_t kHUnit = NP * kUnitK * 2;      // bytes of a unit of h: two blocks of 64 columns
   constexpr int kChunkUnits = kAccUnits * kMma;              // units per set of accumulators
-  constexpr uint32_t kABufs = (512 - 2 * kMma * NP) / 64;   // units of A in tensor memory, beside two sets
-  constexpr uint32_t kTmemA = 512 - 64 * kABufs;            // first column of A; the sets start at 0
+  // Units of A in tensor memory, beside two sets of accumulators.  A parity wait is sound only for a waiter
+  // that sees every phase of its barrier, so no slot of a ring changes hands: buffers are a multiple of the
+  // groups and of the issuing warps, weight stages of what takes turns on them (ring_stages).
+  constexpr uint32_t kABufs = 4;
+  constexpr uint32_t kTmemA = 512 - 64 * kABufs;  // first column of A; the sets start at 0
   constexpr int kSums = sum_groups(NP), kCols = NP / kSums, kFirstDequantWarp = first_dequant_warp(NP);
-  static_assert(2 * kMma * NP <= kTmemA && kABufs <= kMaxABufs && kGroups <= kABufs, "tensor memory");
+  static_assert(2 * kMma * NP <= kTmemA && kABufs <= kMaxABufs && kABufs % kGroups == 0 && kABufs % kMma == 0, "tensor memory");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const LogitsArgs& a = p.a;
   uint8_t* const ring = smem;
   uint8_t* const hbuf = ring + p.stages * kStageBytes;
-  uint8_t* const sring = hbuf + (p.hslots ? p.hslots : p.units) * kHUnit;  // scale words, by ring stage
-  uint8_t* const scratch = sring + p.stages * kScaleBytes;
-  TcCtl* const ctl = reinterpret_cast<TcCtl*>(scratch + kScratchBytes);
+  uint8_t* const sring = hbuf + (resident ? p.units : p.hslots) * kHUnit;  // scale words, by ring stage
+  TcCtl* const ctl = reinterpret_cast<TcCtl*>(sring + p.stages * kScaleBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = blockIdx.y * NP;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 4), mbar_init(&ctl->w_empty[i], 4 * kUnits);
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 2), mbar_init(&ctl->w_empty[i], 4 * kUnits);
     for (int i = 0; i < kMaxABufs; ++i) mbar_init(&ctl->a_full[i], 4), mbar_init(&ctl->a_empty[i], 1);
     for (int i = 0; i < 2 * kMma; ++i) mbar_init(&ctl->d_full[i], 1), mbar_init(&ctl->d_empty[i], 4 * kSums);
     for (int i = 0; i < kMaxH; ++i)
-      mbar_init(&ctl->h_raw[i], 1), mbar_init(&ctl->h_full[i], 4 * kSums), mbar_init(&ctl->h_empty[i], 1);
+      mbar_init(&ctl->h_raw[i], 1), mbar_init(&ctl->h_full[i], resident ? 4 * kSums : 4), mbar_init(&ctl->h_empty[i], 1);
     for (int i = 0; i < kMma; ++i) mbar_init(&ctl->drain[i], 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -226,59 +348,63 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const int my_tiles = (p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  const bool resident = p.hslots == 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---- TMA
-      const int64_t total = (int64_t)my_tiles * p.segs;
-      uint32_t hu = 0;  // streamed h units issued
-      bool ok = true;
-      auto load_h = [&](uint64_t* bar, uint8_t* dst, int unit) {
-        tma_load_2d(&map_h, smem_u32(bar), dst, unit * kUnitK, m0);
-        tma_load_2d(&map_h, smem_u32(bar), dst + kHUnit / 2, unit * kUnitK + 64, m0);
-      };
-      int tile = blockIdx.x, seg = 0;
-      uint32_t it = 0;
-      if (resident) {
+    // ---- TMA: the whole warp walks the loop and one elected lane issues, as below
+    const bool leader = elect_one();
+    uint32_t it = 0;          // segments issued
+    uint32_t st = 0, ph = 1;  // weight ring: stage, parity of its release
+    bool ok = true;
+    auto load_w = [&](int seg, int row0) {
+      if (leader) {
+        mbar_arrive_expect_tx(&ctl->w_full[st], kStageBytes);
+        tma_load_2d(&map_w, smem_u32(&ctl->w_full[st]), ring + st * kStageBytes, seg * kSegBytes, row0);
+      }
+      ++it;
+      if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
+    };
+    int row0 = blockIdx.x * kTileRows;
+    for (int i = 0; ok && i < my_tiles; ++i, row0 += gridDim.x * kTileRows) {
+      for (int seg = 0; seg < p.segs; ++seg) {
+        ok = wait_warp(ctl, &ctl->w_empty[st], ph, a.status);
+        if (!ok) break;
+        load_w(seg, row0);
+      }
+    }
+    if (!ok && leader) {  // let the loads in flight land before the CTA can exit
+      const uint32_t k0 = it > (uint32_t)p.stages ? it - p.stages : 0;
+      for (uint32_t k = k0; k < it; ++k) drain_bar(&ctl->w_full[k % p.stages], (k / p.stages) & 1u);
+    }
+  } else if (warp == kHWarp) {
+    // ---- TMA of h
+    const bool leader = elect_one();
+    uint32_t it = 0, hs = 0, hp = 1;  // units issued; streamed: slot, parity of its release
+    bool ok = true;
+    auto load_h = [&](uint64_t* bar, uint8_t* dst, int unit) {
+      tma_load_2d(&map_h, smem_u32(bar), dst, unit * kUnitK, m0);
+      tma_load_2d(&map_h, smem_u32(bar), dst + kHUnit / 2, unit * kUnitK + 64, m0);
+    };
+    if constexpr (resident) {
+      if (leader) {
         mbar_arrive_expect_tx(&ctl->h_raw[0], p.units * kHUnit);
         for (int u = 0; u < p.units; ++u) load_h(&ctl->h_raw[0], hbuf + u * kHUnit, u);
-        hu = 1;
+        drain_bar(&ctl->h_raw[0], 0);  // the loads land before the CTA can exit, whatever the others do
       }
-      for (; (int64_t)it < total; ++it) {
-        const uint32_t s = it % p.stages, ph = (it / p.stages) & 1u;
-        if (!wait_bar(ctl, &ctl->w_empty[s], ph ^ 1u, a.status)) {
-          ok = false;
-          break;
-        }
-        mbar_arrive_expect_tx(&ctl->w_full[s], kStageBytes);
-        tma_load_2d(&map_w, smem_u32(&ctl->w_full[s]), ring + s * kStageBytes, seg * kSegBytes, tile * kTileRows);
-        if (!resident) {
-          for (int j = 0; ok && j < kUnits; ++j, ++hu) {
-            const uint32_t hs = hu % p.hslots, hp = (hu / p.hslots) & 1u;
-            if (!wait_bar(ctl, &ctl->h_empty[hs], hp ^ 1u, a.status)) {
-              ok = false;
-              break;
-            }
+    } else {
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        for (int u = 0; u < p.units; ++u, ++it) {
+          ok = wait_warp(ctl, &ctl->h_empty[hs], hp, a.status);
+          if (!ok) break;
+          if (leader) {
             mbar_arrive_expect_tx(&ctl->h_raw[hs], kHUnit);
-            load_h(&ctl->h_raw[hs], hbuf + hs * kHUnit, seg * kUnits + j);
+            load_h(&ctl->h_raw[hs], hbuf + hs * kHUnit, u);
           }
-          if (!ok) {
-            ++it;
-            break;
-          }
+          if (++hs == (uint32_t)p.hslots) hs = 0, hp ^= 1u;
         }
-        if (++seg == p.segs) seg = 0, tile += gridDim.x;
       }
-      if (!ok) {  // let the loads in flight land before the CTA can exit
-        const uint32_t w0 = it > (uint32_t)p.stages ? it - p.stages : 0;
-        for (uint32_t k = w0; k < it; ++k) drain_bar(&ctl->w_full[k % p.stages], (k / p.stages) & 1u);
-        if (resident) {
-          if (hu) drain_bar(&ctl->h_raw[0], 0);
-        } else {
-          const uint32_t h0 = hu > (uint32_t)p.hslots ? hu - p.hslots : 0;
-          for (uint32_t k = h0; k < hu; ++k) drain_bar(&ctl->h_raw[k % p.hslots], (k / p.hslots) & 1u);
-        }
+      if (!ok && leader) {
+        const uint32_t k0 = it > (uint32_t)p.hslots ? it - p.hslots : 0;
+        for (uint32_t k = k0; k < it; ++k) drain_bar(&ctl->h_raw[k % p.hslots], (k / p.hslots) & 1u);
       }
     }
   } else if (warp <= kMma) {
@@ -335,84 +461,37 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       umma_commit(&ctl->drain[me]);
       drain_bar(&ctl->drain[me], 0);
     }
-  } else if (warp < kScaleWarp) {
-    // spare
   } else if (warp < kSumWarp) {
-    // ---- scales and biases of row (warp - kScaleWarp) * 32 + lane of the tile
-    const int row = (warp - kScaleWarp) * 32 + lane;
-    uint32_t cur[16], nxt[16];  // 16 groups: 8 words of scales, 8 of biases
-    auto fetch = [&](uint32_t (&r)[16], int tile, int g0) {
-      const int64_t v = (int64_t)tile * kTileRows + row;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) r[i] = 0;
-      if (v >= a.V) return;
-      const uint16_t* src[2] = {a.scales + v * p.ngroups + g0, a.biases + v * p.ngroups + g0};
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (p.wide_scales) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (g0 + 8 * i < p.ngroups) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(src[w]) + i);
-              r[8 * w + 4 * i] = x.x, r[8 * w + 4 * i + 1] = x.y, r[8 * w + 4 * i + 2] = x.z, r[8 * w + 4 * i + 3] = x.w;
-            }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (g0 + i < p.ngroups) r[8 * w + i / 2] |= (uint32_t)__ldg(src[w] + i) << (16 * (i & 1));
-        }
-      }
-    };
-    const uint32_t mine = smem_u32(scratch) + row * 4;  // written and read by this thread only
-    const uint32_t out = smem_u32(sring) + row * 4;
-    uint32_t stage = 0, ph = 0;
-    bool ok = true;
-    fetch(nxt, blockIdx.x, 0);
-    for (int i = 0; ok && i < my_tiles; ++i) {
-      const int tile = blockIdx.x + i * (int)gridDim.x;
-      for (int seg = 0, in = 0; seg < p.segs; ++seg) {
-        if (in == 0) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) cur[j] = nxt[j];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sts32(mine + (2 * j) * (kTileRows * 4), __byte_perm(cur[j], cur[8 + j], 0x5410));
-            sts32(mine + (2 * j + 1) * (kTileRows * 4), __byte_perm(cur[j], cur[8 + j], 0x7632));
-          }
-          const int g1 = (seg / p.spb + 1) * kScaleGroups;  // the next 16, of this tile or the next
-          if (g1 < p.ngroups)
-            fetch(nxt, tile, g1);
-          else if (i + 1 < my_tiles)
-            fetch(nxt, tile + (int)gridDim.x, 0);
-        }
-        ok = wait_warp(ctl, &ctl->w_empty[stage], ph ^ 1u, a.status);
-        if (!ok) break;
-#pragma unroll
-        for (int j = 0; j < kSegK / 32; ++j) {
-          const uint32_t gi = (uint32_t)(((uint64_t)(uint32_t)(in * (kSegK / 32) + j) * p.gmul) >> 31);
-          sts32(out + stage * kScaleBytes + j * (kTileRows * 4), lds32(mine + gi * (kTileRows * 4)));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->w_full[stage]);
-        if (++stage == (uint32_t)p.stages) stage = 0, ph ^= 1u;
-        if (++in == p.spb) in = 0;
-      }
-    }
+    // ---- scales and biases
+    const ScaleRole<kUnits * kUnitK> role{p, ctl, smem_u32(sring), my_tiles, (warp - kScaleWarp) & 1, (warp - kScaleWarp) / 2 * 64, lane};
+    if (p.wide_scales && p.seg_words == 8)
+      role.template run<8>();
+    else if (p.wide_scales && p.seg_words == 4)
+      role.template run<4>();
+    else if (p.wide_scales && p.seg_words == 2)
+      role.template run<2>();
+    else
+      role.template run<0>();
   } else if (warp < kFirstDequantWarp) {
     // ---- h into the dequantised order, sums and output
     const int q = warp & 3, n0 = (warp - kSumWarp) / 4 * kCols, tid = threadIdx.x - 32 * kSumWarp;
     const int live = min(NP, a.M - m0);           // rows of h; the others are zero
-    auto reorder_h = [&](uint8_t* base, int n) {  // n blocks of [NP rows, 64 columns], in place
-      const uint32_t b = smem_u32(base);
-      for (int j = tid; j < n * live * 8; j += 128 * kSums) {
-        const int blk = j / (live * 8), i = blk * (NP * 8) + j - blk * (live * 8);  // 16-byte piece
-        const uint4 x = lds128(b + i * 16);
-        if constexpr (kBits == 4)
-          st_shared_v4(b + i * 16, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-        else
-          st_shared_v4(b + i * 16, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
-                       __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
+    // n blocks of [NP rows, 64 columns], in place, by 128 threads: 16 rows of 8 16-byte pieces at a time
+    const int t128 = tid & 127;
+    auto reorder_h = [&](uint8_t* base, int blk0, int step, int n) {
+      for (int blk = blk0; blk < n; blk += step) {
+        const uint32_t b = smem_u32(base) + blk * (NP * 128) + t128 * 16;
+#pragma unroll
+        for (int r = 0; r < NP; r += 16) {
+          if (r >= live) break;
+          const uint4 x = lds128(b + r * 128);
+          if constexpr (kBits == 4)
+            st_shared_v4(b + r * 128, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                         __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+          else
+            st_shared_v4(b + r * 128, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
+                         __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -421,26 +500,30 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     if (resident) {
       ok = wait_warp(ctl, &ctl->h_raw[0], 0, a.status);
       if (ok) {
-        reorder_h(hbuf, p.units * 2);
+        reorder_h(hbuf, tid >> 7, kSums, p.units * 2);
         if (lane == 0) mbar_arrive(&ctl->h_full[0]);
       }
     }
     float acc[kCols];  // columns n0 on
-    uint32_t hu = 0;
+    uint32_t hs = 0, hp = 0;  // streamed h: slot and parity
     const int chunks = (p.units + kChunkUnits - 1) / kChunkUnits;
     const int64_t total = (int64_t)my_tiles * chunks;
     // streamed h runs one set of accumulators ahead of the one that is read
     int64_t fed = 0;
+    int fchunk = 0;
     auto feed = [&]() {
-      const int n = min(kChunkUnits, p.units - (int)(fed % chunks) * kChunkUnits);
-      for (int j = 0; ok && j < n; ++j, ++hu) {
-        const uint32_t hs = hu % p.hslots;
-        ok = wait_warp(ctl, &ctl->h_raw[hs], (hu / p.hslots) & 1u, a.status);
-        if (!ok) break;
-        reorder_h(hbuf + hs * kHUnit, 2);
-        if (lane == 0) mbar_arrive(&ctl->h_full[hs]);
+      const int n = min(kChunkUnits, p.units - fchunk * kChunkUnits);
+      for (int j = 0; ok && j < n; ++j) {
+        if (kSums == 1 || (hs & 1) == (uint32_t)(tid >> 7)) {  // four warps to a unit (slots are even)
+          ok = wait_warp(ctl, &ctl->h_raw[hs], hp, a.status);
+          if (!ok) break;
+          reorder_h(hbuf + hs * kHUnit, 0, 1, 2);
+          if (lane == 0) mbar_arrive(&ctl->h_full[hs]);
+        }
+        if (++hs == (uint32_t)p.hslots) hs = 0, hp ^= 1u;
       }
       ++fed;
+      if (++fchunk == chunks) fchunk = 0;
     };
     uint32_t db[kMma] = {}, dp[kMma] = {};  // per MMA warp: set and parity
     int first[kMma];                        // and its first unit of the tile
@@ -489,11 +572,14 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     // ---- dequantisation
     const int wg = (warp - kFirstDequantWarp) >> 2, q = warp & 3, row = 32 * q + lane;
     // unit u: half u % kUnits of segment u / kUnits; the group goes on by kGroups units at a time
-    constexpr uint32_t kStep = kGroups / kUnits;
+    constexpr uint32_t kStep = seg_step(kBits, kGroups);
     static_assert(kGroups % kUnits == 0, "a group keeps to one half of the segments");
     const uint32_t half = wg % kUnits, swz = (uint32_t)(row & 7) << 4;
     const uint32_t wrow = smem_u32(ring) + row * kSegBytes;
-    const uint32_t srow = smem_u32(sring) + row * 4 + half * (4 * kTileRows * 4);
+    const uint32_t srow = smem_u32(sring) + row * 4;
+    uint32_t soff[4];  // the unit's four scale words
+#pragma unroll
+    for (int i = 0; i < 4; ++i) soff[i] = ((half * 4 + i) >> p.shift) * (kTileRows * 4);
     const uint32_t trow = tmem + kTmemA + ((uint32_t)(32 * q) << 16);
     uint32_t stage = wg / kUnits, wph = 0;  // weight ring (kStep <= stages)
     uint32_t buf = wg, aph = 0;             // A buffer (kGroups <= kABufs)
@@ -502,35 +588,62 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       ok = wait_warp(ctl, &ctl->w_full[stage], wph, a.status);
       if (!ok) break;
       const uint32_t wst = wrow + stage * kStageBytes, sst = srow + stage * kScaleBytes;
-#pragma unroll 1  // one copy of the body: more would not stay in the instruction cache
+      // The unit's 64 (8-bit: 128) bytes and 4 words.  The stage is given back behind the tensor-memory store
+      // that takes what they became: a release right behind the loads does not hold them back, and the next
+      // box landed first.
+      constexpr int kVec = kBits == 4 ? 4 : 8;
+      uint4 w[kVec];
+      uint32_t sw[4];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) w[i] = lds128(wst + (((half * 4 + i) << 4) ^ swz));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sw[i] = lds32(sst + soff[i]);
+      const bool plain = lds32(smem_u32(&ctl->plain[stage][q])) != 0;
+      const uint32_t dst = trow + buf * 64;
+#pragma unroll
       for (int part = 0; part < 2; ++part) {  // 64 columns: 32 words of tensor memory
         uint32_t r[32];
+        if (!plain) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // 32 columns: one group
-          const uint32_t sw = lds32(sst + (part * 2 + i) * (kTileRows * 4));
-          const uint32_t s2 = __byte_perm(sw, 0, 0x1010), b2 = __byte_perm(sw, 0, 0x3232);
-          const uint32_t piece = half * 4 + part * 2 + i;
-          if constexpr (kBits == 4) {
-            const uint4 w = lds128(wst + ((piece << 4) ^ swz));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t s133 = __byte_perm(sw[part * 2 + i], 0, 0x1010), b2 = __byte_perm(sw[part * 2 + i], 0, 0x3232);
+            if constexpr (kBits == 4) {
+              const uint32_t s129 = bf16x2_fma(s133, 0x3D803D80u, 0x80008000u);  // times 2^-4, plus -0
+              unpack(w[part * 2 + i], [&](int e, uint32_t v) {
+                uint32_t x[4];
+                dequant4_scaled(v, s133, s129, b2, x);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t x[4];
-              dequant4(ww[e], s2, b2, x);
+                for (int f = 0; f < 4; ++f) r[16 * i + 4 * e + f] = x[f];
+              });
+            } else {
 #pragma unroll
-              for (int f = 0; f < 4; ++f) r[16 * i + 4 * e + f] = x[f];
+              for (int o = 0; o < 2; ++o)
+                unpack(w[(part * 2 + i) * 2 + o], [&](int e, uint32_t v) {
+                  uint32_t x[2];
+                  dequant8_scaled(v, s133, b2, x);
+                  r[16 * i + 8 * o + 2 * e] = x[0], r[16 * i + 8 * o + 2 * e + 1] = x[1];
+                });
             }
-          } else {
+          }
+        } else {
 #pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const uint4 w = lds128(wst + (((2 * piece + o) << 4) ^ swz));
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t s2 = __byte_perm(sw[part * 2 + i], 0, 0x1010), b2 = __byte_perm(sw[part * 2 + i], 0, 0x3232);
+            if constexpr (kBits == 4) {
+              unpack(w[part * 2 + i], [&](int e, uint32_t v) {
+                uint32_t x[4];
+                dequant4(v, s2, b2, x);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t x[2];
-                dequant8(ww[e], s2, b2, x);
-                r[16 * i + 8 * o + 2 * e] = x[0], r[16 * i + 8 * o + 2 * e + 1] = x[1];
-              }
+                for (int f = 0; f < 4; ++f) r[16 * i + 4 * e + f] = x[f];
+              });
+            } else {
+#pragma unroll
+              for (int o = 0; o < 2; ++o)
+                unpack(w[(part * 2 + i) * 2 + o], [&](int e, uint32_t v) {
+                  uint32_t x[2];
+                  dequant8(v, s2, b2, x);
+                  r[16 * i + 8 * o + 2 * e] = x[0], r[16 * i + 8 * o + 2 * e + 1] = x[1];
+                });
             }
           }
         }
@@ -539,15 +652,16 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
           if (!ok) break;
           tc_fence_after();
         }
-        tmem_st32(trow + buf * 64 + part * 32, r);
+        tmem_st32(dst + part * 32, r);
       }
       if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->w_empty[stage]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->a_full[buf]);
+      if (lane == 0) {
+        mbar_arrive(&ctl->w_empty[stage]);
+        mbar_arrive(&ctl->a_full[buf]);
+      }
       buf += kGroups;
       if (buf >= kABufs) buf -= kABufs, aph ^= 1u;
       stage += kStep;
@@ -567,9 +681,6 @@ template <int kBits, int NP, int kGroups>
 cudaError_t launch_np(const LogitsArgs& a, int sms, cudaStream_t st) {
   constexpr int kUnits = kBits == 4 ? 2 : 1;
   constexpr int kHUnit = NP * kUnitK * 2;
-  static std::atomic<int> done[64];
-  auto kernel = logits_tc_kernel<kBits, NP, kGroups>;
-  if (cudaError_t e = opt_in_smem(kernel, kSmemLimit + 1024, done)) return e;
   TcArgs p;
   p.a = a;
   const int64_t row_bytes = (int64_t)a.d * kBits / 8;
@@ -577,19 +688,32 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, cudaStream_t st) {
   p.segs = (int)cdiv(row_bytes, kSegBytes);
   p.units = p.segs * kUnits;
   p.ngroups = a.d / a.group;
-  p.spb = kScaleGroups * a.group / (kUnits * kUnitK);
-  const uint32_t per = (uint32_t)(a.group / 32);
-  p.gmul = (uint32_t)(((1ull << 31) + per - 1) / per);
-  p.wide_scales = p.ngroups % 8 == 0 && aligned16(a.scales) && aligned16(a.biases);
+  constexpr int kSegK = kUnits * kUnitK;
+  // A scale word per group where groups of a power of two columns fit a segment; else one per 32 columns
+  // (or per segment, for groups of whole segments), the group's repeated.
+  const int per = a.group / 32;
+  p.shift = 0;
+  if (a.group % kSegK == 0)
+    while (32 << p.shift < kSegK) ++p.shift;
+  else if ((per & (per - 1)) == 0)
+    while (1 << p.shift < per) ++p.shift;
+  p.seg_words = (kSegK / 32) >> p.shift;
+  const uint32_t repeat = (uint32_t)(per >> p.shift);  // words per group
+  p.gmul = repeat > 1 ? (uint32_t)(((1ull << 32) + repeat - 1) / repeat) : 0u;
+  p.wide_scales = repeat == 1 && p.ngroups % p.seg_words == 0 && aligned16(a.scales) && aligned16(a.biases);
   // h resident where at least four weight stages fit beside it, else streamed through up to 8 units
-  const int fixed = kScratchBytes + kCtlBytes, stage = kStageBytes + kScaleBytes;
+  const int fixed = kCtlBytes, stage = kStageBytes + kScaleBytes;
   const int64_t all_h = (int64_t)p.units * kHUnit;
+  constexpr int kMul = ring_multiple(kBits, kGroups);
+  static_assert(kMul <= 4 && kMaxStages % kMul == 0, "weight ring");
+  auto ring_stages = [&](int64_t left) { return (int)std::min<int64_t>(kMaxStages, left / stage) / kMul * kMul; };
   if (all_h <= kSmemLimit - fixed - 4 * stage) {
     p.hslots = 0;
-    p.stages = (int)std::min<int64_t>(kMaxStages, (kSmemLimit - fixed - all_h) / stage);
+    p.stages = ring_stages(kSmemLimit - fixed - all_h);
   } else {
-    p.hslots = std::min(kMaxH, (64 << 10) / kHUnit);
-    p.stages = std::min(kMaxStages, (kSmemLimit - fixed - p.hslots * kHUnit) / stage);
+    // four stages at least, then as many slots as fit (an even number)
+    p.hslots = std::min(kMaxH, (kSmemLimit - fixed - 4 * stage) / kHUnit / 2 * 2);
+    p.stages = ring_stages(kSmemLimit - fixed - p.hslots * kHUnit);
   }
   const int smem = p.stages * stage + (p.hslots ? p.hslots * kHUnit : (int)all_h) + fixed + 1024;
   CUtensorMap mw, mh;
@@ -597,6 +721,9 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, cudaStream_t st) {
       !encode_map_2d(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.h, a.d, a.M, a.ld_h * 2, 64, NP))
     return cudaErrorNotSupported;
   const dim3 grid((unsigned)std::min(p.tiles, sms), (unsigned)cdiv(a.M, NP));
+  static std::atomic<int> done[2][64];
+  auto kernel = p.hslots ? logits_tc_kernel<kBits, NP, kGroups, false> : logits_tc_kernel<kBits, NP, kGroups, true>;
+  if (cudaError_t e = opt_in_smem(kernel, kSmemLimit + 1024, done[p.hslots != 0])) return e;
   kernel<<<grid, tc_threads(NP, kGroups), smem, st>>>(mw, mh, p);
   return cudaGetLastError();
 }
