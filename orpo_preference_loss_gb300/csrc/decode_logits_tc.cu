@@ -11,7 +11,7 @@
 //
 // Roles (warps):
 //   0       TMA of q: 128-byte segments of the tile's 128 rows (16 KiB boxes, 128-byte swizzle) into a ring
-//   1, 2    MMA issue: the even and the odd units of 128 columns, each into accumulators of its own
+//   1, 2    MMA issue: the even and the odd segments, each into accumulators of its own
 //   3       TMA of h, either all of it once (resident) or per 128 columns (streamed)
 //   4..7    scales and biases, every second segment and half of the rows each: (scale, bias) words beside
 //           the segment of q in the ring; scales multiplied by 2^133 where those of 32 rows are all small
@@ -40,7 +40,7 @@ constexpr int kTileRows = 128;
 constexpr int kSegBytes = 128;                        // bytes of a row per segment
 constexpr int kStageBytes = kTileRows * kSegBytes;    // 16 KiB
 constexpr int kUnitK = 128;                           // columns per A buffer (64 tensor-memory columns)
-constexpr int kAccUnits = 4;                          // units per accumulator: 512 columns
+constexpr int kAccK = 512;                            // columns per accumulator
 constexpr int kScaleBytes = kSegBytes / 16 * kTileRows * 4;  // words of a segment: 4 KiB (8-bit: half used)
 constexpr int kMaxStages = 8;
 constexpr int kMaxH = 8;  // streamed h: units in the ring
@@ -311,14 +311,16 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
                      const __grid_constant__ TcArgs p) {
   constexpr int kUnits = kBits == 4 ? 2 : 1;        // units per segment
   constexpr uint32_t kHUnit = NP * kUnitK * 2;      // bytes of a unit of h: two blocks of 64 columns
-  constexpr int kChunkUnits = kAccUnits * kMma;              // units per set of accumulators
-  // Units of A in tensor memory, beside two sets of accumulators.  A parity wait is sound only for a waiter
-  // that sees every phase of its barrier, so no slot of a ring changes hands: buffers are a multiple of the
-  // groups and of the issuing warps, weight stages of what takes turns on them (ring_stages).
-  constexpr uint32_t kABufs = 4;
-  constexpr uint32_t kTmemA = 512 - 64 * kABufs;  // first column of A; the sets start at 0
+  constexpr int kAccSegs = kAccK / (kUnits * kUnitK), kChunkSegs = kAccSegs * kMma;  // segments per (set of) accumulators
+  // Segments of A in tensor memory (256 columns of it), beside two sets of accumulators.  A parity wait is
+  // sound only for a waiter that sees every phase of its barrier, so no slot of a ring changes hands: the
+  // slots of A are a multiple of the segments that the groups work on at a time and of the issuing
+  // warps, the weight stages of what takes turns on them (ring_stages), the slots of h of both.
+  constexpr uint32_t kASlots = 4 / kUnits;
+  constexpr uint32_t kTmemA = 512 - 256;  // first column of A; the sets start at 0
+  constexpr uint32_t kStep = seg_step(kBits, kGroups);
   constexpr int kSums = sum_groups(NP), kCols = NP / kSums, kFirstDequantWarp = first_dequant_warp(NP);
-  static_assert(2 * kMma * NP <= kTmemA && kABufs <= kMaxABufs && kABufs % kGroups == 0 && kABufs % kMma == 0, "tensor memory");
+  static_assert(2 * kMma * NP <= kTmemA && kASlots <= kMaxABufs && kASlots % kStep == 0 && kASlots % kMma == 0, "tensor memory");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const LogitsArgs& a = p.a;
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 2), mbar_init(&ctl->w_empty[i], 4 * kUnits);
-    for (int i = 0; i < kMaxABufs; ++i) mbar_init(&ctl->a_full[i], 4), mbar_init(&ctl->a_empty[i], 1);
+    for (int i = 0; i < kMaxABufs; ++i) mbar_init(&ctl->a_full[i], 4 * kUnits), mbar_init(&ctl->a_empty[i], 1);
     for (int i = 0; i < 2 * kMma; ++i) mbar_init(&ctl->d_full[i], 1), mbar_init(&ctl->d_empty[i], 4 * kSums);
     for (int i = 0; i < kMaxH; ++i)
       mbar_init(&ctl->h_raw[i], 1), mbar_init(&ctl->h_full[i], resident ? 4 * kSums : 4), mbar_init(&ctl->h_empty[i], 1);
@@ -408,7 +410,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       }
     }
   } else if (warp <= kMma) {
-    // ---- MMA: units me, me + kMma, ... of every tile.  The whole warp walks the loop, so that addresses
+    // ---- MMA: segments me, me + kMma, ... of every tile.  The whole warp walks the loop, so that addresses
     // and descriptors stay in uniform registers, and one elected lane issues: with a single thread in
     // the loop a product took 109 clocks to issue.
     const int me = warp - 1;
@@ -416,29 +418,35 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     const uint32_t idesc = make_idesc_bf16(kTileRows, NP, 0, 0);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t desc0 = smem_desc_sw128(smem_u32(hbuf), 16, 1024);
-    uint32_t buf = me, ap = 0;  // A buffer and parity
-    uint32_t db = 0, dp = 1;    // set of accumulators, parity of its release
-    uint32_t hs = me, hp = 0;   // streamed h: ring slot and parity
+    uint32_t slot = me, ap = 0;       // segment's place in tensor memory, parity
+    uint32_t db = 0, dp = 1;          // set of accumulators, parity of its release
+    uint32_t hs = me * kUnits, hp = 0;  // streamed h: ring slot and parity
     bool ok = !resident || wait_warp(ctl, &ctl->h_full[0], 0, a.status);
-    int first = me;             // my first unit of the tile
+    int first = me;                   // my first segment of the tile
     for (int i = 0; ok && i < my_tiles; ++i) {
-      int j = 0, ku = first;    // units in the accumulator, unit of the tile
-      for (; ku < p.units; ku += kMma) {
+      int j = 0, seg = first;         // segments in the accumulator, segment of the tile
+      for (; seg < p.segs; seg += kMma) {
         if (j == 0) ok = wait_warp(ctl, &ctl->d_empty[2 * me + db], dp, a.status);
-        ok = ok && wait_warp(ctl, &ctl->a_full[buf], ap, a.status);
-        if (!resident) ok = ok && wait_warp(ctl, &ctl->h_full[hs], hp, a.status);
+        ok = ok && wait_warp(ctl, &ctl->a_full[slot], ap, a.status);
+        if constexpr (!resident) {
+#pragma unroll
+          for (int k = 0; k < kUnits; ++k) ok = ok && wait_warp(ctl, &ctl->h_full[hs + k], hp, a.status);
+        }
         if (!ok) break;
         tc_fence_after();
-        const bool last = j == kAccUnits - 1 || ku + kMma >= p.units;
+        const bool last = j == kAccSegs - 1 || seg + kMma >= p.segs;
         if (leader) {
-          const uint64_t desc = desc0 + (uint64_t)((resident ? (uint32_t)ku : hs) * (kHUnit >> 4));
-          const uint32_t at = tm + kTmemA + buf * 64, dt = tm + (2 * me + db) * NP;
+          const uint64_t desc = desc0 + (uint64_t)((resident ? (uint32_t)seg * kUnits : hs) * (kHUnit >> 4));
+          const uint32_t at = tm + kTmemA + slot * (64 * kUnits), dt = tm + (2 * me + db) * NP;
 #pragma unroll
-          for (int kk = 0; kk < kUnitK / 16; ++kk)
+          for (int kk = 0; kk < kUnits * kUnitK / 16; ++kk)
             umma_bf16_ta(dt, at + kk * 8, desc + ((kk >> 2) * (kHUnit / 2) + (kk & 3) * 32) / 16, idesc,
                          (kk | j) != 0 ? 1u : 0u);
-          umma_commit(&ctl->a_empty[buf]);
-          if (!resident) umma_commit(&ctl->h_empty[hs]);
+          umma_commit(&ctl->a_empty[slot]);
+          if constexpr (!resident) {
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) umma_commit(&ctl->h_empty[hs + k]);
+          }
           if (last) umma_commit(&ctl->d_full[2 * me + db]);
         }
         __syncwarp();
@@ -448,14 +456,14 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
           db ^= 1u;
           dp ^= db ^ 1u;  // after both sets
         }
-        buf += kMma;
-        if (buf >= kABufs) buf -= kABufs, ap ^= 1u;
-        if (!resident) {
-          hs += kMma;
+        slot += kMma;
+        if (slot >= kASlots) slot -= kASlots, ap ^= 1u;
+        if constexpr (!resident) {
+          hs += kMma * kUnits;
           if (hs >= (uint32_t)p.hslots) hs -= p.hslots, hp ^= 1u;
         }
       }
-      first = ku - p.units;  // units alternate across tiles too
+      first = seg - p.segs;  // segments alternate across tiles too
     }
     if (leader) {  // every issued MMA has finished before tensor memory is released
       umma_commit(&ctl->drain[me]);
@@ -506,13 +514,13 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     }
     float acc[kCols];  // columns n0 on
     uint32_t hs = 0, hp = 0;  // streamed h: slot and parity
-    const int chunks = (p.units + kChunkUnits - 1) / kChunkUnits;
+    const int chunks = (p.segs + kChunkSegs - 1) / kChunkSegs;
     const int64_t total = (int64_t)my_tiles * chunks;
     // streamed h runs one set of accumulators ahead of the one that is read
     int64_t fed = 0;
     int fchunk = 0;
     auto feed = [&]() {
-      const int n = min(kChunkUnits, p.units - fchunk * kChunkUnits);
+      const int n = min(kChunkSegs, p.segs - fchunk * kChunkSegs) * kUnits;
       for (int j = 0; ok && j < n; ++j) {
         if (kSums == 1 || (hs & 1) == (uint32_t)(tid >> 7)) {  // four warps to a unit (slots are even)
           ok = wait_warp(ctl, &ctl->h_raw[hs], hp, a.status);
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       if (++fchunk == chunks) fchunk = 0;
     };
     uint32_t db[kMma] = {}, dp[kMma] = {};  // per MMA warp: set and parity
-    int first[kMma];                        // and its first unit of the tile
+    int first[kMma];                        // and its first segment of the tile
 #pragma unroll
     for (int w = 0; w < kMma; ++w) first[w] = w;
     for (int i = 0; ok && i < my_tiles; ++i) {
@@ -537,7 +545,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
           while (ok && fed < total && fed <= (int64_t)i * chunks + c + 1) feed();
 #pragma unroll
         for (int w = 0; w < kMma; ++w) {
-          if (!ok || first[w] + c * kChunkUnits >= p.units) continue;  // no unit of this warp's here
+          if (!ok || first[w] + c * kChunkSegs >= p.segs) continue;  // no segment of this warp's here
           ok = wait_warp(ctl, &ctl->d_full[2 * w + db[w]], dp[w], a.status);
           if (!ok) continue;
           tc_fence_after();
@@ -563,16 +571,15 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
           if (m0 + n0 + n < a.M) store_logit(a, m0 + n0 + n, (int)v, acc[n]);
       }
 #pragma unroll
-      for (int w = 0; w < kMma; ++w) {  // the warp's units go on alternating in the next tile
-        const int over = (p.units - first[w] + kMma - 1) / kMma * kMma + first[w] - p.units;
-        first[w] = first[w] < p.units ? over : first[w] - p.units;
+      for (int w = 0; w < kMma; ++w) {  // the warp's segments go on alternating in the next tile
+        const int over = (p.segs - first[w] + kMma - 1) / kMma * kMma + first[w] - p.segs;
+        first[w] = first[w] < p.segs ? over : first[w] - p.segs;
       }
     }
   } else {
     // ---- dequantisation
     const int wg = (warp - kFirstDequantWarp) >> 2, q = warp & 3, row = 32 * q + lane;
     // unit u: half u % kUnits of segment u / kUnits; the group goes on by kGroups units at a time
-    constexpr uint32_t kStep = seg_step(kBits, kGroups);
     static_assert(kGroups % kUnits == 0, "a group keeps to one half of the segments");
     const uint32_t half = wg % kUnits, swz = (uint32_t)(row & 7) << 4;
     const uint32_t wrow = smem_u32(ring) + row * kSegBytes;
@@ -582,7 +589,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     for (int i = 0; i < 4; ++i) soff[i] = ((half * 4 + i) >> p.shift) * (kTileRows * 4);
     const uint32_t trow = tmem + kTmemA + ((uint32_t)(32 * q) << 16);
     uint32_t stage = wg / kUnits, wph = 0;  // weight ring (kStep <= stages)
-    uint32_t buf = wg, aph = 0;             // A buffer (kGroups <= kABufs)
+    uint32_t slot = wg / kUnits, aph = 0;   // place in tensor memory (kStep <= kASlots)
     bool ok = true;
     for (int64_t left = (int64_t)my_tiles * p.segs - wg / kUnits; left > 0; left -= kStep) {
       ok = wait_warp(ctl, &ctl->w_full[stage], wph, a.status);
@@ -599,7 +606,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sw[i] = lds32(sst + soff[i]);
       const bool plain = lds32(smem_u32(&ctl->plain[stage][q])) != 0;
-      const uint32_t dst = trow + buf * 64;
+      const uint32_t dst = trow + (slot * kUnits + half) * 64;
 #pragma unroll
       for (int part = 0; part < 2; ++part) {  // 64 columns: 32 words of tensor memory
         uint32_t r[32];
@@ -648,7 +655,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
           }
         }
         if (part == 0) {
-          ok = wait_warp(ctl, &ctl->a_empty[buf], aph ^ 1u, a.status);
+          ok = wait_warp(ctl, &ctl->a_empty[slot], aph ^ 1u, a.status);
           if (!ok) break;
           tc_fence_after();
         }
@@ -660,10 +667,10 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&ctl->w_empty[stage]);
-        mbar_arrive(&ctl->a_full[buf]);
+        mbar_arrive(&ctl->a_full[slot]);
       }
-      buf += kGroups;
-      if (buf >= kABufs) buf -= kABufs, aph ^= 1u;
+      slot += kStep;
+      if (slot >= kASlots) slot -= kASlots, aph ^= 1u;
       stage += kStep;
       if (stage >= (uint32_t)p.stages) stage -= p.stages, wph ^= 1u;
     }
@@ -711,8 +718,8 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, cudaStream_t st) {
     p.hslots = 0;
     p.stages = ring_stages(kSmemLimit - fixed - all_h);
   } else {
-    // four stages at least, then as many slots as fit (an even number)
-    p.hslots = std::min(kMaxH, (kSmemLimit - fixed - 4 * stage) / kHUnit / 2 * 2);
+    // four stages at least, then as many slots as fit (a multiple of both issuing warps' segments)
+    p.hslots = std::min(kMaxH, (kSmemLimit - fixed - 4 * stage) / kHUnit) / (kMma * kUnits) * (kMma * kUnits);
     p.stages = ring_stages(kSmemLimit - fixed - p.hslots * kHUnit);
   }
   const int smem = p.stages * stage + (p.hslots ? p.hslots * kHUnit : (int)all_h) + fixed + 1024;
