@@ -131,10 +131,18 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a Stream object (3 us a call); torch's own code generators
+# use the same two functions.  The public way where they are missing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None:
+            return _raw_stream(_raw_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _check(code, what):
@@ -151,7 +159,7 @@ def _dev(t, name, dtypes, shape=None):
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 
@@ -402,32 +410,48 @@ def _rows(t, name, dtypes, cols=None, rows=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols) or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+    shape = t.shape
+    if len(shape) != 2 or (cols is not None and shape[1] != cols) or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected "
                          f"({'rows' if rows is None else rows}, {'columns' if cols is None else cols})")
-    pitch = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if (t.shape[1] > 1 and t.stride(1) != 1) or pitch < t.shape[1]:
+    r, c = shape
+    pitch, step = t.stride()
+    if r <= 1:
+        pitch = c
+    if (step != 1 and c > 1) or pitch < c:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return pitch
 
 
 LOGITS = (torch.float32, torch.bfloat16)
+F32, I32, U8, FLAGS = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.uint8, torch.bool)
 
 
 def orpo_head_logits_q(h, wq, scales, biases, bits, group, softcap, logits, status, stream=None):
     """Logits [M, V] (fp32 or bf16) of the rows of h [M, d] under the affine group-quantised head.
 
     h and logits may have any row pitch, e.g. hidden[:, -1] of [M, T, d] hidden states."""
-    ld_h = _rows(h, "h", BF16)
     M, d = h.shape
     V = wq.shape[0]
-    _quant_args(wq, scales, biases, V, d, bits, group)
-    ld_logits = _rows(logits, "logits", LOGITS, cols=V, rows=M)
-    _dev(status, "status", (torch.int32,))
-    _check(load().orpo_head_logits_q(_ptr(h), ld_h, _ptr(wq), _ptr(scales), _ptr(biases), int(bits), int(group), M, V,
-                                     d, float(softcap), _ptr(logits), ld_logits,
-                                     1 if logits.dtype == torch.bfloat16 else 0, _ptr(status), _stream(stream)),
-           "orpo_head_logits_q")
+    # A decode step is a few microseconds of GPU work, so the usual, right arguments pass one plain test;
+    # whatever fails it is looked at in full for its message.
+    hp, hs = h.stride()
+    lp, ls = logits.stride()
+    if not (h.is_cuda and h.dtype in BF16 and hs == 1 and hp >= d and wq.is_cuda and wq.dtype is torch.uint8
+            and wq.is_contiguous() and wq.shape == (V, d * bits // 8) and scales.is_cuda and scales.dtype in BF16
+            and scales.is_contiguous() and scales.shape == (V, d // group) and biases.is_cuda and biases.dtype in BF16
+            and biases.is_contiguous() and biases.shape == (V, d // group) and logits.is_cuda
+            and logits.dtype in LOGITS and logits.shape == (M, V) and ls == 1 and lp >= V and status.is_cuda
+            and status.dtype is torch.int32):
+        hp = _rows(h, "h", BF16)
+        _quant_args(wq, scales, biases, V, d, bits, group)
+        lp = _rows(logits, "logits", LOGITS, cols=V, rows=M)
+        _dev(status, "status", I32)
+    code = (_lib or load()).orpo_head_logits_q(
+        h.data_ptr(), hp, wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), bits, group, M, V, d, softcap,
+        logits.data_ptr(), lp, logits.dtype is torch.bfloat16, status.data_ptr(), _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_head_logits_q")
 
 
 def orpo_beam_select_workspace_bytes(batch: int, beams: int, V: int, n: int) -> int:
@@ -439,47 +463,71 @@ def orpo_beam_select(logits, score, finished, eos, beams, out_score, out_parent,
     """The n best continuations (out_* are [batch, n]) over beams x vocabulary of logits [batch * beams, V].
 
     finished and out_finished may be None; eos is -1 when no token ends a response."""
-    V = logits.shape[1]
-    batch, n = out_score.shape
-    rows = batch * beams
-    ld_logits = _rows(logits, "logits", LOGITS, rows=rows)
-    _dev(score, "score", (torch.float32,))
-    if score.numel() != rows:
-        raise ValueError(f"score has {score.numel()} elements, expected batch * beams = {rows}")
-    if finished is not None:
-        _dev(finished, "finished", (torch.uint8, torch.bool))
-        if finished.numel() != rows:
-            raise ValueError(f"finished has {finished.numel()} elements, expected batch * beams = {rows}")
-    _dev(out_score, "out_score", (torch.float32,))
-    _dev(out_parent, "out_parent", (torch.int32,), (batch, n))
-    _dev(out_token, "out_token", (torch.int32,), (batch, n))
-    if out_finished is not None:
-        _dev(out_finished, "out_finished", (torch.uint8, torch.bool), (batch, n))
-    _dev(workspace, "workspace", (torch.uint8,))
-    _dev(status, "status", (torch.int32,))
-    _check(load().orpo_beam_select(_ptr(logits), ld_logits, 1 if logits.dtype == torch.bfloat16 else 0, _ptr(score),
-                                   _ptr(finished), int(eos), batch, int(beams), V, n, _ptr(out_score),
-                                   _ptr(out_parent), _ptr(out_token), _ptr(out_finished), _ptr(workspace),
-                                   workspace.numel(), _ptr(status), _stream(stream)), "orpo_beam_select")
+    rows, V = logits.shape
+    batch, n = out = out_score.shape
+    pitch, step = logits.stride()
+    if not (rows == batch * beams and logits.is_cuda and logits.dtype in LOGITS and step == 1 and pitch >= V
+            and score.is_cuda and score.dtype is torch.float32 and score.is_contiguous() and score.numel() == rows
+            and (finished is None or (finished.is_cuda and finished.dtype in FLAGS and finished.is_contiguous()
+                                      and finished.numel() == rows))
+            and out_score.is_cuda and out_score.dtype is torch.float32 and out_score.is_contiguous()
+            and out_parent.is_cuda and out_parent.dtype is torch.int32 and out_parent.is_contiguous()
+            and out_parent.shape == out and out_token.is_cuda and out_token.dtype is torch.int32
+            and out_token.is_contiguous() and out_token.shape == out
+            and (out_finished is None or (out_finished.is_cuda and out_finished.dtype in FLAGS
+                                          and out_finished.is_contiguous() and out_finished.shape == out))
+            and workspace.is_cuda and workspace.dtype is torch.uint8 and workspace.is_contiguous() and status.is_cuda
+            and status.dtype is torch.int32):
+        rows = batch * beams
+        pitch = _rows(logits, "logits", LOGITS, rows=rows)
+        _dev(score, "score", F32)
+        if score.numel() != rows:
+            raise ValueError(f"score has {score.numel()} elements, expected batch * beams = {rows}")
+        if finished is not None:
+            _dev(finished, "finished", FLAGS)
+            if finished.numel() != rows:
+                raise ValueError(f"finished has {finished.numel()} elements, expected batch * beams = {rows}")
+        _dev(out_score, "out_score", F32)
+        _dev(out_parent, "out_parent", I32, (batch, n))
+        _dev(out_token, "out_token", I32, (batch, n))
+        if out_finished is not None:
+            _dev(out_finished, "out_finished", FLAGS, (batch, n))
+        _dev(workspace, "workspace", U8)
+        _dev(status, "status", I32)
+    code = (_lib or load()).orpo_beam_select(
+        logits.data_ptr(), pitch, logits.dtype is torch.bfloat16, score.data_ptr(),
+        None if finished is None else finished.data_ptr(), eos, batch, beams, V, n, out_score.data_ptr(),
+        out_parent.data_ptr(), out_token.data_ptr(), None if out_finished is None else out_finished.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), status.data_ptr(), _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_beam_select")
 
 
 def orpo_beam_reorder(state, parent, length, status, stream=None):
     """state [outer, batch * beams, rows, capacity, unit] (any dtype) follows parent [batch, beams] in place.
 
     Only positions t < length[b] (int32 [batch]; None: all) of the capacity dimension move."""
-    if state is None or not state.is_cuda or not state.is_contiguous() or state.dim() != 5:
-        raise ValueError("state must be a contiguous CUDA tensor [outer, batch * beams, rows, capacity, unit]")
-    ld_parent = _rows(parent, "parent", (torch.int32,))
     batch, beams = parent.shape
-    if state.shape[1] != batch * beams:
-        raise ValueError(f"state has {state.shape[1]} beams, expected batch * beams = {batch * beams}")
-    if length is not None:
-        _dev(length, "length", (torch.int32,), (batch,))
-    _dev(status, "status", (torch.int32,))
+    pitch, step = parent.stride()
+    if not (state.is_cuda and state.is_contiguous() and state.dim() == 5 and state.shape[1] == batch * beams
+            and parent.is_cuda and parent.dtype is torch.int32 and step == 1 and pitch >= beams
+            and (length is None or (length.is_cuda and length.dtype is torch.int32 and length.is_contiguous()
+                                    and length.shape == (batch,)))
+            and status.is_cuda and status.dtype is torch.int32):
+        if not state.is_cuda or not state.is_contiguous() or state.dim() != 5:
+            raise ValueError("state must be a contiguous CUDA tensor [outer, batch * beams, rows, capacity, unit]")
+        pitch = _rows(parent, "parent", I32)
+        if state.shape[1] != batch * beams:
+            raise ValueError(f"state has {state.shape[1]} beams, expected batch * beams = {batch * beams}")
+        if length is not None:
+            _dev(length, "length", I32, (batch,))
+        _dev(status, "status", I32)
     outer, _, rows, capacity, unit = state.shape
-    _check(load().orpo_beam_reorder(_ptr(state), _ptr(parent), ld_parent, _ptr(length), outer, batch, beams, rows,
-                                    capacity, unit * state.element_size(), _ptr(status), _stream(stream)),
-           "orpo_beam_reorder")
+    code = (_lib or load()).orpo_beam_reorder(
+        state.data_ptr(), parent.data_ptr(), pitch, None if length is None else length.data_ptr(), outer, batch,
+        beams, rows, capacity, unit * state.element_size(), status.data_ptr(), _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_beam_reorder")
 
 
 def orpo_debug_gemm(A, B, C, M, N, K, a_mn_major, b_mn_major, status, stream=None):

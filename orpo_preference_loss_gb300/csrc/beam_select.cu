@@ -7,8 +7,10 @@
 // logit's bits mapped to an order-preserving integer, then the complement of the token), which is
 // total, so ties and scheduling cannot change the result.
 //
-// Row kernel: a CTA reads a part of one beam's row once, 8192 logits at a time in registers (32 per
-// thread, all loads in flight together), and leaves the part's max, sum of exp and n largest keys.
+// Row kernel: a CTA reads a part of one beam's row once, 8192 fp32 or 16384 bf16 logits at a time in
+// registers (32 words per thread, all loads in flight together), and leaves the part's max, sum of exp
+// and n largest keys.  It is bound by instructions before it is by memory, so a logit costs about five
+// (bf16): unpack, half a packed max, and multiply-add, ex2 and add of the sum, two at a time.
 // The n largest come without sorting: the r-th largest of a warp's 32 lane maxima, r = ceil(n / warps),
 // has r elements of that warp at or above it, so the least of these over the warps has n of the CTA;
 // what reaches it (20 to 140 elements for n = 1 to 64 of well-mixed logits) goes to shared memory, and each
@@ -30,13 +32,20 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kElems = 32;                      // logits per thread and chunk
-constexpr int kChunk = kThreads * kElems;       // 8192
+constexpr int kWords = 32;                      // 32-bit words of logits per thread and chunk
+constexpr int chunk_of(bool bf16) { return kThreads * kWords * (bf16 ? 2 : 1); }
 constexpr int kCap = 256;                       // candidates of a chunk, one per thread
 constexpr int kMaxParts = 64;                   // parts of a row: two lists per lane of the merging warp
 constexpr int kMergeThreads = 512;
 constexpr int kMergeSmem = 160 << 10;
 constexpr uint32_t kNinf = 0x007FFFFFu;         // ord_of(-inf); 0 stands for no element
+
+// packed maximum, which passes over NaN
+__device__ __forceinline__ uint32_t bf16x2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 // order-preserving map of a non-NaN float to uint32 (-inf is the least value any float maps to)
 __device__ __forceinline__ uint32_t ord_of(float x) {
@@ -59,6 +68,7 @@ struct SelectArgs {
   uint64_t* keys;  // [rows, parts, n], descending; 0: none
   float2* stats;   // [rows, parts] max, sum of exp(x - max)
   int parts, chunks;  // parts of a row, chunks of a row
+  int len;            // grid elements of a chunk, a multiple of 256 (the last may be short, or empty)
   int list_warps;     // merge: warps that merge beams
   int32_t* status;
 };
@@ -69,13 +79,16 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
   return ((uint64_t)hi << 32) | lo;
 }
 
+constexpr int kVecCap = 256;  // vectors with a candidate
+
 struct RowShared {
+  uint32_t words[kWords][kThreads];  // the chunk, in the rare paths; else the vectors with a candidate
   uint64_t cand[kCap + ORPO_MAX_SELECT];
   uint64_t best[ORPO_MAX_SELECT];
   uint32_t part[kWarps];
   float sum[kWarps];
   uint32_t thr[kWarps];
-  int count, total;
+  int vecs, count, total;
 };
 
 // Sum over the CTA of v; every thread gets it.
@@ -89,10 +102,78 @@ __device__ __forceinline__ int cta_sum(RowShared& sh, int v) {
   return sh.total;
 }
 
+// (a.x * b + c.x, a.y * b + c.y) and the like, two fp32 operations an instruction
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  return ((uint64_t)__float_as_uint(y) << 32) | __float_as_uint(x);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float lo2(uint64_t a) { return __uint_as_float((uint32_t)a); }
+__device__ __forceinline__ float hi2(uint64_t a) { return __uint_as_float((uint32_t)(a >> 32)); }
+
+// a thread's logits of a chunk, as loaded: word w of fp32, or words of two bf16
+template <bool kBf16>
+struct Elems {
+  static constexpr int kVec = kBf16 ? 8 : 4;             // logits per 16-byte load
+  static constexpr int kSize = kBf16 ? 2 : 4;
+  static constexpr int kN = kWords * (kBf16 ? 2 : 1);    // logits
+  static constexpr uint32_t kNone = kBf16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  uint32_t w[kWords];
+  __device__ __forceinline__ void put(RowShared& sh) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) sh.words[i][threadIdx.x] = w[i];
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (kBf16)
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    else
+      return __uint_as_float(w[i]);
+  }
+};
+
+__device__ __forceinline__ bool bf16_is_bad(uint32_t bits) {  // NaN or +inf
+  return (bits & 0x7fffu) > 0x7f80u || bits == 0x7f80u;
+}
+
+// Rare paths, on the chunk in shared memory (words[i][thread]); NaN counts as -inf.
+template <bool kBf16>
+struct Chunk {
+  const RowShared& sh;
+  int first, last;  // logit of this thread's element 0; the chunk's end
+  __device__ __forceinline__ int token_of(int i) const {
+    return first + i / Elems<kBf16>::kVec * (kThreads * Elems<kBf16>::kVec) + i % Elems<kBf16>::kVec;
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = sh.words[kBf16 ? i / 2 : i][threadIdx.x];
+    const float f = __uint_as_float(!kBf16 ? w : i & 1 ? w & 0xffff0000u : w << 16);
+    return f == f ? f : -INFINITY;
+  }
+  template <class F>
+  __device__ __forceinline__ int count(F f) const {
+    int k = 0;
+#pragma unroll 4
+    for (int i = 0; i < Elems<kBf16>::kN; ++i) k += f(i) ? 1 : 0;
+    return k;
+  }
+};
+
+__device__ __forceinline__ uint64_t key_of(float x, int token) {
+  return ((uint64_t)ord_of(x) << 32) | (uint32_t)~(uint32_t)token;
+}
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) {
-  constexpr int kVec = kBf16 ? 8 : 4;        // logits per 16-byte load
-  constexpr int kSize = kBf16 ? 2 : 4;
+  using E = Elems<kBf16>;
+  constexpr int kVec = E::kVec, kSize = E::kSize, kN = E::kN;
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel may be set up meanwhile
   const int64_t r = blockIdx.y;
   if (a.finished != nullptr && a.finished[r]) return;
   __shared__ RowShared sh;
@@ -101,58 +182,56 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
   // the row's 16-byte grid starts `off` logits before it: element e of the grid is logit e - off
   const int off = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / kSize);
   const int64_t grid_len = (int64_t)a.V + off;
-  const int c0 = (int)((int64_t)a.chunks * blockIdx.x / a.parts), c1 = (int)((int64_t)a.chunks * (blockIdx.x + 1) / a.parts);
-  // chunks of equal length, a multiple of 256 grid elements (the last may be short, or empty)
-  const int64_t len = (grid_len + (int64_t)a.chunks * 256 - 1) / ((int64_t)a.chunks * 256) * 256;
+  const int c0 = (int)((uint32_t)a.chunks * blockIdx.x / (uint32_t)a.parts);
+  const int c1 = (int)((uint32_t)a.chunks * (blockIdx.x + 1) / (uint32_t)a.parts);
   float run_m = -INFINITY, run_s = 0.f;
   int have = 0;  // keys in sh.best
   for (int c = c0; c < c1; ++c) {
-    const int64_t e0 = c * len, e1 = min(e0 + len, grid_len);
-    // ---- load: ord_of of each logit, 0 where there is none
-    uint32_t o[kElems];
-    bool bad = false;
+    const int64_t e0 = min((int64_t)c * a.len, grid_len), e1 = min(e0 + a.len, grid_len);
+    const int first = (int)(e0 - off) + tid * kVec;  // logit of this thread's element 0
+    auto token_of = [&](int i) { return first + i / kVec * (kThreads * kVec) + i % kVec; };
+    // ---- load; -inf where there is no logit
+    E x;
+    const int last = (int)(e1 - off);  // logits of the chunk end here (at most V)
 #pragma unroll
-    for (int i = 0; i < kElems / kVec; ++i) {
-      const int64_t e = e0 + ((int64_t)i * kThreads + tid) * kVec, v = e - off;
-      uint32_t w[kVec];  // fp32 bits
-      if (e < e1 && v >= 0 && v + kVec <= a.V) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + v * kSize));
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) w[j] = kBf16 ? (j & 1 ? y[j / 2] & 0xffff0000u : y[j / 2] << 16) : y[j];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          const float f = __uint_as_float(w[j]);
-          bad |= !(f < INFINITY);
-          o[i * kVec + j] = f == f ? ord_of(f) : kNinf;
-        }
+    for (int i = 0; i < kN / kVec; ++i) {
+      const int v = token_of(i * kVec);
+      uint32_t* w = x.w + i * 4;
+      if (v >= 0 && v <= last - kVec) {
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)v * kSize));
+        w[0] = y.x, w[1] = y.y, w[2] = y.z, w[3] = y.w;
       } else {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          o[i * kVec + j] = 0;
-          if (e < e1 && v + j >= 0 && v + j < a.V) {
-            float f;
-            if constexpr (kBf16)
-              f = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(row) + v + j) << 16);
-            else
-              f = __ldg(reinterpret_cast<const float*>(row) + v + j);
-            bad |= !(f < INFINITY);
-            o[i * kVec + j] = f == f ? ord_of(f) : kNinf;
+        for (int j = 0; j < 4; ++j) {
+          w[j] = E::kNone;
+          if constexpr (kBf16) {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + v + 2 * j;
+            if (v + 2 * j >= 0 && v + 2 * j < last) w[j] = (w[j] & 0xffff0000u) | __ldg(p);
+            if (v + 2 * j + 1 >= 0 && v + 2 * j + 1 < last) w[j] = (w[j] & 0xffffu) | ((uint32_t)__ldg(p + 1) << 16);
+          } else if (v + j >= 0 && v + j < last) {
+            w[j] = __ldg(reinterpret_cast<const uint32_t*>(row) + v + j);
           }
         }
       }
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, ORPO_STATUS_NONFINITE);
-    // logit of element i of this thread
-    auto token_of = [&](int i) { return (int)(e0 + ((int64_t)(i / kVec) * kThreads + tid) * kVec + i % kVec - off); };
-    // ---- max; threshold
-    uint32_t top = 0;
+    // ---- maxima (which pass over NaN) of each vector and of the thread
+    float vmax[kN / kVec], top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kElems; ++i) top = max(top, o[i]);
+    for (int i = 0; i < kN / kVec; ++i) {
+      const uint32_t* w = x.w + i * 4;
+      if constexpr (kBf16) {
+        const uint32_t m2 = bf16x2_max(bf16x2_max(w[0], w[1]), bf16x2_max(w[2], w[3]));
+        vmax[i] = fmaxf(__uint_as_float(m2 << 16), __uint_as_float(m2 & 0xffff0000u));
+      } else {
+        vmax[i] = fmaxf(fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1])), fmaxf(__uint_as_float(w[2]), __uint_as_float(w[3])));
+      }
+      top = fmaxf(top, vmax[i]);
+    }
+    // ---- CTA maximum; threshold
     // warps that hold an element: the grid is dealt out 32 lanes x kVec at a time
-    const int active = (int)max((int64_t)1, min((int64_t)kWarps, (e1 - e0 + 32 * kVec - 1) / (32 * kVec)));
-    const int need = (a.n + active - 1) / active;
-    uint32_t rest = top, rth = 0, wmax = 0;
+    const int active = max(1, min(kWarps, (int)(e1 - e0 + 32 * kVec - 1) / (32 * kVec)));
+    const int need = active == kWarps ? (a.n + kWarps - 1) / kWarps : (a.n + active - 1) / active;
+    uint32_t rest = ord_of(top), rth = 0, wmax = 0;
     for (int i = 0; i < min(need, 32); ++i) {
       rth = __reduce_max_sync(0xffffffffu, rest);
       if (i == 0) wmax = rth;
@@ -165,77 +244,127 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
       sh.part[warp] = wmax;
       sh.thr[warp] = warp < active ? rth : 0xffffffffu;
     }
-    if (tid == 0) sh.count = 0;
+    if (tid == 0) sh.count = sh.vecs = 0;
     __syncthreads();
     uint32_t cmax = 0, thr = 0xffffffffu;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) cmax = max(cmax, sh.part[w]), thr = min(thr, sh.thr[w]);
     if (have == a.n) thr = max(thr, (uint32_t)(sh.best[a.n - 1] >> 32));  // the n-th best of the chunks before
-    // ---- sum of exp(x - max)
-    const float m = cmax > kNinf ? ord_to_float(cmax) : -INFINITY;
+    const float m = ord_to_float(cmax);
+    // ---- sum of exp(x - m): 2^(x L - c) with c = m L rounded, which is put right after the sum
     float s = 0.f;
-    if (m > -INFINITY && m < INFINITY) {
+    const float c2 = m * kLog2e;
+    if (m < INFINITY && fabsf(c2) < INFINITY) {
+      uint64_t s2 = 0;
+      const uint64_t l2 = pack2(kLog2e, kLog2e), mc2 = pack2(-c2, -c2);
 #pragma unroll
-      for (int i = 0; i < kElems; ++i)
-        if (o[i] > kNinf) s += ex2_approx((ord_to_float(o[i]) - m) * kLog2e);
+      for (int i = 0; i < kN; i += 2) {
+        const uint64_t y = fma2(pack2(x.at(i), x.at(i + 1)), l2, mc2);
+        s2 = add2(s2, pack2(ex2_approx(lo2(y)), ex2_approx(hi2(y))));
+      }
+      s = (lo2(s2) + hi2(s2)) * ex2_approx(-fmaf(m, kLog2e, -c2));
+    } else if (m > -INFINITY && m < INFINITY) {  // near the type's lowest value
+      s = NAN;                                   // the slow sum below
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    // ---- NaN or +inf among the warp's logits (a NaN reaches every sum but that of a row without a maximum)
+    if (s != s || !(m < INFINITY && m > -INFINITY)) {
+      x.put(sh);
+      const Chunk<kBf16> ch{sh, first, last};
+      bool bad = false;
+      s = 0.f;
+#pragma unroll 2
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t w = sh.words[i][tid];
+        bad |= kBf16 ? bf16_is_bad(w & 0xffffu) || bf16_is_bad(w >> 16) : !(__uint_as_float(w) < INFINITY);
+      }
+      if (m > -INFINITY && m < INFINITY) {
+#pragma unroll 2
+        for (int i = 0; i < kN; ++i) s += ex2_approx((ch.at(i) - m) * kLog2e);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      if (bad) atomicOr(a.status, ORPO_STATUS_NONFINITE);
+    }
     if (lane == 0) sh.sum[warp] = s;
     // ---- candidates: what reaches the threshold; of masked logits only what is needed, below
-    const uint32_t live = max(thr, kNinf + 1);
+    const float live = thr > kNinf ? ord_to_float(thr) : -3.402823466e38f;
+    // first the vectors that hold one (most words of a warp's 32 x kVec have none), then their elements
+    __syncthreads();  // rare path: its readers of sh.words are done
 #pragma unroll
-    for (int i = 0; i < kElems; ++i)
-      if (o[i] >= live) {
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < kCap) sh.cand[at] = ((uint64_t)o[i] << 32) | (uint32_t)~(uint32_t)token_of(i);
+    for (int i = 0; i < kN / kVec; ++i)
+      if (vmax[i] >= live) {
+        const int at = atomicAdd(&sh.vecs, 1);
+        if (at < kVecCap) {
+          uint32_t* v = &sh.words[0][0] + at * 8;
+          v[0] = token_of(i * kVec);
+          *reinterpret_cast<uint4*>(v + 4) = make_uint4(x.w[i * 4], x.w[i * 4 + 1], x.w[i * 4 + 2], x.w[i * 4 + 3]);
+        }
       }
     __syncthreads();
-    int count = sh.count;
+    const int vecs = sh.vecs;
+    if (vecs <= kVecCap) {
+      for (int i = tid; i < vecs * kVec; i += kThreads) {
+        const uint32_t* v = &sh.words[0][0] + i / kVec * 8;
+        const int j = i % kVec;
+        const uint32_t w = v[4 + (kBf16 ? j / 2 : j)];
+        const float f = __uint_as_float(!kBf16 ? w : j & 1 ? w & 0xffff0000u : w << 16);
+        if (f >= live) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < kCap) sh.cand[at] = key_of(f, (int)v[0] + j);
+        }
+      }
+    }
+    __syncthreads();
+    int count = vecs <= kVecCap ? sh.count : kCap + 1;
     __syncthreads();
     if (count > kCap) {
-      // ---- exact: the largest t that n elements reach (at least kCap > n do reach `live`)
-      uint32_t lo = live, hi = cmax;
+      // ---- exact: the largest t that n logits reach, by bisection, if that many reach `live` at all
+      x.put(sh);
+      const Chunk<kBf16> ch{sh, first, last};
+      uint32_t lo = ord_of(live), hi = cmax;
+      const int all = cta_sum(sh, ch.count([&](int i) { return ord_of(ch.at(i)) >= lo; }));
+      const int want = min(a.n, all);
       while (lo < hi) {
         const uint32_t mid = lo + (hi - lo + 1) / 2;
-        int k = 0;
-#pragma unroll
-        for (int i = 0; i < kElems; ++i) k += o[i] >= mid;
-        if (cta_sum(sh, k) >= a.n)
+        if (cta_sum(sh, ch.count([&](int i) { return ord_of(ch.at(i)) >= mid; })) >= want)
           lo = mid;
         else
           hi = mid - 1;
       }
-      int k = 0;
-#pragma unroll
-      for (int i = 0; i < kElems; ++i) k += o[i] > lo;
-      const int equal = a.n - cta_sum(sh, k);  // so many of those equal to t, the lowest tokens
-      int64_t b0 = e0 - off, b1 = e1 - off;    // the least bound that so many lie below
+      // of those equal to t the lowest tokens, so many as are missing: the least bound that they lie below
+      const int equal = want - cta_sum(sh, ch.count([&](int i) { return ord_of(ch.at(i)) > lo; }));
+      int b0 = (int)(e0 - off), b1 = last;
       while (b0 < b1) {
-        const int64_t mid = b0 + (b1 - b0) / 2;
-        k = 0;
-#pragma unroll
-        for (int i = 0; i < kElems; ++i) k += o[i] == lo && token_of(i) < mid;
-        if (cta_sum(sh, k) >= equal)
+        const int mid = b0 + (b1 - b0) / 2;
+        if (cta_sum(sh, ch.count([&](int i) { return ord_of(ch.at(i)) == lo && ch.token_of(i) < mid; })) >= equal)
           b1 = mid;
         else
           b0 = mid + 1;
       }
       if (tid == 0) sh.count = 0;
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kElems; ++i)
-        if (o[i] > lo || (o[i] == lo && token_of(i) < b0))
-          sh.cand[atomicAdd(&sh.count, 1)] = ((uint64_t)o[i] << 32) | (uint32_t)~(uint32_t)token_of(i);
+#pragma unroll 2
+      for (int i = 0; i < kN; ++i) {
+        const float f = ch.at(i);
+        const uint32_t o = ord_of(f);
+        if (o > lo || (o == lo && ch.token_of(i) < b0)) sh.cand[atomicAdd(&sh.count, 1)] = key_of(f, ch.token_of(i));
+      }
       __syncthreads();
       count = sh.count;
-    } else if (count < a.n && have < a.n) {
+      __syncthreads();
+    }
+    if (count < a.n && have < a.n) {
       // ---- too few live logits: masked ones by lowest token, all among the first n + count of the chunk
-      const int64_t bound = max(e0 - off, (int64_t)0) + a.n + count;
-#pragma unroll
-      for (int i = 0; i < kElems; ++i)
-        if (o[i] == kNinf && token_of(i) < bound)
-          sh.cand[atomicAdd(&sh.count, 1)] = ((uint64_t)o[i] << 32) | (uint32_t)~(uint32_t)token_of(i);
+      x.put(sh);
+      const Chunk<kBf16> ch{sh, first, last};
+      const int from = max((int)(e0 - off), 0), bound = min(last, from + a.n + count);
+#pragma unroll 2
+      for (int i = 0; i < kN; ++i) {
+        const int v = ch.token_of(i);
+        if (v >= from && v < bound && ch.at(i) == -INFINITY) sh.cand[atomicAdd(&sh.count, 1)] = key_of(-INFINITY, v);
+      }
       __syncthreads();
       count = sh.count;
     }
@@ -271,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
 
 __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs a) {
   extern __shared__ uint64_t lists[];  // one per warp: the keys of its beam's parts; then values and tokens
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the row kernel's lists are there
   const int64_t b = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ uint8_t over[ORPO_MAX_BEAMS];
@@ -308,7 +438,8 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
       lse = m + logf(s);
     }
     __syncwarp();
-    // the n largest of the sorted lists: each lane holds the heads of lists lane and lane + 32
+    // the n largest of the sorted lists: each lane holds the heads of lists lane and lane + 32 (a threshold
+    // and ranks by counting, as in the row kernel, took 1.6 to 2.4 us longer here)
     int h0 = 0, h1 = 0;
     uint64_t k0 = lane < a.parts ? mine[lane * a.n] : 0, k1 = lane + 32 < a.parts ? mine[(lane + 32) * a.n] : 0;
     for (int i = 0; i < a.n; ++i) {
@@ -357,12 +488,14 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
 
 // Chunks of a row, and the parts (CTAs) they are dealt to.
 struct RowPlan {
-  int chunks, parts;
+  int chunks, parts, len;
 };
-RowPlan row_plan(int64_t V, bool aligned) {
+RowPlan row_plan(int64_t V, bool bf16, bool aligned) {
   RowPlan p;
-  p.chunks = (int)cdiv(V + (aligned ? 0 : 7), kChunk);  // up to 7 elements of a row's grid lie before it
+  const int64_t grid = V + (aligned ? 0 : 7);  // up to 7 elements of a row's grid lie before it
+    p.chunks = (int)cdiv(grid, chunk_of(bf16));
   p.parts = std::min(p.chunks, kMaxParts);
+  p.len = (int)(cdiv(grid, (int64_t)p.chunks * 256) * 256);
   return p;
 }
 
@@ -378,7 +511,7 @@ using namespace orpo;
 
 extern "C" size_t orpo_beam_select_workspace_bytes(int64_t batch, int beams, int64_t V, int n) {
   if (!select_sizes_ok(batch, beams, V, n)) return 0;
-  return (size_t)(batch * beams) * row_plan(V, false).parts * ((size_t)n * 8 + 8) + 16;
+  return (size_t)(batch * beams) * row_plan(V, false, false).parts * ((size_t)n * 8 + 8) + 16;
 }
 
 extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logits_bf16, const float* score,
@@ -400,9 +533,9 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = batch * beams;
   const int size = logits_bf16 ? 2 : 4;
-  const RowPlan plan = row_plan(V, aligned16(logits) && (ld_logits * size) % 16 == 0);
+  const RowPlan plan = row_plan(V, logits_bf16 != 0, aligned16(logits) && (ld_logits * size) % 16 == 0);
   SelectArgs a{logits, ld_logits, score, finished, eos, beams, (int)V, n, out_score, out_parent, out_token,
-               out_finished, static_cast<uint64_t*>(workspace), nullptr, plan.parts, plan.chunks, 0, status};
+               out_finished, static_cast<uint64_t*>(workspace), nullptr, plan.parts, plan.chunks, plan.len, 0, status};
   a.stats = reinterpret_cast<float2*>(a.keys + rows * plan.parts * n);
   // rows in launches of at most 65535
   prof_begin(K_BEAM, st);
@@ -428,7 +561,18 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
   static std::atomic<int> done[64];
   if (opt_in_smem(select_merge_kernel, kMergeSmem, done) != cudaSuccess) return ORPO_ERR_CUDA;
   prof_begin(K_BEAM, st);
-  select_merge_kernel<<<(unsigned)batch, std::max(warps, 4) * 32, smem, st>>>(a);
+  // launched while the row kernel runs; it waits for it on the device
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)batch);
+  cfg.blockDim = dim3((unsigned)std::max(warps, 4) * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, select_merge_kernel, a);
   prof_end(K_BEAM, st);
-  return cudaGetLastError() == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
+  return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
 }
