@@ -58,7 +58,7 @@ struct TcCtl {
   uint64_t drain[kMma];
   uint32_t tmem_base;
   volatile int abort_flag;
-  uint32_t plain[kMaxStages][4];  // per stage and warp of rows: scales as they are, not times 2^133
+  uint16_t plain[kMaxStages][2];  // per stage a byte for each 32 rows: 1 if their scales are as they are, not times 2^133
 };
 constexpr int kCtlBytes = 1024;
 static_assert(sizeof(TcCtl) <= kCtlBytes, "control block");
@@ -193,7 +193,7 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
 }
 
 // One of the four warps that bring scales and biases beside the segments of q: segments turn, turn + 2, ...,
-// rows row0 + lane and + 32 of the tile.
+// rows row0 + lane and + 32 of the tile.  (Two warps with four rows a lane took 3 to 10% longer.)
 template <int kSegK>
 struct ScaleRole {
   const TcArgs& p;
@@ -206,43 +206,52 @@ struct ScaleRole {
   __device__ __forceinline__ void run() const {
     constexpr int kPairs = W ? W / 2 : kSegK / 64;
     const LogitsArgs& a = p.a;
-    const int64_t total = (int64_t)my_tiles * p.segs;
     uint32_t sc[2][kPairs], bi[2][kPairs];  // per row the groups of the segment, in pairs
-    int seg = turn;                         // of the next fetch
+    // the next fetch: its segment, its tile's first row, and where the first of my rows' scales and biases are
+    int seg = turn;
     int64_t row = (int64_t)blockIdx.x * kTileRows + row0 + lane;
+    const uint16_t *s, *b;
+    int rows = 0;  // of my two, those inside the vocabulary
+    auto enter_tile = [&]() {
+      s = a.scales + row * p.ngroups;
+      b = a.biases + row * p.ngroups;
+      rows = row >= a.V ? 0 : row + 32 < a.V ? 2 : 1;
+    };
+    const int64_t pitch = (int64_t)32 * p.ngroups;
     auto fetch = [&]() {
       const int g0 = W ? seg * W : (int)group_of(p, (uint32_t)(seg * p.seg_words));
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int64_t v = row + 32 * r;
+        const uint16_t* sr = s + r * pitch + g0;
+        const uint16_t* br = b + r * pitch + g0;
+        if (r >= rows) {
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) sc[r][i] = bi[r][i] = 0;
-        if (v >= a.V) continue;
-        const uint16_t* s = a.scales + v * p.ngroups + g0;
-        const uint16_t* b = a.biases + v * p.ngroups + g0;
-        if constexpr (W == 8) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(s)), y = __ldg(reinterpret_cast<const uint4*>(b));
+          for (int i = 0; i < kPairs; ++i) sc[r][i] = bi[r][i] = 0;
+        } else if constexpr (W == 8) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(sr)), y = __ldg(reinterpret_cast<const uint4*>(br));
           sc[r][0] = x.x, sc[r][1] = x.y, sc[r][2] = x.z, sc[r][3] = x.w;
           bi[r][0] = y.x, bi[r][1] = y.y, bi[r][2] = y.z, bi[r][3] = y.w;
         } else if constexpr (W == 4) {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(s)), y = __ldg(reinterpret_cast<const uint2*>(b));
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(sr)), y = __ldg(reinterpret_cast<const uint2*>(br));
           sc[r][0] = x.x, sc[r][1] = x.y, bi[r][0] = y.x, bi[r][1] = y.y;
         } else if constexpr (W == 2) {
-          sc[r][0] = __ldg(reinterpret_cast<const uint32_t*>(s)), bi[r][0] = __ldg(reinterpret_cast<const uint32_t*>(b));
+          sc[r][0] = __ldg(reinterpret_cast<const uint32_t*>(sr)), bi[r][0] = __ldg(reinterpret_cast<const uint32_t*>(br));
         } else {
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) sc[r][i] = bi[r][i] = 0;
 #pragma unroll
           for (int i = 0; i < 2 * kPairs; ++i) {
             const int gi = (int)group_of(p, (uint32_t)(seg * p.seg_words + i)) - g0;
             if (i < p.seg_words && g0 + gi < p.ngroups) {
-              sc[r][i / 2] |= (uint32_t)__ldg(s + gi) << (16 * (i & 1));
-              bi[r][i / 2] |= (uint32_t)__ldg(b + gi) << (16 * (i & 1));
+              sc[r][i / 2] |= (uint32_t)__ldg(sr + gi) << (16 * (i & 1));
+              bi[r][i / 2] |= (uint32_t)__ldg(br + gi) << (16 * (i & 1));
             }
           }
         }
       }
     };
-    // A segment's scales are fetched two segments ahead, which covers the way from L2 and
-    // not from memory: the rows' scales of the next tile, contiguous, are brought to L2 a tile ahead.
+    // A segment's scales are fetched two segments ahead, which covers the way from L2 and not from memory:
+    // the rows' scales of the next tile, contiguous, are brought to L2 a tile ahead.
     const uint32_t tile_bytes = (uint32_t)(kTileRows * 2) * p.ngroups;
     int64_t ahead = (int64_t)blockIdx.x + gridDim.x;
     auto prefetch = [&]() {
@@ -253,9 +262,12 @@ struct ScaleRole {
     auto wrap = [&]() {
       while (seg >= p.segs) {
         seg -= p.segs, row += (int64_t)gridDim.x * kTileRows;
+        enter_tile();
         prefetch();
       }
     };
+    const int64_t total = (int64_t)my_tiles * p.segs;
+    enter_tile();
     prefetch();
     wrap();
     if (turn < total) fetch();
@@ -263,6 +275,7 @@ struct ScaleRole {
     for (int64_t left = total - turn; left > 0; left -= 2) {
       if (!wait_warp(ctl, &ctl->w_empty[stage], ph ^ 1u, a.status)) break;
       const uint32_t out = sring + stage * kScaleBytes + (row0 + lane) * 4;
+      uint32_t flags = 0;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         uint32_t big[kPairs], odd = 0;  // times 2^133; odd: NaN where one is infinite or NaN, else 0
@@ -271,8 +284,8 @@ struct ScaleRole {
           big[i] = bf16x2_mul(bf16x2_mul(sc[r][i], 0x7F007F00u), 0x42804280u);  // 2^127, 2^6
           odd = bf16x2_fma(big[i], 0u, odd);
         }
-        const bool plain = __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0);
-        if (plain) {
+        if (__any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0)) {
+          flags |= 1u << (8 * r);
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) big[i] = sc[r][i];
         }
@@ -283,8 +296,8 @@ struct ScaleRole {
           if (W || 2 * i + 1 < p.seg_words)
             sts32(out + r * 128 + (2 * i + 1) * (kTileRows * 4), __byte_perm(big[i], bi[r][i], 0x7632));
         }
-        if (lane == 0) ctl->plain[stage][row0 / 32 + r] = plain ? 1u : 0u;
       }
+      if (lane == 0) ctl->plain[stage][row0 / 64] = (uint16_t)flags;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->w_full[stage]);
       seg += 2;
@@ -605,7 +618,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       for (int i = 0; i < kVec; ++i) w[i] = lds128(wst + (((half * 4 + i) << 4) ^ swz));
 #pragma unroll
       for (int i = 0; i < 4; ++i) sw[i] = lds32(sst + soff[i]);
-      const bool plain = lds32(smem_u32(&ctl->plain[stage][q])) != 0;
+      const bool plain = (lds32(smem_u32(ctl->plain[stage])) >> (8 * q) & 1u) != 0;
       const uint32_t dst = trow + (slot * kUnits + half) * 64;
 #pragma unroll
       for (int part = 0; part < 2; ++part) {  // 64 columns: 32 words of tensor memory
