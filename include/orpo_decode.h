@@ -47,12 +47,16 @@ extern "C" {
  * row's logits and no other.  The sum's order depends on the sizes alone, so results repeat bit
  * for bit.
  * Meant for few rows: the quantised weights are read once per 64 rows of h.
+ * Workspace: orpo_head_logits_q_workspace_bytes(M, d, bits) bytes, 16-byte aligned; 0 (workspace may be
+ * NULL) for up to 16 rows that fit on chip (d <= 4608, 8-bit d <= 2560), else about 2 M d: a copy of h in
+ * the order the kernel takes it.
  * Limits: 0 <= M <= 2^31 - 2^16, 1 <= V <= 2^31 - 2^16, 8 <= d < 2^20, d a multiple of 8.
  */
+size_t orpo_head_logits_q_workspace_bytes(int64_t M, int64_t d, int bits);
 int orpo_head_logits_q(const void* h_bf16, int64_t ld_h, const uint8_t* wq, const void* scales_bf16,
                        const void* biases_bf16, int bits, int group, int64_t M, int64_t V, int64_t d,
                        float softcap, void* logits, int64_t ld_logits, int logits_bf16,
-                       int32_t* status, void* stream);
+                       void* workspace, size_t ws_bytes, int32_t* status, void* stream);
 
 /*
  * The n best continuations of each of `batch` entries with `beams` beams.

@@ -21,7 +21,7 @@ __all__ = [
     "orpo_head_bwd", "orpo_status_string", "orpo_debug_gemm", "OrpoHead", "STATUS_BITS",
     "orpo_profile_start", "orpo_profile_stop", "orpo_head_fwd_static", "orpo_debug_wait_timeout",
     "orpo_pref_loss", "PREF_KINDS", "orpo_head_q_workspace_bytes", "orpo_head_fwd_q", "orpo_head_bwd_q",
-    "use_bounds_checked_library", "orpo_head_logits_q", "orpo_beam_select", "orpo_beam_select_workspace_bytes",
+    "use_bounds_checked_library", "orpo_head_logits_q", "orpo_head_logits_q_workspace_bytes", "orpo_beam_select", "orpo_beam_select_workspace_bytes",
     "orpo_beam_reorder", "BeamDecoder",
 ]
 
@@ -108,8 +108,10 @@ def load():
                                        i64, f32, vp, vp, ctypes.c_int, vp, sz, vp, vp]
     L.orpo_head_bwd_q_skip.restype = ctypes.c_int
     L.orpo_head_logits_q.argtypes = [vp, i64, vp, vp, vp, ctypes.c_int, ctypes.c_int, i64, i64, i64, f32, vp, i64,
-                                     ctypes.c_int, vp, vp]
+                                     ctypes.c_int, vp, sz, vp, vp]
     L.orpo_head_logits_q.restype = ctypes.c_int
+    L.orpo_head_logits_q_workspace_bytes.argtypes = [i64, i64, ctypes.c_int]
+    L.orpo_head_logits_q_workspace_bytes.restype = sz
     L.orpo_beam_select_workspace_bytes.argtypes = [i64, ctypes.c_int, i64, ctypes.c_int]
     L.orpo_beam_select_workspace_bytes.restype = sz
     L.orpo_beam_select.argtypes = [vp, i64, ctypes.c_int, vp, vp, i32, i64, ctypes.c_int, i64, ctypes.c_int, vp, vp,
@@ -427,12 +429,26 @@ LOGITS = (torch.float32, torch.bfloat16)
 F32, I32, U8, FLAGS = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.uint8, torch.bool)
 
 
-def orpo_head_logits_q(h, wq, scales, biases, bits, group, softcap, logits, status, stream=None):
+def orpo_head_logits_q_workspace_bytes(M: int, d: int, bits: int) -> int:
+    return int(load().orpo_head_logits_q_workspace_bytes(M, d, bits))
+
+
+def orpo_head_logits_q(h, wq, scales, biases, bits, group, softcap, logits, status, stream=None, workspace=None):
     """Logits [M, V] (fp32 or bf16) of the rows of h [M, d] under the affine group-quantised head.
 
-    h and logits may have any row pitch, e.g. hidden[:, -1] of [M, T, d] hidden states."""
+    h and logits may have any row pitch, e.g. hidden[:, -1] of [M, T, d] hidden states.  workspace: uint8,
+    orpo_head_logits_q_workspace_bytes(M, d, bits) of them; None takes what is needed from PyTorch's
+    allocator."""
     M, d = h.shape
     V = wq.shape[0]
+    if workspace is not None:
+        _dev(workspace, "workspace", U8)
+    elif M > 16 or d > 2048:
+        need = (_lib or load()).orpo_head_logits_q_workspace_bytes(M, d, bits)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
+            if stream is not None:
+                workspace.record_stream(stream)
     # A decode step is a few microseconds of GPU work, so the usual, right arguments pass one plain test;
     # whatever fails it is looked at in full for its message.
     hp, hs = h.stride()
@@ -449,7 +465,8 @@ def orpo_head_logits_q(h, wq, scales, biases, bits, group, softcap, logits, stat
         _dev(status, "status", I32)
     code = (_lib or load()).orpo_head_logits_q(
         h.data_ptr(), hp, wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), bits, group, M, V, d, softcap,
-        logits.data_ptr(), lp, logits.dtype is torch.bfloat16, status.data_ptr(), _stream(stream))
+        logits.data_ptr(), lp, logits.dtype is torch.bfloat16, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel(), status.data_ptr(), _stream(stream))
     if code:
         raise OrpoError(code, "orpo_head_logits_q")
 
@@ -635,6 +652,8 @@ class BeamDecoder:
         if ws == 0:
             raise ValueError(f"batch {batch}, beams {beams}, V {V} are out of orpo_beam_select's range")
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        self.logits_workspace = torch.empty(orpo_head_logits_q_workspace_bytes(batch * beams, d, bits), dtype=torch.uint8,
+                                            device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.logits = torch.empty((batch * beams, V), dtype=logits_dtype, device=dev)
         self.score = torch.empty((batch, beams), dtype=torch.float32, device=dev)
@@ -656,7 +675,7 @@ class BeamDecoder:
         states: tensors [outer, batch * beams, rows, capacity, unit] that follow their parents, up to
         position length[b] of each entry."""
         orpo_head_logits_q(h, wq, scales, biases, self.bits, self.group, self.softcap, self.logits, self.status,
-                           stream)
+                           stream, self.logits_workspace)
         orpo_beam_select(self.logits, self.score, self.finished, self.eos, self.beams, self.score, self.parent,
                          self.token, self.finished, self.workspace, self.status, stream)
         for state in states:

@@ -308,10 +308,15 @@ cudaError_t launch_generic(const LogitsArgs& a, int bits, cudaStream_t st) {
 
 using namespace orpo;
 
+extern "C" size_t orpo_head_logits_q_workspace_bytes(int64_t M, int64_t d, int bits) {
+  if (M < 1 || M > kMaxRows || d < 8 || d >= (1 << 20) || (bits != 4 && bits != 8)) return 0;
+  return logits_tc_workspace(bits, M, d);
+}
+
 extern "C" int orpo_head_logits_q(const void* h, int64_t ld_h, const uint8_t* wq, const void* scales,
                                   const void* biases, int bits, int group, int64_t M, int64_t V, int64_t d,
-                                  float softcap, void* logits, int64_t ld_logits, int logits_bf16, int32_t* status,
-                                  void* stream) {
+                                  float softcap, void* logits, int64_t ld_logits, int logits_bf16, void* workspace,
+                                  size_t ws_bytes, int32_t* status, void* stream) {
   if (M < 0 || M > kMaxRows || V < 1 || V > kMaxRows || d < 8 || d >= (1 << 20)) return ORPO_ERR_SHAPE;
   if (M == 0) return ORPO_OK;
   if (ld_h < d || ld_logits < V || ld_h > (1ll << 40) || ld_logits > (1ll << 40)) return ORPO_ERR_SHAPE;
@@ -322,6 +327,11 @@ extern "C" int orpo_head_logits_q(const void* h, int64_t ld_h, const uint8_t* wq
   if (d % 8 != 0 || ld_h % 8 != 0 || !aligned16(h) || (reinterpret_cast<uintptr_t>(logits) & out_align))
     return ORPO_ERR_ALIGN;
   if (!isfinite(softcap)) return ORPO_ERR_ARG;
+  if (const size_t need = logits_tc_workspace(bits, M, d)) {
+    if (!workspace) return ORPO_ERR_NULL;
+    if (!aligned16(workspace)) return ORPO_ERR_ALIGN;
+    if (ws_bytes < need) return ORPO_ERR_WORKSPACE;
+  }
   int sms = 0;
   if (int e = device_check(&sms)) return e;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -339,7 +349,7 @@ extern "C" int orpo_head_logits_q(const void* h, int64_t ld_h, const uint8_t* wq
     a.out = static_cast<uint8_t*>(logits) + m * ld_logits * (logits_bf16 ? 2 : 4);
     a.M = (int)std::min(chunk, M - m);
     prof_begin(K_LOGITS, st);
-    const cudaError_t e = tensor     ? launch_logits_tc(a, bits, sms, st)
+    const cudaError_t e = tensor     ? launch_logits_tc(a, bits, sms, workspace, st)
                           : streamed ? (bits == 4 ? launch_stream_rows<4>(a, sms, st) : launch_stream_rows<8>(a, sms, st))
                                    : launch_generic(a, bits, st);
     prof_end(K_LOGITS, st);

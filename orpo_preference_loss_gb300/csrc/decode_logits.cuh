@@ -24,15 +24,17 @@ struct LogitsArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ float softcap_of(float z, float cap) {
-  if (cap <= 0.f) return z;
-  const float u = z / cap;
+// cap tanh(z / cap), inv = 1 / cap: the series for small |z / cap| (no cancellation), else by ex2; both are
+// computed and one taken, so that lanes do not part
+__device__ __forceinline__ float softcap_of(float z, float cap, float inv) {
+  const float u = z * inv;
   float q;
-  return cap * (fabsf(u) < kTanhSmall ? tanh_small(u) : tanh_exp(u, &q));
+  const float s = tanh_small(u), e = tanh_exp(u, &q);
+  return cap * (fabsf(u) < kTanhSmall ? s : e);
 }
 
 __device__ __forceinline__ void store_logit(const LogitsArgs& a, int m, int v, float z) {
-  const float x = softcap_of(z, a.softcap);
+  const float x = a.softcap > 0.f ? softcap_of(z, a.softcap, 1.f / a.softcap) : z;
   const int64_t at = (int64_t)m * a.ld_out + v;
   if (a.out_bf16)
     static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
@@ -104,7 +106,9 @@ __device__ __forceinline__ void dequant8_scaled(uint32_t w, uint32_t s133, uint3
   p[1] = bf16x2_fma((w >> 8) & 0x00FF00FFu, s133, b);
 }
 
-// Tensor-core kernel (decode_logits_tc.cu); cudaErrorNotSupported when a tensor map cannot be made.
-cudaError_t launch_logits_tc(const LogitsArgs& a, int bits, int sms, cudaStream_t st);
+// Tensor-core kernel (decode_logits_tc.cu), its workspace, and a cudaErrorNotSupported when a tensor map
+// cannot be made.
+size_t logits_tc_workspace(int bits, int64_t M, int64_t d);
+cudaError_t launch_logits_tc(const LogitsArgs& a, int bits, int sms, void* workspace, cudaStream_t st);
 
 }  // namespace orpo

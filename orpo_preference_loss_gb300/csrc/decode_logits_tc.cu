@@ -10,18 +10,24 @@
 // into bf16: 9 instructions per 8 weights where the scales allow it (dequant4_scaled), 15 where not.
 //
 // Roles (warps):
-//   0       TMA of q: 128-byte segments of the tile's 128 rows (16 KiB boxes, 128-byte swizzle) into a ring
+//   0       TMA of q: segments of 256 columns of the tile's 128 rows (one 16 KiB box of 128-byte swizzled
+//           rows, 8-bit: two) into a ring
 //   1, 2    MMA issue: the even and the odd segments, each into accumulators of its own
-//   3       TMA of h, either all of it once (resident) or per 128 columns (streamed)
+//   3       h (below)
 //   4..7    scales and biases, every second segment and half of the rows each: (scale, bias) words beside
 //           the segment of q in the ring; scales multiplied by 2^133 where those of 32 rows are all small
 //           enough, which a flag of the stage says
-//   8..11   h into the dequantised order (below), then sums and output of the accumulators
-//   12..    dequantisation, 4 warps per group, a thread per vocabulary row; group i takes units of 128
+//   8..     sums and output of the accumulators, a thread per vocabulary row and up to 32 columns
+//   then    dequantisation, 4 warps per group, a thread per vocabulary row; group i takes units of 128
 //           columns i, i + kGroups, ...
 //
 // Order of k: 4-bit dequantisation yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights
-// (8-bit: (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes in place.
+// (8-bit: (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes at a
+// time.  Up to 16 rows of h that fit beside the weights (d up to 4608, 8-bit 2560) are loaded and put in
+// that order by each CTA, once.  More are streamed: a small kernel first writes h in that order, and as
+// shared memory holds it, to the workspace, and the CTAs work in pairs (clusters) on neighbouring tiles,
+// each fetching half of every unit of h for both (multicast), since h crosses from L2 once per tile: at 64
+// rows that is twice the weights' bytes.
 // Accuracy: the tensor core truncates as it accumulates (measured: 1e-9 of the result per product, one
 // sign), so an accumulator spans 512 columns and those sums are added in registers, rounding.
 #include <math.h>
@@ -37,11 +43,11 @@ namespace orpo {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kSegBytes = 128;                        // bytes of a row per segment
-constexpr int kStageBytes = kTileRows * kSegBytes;    // 16 KiB
+constexpr int kBoxBytes = kTileRows * 128;            // a TMA box: 128 bytes of every row, up to 16 KiB
 constexpr int kUnitK = 128;                           // columns per A buffer (64 tensor-memory columns)
 constexpr int kAccK = 512;                            // columns per accumulator
-constexpr int kScaleBytes = kSegBytes / 16 * kTileRows * 4;  // words of a segment: 4 KiB (8-bit: half used)
+constexpr int kUnits = 2, kSegK = kUnits * kUnitK;    // units and columns per segment
+constexpr int kScaleBytes = kSegK / 32 * kTileRows * 4;  // (scale, bias) words of a segment, at most one per 32 columns
 constexpr int kMaxStages = 8;
 constexpr int kMaxH = 8;  // streamed h: units in the ring
 constexpr int kMaxABufs = 4;
@@ -54,7 +60,8 @@ struct TcCtl {
   uint64_t w_full[kMaxStages], w_empty[kMaxStages];
   uint64_t a_full[kMaxABufs], a_empty[kMaxABufs];
   uint64_t d_full[2 * kMma], d_empty[2 * kMma];  // [MMA warp][set]
-  uint64_t h_raw[kMaxH], h_full[kMaxH], h_empty[kMaxH];
+  uint64_t h_full[kMaxH], h_empty[kMaxH];  // streamed h; h_full[0]: resident h is loaded
+  uint64_t h_ready;                        // resident h is in order
   uint64_t drain[kMma];
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -65,40 +72,49 @@ static_assert(sizeof(TcCtl) <= kCtlBytes, "control block");
 
 struct TcArgs {
   LogitsArgs a;
-  int tiles, segs;        // tiles of 128 rows, segments per row
+  int tiles, segs;        // tiles, segments per row
+  int rows;               // vocabulary rows per tile, at most 128
   int units;              // 128-column units per row: segs * units per segment
   int ngroups;            // groups per row
   int seg_words, shift;   // scale words per segment: one per 2^shift times 32 columns
   uint32_t gmul;          // group of word j of a row: j if 0, else umulhi(j, gmul)
   int stages;             // weight ring
-  int hslots;             // streamed h: ring slots; 0: h is resident
+  int hslots;             // streamed h: ring slots
+  const uint8_t* image;   // streamed h: [m tiles][units] units as shared memory holds them
   int wide_scales;        // a segment's scales and biases are one aligned word of up to 16 bytes
 };
 
 // One wait of up to kPollNs in the barrier unit: the polls of eight waiting warps at the default
 // interval took as many issue slots as the dequantisation.
 constexpr uint32_t kPollNs = 20000;
+template <bool kCluster>  // acquire at cluster scope: the other CTA of a pair arrives on the barrier too
 __device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
-      : "memory");
+  if constexpr (kCluster)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
+        : "memory");
   return ok != 0;
 }
 
-__device__ __forceinline__ uint32_t group_of(const TcArgs& p, uint32_t word) {
-  return p.gmul ? __umulhi(word, p.gmul) : word;
-}
-
 // Bounded wait: false on a timeout (reported) or when another role gave up.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(TcCtl* ctl, uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (poll_bar(bar, parity)) return true;
+  if (__builtin_expect(poll_bar<kCluster>(bar, parity), 1)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!poll_bar(bar, parity)) {
+  while (!poll_bar<kCluster>(bar, parity)) {
     if (ctl->abort_flag) return false;
     if (globaltimer_ns() - t0 > kLimitNs) {
       atomicOr(status, ORPO_STATUS_TIMEOUT);
@@ -110,8 +126,9 @@ __device__ __forceinline__ bool wait_bar(TcCtl* ctl, uint64_t* bar, uint32_t par
 }
 
 // The same for a whole warp: every lane gets the same answer.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_warp(TcCtl* ctl, uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, wait_bar(ctl, bar, parity, status));
+  return __all_sync(0xffffffffu, wait_bar<kCluster>(ctl, bar, parity, status));
 }
 
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
@@ -130,6 +147,25 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b_
       : "memory");
 }
 
+// `bytes` (a multiple of 16) of global memory to the same shared-memory offset of both CTAs of the pair, counted
+// on the barrier at the same offset of each.
+__device__ __forceinline__ void bulk_load_pair(const void* src, uint32_t bytes, void* dst, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"((uint16_t)3)
+      : "memory");
+}
+
+// Arrive on the barrier at this offset of both CTAs once every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -141,18 +177,24 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-#define ORPO_IN32(r)                                                                                          \
-  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),   \
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),            \
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),            \
-      "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+#define ORPO_IN16(r, o)                                                                                              \
+  "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7]), \
+      "r"(r[o + 8]), "r"(r[o + 9]), "r"(r[o + 10]), "r"(r[o + 11]), "r"(r[o + 12]), "r"(r[o + 13]), "r"(r[o + 14]),  \
+      "r"(r[o + 15])
 
-// 32 columns of this thread's lane (warp's quadrant)
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// 16 or 32 columns of this thread's lane (warp's quadrant)
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      ORPO_IN16(r, 0)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
       "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      ORPO_IN32(r)
+      ORPO_IN16(r, 0), ORPO_IN16(r, 16)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -178,6 +220,17 @@ __device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// 8 values of h in the order of the dequantised weights' pairs
+template <int kBits>
+__device__ __forceinline__ uint4 reorder_pairs(const uint4& x) {
+  if constexpr (kBits == 4)
+    return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                      __byte_perm(x.y, x.w, 0x7632));
+  else
+    return make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x5410),
+                      __byte_perm(x.z, x.w, 0x7632));
+}
+
 // f(0..3, word) over a vector's words
 template <class F>
 __device__ __forceinline__ void unpack(const uint4& v, F f) {
@@ -192,9 +245,12 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ uint32_t group_of(const TcArgs& p, uint32_t word) {
+  return p.gmul ? __umulhi(word, p.gmul) : word;
+}
+
 // One of the four warps that bring scales and biases beside the segments of q: segments turn, turn + 2, ...,
 // rows row0 + lane and + 32 of the tile.  (Two warps with four rows a lane took 3 to 10% longer.)
-template <int kSegK>
 struct ScaleRole {
   const TcArgs& p;
   TcCtl* ctl;
@@ -209,7 +265,7 @@ struct ScaleRole {
     uint32_t sc[2][kPairs], bi[2][kPairs];  // per row the groups of the segment, in pairs
     // the next fetch: its segment, its tile's first row, and where the first of my rows' scales and biases are
     int seg = turn;
-    int64_t row = (int64_t)blockIdx.x * kTileRows + row0 + lane;
+    int64_t row = (int64_t)blockIdx.x * p.rows + row0 + lane;
     const uint16_t *s, *b;
     int rows = 0;  // of my two, those inside the vocabulary
     auto enter_tile = [&]() {
@@ -252,16 +308,16 @@ struct ScaleRole {
     };
     // A segment's scales are fetched two segments ahead, which covers the way from L2 and not from memory:
     // the rows' scales of the next tile, contiguous, are brought to L2 a tile ahead.
-    const uint32_t tile_bytes = (uint32_t)(kTileRows * 2) * p.ngroups;
+    const uint32_t tile_bytes = (uint32_t)(p.rows * 2) * p.ngroups;  // a multiple of 16 where W > 0 (the host sees to it)
     int64_t ahead = (int64_t)blockIdx.x + gridDim.x;
     auto prefetch = [&]() {
-      if (W && turn == 0 && row0 == 0 && lane < 2 && (ahead + 1) * kTileRows <= a.V)
+      if (W && turn == 0 && row0 == 0 && lane < 2 && (ahead + 1) * p.rows <= a.V)
         l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + ahead * tile_bytes, tile_bytes);
       ahead += gridDim.x;
     };
     auto wrap = [&]() {
       while (seg >= p.segs) {
-        seg -= p.segs, row += (int64_t)gridDim.x * kTileRows;
+        seg -= p.segs, row += (int64_t)gridDim.x * p.rows;
         enter_tile();
         prefetch();
       }
@@ -314,24 +370,24 @@ constexpr int sum_groups(int np) { return np > 32 ? np / 32 : 1; }
 constexpr int first_dequant_warp(int np) { return kSumWarp + 4 * sum_groups(np); }
 // Segments between a group's turns, and the least common multiple of that and the two scale turns: weight
 // stages are a multiple of it.
-constexpr int seg_step(int bits, int groups) { return groups / (bits == 4 ? 2 : 1); }
-constexpr int ring_multiple(int bits, int groups) { return seg_step(bits, groups) < 2 ? 2 : seg_step(bits, groups); }
+constexpr int seg_step(int groups) { return groups / kUnits; }
+constexpr int ring_multiple(int groups) { return seg_step(groups) < 2 ? 2 : seg_step(groups); }
 constexpr int tc_threads(int np, int groups) { return 32 * (first_dequant_warp(np) + 4 * groups); }
 
-template <int kBits, int NP, int kGroups, bool resident>
+template <int kBits, int NP, int kGroups, bool kStream>
 __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     logits_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
                      const __grid_constant__ TcArgs p) {
-  constexpr int kUnits = kBits == 4 ? 2 : 1;        // units per segment
+  constexpr int kBoxes = kBits / 4, kStageBytes = kBoxes * kBoxBytes;  // of q, per segment
   constexpr uint32_t kHUnit = NP * kUnitK * 2;      // bytes of a unit of h: two blocks of 64 columns
-  constexpr int kAccSegs = kAccK / (kUnits * kUnitK), kChunkSegs = kAccSegs * kMma;  // segments per (set of) accumulators
+  constexpr int kAccSegs = kAccK / kSegK, kChunkSegs = kAccSegs * kMma;  // segments per (set of) accumulators
   // Segments of A in tensor memory (256 columns of it), beside two sets of accumulators.  A parity wait is
   // sound only for a waiter that sees every phase of its barrier, so no slot of a ring changes hands: the
   // slots of A are a multiple of the segments that the groups work on at a time and of the issuing
   // warps, the weight stages of what takes turns on them (ring_stages), the slots of h of both.
   constexpr uint32_t kASlots = 4 / kUnits;
   constexpr uint32_t kTmemA = 512 - 256;  // first column of A; the sets start at 0
-  constexpr uint32_t kStep = seg_step(kBits, kGroups);
+  constexpr uint32_t kStep = seg_step(kGroups);
   constexpr int kSums = sum_groups(NP), kCols = NP / kSums, kFirstDequantWarp = first_dequant_warp(NP);
   static_assert(2 * kMma * NP <= kTmemA && kASlots <= kMaxABufs && kASlots % kStep == 0 && kASlots % kMma == 0, "tensor memory");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -339,7 +395,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
   const LogitsArgs& a = p.a;
   uint8_t* const ring = smem;
   uint8_t* const hbuf = ring + p.stages * kStageBytes;
-  uint8_t* const sring = hbuf + (resident ? p.units : p.hslots) * kHUnit;  // scale words, by ring stage
+  uint8_t* const sring = hbuf + (kStream ? p.hslots : p.units) * kHUnit;  // scale words, by ring stage
   TcCtl* const ctl = reinterpret_cast<TcCtl*>(sring + p.stages * kScaleBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = blockIdx.y * NP;
@@ -349,7 +405,8 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     for (int i = 0; i < kMaxABufs; ++i) mbar_init(&ctl->a_full[i], 4 * kUnits), mbar_init(&ctl->a_empty[i], 1);
     for (int i = 0; i < 2 * kMma; ++i) mbar_init(&ctl->d_full[i], 1), mbar_init(&ctl->d_empty[i], 4 * kSums);
     for (int i = 0; i < kMaxH; ++i)
-      mbar_init(&ctl->h_raw[i], 1), mbar_init(&ctl->h_full[i], resident ? 4 * kSums : 4), mbar_init(&ctl->h_empty[i], 1);
+      mbar_init(&ctl->h_full[i], 1), mbar_init(&ctl->h_empty[i], 2);  // a commit of each CTA of the pair
+    mbar_init(&ctl->h_ready, 4 * kSums);
     for (int i = 0; i < kMma; ++i) mbar_init(&ctl->drain[i], 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -360,9 +417,12 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kStream) cluster_sync();  // the other CTA's barriers exist
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  const int my_tiles = (p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  // Tiles blockIdx.x, blockIdx.x + gridDim.x, ...; the CTAs of a pair take equally many, the odd one's last
+  // may lie past the vocabulary (zero weights, nothing written).
+  const int my_tiles = (p.tiles - (int)(kStream ? blockIdx.x & ~1u : blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
 
   if (warp == 0) {
     // ---- TMA: the whole warp walks the loop and one elected lane issues, as below
@@ -372,14 +432,16 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     bool ok = true;
     auto load_w = [&](int seg, int row0) {
       if (leader) {
-        mbar_arrive_expect_tx(&ctl->w_full[st], kStageBytes);
-        tma_load_2d(&map_w, smem_u32(&ctl->w_full[st]), ring + st * kStageBytes, seg * kSegBytes, row0);
+        mbar_arrive_expect_tx(&ctl->w_full[st], kBoxes * 128 * p.rows);
+#pragma unroll
+        for (int i = 0; i < kBoxes; ++i)
+          tma_load_2d(&map_w, smem_u32(&ctl->w_full[st]), ring + st * kStageBytes + i * kBoxBytes, (seg * kBoxes + i) * 128, row0);
       }
       ++it;
       if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
     };
-    int row0 = blockIdx.x * kTileRows;
-    for (int i = 0; ok && i < my_tiles; ++i, row0 += gridDim.x * kTileRows) {
+    int row0 = blockIdx.x * p.rows;
+    for (int i = 0; ok && i < my_tiles; ++i, row0 += gridDim.x * p.rows) {
       for (int seg = 0; seg < p.segs; ++seg) {
         ok = wait_warp(ctl, &ctl->w_empty[st], ph, a.status);
         if (!ok) break;
@@ -391,35 +453,38 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       for (uint32_t k = k0; k < it; ++k) drain_bar(&ctl->w_full[k % p.stages], (k / p.stages) & 1u);
     }
   } else if (warp == kHWarp) {
-    // ---- TMA of h
+    // ---- h
     const bool leader = elect_one();
-    uint32_t it = 0, hs = 0, hp = 1;  // units issued; streamed: slot, parity of its release
-    bool ok = true;
-    auto load_h = [&](uint64_t* bar, uint8_t* dst, int unit) {
-      tma_load_2d(&map_h, smem_u32(bar), dst, unit * kUnitK, m0);
-      tma_load_2d(&map_h, smem_u32(bar), dst + kHUnit / 2, unit * kUnitK + 64, m0);
-    };
-    if constexpr (resident) {
+    if constexpr (!kStream) {
       if (leader) {
-        mbar_arrive_expect_tx(&ctl->h_raw[0], p.units * kHUnit);
-        for (int u = 0; u < p.units; ++u) load_h(&ctl->h_raw[0], hbuf + u * kHUnit, u);
-        drain_bar(&ctl->h_raw[0], 0);  // the loads land before the CTA can exit, whatever the others do
+        mbar_arrive_expect_tx(&ctl->h_full[0], p.units * kHUnit);
+        for (int u = 0; u < p.units; ++u) {
+          tma_load_2d(&map_h, smem_u32(&ctl->h_full[0]), hbuf + u * kHUnit, u * kUnitK, m0);
+          tma_load_2d(&map_h, smem_u32(&ctl->h_full[0]), hbuf + u * kHUnit + kHUnit / 2, u * kUnitK + 64, m0);
+        }
+        drain_bar(&ctl->h_full[0], 0);  // the loads land before the CTA can exit, whatever the others do
       }
     } else {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel that writes the image is done
+      const uint32_t rank = cluster_ctarank();
+      const uint8_t* const image = p.image + (int64_t)blockIdx.y * p.units * kHUnit + rank * (kHUnit / 2);
+      uint32_t it = 0, hs = 0, hp = 1;  // units issued; slot, parity of its release
+      bool ok = true;
       for (int i = 0; ok && i < my_tiles; ++i) {
-        for (int u = 0; u < p.units; ++u, ++it) {
-          ok = wait_warp(ctl, &ctl->h_empty[hs], hp, a.status);
+        const uint8_t* src = image;
+        for (int u = 0; u < p.units; ++u, ++it, src += kHUnit) {
+          ok = wait_warp<true>(ctl, &ctl->h_empty[hs], hp, a.status);  // both CTAs are done with the slot
           if (!ok) break;
           if (leader) {
-            mbar_arrive_expect_tx(&ctl->h_raw[hs], kHUnit);
-            load_h(&ctl->h_raw[hs], hbuf + hs * kHUnit, u);
+            mbar_arrive_expect_tx(&ctl->h_full[hs], kHUnit);  // this half and the other CTA's
+            bulk_load_pair(src, kHUnit / 2, hbuf + hs * kHUnit + rank * (kHUnit / 2), &ctl->h_full[hs]);
           }
           if (++hs == (uint32_t)p.hslots) hs = 0, hp ^= 1u;
         }
       }
-      if (!ok && leader) {
+      if (!ok && leader) {  // loads in flight, as far as the other CTA's halves came too
         const uint32_t k0 = it > (uint32_t)p.hslots ? it - p.hslots : 0;
-        for (uint32_t k = k0; k < it; ++k) drain_bar(&ctl->h_raw[k % p.hslots], (k / p.hslots) & 1u);
+        for (uint32_t k = k0; k < it; ++k) drain_bar(&ctl->h_full[k % p.hslots], (k / p.hslots) & 1u);
       }
     }
   } else if (warp <= kMma) {
@@ -434,31 +499,31 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     uint32_t slot = me, ap = 0;       // segment's place in tensor memory, parity
     uint32_t db = 0, dp = 1;          // set of accumulators, parity of its release
     uint32_t hs = me * kUnits, hp = 0;  // streamed h: ring slot and parity
-    bool ok = !resident || wait_warp(ctl, &ctl->h_full[0], 0, a.status);
+    bool ok = kStream || wait_warp(ctl, &ctl->h_ready, 0, a.status);
     int first = me;                   // my first segment of the tile
     for (int i = 0; ok && i < my_tiles; ++i) {
       int j = 0, seg = first;         // segments in the accumulator, segment of the tile
       for (; seg < p.segs; seg += kMma) {
         if (j == 0) ok = wait_warp(ctl, &ctl->d_empty[2 * me + db], dp, a.status);
         ok = ok && wait_warp(ctl, &ctl->a_full[slot], ap, a.status);
-        if constexpr (!resident) {
+        if constexpr (kStream) {
 #pragma unroll
-          for (int k = 0; k < kUnits; ++k) ok = ok && wait_warp(ctl, &ctl->h_full[hs + k], hp, a.status);
+          for (int k = 0; k < kUnits; ++k) ok = ok && wait_warp<true>(ctl, &ctl->h_full[hs + k], hp, a.status);
         }
         if (!ok) break;
         tc_fence_after();
         const bool last = j == kAccSegs - 1 || seg + kMma >= p.segs;
         if (leader) {
-          const uint64_t desc = desc0 + (uint64_t)((resident ? (uint32_t)seg * kUnits : hs) * (kHUnit >> 4));
+          const uint64_t desc = desc0 + (uint64_t)((kStream ? hs : (uint32_t)seg * kUnits) * (kHUnit >> 4));
           const uint32_t at = tm + kTmemA + slot * (64 * kUnits), dt = tm + (2 * me + db) * NP;
 #pragma unroll
           for (int kk = 0; kk < kUnits * kUnitK / 16; ++kk)
             umma_bf16_ta(dt, at + kk * 8, desc + ((kk >> 2) * (kHUnit / 2) + (kk & 3) * 32) / 16, idesc,
                          (kk | j) != 0 ? 1u : 0u);
           umma_commit(&ctl->a_empty[slot]);
-          if constexpr (!resident) {
+          if constexpr (kStream) {
 #pragma unroll
-            for (int k = 0; k < kUnits; ++k) umma_commit(&ctl->h_empty[hs + k]);
+            for (int k = 0; k < kUnits; ++k) umma_commit_pair(&ctl->h_empty[hs + k]);
           }
           if (last) umma_commit(&ctl->d_full[2 * me + db]);
         }
@@ -471,7 +536,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
         }
         slot += kMma;
         if (slot >= kASlots) slot -= kASlots, ap ^= 1u;
-        if constexpr (!resident) {
+        if constexpr (kStream) {
           hs += kMma * kUnits;
           if (hs >= (uint32_t)p.hslots) hs -= p.hslots, hp ^= 1u;
         }
@@ -484,7 +549,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     }
   } else if (warp < kSumWarp) {
     // ---- scales and biases
-    const ScaleRole<kUnits * kUnitK> role{p, ctl, smem_u32(sring), my_tiles, (warp - kScaleWarp) & 1, (warp - kScaleWarp) / 2 * 64, lane};
+    const ScaleRole role{p, ctl, smem_u32(sring), my_tiles, (warp - kScaleWarp) & 1, (warp - kScaleWarp) / 2 * 64, lane};
     if (p.wide_scales && p.seg_words == 8)
       role.template run<8>();
     else if (p.wide_scales && p.seg_words == 4)
@@ -494,58 +559,29 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
     else
       role.template run<0>();
   } else if (warp < kFirstDequantWarp) {
-    // ---- h into the dequantised order, sums and output
-    const int q = warp & 3, n0 = (warp - kSumWarp) / 4 * kCols, tid = threadIdx.x - 32 * kSumWarp;
-    const int live = min(NP, a.M - m0);           // rows of h; the others are zero
-    // n blocks of [NP rows, 64 columns], in place, by 128 threads: 16 rows of 8 16-byte pieces at a time
-    const int t128 = tid & 127;
-    auto reorder_h = [&](uint8_t* base, int blk0, int step, int n) {
-      for (int blk = blk0; blk < n; blk += step) {
-        const uint32_t b = smem_u32(base) + blk * (NP * 128) + t128 * 16;
+    // ---- sums and output
+    const int q = warp & 3, n0 = (warp - kSumWarp) / 4 * kCols;
+    bool ok = true;
+    if constexpr (!kStream) {
+      // resident h into the dequantised order, in place: 128 threads per sum group, a 16-byte piece of 16 rows each
+      const int tid = threadIdx.x - 32 * kSumWarp, live = min(NP, a.M - m0);  // the other rows are zero
+      ok = wait_warp(ctl, &ctl->h_full[0], 0, a.status);
+      for (int blk = tid >> 7; ok && blk < p.units * 2; blk += kSums) {
+        const uint32_t b = smem_u32(hbuf) + blk * (NP * 128) + (tid & 127) * 16;
 #pragma unroll
         for (int r = 0; r < NP; r += 16) {
-          if (r >= live) break;
-          const uint4 x = lds128(b + r * 128);
-          if constexpr (kBits == 4)
-            st_shared_v4(b + r * 128, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                         __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-          else
-            st_shared_v4(b + r * 128, __byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
-                         __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
+          if (r + ((tid & 127) >> 3) >= live) break;
+          const uint4 x = reorder_pairs<kBits>(lds128(b + r * 128));
+          st_shared_v4(b + r * 128, x.x, x.y, x.z, x.w);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-    };
-    bool ok = true;
-    if (resident) {
-      ok = wait_warp(ctl, &ctl->h_raw[0], 0, a.status);
-      if (ok) {
-        reorder_h(hbuf, tid >> 7, kSums, p.units * 2);
-        if (lane == 0) mbar_arrive(&ctl->h_full[0]);
-      }
+      if (ok && lane == 0) mbar_arrive(&ctl->h_ready);
     }
     float acc[kCols];  // columns n0 on
-    uint32_t hs = 0, hp = 0;  // streamed h: slot and parity
+    const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
     const int chunks = (p.segs + kChunkSegs - 1) / kChunkSegs;
-    const int64_t total = (int64_t)my_tiles * chunks;
-    // streamed h runs one set of accumulators ahead of the one that is read
-    int64_t fed = 0;
-    int fchunk = 0;
-    auto feed = [&]() {
-      const int n = min(kChunkSegs, p.segs - fchunk * kChunkSegs) * kUnits;
-      for (int j = 0; ok && j < n; ++j) {
-        if (kSums == 1 || (hs & 1) == (uint32_t)(tid >> 7)) {  // four warps to a unit (slots are even)
-          ok = wait_warp(ctl, &ctl->h_raw[hs], hp, a.status);
-          if (!ok) break;
-          reorder_h(hbuf + hs * kHUnit, 0, 1, 2);
-          if (lane == 0) mbar_arrive(&ctl->h_full[hs]);
-        }
-        if (++hs == (uint32_t)p.hslots) hs = 0, hp ^= 1u;
-      }
-      ++fed;
-      if (++fchunk == chunks) fchunk = 0;
-    };
     uint32_t db[kMma] = {}, dp[kMma] = {};  // per MMA warp: set and parity
     int first[kMma];                        // and its first segment of the tile
 #pragma unroll
@@ -554,8 +590,6 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
 #pragma unroll
       for (int n = 0; n < kCols; ++n) acc[n] = 0.f;
       for (int c = 0; ok && c < chunks; ++c) {
-        if (!resident)
-          while (ok && fed < total && fed <= (int64_t)i * chunks + c + 1) feed();
 #pragma unroll
         for (int w = 0; w < kMma; ++w) {
           if (!ok || first[w] + c * kChunkSegs >= p.segs) continue;  // no segment of this warp's here
@@ -577,11 +611,26 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
         }
       }
       if (!ok) break;
-      const int64_t v = (int64_t)(blockIdx.x + i * gridDim.x) * kTileRows + 32 * q + lane;
-      if (v < a.V) {
+      const int row = 32 * q + lane;
+      const int64_t v = (int64_t)(blockIdx.x + i * gridDim.x) * p.rows + row;
+      if (row < p.rows && v < a.V) {
+        const int64_t at = (int64_t)(m0 + n0) * a.ld_out + v;
+        float* f32 = static_cast<float*>(a.out) + at;
+        uint16_t* b16 = static_cast<uint16_t*>(a.out) + at;
+        const int n_live = a.M - m0 - n0;
 #pragma unroll
-        for (int n = 0; n < kCols; ++n)
-          if (m0 + n0 + n < a.M) store_logit(a, m0 + n0 + n, (int)v, acc[n]);
+        for (int n = 0; n < kCols; ++n) {
+          if (n >= n_live) break;
+          float x = acc[n];
+          if (a.softcap > 0.f) x = softcap_of(x, a.softcap, inv_cap);
+          if (a.out_bf16) {
+            *b16 = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
+            b16 += a.ld_out;
+          } else {
+            *f32 = x;
+            f32 += a.ld_out;
+          }
+        }
       }
 #pragma unroll
       for (int w = 0; w < kMma; ++w) {  // the warp's segments go on alternating in the next tile
@@ -592,10 +641,10 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
   } else {
     // ---- dequantisation
     const int wg = (warp - kFirstDequantWarp) >> 2, q = warp & 3, row = 32 * q + lane;
-    // unit u: half u % kUnits of segment u / kUnits; the group goes on by kGroups units at a time
-    static_assert(kGroups % kUnits == 0, "a group keeps to one half of the segments");
+    // the group keeps to one half of every kStep-th segment
+    static_assert(kGroups % kUnits == 0, "a group keeps to one half");
     const uint32_t half = wg % kUnits, swz = (uint32_t)(row & 7) << 4;
-    const uint32_t wrow = smem_u32(ring) + row * kSegBytes;
+    const uint32_t wrow = smem_u32(ring) + row * 128 + (kBits == 8 ? half * kBoxBytes : 0);  // 8-bit: the half's box
     const uint32_t srow = smem_u32(sring) + row * 4;
     uint32_t soff[4];  // the unit's four scale words
 #pragma unroll
@@ -615,54 +664,59 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       uint4 w[kVec];
       uint32_t sw[4];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) w[i] = lds128(wst + (((half * 4 + i) << 4) ^ swz));
+      for (int i = 0; i < kVec; ++i) w[i] = lds128(wst + (((kBits == 4 ? half * 4 + i : i) << 4) ^ swz));
 #pragma unroll
       for (int i = 0; i < 4; ++i) sw[i] = lds32(sst + soff[i]);
       const bool plain = (lds32(smem_u32(ctl->plain[stage])) >> (8 * q) & 1u) != 0;
       const uint32_t dst = trow + (slot * kUnits + half) * 64;
+      // pieces of 32 columns per store: two, or one where 1024 threads leave 64 registers each
+      constexpr int kPieces = tc_threads(NP, kGroups) == 1024 ? 1 : 2;
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {  // 64 columns: 32 words of tensor memory
-        uint32_t r[32];
-        if (!plain) {
+      for (int part = 0; part < 4 / kPieces; ++part) {
+        uint32_t r[16 * kPieces];
+        // 32 columns, 16 words of tensor memory, per piece
+        if (__builtin_expect(!plain, 1)) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t s133 = __byte_perm(sw[part * 2 + i], 0, 0x1010), b2 = __byte_perm(sw[part * 2 + i], 0, 0x3232);
+          for (int j = 0; j < kPieces; ++j) {
+            const int i = part * kPieces + j;
+            const uint32_t s2 = __byte_perm(sw[i], 0, 0x1010), b2 = __byte_perm(sw[i], 0, 0x3232);
             if constexpr (kBits == 4) {
-              const uint32_t s129 = bf16x2_fma(s133, 0x3D803D80u, 0x80008000u);  // times 2^-4, plus -0
-              unpack(w[part * 2 + i], [&](int e, uint32_t v) {
+              const uint32_t s129 = bf16x2_fma(s2, 0x3D803D80u, 0x80008000u);  // times 2^-4, plus -0
+              unpack(w[i], [&](int e, uint32_t v) {
                 uint32_t x[4];
-                dequant4_scaled(v, s133, s129, b2, x);
+                dequant4_scaled(v, s2, s129, b2, x);
 #pragma unroll
-                for (int f = 0; f < 4; ++f) r[16 * i + 4 * e + f] = x[f];
+                for (int f = 0; f < 4; ++f) r[16 * j + 4 * e + f] = x[f];
               });
             } else {
 #pragma unroll
               for (int o = 0; o < 2; ++o)
-                unpack(w[(part * 2 + i) * 2 + o], [&](int e, uint32_t v) {
+                unpack(w[2 * i + o], [&](int e, uint32_t v) {
                   uint32_t x[2];
-                  dequant8_scaled(v, s133, b2, x);
-                  r[16 * i + 8 * o + 2 * e] = x[0], r[16 * i + 8 * o + 2 * e + 1] = x[1];
+                  dequant8_scaled(v, s2, b2, x);
+                  r[16 * j + 8 * o + 2 * e] = x[0], r[16 * j + 8 * o + 2 * e + 1] = x[1];
                 });
             }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t s2 = __byte_perm(sw[part * 2 + i], 0, 0x1010), b2 = __byte_perm(sw[part * 2 + i], 0, 0x3232);
+          for (int j = 0; j < kPieces; ++j) {
+            const int i = part * kPieces + j;
+            const uint32_t s2 = __byte_perm(sw[i], 0, 0x1010), b2 = __byte_perm(sw[i], 0, 0x3232);
             if constexpr (kBits == 4) {
-              unpack(w[part * 2 + i], [&](int e, uint32_t v) {
+              unpack(w[i], [&](int e, uint32_t v) {
                 uint32_t x[4];
                 dequant4(v, s2, b2, x);
 #pragma unroll
-                for (int f = 0; f < 4; ++f) r[16 * i + 4 * e + f] = x[f];
+                for (int f = 0; f < 4; ++f) r[16 * j + 4 * e + f] = x[f];
               });
             } else {
 #pragma unroll
               for (int o = 0; o < 2; ++o)
-                unpack(w[(part * 2 + i) * 2 + o], [&](int e, uint32_t v) {
+                unpack(w[2 * i + o], [&](int e, uint32_t v) {
                   uint32_t x[2];
                   dequant8(v, s2, b2, x);
-                  r[16 * i + 8 * o + 2 * e] = x[0], r[16 * i + 8 * o + 2 * e + 1] = x[1];
+                  r[16 * j + 8 * o + 2 * e] = x[0], r[16 * j + 8 * o + 2 * e + 1] = x[1];
                 });
             }
           }
@@ -672,7 +726,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
           if (!ok) break;
           tc_fence_after();
         }
-        tmem_st32(dst + part * 32, r);
+        tmem_st(dst + part * (16 * kPieces), r);
       }
       if (!ok) break;
       tmem_st_wait();
@@ -691,24 +745,54 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  // pair: the other CTA's loads write here and its commits arrive here, so neither leaves before both are done
+  if constexpr (kStream) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, 512);
   }
 }
 
-template <int kBits, int NP, int kGroups>
-cudaError_t launch_np(const LogitsArgs& a, int sms, cudaStream_t st) {
-  constexpr int kUnits = kBits == 4 ? 2 : 1;
+// h for the streamed form: per m tile of `rows` rows and block of 64 columns the block as shared memory holds it
+// (128-byte swizzled rows), 16-byte pieces in the dequantised order, zero where h has no element.
+template <int kBits>
+__global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, int blocks, int64_t pieces, uint4* image) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= pieces) return;
+  const int row = (int)(i / 8 % rows);
+  const int64_t blk = i / 8 / rows % blocks, m = i / 8 / rows / blocks * rows + row;
+  const int64_t k = blk * 64 + (int)((i ^ row) & 7) * 8;
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  if (m < a.M && k < a.d) x = reorder_pairs<kBits>(__ldg(reinterpret_cast<const uint4*>(a.h + m * a.ld_h + k)));
+  image[i] = x;
+}
+
+constexpr int kMinStages = 4;
+constexpr int stage_bytes(int bits) { return bits / 4 * kBoxBytes + kScaleBytes; }
+int64_t units_of(int64_t d) { return cdiv(d, kSegK) * kUnits; }
+// up to 16 rows, beside at least kMinStages of weights
+bool resident(int bits, int64_t M, int64_t d) {
+  return M <= 16 && units_of(d) * (16 * kUnitK * 2) <= kSmemLimit - kCtlBytes - kMinStages * stage_bytes(bits);
+}
+int rows_per_pass(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
+template <int kBits, int NP, int kGroups, bool kStream>
+cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_t st) {
   constexpr int kHUnit = NP * kUnitK * 2;
   TcArgs p;
   p.a = a;
   const int64_t row_bytes = (int64_t)a.d * kBits / 8;
-  p.tiles = (int)cdiv(a.V, kTileRows);
-  p.segs = (int)cdiv(row_bytes, kSegBytes);
+  // Tiles of as many rows as deal the vocabulary out evenly in the fewest rounds of 128 rows: with 128 in every
+  // one, V = 32000 on 152 SMs takes two rounds of which the second is 64% full.  A multiple of 8, so that a
+  // tile's scales start on 16 bytes.
+  const int slots = kStream ? std::max(1, sms / 2) * 2 : sms;
+  const int64_t rounds = cdiv(a.V, (int64_t)kTileRows * slots);
+  p.rows = (int)std::min<int64_t>(kTileRows, cdiv(cdiv(a.V, rounds * slots), 8) * 8);
+  p.tiles = (int)cdiv(a.V, p.rows);
+  p.segs = (int)cdiv(a.d, kSegK);
   p.units = p.segs * kUnits;
   p.ngroups = a.d / a.group;
-  constexpr int kSegK = kUnits * kUnitK;
   // A scale word per group where groups of a power of two columns fit a segment; else one per 32 columns
   // (or per segment, for groups of whole segments), the group's repeated.
   const int per = a.group / 32;
@@ -721,39 +805,65 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, cudaStream_t st) {
   const uint32_t repeat = (uint32_t)(per >> p.shift);  // words per group
   p.gmul = repeat > 1 ? (uint32_t)(((1ull << 32) + repeat - 1) / repeat) : 0u;
   p.wide_scales = repeat == 1 && p.ngroups % p.seg_words == 0 && aligned16(a.scales) && aligned16(a.biases);
-  // h resident where at least four weight stages fit beside it, else streamed through up to 8 units
-  const int fixed = kCtlBytes, stage = kStageBytes + kScaleBytes;
-  const int64_t all_h = (int64_t)p.units * kHUnit;
-  constexpr int kMul = ring_multiple(kBits, kGroups);
-  static_assert(kMul <= 4 && kMaxStages % kMul == 0, "weight ring");
-  auto ring_stages = [&](int64_t left) { return (int)std::min<int64_t>(kMaxStages, left / stage) / kMul * kMul; };
-  if (all_h <= kSmemLimit - fixed - 4 * stage) {
-    p.hslots = 0;
-    p.stages = ring_stages(kSmemLimit - fixed - all_h);
-  } else {
-    // four stages at least, then as many slots as fit (a multiple of both issuing warps' segments)
-    p.hslots = std::min(kMaxH, (kSmemLimit - fixed - 4 * stage) / kHUnit) / (kMma * kUnits) * (kMma * kUnits);
-    p.stages = ring_stages(kSmemLimit - fixed - p.hslots * kHUnit);
-  }
-  const int smem = p.stages * stage + (p.hslots ? p.hslots * kHUnit : (int)all_h) + fixed + 1024;
+  constexpr int kMul = ring_multiple(kGroups);
+  static_assert(kMaxStages % kMul == 0 && kMinStages % kMul == 0, "weight ring");
+  const int fixed = kCtlBytes, stage = stage_bytes(kBits);
+  // streamed: kMinStages of weights, then as many slots as fit (a multiple of both issuing warps' segments)
+  p.hslots = kStream ? std::min(kMaxH, (kSmemLimit - fixed - kMinStages * stage) / kHUnit) / (kMma * kUnits) * (kMma * kUnits) : 0;
+  const int h_bytes = (kStream ? p.hslots : p.units) * kHUnit;
+  p.stages = std::min(kMaxStages, (kSmemLimit - fixed - h_bytes) / stage) / kMul * kMul;
+  p.image = static_cast<const uint8_t*>(workspace);
+  const int smem = p.stages * stage + h_bytes + fixed + 1024;
   CUtensorMap mw, mh;
-  if (!encode_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq, row_bytes, a.V, row_bytes, kSegBytes, kTileRows) ||
-      !encode_map_2d(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.h, a.d, a.M, a.ld_h * 2, 64, NP))
-    return cudaErrorNotSupported;
-  const dim3 grid((unsigned)std::min(p.tiles, sms), (unsigned)cdiv(a.M, NP));
-  static std::atomic<int> done[2][64];
-  auto kernel = p.hslots ? logits_tc_kernel<kBits, NP, kGroups, false> : logits_tc_kernel<kBits, NP, kGroups, true>;
-  if (cudaError_t e = opt_in_smem(kernel, kSmemLimit + 1024, done[p.hslots != 0])) return e;
-  kernel<<<grid, tc_threads(NP, kGroups), smem, st>>>(mw, mh, p);
-  return cudaGetLastError();
+  if (!encode_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq, row_bytes, a.V, row_bytes, 128, p.rows)) return cudaErrorNotSupported;
+  mh = mw;
+  if (!kStream && !encode_map_2d(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.h, a.d, a.M, a.ld_h * 2, 64, NP)) return cudaErrorNotSupported;
+  static std::atomic<int> done[64];
+  auto kernel = logits_tc_kernel<kBits, NP, kGroups, kStream>;
+  if (cudaError_t e = opt_in_smem(kernel, kSmemLimit + 1024, done)) return e;
+  const int mt = (int)cdiv(a.M, NP);
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3((unsigned)tc_threads(NP, kGroups));
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if constexpr (kStream) {
+    const int blocks = p.units * 2;
+    const int64_t pieces = (int64_t)mt * blocks * NP * 8;
+    h_image_kernel<kBits><<<(unsigned)cdiv(pieces, 256), 256, 0, st>>>(a, NP, blocks, pieces, static_cast<uint4*>(workspace));
+    if (cudaError_t e = cudaGetLastError()) return e;
+    cfg.gridDim = dim3((unsigned)std::min((p.tiles + 1) / 2 * 2, slots), (unsigned)mt);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its weights may come before the image is there
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+  } else {
+    cfg.gridDim = dim3((unsigned)std::min(p.tiles, slots), (unsigned)mt);
+    cfg.numAttrs = 0;
+  }
+  return cudaLaunchKernelEx(&cfg, kernel, mw, mh, p);
+}
+
+template <int kBits>
+cudaError_t launch_bits(const LogitsArgs& a, int sms, void* workspace, cudaStream_t st) {
+  if (resident(kBits, a.M, a.d)) return launch_np<kBits, 16, 4, false>(a, sms, workspace, st);
+  if (a.M <= 16) return launch_np<kBits, 16, 4, true>(a, sms, workspace, st);
+  if (a.M <= 32) return launch_np<kBits, 32, 4, true>(a, sms, workspace, st);
+  return launch_np<kBits, 64, 4, true>(a, sms, workspace, st);
 }
 
 }  // namespace
 
-cudaError_t launch_logits_tc(const LogitsArgs& a, int bits, int sms, cudaStream_t st) {
-  if (a.M <= 16) return bits == 4 ? launch_np<4, 16, 4>(a, sms, st) : launch_np<8, 16, 4>(a, sms, st);
-  if (a.M <= 32) return bits == 4 ? launch_np<4, 32, 4>(a, sms, st) : launch_np<8, 32, 4>(a, sms, st);
-  return bits == 4 ? launch_np<4, 64, 2>(a, sms, st) : launch_np<8, 64, 2>(a, sms, st);
+size_t logits_tc_workspace(int bits, int64_t M, int64_t d) {
+  if (resident(bits, M, d)) return 0;
+  const int rows = rows_per_pass(M);
+  return (size_t)(cdiv(M, rows) * rows * units_of(d) * kUnitK * 2);
+}
+
+cudaError_t launch_logits_tc(const LogitsArgs& a, int bits, int sms, void* workspace, cudaStream_t st) {
+  return bits == 4 ? launch_bits<4>(a, sms, workspace, st) : launch_bits<8>(a, sms, workspace, st);
 }
 
 }  // namespace orpo

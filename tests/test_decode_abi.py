@@ -23,8 +23,9 @@ def lib():
 
 def test_logits_host_checks(lib):
     def call(h=FAKE, ld_h=64, wq=FAKE, sc=FAKE, bi=FAKE, bits=4, group=32, M=2, V=128, d=64, cap=0.0, out=FAKE,
-             ld=128, bf16=0, st=FAKE):
-        return lib.orpo_head_logits_q(h, ld_h, wq, sc, bi, bits, group, M, V, d, cap, out, ld, bf16, st, None)
+             ld=128, bf16=0, ws=None, ws_bytes=0, st=FAKE):
+        return lib.orpo_head_logits_q(h, ld_h, wq, sc, bi, bits, group, M, V, d, cap, out, ld, bf16, ws, ws_bytes, st,
+                                      None)
 
     assert call(M=0) == OK
     for bad in (dict(M=-1), dict(M=MAX_ROWS + 1), dict(V=0), dict(V=MAX_ROWS + 1), dict(d=0), dict(d=1 << 20),
@@ -37,6 +38,21 @@ def test_logits_host_checks(lib):
     for bad in (dict(ld_h=68), dict(h=P(0x10008)), dict(wq=P(0x10002)), dict(bits=8, wq=P(0x10004)),
                 dict(out=P(0x10002)), dict(out=P(0x10001), bf16=1), dict(sc=P(0x10001))):
         assert call(**bad) == ERR_ALIGN, bad
+    # more than 16 rows need a workspace
+    need = lib.orpo_head_logits_q_workspace_bytes(17, 64, 4)
+    assert need >= 17 * 64 * 2
+    assert call(M=17) == ERR_NULL
+    assert call(M=17, ws=P(0x10008), ws_bytes=need) == ERR_ALIGN
+    assert call(M=17, ws=FAKE, ws_bytes=need - 1) == ERR_WS
+
+
+def test_logits_workspace(lib):
+    q = lib.orpo_head_logits_q_workspace_bytes
+    assert q(1, 2560, 4) == q(16, 4608, 4) == q(16, 2560, 8) == 0
+    for M, d, bits in ((17, 256, 4), (64, 4096, 4), (16, 16384, 4), (1, 4096, 8), (1000, 4096, 4)):
+        rows = 16 if M <= 16 else 32 if M <= 32 else -(-M // 64) * 64
+        assert q(M, d, bits) == rows * -(-d // 256) * 256 * 2
+    assert q(0, 256, 4) == q(4, 256, 5) == q(4, 4, 4) == 0
 
 
 def test_select_host_checks(lib):
