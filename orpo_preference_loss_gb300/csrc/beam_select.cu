@@ -493,7 +493,7 @@ struct RowPlan {
 RowPlan row_plan(int64_t V, bool bf16, bool aligned) {
   RowPlan p;
   const int64_t grid = V + (aligned ? 0 : 7);  // up to 7 elements of a row's grid lie before it
-    p.chunks = (int)cdiv(grid, chunk_of(bf16));
+  p.chunks = (int)cdiv(grid, chunk_of(bf16));
   p.parts = std::min(p.chunks, kMaxParts);
   p.len = (int)(cdiv(grid, (int64_t)p.chunks * 256) * 256);
   return p;
