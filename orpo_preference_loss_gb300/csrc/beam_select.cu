@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
         value[k * a.n + i] = y == y ? y : -INFINITY;
         token[k * a.n + i] = (int)~(uint32_t)best;
       }
-      if (best == k0) k0 = ++h0 < a.n ? mine[lane * a.n + h0] : 0;
-      if (best == k1) k1 = ++h1 < a.n ? mine[(lane + 32) * a.n + h1] : 0;
+      if (best == k0 && k0 != 0) k0 = ++h0 < a.n ? mine[lane * a.n + h0] : 0;
+      if (best == k1 && k1 != 0) k1 = ++h1 < a.n ? mine[(lane + 32) * a.n + h1] : 0;
     }
   }
   __syncthreads();
