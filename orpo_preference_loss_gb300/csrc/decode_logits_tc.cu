@@ -10,21 +10,25 @@
 // into bf16: 9 instructions per 8 weights where the scales allow it (dequant4_scaled), 15 where not.
 //
 // Roles (warps):
-//   0       TMA of q: segments of 256 columns of the tile's 128 rows (one 16 KiB box of 128-byte swizzled
-//           rows, 8-bit: two) into a ring
-//   1, 2    MMA issue: the even and the odd segments, each into accumulators of its own
-//   3       h (below)
-//   4..7    scales and biases, every second segment and half of the rows each: (scale, bias) words beside
-//           the segment of q in the ring; scales multiplied by 2^133 where those of 32 rows are all small
-//           enough, which a flag of the stage says
+//   0       TMA of q: segments (128 bytes of each of the tile's rows: 256 columns, 8-bit 128; one swizzled
+//           16 KiB box) into a ring
+//   1       MMA issue
+//   2       streamed h (below)
+//   4..7    scales and biases, 32 rows each: (scale, bias) words beside the segment of q in the ring; scales
+//           multiplied by 2^133 where those of 32 rows are all small enough, which a flag of the stage says
 //   8..     sums and output of the accumulators, a thread per vocabulary row and up to 32 columns
-//   then    dequantisation, 4 warps per group, a thread per vocabulary row; group i takes units of 128
-//           columns i, i + kGroups, ...
+//   then    dequantisation: three groups of 4 warps in turns, a thread per vocabulary row of a segment
+//
+// Why turns and whole segments: a warp's fixed costs per segment (waits that find nothing to wait for take 90
+// clocks each, first loads 150, releases) are hidden only by warps that are at another point of their segment.
+// Four groups with a quarter of every segment each went in step and took 91 us where this takes 70 (one row,
+// d 2560, V 262144), pairs of groups with half segments 75.  Tensor memory holds A of three segments (8-bit: six)
+// beside two sets of accumulators.
 //
 // Order of k: 4-bit dequantisation yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights
 // (8-bit: (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes at a
-// time.  Up to 16 rows of h that fit beside the weights (d up to 4608, 8-bit 2560) are loaded and put in
-// that order by each CTA, once.  More are streamed: a small kernel first writes h in that order, and as
+// time.  Up to 16 rows of h that fit beside the weights (d up to 5120) are loaded and put in that order by
+// each CTA, once.  More are streamed: a small kernel first writes h in that order, and as
 // shared memory holds it, to the workspace, and the CTAs work in pairs (clusters) on neighbouring tiles,
 // each fetching half of every unit of h for both (multicast), since h crosses from L2 once per tile: at 64
 // rows that is twice the weights' bytes.
@@ -44,28 +48,30 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kBoxBytes = kTileRows * 128;            // a TMA box: 128 bytes of every row, up to 16 KiB
-constexpr int kUnitK = 128;                           // columns per A buffer (64 tensor-memory columns)
+constexpr int kUnitK = 128;                           // columns per unit of h
 constexpr int kAccK = 512;                            // columns per accumulator
-constexpr int kUnits = 2, kSegK = kUnits * kUnitK;    // units and columns per segment
-constexpr int kScaleBytes = kSegK / 32 * kTileRows * 4;  // (scale, bias) words of a segment, at most one per 32 columns
-constexpr int kMaxStages = 8;
+constexpr int seg_k(int bits) { return 1024 / bits; } // columns per segment: a box of q
+constexpr int scale_bytes(int bits) { return seg_k(bits) / 32 * kTileRows * 4; }  // (scale, bias) words of a segment, at most one per 32 columns
+constexpr int kMaxStages = 9;
 constexpr int kMaxH = 8;  // streamed h: units in the ring
-constexpr int kMaxABufs = 4;
-constexpr int kMma = 2;  // warps that issue
-constexpr int kHWarp = 3, kScaleWarp = 4, kSumWarp = 8;
+constexpr int kGroups = 3;                            // dequantising groups
+constexpr int kTmemA = 128, kTmemACols = 384;         // A in tensor memory, beside two sets of accumulators
+constexpr int a_slots(int bits) { return kTmemACols / (seg_k(bits) / 2); }
+constexpr int kMaxASlots = a_slots(8);
+constexpr int kHWarp = 2, kScaleWarp = 4, kSumWarp = 8;
 constexpr uint64_t kLimitNs = 4000000000ull;          // far above any legitimate wait
 constexpr int kSmemLimit = 232448 - 1024;             // less the slack that aligns the base
 
 struct TcCtl {
   uint64_t w_full[kMaxStages], w_empty[kMaxStages];
-  uint64_t a_full[kMaxABufs], a_empty[kMaxABufs];
-  uint64_t d_full[2 * kMma], d_empty[2 * kMma];  // [MMA warp][set]
-  uint64_t h_full[kMaxH], h_empty[kMaxH];  // streamed h; h_full[0]: resident h is loaded
-  uint64_t h_ready;                        // resident h is in order
-  uint64_t drain[kMma];
+  uint64_t a_full[kMaxASlots], a_empty[kMaxASlots];
+  uint64_t d_full[2], d_empty[2];          // [set]
+  uint64_t h_full[kMaxH], h_empty[kMaxH];  // streamed h
+  uint64_t h_ready;                        // resident h is there
+  uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
-  uint16_t plain[kMaxStages][2];  // per stage a byte for each 32 rows: 1 if their scales are as they are, not times 2^133
+  uint8_t plain[kMaxStages][4];  // per stage a byte for each 32 rows: 1 if their scales are as they are, not times 2^133
 };
 constexpr int kCtlBytes = 1024;
 static_assert(sizeof(TcCtl) <= kCtlBytes, "control block");
@@ -182,14 +188,7 @@ __device__ __forceinline__ bool elect_one() {
       "r"(r[o + 8]), "r"(r[o + 9]), "r"(r[o + 10]), "r"(r[o + 11]), "r"(r[o + 12]), "r"(r[o + 13]), "r"(r[o + 14]),  \
       "r"(r[o + 15])
 
-// 16 or 32 columns of this thread's lane (warp's quadrant)
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      ORPO_IN16(r, 0)
-      : "memory");
-}
+// 32 columns of this thread's lane (warp's quadrant)
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -249,167 +248,185 @@ __device__ __forceinline__ uint32_t group_of(const TcArgs& p, uint32_t word) {
   return p.gmul ? __umulhi(word, p.gmul) : word;
 }
 
-// One of the four warps that bring scales and biases beside the segments of q: segments turn, turn + 2, ...,
-// rows row0 + lane and + 32 of the tile.  (Two warps with four rows a lane took 3 to 10% longer.)
+// One of the four warps that bring scales and biases beside the segments of q: rows row0 + lane of the tile.
+template <int kSegK>
 struct ScaleRole {
   const TcArgs& p;
   TcCtl* ctl;
   uint32_t sring;
-  int my_tiles, turn, row0, lane;
+  int my_tiles, row0, lane;
 
   // W: words per segment, their groups' scales and biases aligned vectors; 0: any number, element by element
   template <int W>
   __device__ __forceinline__ void run() const {
-    constexpr int kPairs = W ? W / 2 : kSegK / 64;
+    constexpr int kWords = W ? W : kSegK / 32, kPairs = (kWords + 1) / 2;
     const LogitsArgs& a = p.a;
-    uint32_t sc[2][kPairs], bi[2][kPairs];  // per row the groups of the segment, in pairs
-    // the next fetch: its segment, its tile's first row, and where the first of my rows' scales and biases are
-    int seg = turn;
-    int64_t row = (int64_t)blockIdx.x * p.rows + row0 + lane;
+    struct Set {
+      uint32_t sc[kPairs], bi[kPairs];  // the groups of the segment, in pairs
+    };
+    // the next fetch: its segment, its tile's row that is mine, and where the row's scales and biases are
+    int seg = 0;
+    int64_t row = (int64_t)blockIdx.x * p.rows + row0 + lane, ahead = (int64_t)blockIdx.x + gridDim.x;
     const uint16_t *s, *b;
-    int rows = 0;  // of my two, those inside the vocabulary
+    // Scales are fetched two segments ahead, which covers the way from L2 and not from memory: the rows' scales of
+    // the next tile, contiguous, are brought to L2 a tile ahead.
+    const uint32_t tile_bytes = (uint32_t)(p.rows * 2) * p.ngroups;  // a multiple of 16 where W > 0 (the host sees to it)
     auto enter_tile = [&]() {
       s = a.scales + row * p.ngroups;
       b = a.biases + row * p.ngroups;
-      rows = row >= a.V ? 0 : row + 32 < a.V ? 2 : 1;
+      if (W && row0 == 0 && lane < 2 && (ahead + 1) * p.rows <= a.V)
+        l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + ahead * tile_bytes, tile_bytes);
+      ahead += gridDim.x;
     };
-    const int64_t pitch = (int64_t)32 * p.ngroups;
-    auto fetch = [&]() {
+    auto fetch = [&](Set& x) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) x.sc[i] = x.bi[i] = 0;
       const int g0 = W ? seg * W : (int)group_of(p, (uint32_t)(seg * p.seg_words));
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint16_t* sr = s + r * pitch + g0;
-        const uint16_t* br = b + r * pitch + g0;
-        if (r >= rows) {
-#pragma unroll
-          for (int i = 0; i < kPairs; ++i) sc[r][i] = bi[r][i] = 0;
-        } else if constexpr (W == 8) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(sr)), y = __ldg(reinterpret_cast<const uint4*>(br));
-          sc[r][0] = x.x, sc[r][1] = x.y, sc[r][2] = x.z, sc[r][3] = x.w;
-          bi[r][0] = y.x, bi[r][1] = y.y, bi[r][2] = y.z, bi[r][3] = y.w;
+      const uint16_t *sr = s + g0, *br = b + g0;
+      if (row < a.V) {
+        if constexpr (W == 8) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(sr)), v = __ldg(reinterpret_cast<const uint4*>(br));
+          x.sc[0] = u.x, x.sc[1] = u.y, x.sc[2] = u.z, x.sc[3] = u.w;
+          x.bi[0] = v.x, x.bi[1] = v.y, x.bi[2] = v.z, x.bi[3] = v.w;
         } else if constexpr (W == 4) {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(sr)), y = __ldg(reinterpret_cast<const uint2*>(br));
-          sc[r][0] = x.x, sc[r][1] = x.y, bi[r][0] = y.x, bi[r][1] = y.y;
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(sr)), v = __ldg(reinterpret_cast<const uint2*>(br));
+          x.sc[0] = u.x, x.sc[1] = u.y, x.bi[0] = v.x, x.bi[1] = v.y;
         } else if constexpr (W == 2) {
-          sc[r][0] = __ldg(reinterpret_cast<const uint32_t*>(sr)), bi[r][0] = __ldg(reinterpret_cast<const uint32_t*>(br));
+          x.sc[0] = __ldg(reinterpret_cast<const uint32_t*>(sr)), x.bi[0] = __ldg(reinterpret_cast<const uint32_t*>(br));
+        } else if constexpr (W == 1) {
+          x.sc[0] = __ldg(sr), x.bi[0] = __ldg(br);
         } else {
 #pragma unroll
-          for (int i = 0; i < kPairs; ++i) sc[r][i] = bi[r][i] = 0;
-#pragma unroll
-          for (int i = 0; i < 2 * kPairs; ++i) {
+          for (int i = 0; i < kWords; ++i) {
             const int gi = (int)group_of(p, (uint32_t)(seg * p.seg_words + i)) - g0;
             if (i < p.seg_words && g0 + gi < p.ngroups) {
-              sc[r][i / 2] |= (uint32_t)__ldg(sr + gi) << (16 * (i & 1));
-              bi[r][i / 2] |= (uint32_t)__ldg(br + gi) << (16 * (i & 1));
+              x.sc[i / 2] |= (uint32_t)__ldg(sr + gi) << (16 * (i & 1));
+              x.bi[i / 2] |= (uint32_t)__ldg(br + gi) << (16 * (i & 1));
             }
           }
         }
       }
-    };
-    // A segment's scales are fetched two segments ahead, which covers the way from L2 and not from memory:
-    // the rows' scales of the next tile, contiguous, are brought to L2 a tile ahead.
-    const uint32_t tile_bytes = (uint32_t)(p.rows * 2) * p.ngroups;  // a multiple of 16 where W > 0 (the host sees to it)
-    int64_t ahead = (int64_t)blockIdx.x + gridDim.x;
-    auto prefetch = [&]() {
-      if (W && turn == 0 && row0 == 0 && lane < 2 && (ahead + 1) * p.rows <= a.V)
-        l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + ahead * tile_bytes, tile_bytes);
-      ahead += gridDim.x;
-    };
-    auto wrap = [&]() {
-      while (seg >= p.segs) {
-        seg -= p.segs, row += (int64_t)gridDim.x * p.rows;
+      if (++seg == p.segs) {
+        seg = 0, row += (int64_t)gridDim.x * p.rows;
         enter_tile();
-        prefetch();
       }
+    };
+    uint32_t stage = 0, ph = 0;
+    auto put = [&](const Set& x) {
+      if (!wait_warp(ctl, &ctl->w_empty[stage], ph ^ 1u, a.status)) return false;
+      const uint32_t out = sring + stage * scale_bytes(1024 / kSegK) + (row0 + lane) * 4;
+      uint32_t big[kPairs], odd = 0;  // times 2^133; odd: NaN where one is infinite or NaN, else 0
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        big[i] = bf16x2_mul(bf16x2_mul(x.sc[i], 0x7F007F00u), 0x42804280u);  // 2^127, 2^6
+        odd = bf16x2_fma(big[i], 0u, odd);
+      }
+      const bool plain = __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const uint32_t v = plain ? x.sc[i] : big[i];
+        if (W || 2 * i < p.seg_words) sts32(out + 2 * i * (kTileRows * 4), __byte_perm(v, x.bi[i], 0x5410));
+        if (W > 1 || (W == 0 && 2 * i + 1 < p.seg_words))
+          sts32(out + (2 * i + 1) * (kTileRows * 4), __byte_perm(v, x.bi[i], 0x7632));
+      }
+      if (lane == 0) ctl->plain[stage][row0 / 32] = plain;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->w_full[stage]);
+      if (++stage == (uint32_t)p.stages) stage = 0, ph ^= 1u;
+      return true;
     };
     const int64_t total = (int64_t)my_tiles * p.segs;
     enter_tile();
-    prefetch();
-    wrap();
-    if (turn < total) fetch();
-    uint32_t stage = turn, ph = 0;
-    for (int64_t left = total - turn; left > 0; left -= 2) {
-      if (!wait_warp(ctl, &ctl->w_empty[stage], ph ^ 1u, a.status)) break;
-      const uint32_t out = sring + stage * kScaleBytes + (row0 + lane) * 4;
-      uint32_t flags = 0;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t big[kPairs], odd = 0;  // times 2^133; odd: NaN where one is infinite or NaN, else 0
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          big[i] = bf16x2_mul(bf16x2_mul(sc[r][i], 0x7F007F00u), 0x42804280u);  // 2^127, 2^6
-          odd = bf16x2_fma(big[i], 0u, odd);
-        }
-        if (__any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0)) {
-          flags |= 1u << (8 * r);
-#pragma unroll
-          for (int i = 0; i < kPairs; ++i) big[i] = sc[r][i];
-        }
-#pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          if (W || 2 * i < p.seg_words)
-            sts32(out + r * 128 + 2 * i * (kTileRows * 4), __byte_perm(big[i], bi[r][i], 0x5410));
-          if (W || 2 * i + 1 < p.seg_words)
-            sts32(out + r * 128 + (2 * i + 1) * (kTileRows * 4), __byte_perm(big[i], bi[r][i], 0x7632));
-        }
-      }
-      if (lane == 0) ctl->plain[stage][row0 / 64] = (uint16_t)flags;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->w_full[stage]);
-      seg += 2;
-      wrap();
-      if (left > 2) fetch();
-      stage += 2;
-      if (stage >= (uint32_t)p.stages) stage -= p.stages, ph ^= 1u;
+    Set x, y;
+    if (total > 0) fetch(x);
+    if (total > 1) fetch(y);
+    for (int64_t left = total; left > 0; left -= 2) {
+      if (!put(x)) break;
+      if (left > 2) fetch(x);
+      if (left == 1 || !put(y)) break;
+      if (left > 3) fetch(y);
     }
   }
 };
 
+// 64 weights of a row into 32 words of A; sw: (scale, bias) of each 32.
+template <int kBits, bool kScaled>
+__device__ __forceinline__ void dequant_part(const uint4 (&x)[kBits / 2], const uint32_t (&sw)[2], uint32_t (&r)[32]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t s2 = __byte_perm(sw[j], 0, 0x1010), b2 = __byte_perm(sw[j], 0, 0x3232);
+    if constexpr (kBits == 4) {
+      const uint32_t s129 = bf16x2_fma(s2, 0x3D803D80u, 0x80008000u);  // times 2^-4, plus -0
+      unpack(x[j], [&](int e, uint32_t v) {
+        uint32_t y[4];
+        if constexpr (kScaled)
+          dequant4_scaled(v, s2, s129, b2, y);
+        else
+          dequant4(v, s2, b2, y);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) r[16 * j + 4 * e + f] = y[f];
+      });
+    } else {
+#pragma unroll
+      for (int o = 0; o < 2; ++o)
+        unpack(x[2 * j + o], [&](int e, uint32_t v) {
+          uint32_t y[2];
+          if constexpr (kScaled)
+            dequant8_scaled(v, s2, b2, y);
+          else
+            dequant8(v, s2, b2, y);
+          r[16 * j + 8 * o + 2 * e] = y[0], r[16 * j + 8 * o + 2 * e + 1] = y[1];
+        });
+    }
+  }
+}
+
 // Warps that sum: four per 32 columns of the accumulator at most
 constexpr int sum_groups(int np) { return np > 32 ? np / 32 : 1; }
 constexpr int first_dequant_warp(int np) { return kSumWarp + 4 * sum_groups(np); }
-// Segments between a group's turns, and the least common multiple of that and the two scale turns: weight
-// stages are a multiple of it.
-constexpr int seg_step(int groups) { return groups / kUnits; }
-constexpr int ring_multiple(int groups) { return seg_step(groups) < 2 ? 2 : seg_step(groups); }
-constexpr int tc_threads(int np, int groups) { return 32 * (first_dequant_warp(np) + 4 * groups); }
+constexpr int tc_threads(int np) { return 32 * (first_dequant_warp(np) + 4 * kGroups); }
 
-template <int kBits, int NP, int kGroups, bool kStream>
-__global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
-    logits_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
-                     const __grid_constant__ TcArgs p) {
-  constexpr int kBoxes = kBits / 4, kStageBytes = kBoxes * kBoxBytes;  // of q, per segment
+template <int kBits, int NP, bool kStream>
+__global__ void __launch_bounds__(tc_threads(NP), 1)
+    logits_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TcArgs p) {
+  constexpr int kSegK = seg_k(kBits), kUnits = kSegK / kUnitK, kASlots = a_slots(kBits), kScaleBytes = scale_bytes(kBits);
   constexpr uint32_t kHUnit = NP * kUnitK * 2;      // bytes of a unit of h: two blocks of 64 columns
-  constexpr int kAccSegs = kAccK / kSegK, kChunkSegs = kAccSegs * kMma;  // segments per (set of) accumulators
-  // Segments of A in tensor memory (256 columns of it), beside two sets of accumulators.  A parity wait is
-  // sound only for a waiter that sees every phase of its barrier, so no slot of a ring changes hands: the
-  // slots of A are a multiple of the segments that the groups work on at a time and of the issuing
-  // warps, the weight stages of what takes turns on them (ring_stages), the slots of h of both.
-  constexpr uint32_t kASlots = 4 / kUnits;
-  constexpr uint32_t kTmemA = 512 - 256;  // first column of A; the sets start at 0
-  constexpr uint32_t kStep = seg_step(kGroups);
+  constexpr int kAccSegs = kAccK / kSegK;           // segments per set of accumulators
+  // A parity wait is sound only for a waiter that sees every phase of its barrier, so no slot of a ring changes
+  // hands: the slots of A and the stages of weights are multiples of the groups that take turns on them.
+  constexpr int kLoadWarps = 4 * (sum_groups(NP) + kGroups);
   constexpr int kSums = sum_groups(NP), kCols = NP / kSums, kFirstDequantWarp = first_dequant_warp(NP);
-  static_assert(2 * kMma * NP <= kTmemA && kASlots <= kMaxABufs && kASlots % kStep == 0 && kASlots % kMma == 0, "tensor memory");
+  static_assert(2 * NP <= kTmemA && kTmemA + kTmemACols <= 512 && kASlots % kGroups == 0, "tensor memory");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const LogitsArgs& a = p.a;
   uint8_t* const ring = smem;
-  uint8_t* const hbuf = ring + p.stages * kStageBytes;
+  uint8_t* const hbuf = ring + p.stages * kBoxBytes;
   uint8_t* const sring = hbuf + (kStream ? p.hslots : p.units) * kHUnit;  // scale words, by ring stage
   TcCtl* const ctl = reinterpret_cast<TcCtl*>(sring + p.stages * kScaleBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = blockIdx.y * NP;
 
+  // Tiles blockIdx.x, blockIdx.x + gridDim.x, ...; the CTAs of a pair take equally many, the odd one's last
+  // may lie past the vocabulary (zero weights, nothing written).
+  const int my_tiles = (p.tiles - (int)(kStream ? blockIdx.x & ~1u : blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
+  auto load_w = [&](uint32_t st, int seg, int row0) {
+    mbar_arrive_expect_tx(&ctl->w_full[st], 128 * p.rows);
+    tma_load_2d(&map_w, smem_u32(&ctl->w_full[st]), ring + st * kBoxBytes, seg * 128, row0);
+  };
+  // the ring's first loads, which wait for no release, leave before the CTA is set up
+  const int early = (int)min((int64_t)min(p.stages, p.segs), (int64_t)my_tiles * p.segs);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 2), mbar_init(&ctl->w_empty[i], 4 * kUnits);
-    for (int i = 0; i < kMaxABufs; ++i) mbar_init(&ctl->a_full[i], 4 * kUnits), mbar_init(&ctl->a_empty[i], 1);
-    for (int i = 0; i < 2 * kMma; ++i) mbar_init(&ctl->d_full[i], 1), mbar_init(&ctl->d_empty[i], 4 * kSums);
+    for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 4), mbar_init(&ctl->w_empty[i], 4);
+    for (int i = 0; i < kASlots; ++i) mbar_init(&ctl->a_full[i], 4), mbar_init(&ctl->a_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl->d_full[i], 1), mbar_init(&ctl->d_empty[i], 4 * kSums);
     for (int i = 0; i < kMaxH; ++i)
       mbar_init(&ctl->h_full[i], 1), mbar_init(&ctl->h_empty[i], 2);  // a commit of each CTA of the pair
-    mbar_init(&ctl->h_ready, 4 * kSums);
-    for (int i = 0; i < kMma; ++i) mbar_init(&ctl->drain[i], 1);
+    mbar_init(&ctl->h_ready, kLoadWarps);
+    mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
+    for (int i = 0; i < early; ++i) load_w(i, i, blockIdx.x * p.rows);
   }
   if (warp == 1) {
     tmem_alloc<1>(&ctl->tmem_base, 512);
@@ -420,32 +437,51 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
   if constexpr (kStream) cluster_sync();  // the other CTA's barriers exist
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  // Tiles blockIdx.x, blockIdx.x + gridDim.x, ...; the CTAs of a pair take equally many, the odd one's last
-  // may lie past the vocabulary (zero weights, nothing written).
-  const int my_tiles = (p.tiles - (int)(kStream ? blockIdx.x & ~1u : blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
 
+  if constexpr (!kStream) {
+    // resident h, in the dequantised order, by the warps that have nothing else to do yet; rows past M stay as
+    // they are, which their own columns of the accumulators get to see and nobody else
+    if (warp >= kSumWarp) {
+      const int per_row = p.units * (kUnitK / 8), total = min(NP, a.M - m0) * per_row;  // 16-byte pieces
+      constexpr int kT = 32 * kLoadWarps, kBatch = 8;
+      for (int i0 = threadIdx.x - 32 * kSumWarp; i0 < total; i0 += kT * kBatch) {
+        uint4 x[kBatch];
+        uint32_t at[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int i = min(i0 + e * kT, total - 1);  // the last piece again and again
+          const int m = (uint32_t)i / (uint32_t)per_row, k = i - m * per_row;
+          at[e] = smem_u32(hbuf) + (k >> 3) * (NP * 128) + m * 128 + (((k ^ m) & 7) << 4);
+          x[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (8 * k < a.d) x[e] = __ldg(reinterpret_cast<const uint4*>(a.h + (int64_t)(m0 + m) * a.ld_h) + k);
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const uint4 y = reorder_pairs<kBits>(x[e]);
+          st_shared_v4(at[e], y.x, y.y, y.z, y.w);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->h_ready);
+    }
+  }
   if (warp == 0) {
     // ---- TMA: the whole warp walks the loop and one elected lane issues, as below
     const bool leader = elect_one();
     uint32_t it = 0;          // segments issued
     uint32_t st = 0, ph = 1;  // weight ring: stage, parity of its release
     bool ok = true;
-    auto load_w = [&](int seg, int row0) {
-      if (leader) {
-        mbar_arrive_expect_tx(&ctl->w_full[st], kBoxes * 128 * p.rows);
-#pragma unroll
-        for (int i = 0; i < kBoxes; ++i)
-          tma_load_2d(&map_w, smem_u32(&ctl->w_full[st]), ring + st * kStageBytes + i * kBoxBytes, (seg * kBoxes + i) * 128, row0);
-      }
-      ++it;
-      if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
-    };
     int row0 = blockIdx.x * p.rows;
     for (int i = 0; ok && i < my_tiles; ++i, row0 += gridDim.x * p.rows) {
       for (int seg = 0; seg < p.segs; ++seg) {
-        ok = wait_warp(ctl, &ctl->w_empty[st], ph, a.status);
-        if (!ok) break;
-        load_w(seg, row0);
+        if (it >= (uint32_t)early) {
+          ok = wait_warp(ctl, &ctl->w_empty[st], ph, a.status);
+          if (!ok) break;
+          if (leader) load_w(st, seg, row0);
+        }
+        ++it;
+        if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
       }
     }
     if (!ok && leader) {  // let the loads in flight land before the CTA can exit
@@ -453,18 +489,9 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
       for (uint32_t k = k0; k < it; ++k) drain_bar(&ctl->w_full[k % p.stages], (k / p.stages) & 1u);
     }
   } else if (warp == kHWarp) {
-    // ---- h
-    const bool leader = elect_one();
-    if constexpr (!kStream) {
-      if (leader) {
-        mbar_arrive_expect_tx(&ctl->h_full[0], p.units * kHUnit);
-        for (int u = 0; u < p.units; ++u) {
-          tma_load_2d(&map_h, smem_u32(&ctl->h_full[0]), hbuf + u * kHUnit, u * kUnitK, m0);
-          tma_load_2d(&map_h, smem_u32(&ctl->h_full[0]), hbuf + u * kHUnit + kHUnit / 2, u * kUnitK + 64, m0);
-        }
-        drain_bar(&ctl->h_full[0], 0);  // the loads land before the CTA can exit, whatever the others do
-      }
-    } else {
+    // ---- streamed h
+    if constexpr (kStream) {
+      const bool leader = elect_one();
       asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel that writes the image is done
       const uint32_t rank = cluster_ctarank();
       const uint8_t* const image = p.image + (int64_t)blockIdx.y * p.units * kHUnit + rank * (kHUnit / 2);
@@ -487,37 +514,44 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
         for (uint32_t k = k0; k < it; ++k) drain_bar(&ctl->h_full[k % p.hslots], (k / p.hslots) & 1u);
       }
     }
-  } else if (warp <= kMma) {
-    // ---- MMA: segments me, me + kMma, ... of every tile.  The whole warp walks the loop, so that addresses
-    // and descriptors stay in uniform registers, and one elected lane issues: with a single thread in
-    // the loop a product took 109 clocks to issue.
-    const int me = warp - 1;
+  } else if (warp == 1) {
+    // ---- MMA.  The whole warp walks the loop, so that addresses and descriptors stay in uniform registers, and
+    // one elected lane issues: with a single thread in the loop a product took 109 clocks to issue.
     const bool leader = elect_one();
     const uint32_t idesc = make_idesc_bf16(kTileRows, NP, 0, 0);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t desc0 = smem_desc_sw128(smem_u32(hbuf), 16, 1024);
-    uint32_t slot = me, ap = 0;       // segment's place in tensor memory, parity
-    uint32_t db = 0, dp = 1;          // set of accumulators, parity of its release
-    uint32_t hs = me * kUnits, hp = 0;  // streamed h: ring slot and parity
+    uint32_t slot = 0, ap = 0;  // segment's place in tensor memory, parity
+    uint32_t db = 0, dp = 1;    // set of accumulators, parity of its release
+    uint32_t hs = 0, hp = 0;    // streamed h: ring slot and parity
     bool ok = kStream || wait_warp(ctl, &ctl->h_ready, 0, a.status);
-    int first = me;                   // my first segment of the tile
     for (int i = 0; ok && i < my_tiles; ++i) {
-      int j = 0, seg = first;         // segments in the accumulator, segment of the tile
-      for (; seg < p.segs; seg += kMma) {
-        if (j == 0) ok = wait_warp(ctl, &ctl->d_empty[2 * me + db], dp, a.status);
+      int j = 0;  // segments in the accumulators
+      for (int seg = 0; seg < p.segs; ++seg) {
+        // all the waits polled at once: one after the other, each costs its 90 clocks even when there is nothing to
+        // wait for
+        bool ready = poll_bar<false>(&ctl->a_full[slot], ap);
+        if (j == 0) ready = poll_bar<false>(&ctl->d_empty[db], dp) && ready;
+        if constexpr (kStream) {
+#pragma unroll
+          for (int k = 0; k < kUnits; ++k) { const bool x = poll_bar<false>(&ctl->h_full[hs + k], hp); ready = ready && x; }
+        }
+        if (!__all_sync(0xffffffffu, ready)) {
+        if (j == 0) ok = wait_warp(ctl, &ctl->d_empty[db], dp, a.status);
         ok = ok && wait_warp(ctl, &ctl->a_full[slot], ap, a.status);
         if constexpr (kStream) {
 #pragma unroll
-          for (int k = 0; k < kUnits; ++k) ok = ok && wait_warp<true>(ctl, &ctl->h_full[hs + k], hp, a.status);
+          for (int k = 0; k < kUnits; ++k) ok = ok && wait_warp(ctl, &ctl->h_full[hs + k], hp, a.status);
+        }
         }
         if (!ok) break;
         tc_fence_after();
-        const bool last = j == kAccSegs - 1 || seg + kMma >= p.segs;
+        const bool last = j == kAccSegs - 1 || seg + 1 == p.segs;
         if (leader) {
           const uint64_t desc = desc0 + (uint64_t)((kStream ? hs : (uint32_t)seg * kUnits) * (kHUnit >> 4));
-          const uint32_t at = tm + kTmemA + slot * (64 * kUnits), dt = tm + (2 * me + db) * NP;
+          const uint32_t at = tm + kTmemA + slot * (kSegK / 2), dt = tm + db * NP;
 #pragma unroll
-          for (int kk = 0; kk < kUnits * kUnitK / 16; ++kk)
+          for (int kk = 0; kk < kSegK / 16; ++kk)
             umma_bf16_ta(dt, at + kk * 8, desc + ((kk >> 2) * (kHUnit / 2) + (kk & 3) * 32) / 16, idesc,
                          (kk | j) != 0 ? 1u : 0u);
           umma_commit(&ctl->a_empty[slot]);
@@ -525,7 +559,7 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
 #pragma unroll
             for (int k = 0; k < kUnits; ++k) umma_commit_pair(&ctl->h_empty[hs + k]);
           }
-          if (last) umma_commit(&ctl->d_full[2 * me + db]);
+          if (last) umma_commit(&ctl->d_full[db]);
         }
         __syncwarp();
         ++j;
@@ -534,81 +568,59 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
           db ^= 1u;
           dp ^= db ^ 1u;  // after both sets
         }
-        slot += kMma;
-        if (slot >= kASlots) slot -= kASlots, ap ^= 1u;
+        if (++slot == kASlots) slot = 0, ap ^= 1u;
         if constexpr (kStream) {
-          hs += kMma * kUnits;
-          if (hs >= (uint32_t)p.hslots) hs -= p.hslots, hp ^= 1u;
+          hs += kUnits;
+          if (hs >= (uint32_t)p.hslots) hs = 0, hp ^= 1u;
         }
       }
-      first = seg - p.segs;  // segments alternate across tiles too
     }
     if (leader) {  // every issued MMA has finished before tensor memory is released
-      umma_commit(&ctl->drain[me]);
-      drain_bar(&ctl->drain[me], 0);
+      umma_commit(&ctl->drain);
+      drain_bar(&ctl->drain, 0);
     }
+  } else if (warp == 3) {
+    // ---- nothing to do
   } else if (warp < kSumWarp) {
     // ---- scales and biases
-    const ScaleRole role{p, ctl, smem_u32(sring), my_tiles, (warp - kScaleWarp) & 1, (warp - kScaleWarp) / 2 * 64, lane};
-    if (p.wide_scales && p.seg_words == 8)
-      role.template run<8>();
+    const ScaleRole<kSegK> role{p, ctl, smem_u32(sring), my_tiles, (warp - kScaleWarp) * 32, lane};
+    if (kBits == 4 && p.wide_scales && p.seg_words == 8)
+      role.template run<kSegK / 32>();
     else if (p.wide_scales && p.seg_words == 4)
       role.template run<4>();
     else if (p.wide_scales && p.seg_words == 2)
       role.template run<2>();
+    else if (p.wide_scales && p.seg_words == 1)
+      role.template run<1>();
     else
       role.template run<0>();
   } else if (warp < kFirstDequantWarp) {
     // ---- sums and output
     const int q = warp & 3, n0 = (warp - kSumWarp) / 4 * kCols;
     bool ok = true;
-    if constexpr (!kStream) {
-      // resident h into the dequantised order, in place: 128 threads per sum group, a 16-byte piece of 16 rows each
-      const int tid = threadIdx.x - 32 * kSumWarp, live = min(NP, a.M - m0);  // the other rows are zero
-      ok = wait_warp(ctl, &ctl->h_full[0], 0, a.status);
-      for (int blk = tid >> 7; ok && blk < p.units * 2; blk += kSums) {
-        const uint32_t b = smem_u32(hbuf) + blk * (NP * 128) + (tid & 127) * 16;
-#pragma unroll
-        for (int r = 0; r < NP; r += 16) {
-          if (r + ((tid & 127) >> 3) >= live) break;
-          const uint4 x = reorder_pairs<kBits>(lds128(b + r * 128));
-          st_shared_v4(b + r * 128, x.x, x.y, x.z, x.w);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&ctl->h_ready);
-    }
     float acc[kCols];  // columns n0 on
     const float inv_cap = a.softcap > 0.f ? 1.f / a.softcap : 0.f;
-    const int chunks = (p.segs + kChunkSegs - 1) / kChunkSegs;
-    uint32_t db[kMma] = {}, dp[kMma] = {};  // per MMA warp: set and parity
-    int first[kMma];                        // and its first segment of the tile
-#pragma unroll
-    for (int w = 0; w < kMma; ++w) first[w] = w;
+    const int chunks = (p.segs + kAccSegs - 1) / kAccSegs;
+    uint32_t db = 0, dp = 0;  // set and parity
     for (int i = 0; ok && i < my_tiles; ++i) {
 #pragma unroll
       for (int n = 0; n < kCols; ++n) acc[n] = 0.f;
-      for (int c = 0; ok && c < chunks; ++c) {
+      for (int c = 0; c < chunks; ++c) {
+        ok = wait_warp(ctl, &ctl->d_full[db], dp, a.status);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
-        for (int w = 0; w < kMma; ++w) {
-          if (!ok || first[w] + c * kChunkSegs >= p.segs) continue;  // no segment of this warp's here
-          ok = wait_warp(ctl, &ctl->d_full[2 * w + db[w]], dp[w], a.status);
-          if (!ok) continue;
-          tc_fence_after();
+        for (int n = 0; n < kCols; n += 16) {
+          uint32_t r[16];
+          tmem_ld16(tmem + db * NP + n0 + n + ((uint32_t)(32 * q) << 16), r);
 #pragma unroll
-          for (int n = 0; n < kCols; n += 16) {
-            uint32_t r[16];
-            tmem_ld16(tmem + (2 * w + db[w]) * NP + n0 + n + ((uint32_t)(32 * q) << 16), r);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[n + e] += __uint_as_float(r[e]);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->d_empty[2 * w + db[w]]);
-          db[w] ^= 1u;
-          dp[w] ^= db[w] ^ 1u;
+          for (int e = 0; e < 16; ++e) acc[n + e] += __uint_as_float(r[e]);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->d_empty[db]);
+        db ^= 1u;
+        dp ^= db ^ 1u;
       }
       if (!ok) break;
       const int row = 32 * q + lane;
@@ -632,101 +644,62 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
           }
         }
       }
-#pragma unroll
-      for (int w = 0; w < kMma; ++w) {  // the warp's segments go on alternating in the next tile
-        const int over = (p.segs - first[w] + kMma - 1) / kMma * kMma + first[w] - p.segs;
-        first[w] = first[w] < p.segs ? over : first[w] - p.segs;
-      }
     }
   } else {
     // ---- dequantisation
     const int wg = (warp - kFirstDequantWarp) >> 2, q = warp & 3, row = 32 * q + lane;
-    // the group keeps to one half of every kStep-th segment
-    static_assert(kGroups % kUnits == 0, "a group keeps to one half");
-    const uint32_t half = wg % kUnits, swz = (uint32_t)(row & 7) << 4;
-    const uint32_t wrow = smem_u32(ring) + row * 128 + (kBits == 8 ? half * kBoxBytes : 0);  // 8-bit: the half's box
-    const uint32_t srow = smem_u32(sring) + row * 4;
-    uint32_t soff[4];  // the unit's four scale words
-#pragma unroll
-    for (int i = 0; i < 4; ++i) soff[i] = ((half * 4 + i) >> p.shift) * (kTileRows * 4);
+    // segments wg, wg + kGroups, ...
+    constexpr int kParts = kSegK / 64, kVec = 8 / kParts;  // pieces of 64 columns, their 16-byte vectors
+    const uint32_t swz = (uint32_t)(row & 7) << 4;
+    const uint32_t wrow = smem_u32(ring) + row * 128, srow = smem_u32(sring) + row * 4;
     const uint32_t trow = tmem + kTmemA + ((uint32_t)(32 * q) << 16);
-    uint32_t stage = wg / kUnits, wph = 0;  // weight ring (kStep <= stages)
-    uint32_t slot = wg / kUnits, aph = 0;   // place in tensor memory (kStep <= kASlots)
+    uint32_t stage = wg, wph = 0;  // weight ring
+    uint32_t slot = wg, aph = 0;   // place in tensor memory
     bool ok = true;
-    for (int64_t left = (int64_t)my_tiles * p.segs - wg / kUnits; left > 0; left -= kStep) {
+    for (int64_t left = (int64_t)my_tiles * p.segs - wg; left > 0; left -= kGroups) {
       ok = wait_warp(ctl, &ctl->w_full[stage], wph, a.status);
       if (!ok) break;
-      const uint32_t wst = wrow + stage * kStageBytes, sst = srow + stage * kScaleBytes;
-      // The unit's 64 (8-bit: 128) bytes and 4 words.  The stage is given back behind the tensor-memory store
-      // that takes what they became: a release right behind the loads does not hold them back, and the next
-      // box landed first.
-      constexpr int kVec = kBits == 4 ? 4 : 8;
-      uint4 w[kVec];
-      uint32_t sw[4];
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) w[i] = lds128(wst + (((kBits == 4 ? half * 4 + i : i) << 4) ^ swz));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sw[i] = lds32(sst + soff[i]);
+      const uint32_t wst = wrow + stage * kBoxBytes, sst = srow + stage * kScaleBytes;
       const bool plain = (lds32(smem_u32(ctl->plain[stage])) >> (8 * q) & 1u) != 0;
-      const uint32_t dst = trow + (slot * kUnits + half) * 64;
-      // pieces of 32 columns per store: two, or one where 1024 threads leave 64 registers each
-      constexpr int kPieces = tc_threads(NP, kGroups) == 1024 ? 1 : 2;
+      const uint32_t dst = trow + slot * (kSegK / 2);
+      // The stage is given back behind the tensor-memory stores that take what the weights became: a release right
+      // behind the loads does not hold them back, and the next box landed first.
+      auto load = [&](int part, uint4 (&x)[kVec], uint32_t (&y)[2]) {
 #pragma unroll
-      for (int part = 0; part < 4 / kPieces; ++part) {
-        uint32_t r[16 * kPieces];
-        // 32 columns, 16 words of tensor memory, per piece
-        if (__builtin_expect(!plain, 1)) {
+        for (int i = 0; i < kVec; ++i) x[i] = lds128(wst + (((part * kVec + i) << 4) ^ swz));
 #pragma unroll
-          for (int j = 0; j < kPieces; ++j) {
-            const int i = part * kPieces + j;
-            const uint32_t s2 = __byte_perm(sw[i], 0, 0x1010), b2 = __byte_perm(sw[i], 0, 0x3232);
-            if constexpr (kBits == 4) {
-              const uint32_t s129 = bf16x2_fma(s2, 0x3D803D80u, 0x80008000u);  // times 2^-4, plus -0
-              unpack(w[i], [&](int e, uint32_t v) {
-                uint32_t x[4];
-                dequant4_scaled(v, s2, s129, b2, x);
-#pragma unroll
-                for (int f = 0; f < 4; ++f) r[16 * j + 4 * e + f] = x[f];
-              });
-            } else {
-#pragma unroll
-              for (int o = 0; o < 2; ++o)
-                unpack(w[2 * i + o], [&](int e, uint32_t v) {
-                  uint32_t x[2];
-                  dequant8_scaled(v, s2, b2, x);
-                  r[16 * j + 8 * o + 2 * e] = x[0], r[16 * j + 8 * o + 2 * e + 1] = x[1];
-                });
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < kPieces; ++j) {
-            const int i = part * kPieces + j;
-            const uint32_t s2 = __byte_perm(sw[i], 0, 0x1010), b2 = __byte_perm(sw[i], 0, 0x3232);
-            if constexpr (kBits == 4) {
-              unpack(w[i], [&](int e, uint32_t v) {
-                uint32_t x[4];
-                dequant4(v, s2, b2, x);
-#pragma unroll
-                for (int f = 0; f < 4; ++f) r[16 * j + 4 * e + f] = x[f];
-              });
-            } else {
-#pragma unroll
-              for (int o = 0; o < 2; ++o)
-                unpack(w[2 * i + o], [&](int e, uint32_t v) {
-                  uint32_t x[2];
-                  dequant8(v, s2, b2, x);
-                  r[16 * j + 8 * o + 2 * e] = x[0], r[16 * j + 8 * o + 2 * e + 1] = x[1];
-                });
-            }
-          }
-        }
+        for (int i = 0; i < 2; ++i) y[i] = lds32(sst + ((part * 2 + i) >> p.shift) * (kTileRows * 4));
+      };
+      auto store = [&](int part, const uint32_t (&r)[32]) {
         if (part == 0) {
           ok = wait_warp(ctl, &ctl->a_empty[slot], aph ^ 1u, a.status);
-          if (!ok) break;
+          if (!ok) return;
           tc_fence_after();
         }
-        tmem_st(dst + part * (16 * kPieces), r);
+        tmem_st(dst + part * 32, r);
+      };
+      if (__builtin_expect(!plain, 1)) {
+        uint4 w[2][kVec];  // this piece and the next
+        uint32_t sw[2][2];
+        load(0, w[0], sw[0]);
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          if (part + 1 < kParts) load(part + 1, w[(part + 1) & 1], sw[(part + 1) & 1]);
+          uint32_t r[32];
+          dequant_part<kBits, true>(w[part & 1], sw[part & 1], r);
+          store(part, r);
+          if (!ok) break;
+        }
+      } else {  // apart and rolled up: inside the loop above it cost 10 of 78 us
+#pragma unroll 1
+        for (int part = 0; part < kParts; ++part) {
+          uint4 w[kVec];
+          uint32_t sw[2], r[32];
+          load(part, w, sw);
+          dequant_part<kBits, false>(w, sw, r);
+          store(part, r);
+          if (!ok) break;
+        }
       }
       if (!ok) break;
       tmem_st_wait();
@@ -736,9 +709,9 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
         mbar_arrive(&ctl->w_empty[stage]);
         mbar_arrive(&ctl->a_full[slot]);
       }
-      slot += kStep;
+      slot += kGroups;
       if (slot >= kASlots) slot -= kASlots, aph ^= 1u;
-      stage += kStep;
+      stage += kGroups;
       if (stage >= (uint32_t)p.stages) stage -= p.stages, wph ^= 1u;
     }
   }
@@ -757,6 +730,8 @@ __global__ void __launch_bounds__(tc_threads(NP, kGroups), 1)
 // (128-byte swizzled rows), 16-byte pieces in the dequantised order, zero where h has no element.
 template <int kBits>
 __global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, int blocks, int64_t pieces, uint4* image) {
+  // set up while the kernel before it in the stream ends; the products' kernel may be set up once that one has
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= pieces) return;
@@ -768,18 +743,18 @@ __global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, in
   image[i] = x;
 }
 
-constexpr int kMinStages = 4;
-constexpr int stage_bytes(int bits) { return bits / 4 * kBoxBytes + kScaleBytes; }
-int64_t units_of(int64_t d) { return cdiv(d, kSegK) * kUnits; }
+constexpr int kMinStages = 3, kStreamStages = 6;  // of weights beside resident and beside streamed h
+constexpr int stage_bytes(int bits) { return kBoxBytes + scale_bytes(bits); }
+int64_t units_of(int64_t d, int bits) { return cdiv(d, seg_k(bits)) * (seg_k(bits) / kUnitK); }
 // up to 16 rows, beside at least kMinStages of weights
 bool resident(int bits, int64_t M, int64_t d) {
-  return M <= 16 && units_of(d) * (16 * kUnitK * 2) <= kSmemLimit - kCtlBytes - kMinStages * stage_bytes(bits);
+  return M <= 16 && units_of(d, bits) * (16 * kUnitK * 2) <= kSmemLimit - kCtlBytes - kMinStages * stage_bytes(bits);
 }
 int rows_per_pass(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
-template <int kBits, int NP, int kGroups, bool kStream>
+template <int kBits, int NP, bool kStream>
 cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_t st) {
-  constexpr int kHUnit = NP * kUnitK * 2;
+  constexpr int kHUnit = NP * kUnitK * 2, kSegK = seg_k(kBits), kUnits = kSegK / kUnitK;
   TcArgs p;
   p.a = a;
   const int64_t row_bytes = (int64_t)a.d * kBits / 8;
@@ -805,25 +780,21 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
   const uint32_t repeat = (uint32_t)(per >> p.shift);  // words per group
   p.gmul = repeat > 1 ? (uint32_t)(((1ull << 32) + repeat - 1) / repeat) : 0u;
   p.wide_scales = repeat == 1 && p.ngroups % p.seg_words == 0 && aligned16(a.scales) && aligned16(a.biases);
-  constexpr int kMul = ring_multiple(kGroups);
-  static_assert(kMaxStages % kMul == 0 && kMinStages % kMul == 0, "weight ring");
+  static_assert(kMaxStages % kGroups == 0 && kMinStages % kGroups == 0 && kStreamStages % kGroups == 0, "weight ring");
   const int fixed = kCtlBytes, stage = stage_bytes(kBits);
-  // streamed: kMinStages of weights, then as many slots as fit (a multiple of both issuing warps' segments)
-  p.hslots = kStream ? std::min(kMaxH, (kSmemLimit - fixed - kMinStages * stage) / kHUnit) / (kMma * kUnits) * (kMma * kUnits) : 0;
+  p.hslots = kStream ? std::min(kMaxH, (kSmemLimit - fixed - kStreamStages * stage) / kHUnit) / kUnits * kUnits : 0;
   const int h_bytes = (kStream ? p.hslots : p.units) * kHUnit;
-  p.stages = std::min(kMaxStages, (kSmemLimit - fixed - h_bytes) / stage) / kMul * kMul;
+  p.stages = std::min(kMaxStages, (kSmemLimit - fixed - h_bytes) / stage) / kGroups * kGroups;
   p.image = static_cast<const uint8_t*>(workspace);
   const int smem = p.stages * stage + h_bytes + fixed + 1024;
-  CUtensorMap mw, mh;
+  CUtensorMap mw;
   if (!encode_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq, row_bytes, a.V, row_bytes, 128, p.rows)) return cudaErrorNotSupported;
-  mh = mw;
-  if (!kStream && !encode_map_2d(&mh, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.h, a.d, a.M, a.ld_h * 2, 64, NP)) return cudaErrorNotSupported;
   static std::atomic<int> done[64];
-  auto kernel = logits_tc_kernel<kBits, NP, kGroups, kStream>;
+  auto kernel = logits_tc_kernel<kBits, NP, kStream>;
   if (cudaError_t e = opt_in_smem(kernel, kSmemLimit + 1024, done)) return e;
   const int mt = (int)cdiv(a.M, NP);
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3((unsigned)tc_threads(NP, kGroups));
+  cfg.blockDim = dim3((unsigned)tc_threads(NP));
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -831,27 +802,33 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
   if constexpr (kStream) {
     const int blocks = p.units * 2;
     const int64_t pieces = (int64_t)mt * blocks * NP * 8;
-    h_image_kernel<kBits><<<(unsigned)cdiv(pieces, 256), 256, 0, st>>>(a, NP, blocks, pieces, static_cast<uint4*>(workspace));
-    if (cudaError_t e = cudaGetLastError()) return e;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t image = {};
+    image.gridDim = dim3((unsigned)cdiv(pieces, 256));
+    image.blockDim = dim3(256);
+    image.stream = st;
+    image.attrs = attr;
+    image.numAttrs = 1;
+    if (cudaError_t e = cudaLaunchKernelEx(&image, h_image_kernel<kBits>, a, NP, blocks, pieces, static_cast<uint4*>(workspace)))
+      return e;
     cfg.gridDim = dim3((unsigned)std::min((p.tiles + 1) / 2 * 2, slots), (unsigned)mt);
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {2, 1, 1};
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its weights may come before the image is there
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 2;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {2, 1, 1};
+    cfg.numAttrs = 2;  // its weights may come before the image is there
   } else {
     cfg.gridDim = dim3((unsigned)std::min(p.tiles, slots), (unsigned)mt);
     cfg.numAttrs = 0;
   }
-  return cudaLaunchKernelEx(&cfg, kernel, mw, mh, p);
+  return cudaLaunchKernelEx(&cfg, kernel, mw, p);
 }
 
 template <int kBits>
 cudaError_t launch_bits(const LogitsArgs& a, int sms, void* workspace, cudaStream_t st) {
-  if (resident(kBits, a.M, a.d)) return launch_np<kBits, 16, 4, false>(a, sms, workspace, st);
-  if (a.M <= 16) return launch_np<kBits, 16, 4, true>(a, sms, workspace, st);
-  if (a.M <= 32) return launch_np<kBits, 32, 4, true>(a, sms, workspace, st);
-  return launch_np<kBits, 64, 4, true>(a, sms, workspace, st);
+  if (resident(kBits, a.M, a.d)) return launch_np<kBits, 16, false>(a, sms, workspace, st);
+  if (a.M <= 16) return launch_np<kBits, 16, true>(a, sms, workspace, st);
+  if (a.M <= 32) return launch_np<kBits, 32, true>(a, sms, workspace, st);
+  return launch_np<kBits, 64, true>(a, sms, workspace, st);
 }
 
 }  // namespace
@@ -859,7 +836,7 @@ cudaError_t launch_bits(const LogitsArgs& a, int sms, void* workspace, cudaStrea
 size_t logits_tc_workspace(int bits, int64_t M, int64_t d) {
   if (resident(bits, M, d)) return 0;
   const int rows = rows_per_pass(M);
-  return (size_t)(cdiv(M, rows) * rows * units_of(d) * kUnitK * 2);
+  return (size_t)(cdiv(M, rows) * rows * units_of(d, bits) * kUnitK * 2);
 }
 
 cudaError_t launch_logits_tc(const LogitsArgs& a, int bits, int sms, void* workspace, cudaStream_t st) {
