@@ -27,7 +27,7 @@
 //
 // Order of k: 4-bit dequantisation yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights
 // (8-bit: (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes at a
-// time.  Up to 16 rows of h that fit beside the weights (d up to 5120) are loaded and put in that order by
+// time.  Up to 16 rows of h that fit beside the weights (d up to 3328) are loaded and put in that order by
 // each CTA, once.  More are streamed: a small kernel first writes h in that order, and as
 // shared memory holds it, to the workspace, and the CTAs work in pairs (clusters) on neighbouring tiles,
 // each fetching half of every unit of h for both (multicast), since h crosses from L2 once per tile: at 64
@@ -248,6 +248,14 @@ __device__ __forceinline__ uint32_t group_of(const TcArgs& p, uint32_t word) {
   return p.gmul ? __umulhi(word, p.gmul) : word;
 }
 
+// The rows' scales and biases of a tile, contiguous, to L2, by the two threads with lane 0 and 1.
+__device__ __forceinline__ void prefetch_scales(const TcArgs& p, int64_t tile, int lane) {
+  const LogitsArgs& a = p.a;
+  const uint32_t bytes = (uint32_t)(p.rows * 2) * p.ngroups;  // a multiple of 16: p.rows is one of 8
+  if (p.wide_scales && (lane == 0 || lane == 1) && (tile + 1) * p.rows <= a.V)
+    l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + tile * bytes, bytes);
+}
+
 // One of the four warps that bring scales and biases beside the segments of q: rows row0 + lane of the tile.
 template <int kSegK>
 struct ScaleRole {
@@ -268,14 +276,11 @@ struct ScaleRole {
     int seg = 0;
     int64_t row = (int64_t)blockIdx.x * p.rows + row0 + lane, ahead = (int64_t)blockIdx.x + gridDim.x;
     const uint16_t *s, *b;
-    // Scales are fetched two segments ahead, which covers the way from L2 and not from memory: the rows' scales of
-    // the next tile, contiguous, are brought to L2 a tile ahead.
-    const uint32_t tile_bytes = (uint32_t)(p.rows * 2) * p.ngroups;  // a multiple of 16 where W > 0 (the host sees to it)
+    // Scales are fetched two segments ahead, which covers the way from L2 and not from memory.
     auto enter_tile = [&]() {
       s = a.scales + row * p.ngroups;
       b = a.biases + row * p.ngroups;
-      if (W && row0 == 0 && lane < 2 && (ahead + 1) * p.rows <= a.V)
-        l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + ahead * tile_bytes, tile_bytes);
+      if (row0 == 0) prefetch_scales(p, ahead, lane);
       ahead += gridDim.x;
     };
     auto fetch = [&](Set& x) {
@@ -410,12 +415,27 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
   // Tiles blockIdx.x, blockIdx.x + gridDim.x, ...; the CTAs of a pair take equally many, the odd one's last
   // may lie past the vocabulary (zero weights, nothing written).
   const int my_tiles = (p.tiles - (int)(kStream ? blockIdx.x & ~1u : blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
-  auto load_w = [&](uint32_t st, int seg, int row0) {
-    mbar_arrive_expect_tx(&ctl->w_full[st], 128 * p.rows);
-    tma_load_2d(&map_w, smem_u32(&ctl->w_full[st]), ring + st * kBoxBytes, seg * 128, row0);
+  // Resident h, by the warps that sum and dequantise, a thread always the same 16-byte pieces; rows past M stay as
+  // they are, which their own columns of the accumulators get to see and nobody else.  Asked for before any weights:
+  // behind them it came 5000 clocks later, and no product starts without it.
+  auto each_piece = [&](auto f) {  // f(address in shared memory, row, piece of the row)
+    const int live = min(NP, a.M - m0), per_row = p.units * (kUnitK / 8);
+    const int split = kLoadWarps / live, m = (warp - kSumWarp) % live, part = (warp - kSumWarp) / live;
+    if (part >= split) return;
+    for (int k = part * 32 + lane; k < per_row; k += split * 32)
+      f(smem_u32(hbuf) + (k >> 3) * (NP * 128) + m * 128 + (((k ^ m) & 7) << 4), m, k);
   };
-  // the ring's first loads, which wait for no release, leave before the CTA is set up
-  const int early = (int)min((int64_t)min(p.stages, p.segs), (int64_t)my_tiles * p.segs);
+  if constexpr (!kStream) {
+    if (warp >= kSumWarp)
+      each_piece([&](uint32_t at, int m, int k) {
+        if (8 * k < a.d)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(a.h + (int64_t)(m0 + m) * a.ld_h + 8 * k)
+                       : "memory");
+        else
+          st_shared_v4(at, 0u, 0u, 0u, 0u);
+      });
+  }
+  prefetch_scales(p, blockIdx.x, threadIdx.x - 32);  // the same goes for the first tile's scales
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 4), mbar_init(&ctl->w_empty[i], 4);
     for (int i = 0; i < kASlots; ++i) mbar_init(&ctl->a_full[i], 4), mbar_init(&ctl->a_empty[i], 1);
@@ -426,7 +446,6 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
-    for (int i = 0; i < early; ++i) load_w(i, i, blockIdx.x * p.rows);
   }
   if (warp == 1) {
     tmem_alloc<1>(&ctl->tmem_base, 512);
@@ -439,28 +458,12 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
   const uint32_t tmem = ctl->tmem_base;
 
   if constexpr (!kStream) {
-    // resident h, in the dequantised order, by the warps that have nothing else to do yet; rows past M stay as
-    // they are, which their own columns of the accumulators get to see and nobody else
-    if (warp >= kSumWarp) {
-      const int per_row = p.units * (kUnitK / 8), total = min(NP, a.M - m0) * per_row;  // 16-byte pieces
-      constexpr int kT = 32 * kLoadWarps, kBatch = 8;
-      for (int i0 = threadIdx.x - 32 * kSumWarp; i0 < total; i0 += kT * kBatch) {
-        uint4 x[kBatch];
-        uint32_t at[kBatch];
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int i = min(i0 + e * kT, total - 1);  // the last piece again and again
-          const int m = (uint32_t)i / (uint32_t)per_row, k = i - m * per_row;
-          at[e] = smem_u32(hbuf) + (k >> 3) * (NP * 128) + m * 128 + (((k ^ m) & 7) << 4);
-          x[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (8 * k < a.d) x[e] = __ldg(reinterpret_cast<const uint4*>(a.h + (int64_t)(m0 + m) * a.ld_h) + k);
-        }
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const uint4 y = reorder_pairs<kBits>(x[e]);
-          st_shared_v4(at[e], y.x, y.y, y.z, y.w);
-        }
-      }
+    if (warp >= kSumWarp) {  // resident h is here: into the dequantised order
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      each_piece([&](uint32_t at, int, int) {
+        const uint4 x = reorder_pairs<kBits>(lds128(at));
+        st_shared_v4(at, x.x, x.y, x.z, x.w);
+      });
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->h_ready);
@@ -475,10 +478,11 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     int row0 = blockIdx.x * p.rows;
     for (int i = 0; ok && i < my_tiles; ++i, row0 += gridDim.x * p.rows) {
       for (int seg = 0; seg < p.segs; ++seg) {
-        if (it >= (uint32_t)early) {
-          ok = wait_warp(ctl, &ctl->w_empty[st], ph, a.status);
-          if (!ok) break;
-          if (leader) load_w(st, seg, row0);
+        ok = wait_warp(ctl, &ctl->w_empty[st], ph, a.status);
+        if (!ok) break;
+        if (leader) {
+          mbar_arrive_expect_tx(&ctl->w_full[st], 128 * p.rows);
+          tma_load_2d(&map_w, smem_u32(&ctl->w_full[st]), ring + st * kBoxBytes, seg * 128, row0);
         }
         ++it;
         if (++st == (uint32_t)p.stages) st = 0, ph ^= 1u;
@@ -743,10 +747,11 @@ __global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, in
   image[i] = x;
 }
 
-constexpr int kMinStages = 3, kStreamStages = 6;  // of weights beside resident and beside streamed h
+constexpr int kMinStages = 6;  // of weights, beside resident or streamed h
 constexpr int stage_bytes(int bits) { return kBoxBytes + scale_bytes(bits); }
 int64_t units_of(int64_t d, int bits) { return cdiv(d, seg_k(bits)) * (seg_k(bits) / kUnitK); }
-// up to 16 rows, beside at least kMinStages of weights
+// Up to 16 rows, beside at least kMinStages of weights.  (With three stages beside them, 13 rows of d 3840 took
+// 36.4 us resident and 34.7 streamed.)
 bool resident(int bits, int64_t M, int64_t d) {
   return M <= 16 && units_of(d, bits) * (16 * kUnitK * 2) <= kSmemLimit - kCtlBytes - kMinStages * stage_bytes(bits);
 }
@@ -780,9 +785,9 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
   const uint32_t repeat = (uint32_t)(per >> p.shift);  // words per group
   p.gmul = repeat > 1 ? (uint32_t)(((1ull << 32) + repeat - 1) / repeat) : 0u;
   p.wide_scales = repeat == 1 && p.ngroups % p.seg_words == 0 && aligned16(a.scales) && aligned16(a.biases);
-  static_assert(kMaxStages % kGroups == 0 && kMinStages % kGroups == 0 && kStreamStages % kGroups == 0, "weight ring");
+  static_assert(kMaxStages % kGroups == 0 && kMinStages % kGroups == 0, "weight ring");
   const int fixed = kCtlBytes, stage = stage_bytes(kBits);
-  p.hslots = kStream ? std::min(kMaxH, (kSmemLimit - fixed - kStreamStages * stage) / kHUnit) / kUnits * kUnits : 0;
+  p.hslots = kStream ? std::min(kMaxH, (kSmemLimit - fixed - kMinStages * stage) / kHUnit) / kUnits * kUnits : 0;
   const int h_bytes = (kStream ? p.hslots : p.units) * kHUnit;
   p.stages = std::min(kMaxStages, (kSmemLimit - fixed - h_bytes) / stage) / kGroups * kGroups;
   p.image = static_cast<const uint8_t*>(workspace);

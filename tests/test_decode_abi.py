@@ -48,7 +48,7 @@ def test_logits_host_checks(lib):
 
 def test_logits_workspace(lib):
     q = lib.orpo_head_logits_q_workspace_bytes
-    assert q(1, 2560, 4) == q(16, 5120, 4) == q(16, 5120, 8) == 0
+    assert q(1, 2560, 4) == q(16, 3328, 4) == q(16, 3328, 8) == 0
     for M, d, bits in ((17, 256, 4), (64, 4096, 4), (16, 16384, 4), (1, 8200, 8), (1000, 4096, 4)):
         rows, seg = 16 if M <= 16 else 32 if M <= 32 else -(-M // 64) * 64, 1024 // bits
         assert q(M, d, bits) == rows * -(-d // seg) * seg * 2
