@@ -30,7 +30,7 @@
 // time.  Up to 16 rows of h that fit beside the weights (d up to 3328) are loaded and put in that order by
 // each CTA, once.  More are streamed: a small kernel first writes h in that order, and as
 // shared memory holds it, to the workspace, and the CTAs work in pairs (clusters) on neighbouring tiles,
-// each fetching half of every unit of h for both (multicast), since h crosses from L2 once per tile: at 64
+// each fetching half of every segment of h for both (multicast), since h crosses from L2 once per tile: at 64
 // rows that is twice the weights' bytes.
 // Accuracy: the tensor core truncates as it accumulates (measured: 1e-9 of the result per product, one
 // sign), so an accumulator spans 512 columns and those sums are added in registers, rounding.
@@ -53,7 +53,7 @@ constexpr int kAccK = 512;                            // columns per accumulator
 constexpr int seg_k(int bits) { return 1024 / bits; } // columns per segment: a box of q
 constexpr int scale_bytes(int bits) { return seg_k(bits) / 32 * kTileRows * 4; }  // (scale, bias) words of a segment, at most one per 32 columns
 constexpr int kMaxStages = 9;
-constexpr int kMaxH = 8;  // streamed h: units in the ring
+constexpr int kMaxH = 8;  // streamed h: segments in the ring
 constexpr int kGroups = 3;                            // dequantising groups
 constexpr int kTmemA = 128, kTmemACols = 384;         // A in tensor memory, beside two sets of accumulators
 constexpr int a_slots(int bits) { return kTmemACols / (seg_k(bits) / 2); }
@@ -85,7 +85,7 @@ struct TcArgs {
   int seg_words, shift;   // scale words per segment: one per 2^shift times 32 columns
   uint32_t gmul;          // group of word j of a row: j if 0, else umulhi(j, gmul)
   int stages;             // weight ring
-  int hslots;             // streamed h: ring slots
+  int hslots;             // streamed h: segments in the ring
   const uint8_t* image;   // streamed h: [m tiles][units] units as shared memory holds them
   int wide_scales;        // a segment's scales and biases are one aligned word of up to 16 bytes
 };
@@ -395,7 +395,7 @@ template <int kBits, int NP, bool kStream>
 __global__ void __launch_bounds__(tc_threads(NP), 1)
     logits_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ TcArgs p) {
   constexpr int kSegK = seg_k(kBits), kUnits = kSegK / kUnitK, kASlots = a_slots(kBits), kScaleBytes = scale_bytes(kBits);
-  constexpr uint32_t kHUnit = NP * kUnitK * 2;      // bytes of a unit of h: two blocks of 64 columns
+  constexpr uint32_t kHUnit = NP * kUnitK * 2, kHSeg = kUnits * kHUnit;  // bytes of a unit (two blocks of 64 columns) and a segment of h
   constexpr int kAccSegs = kAccK / kSegK;           // segments per set of accumulators
   // A parity wait is sound only for a waiter that sees every phase of its barrier, so no slot of a ring changes
   // hands: the slots of A and the stages of weights are multiples of the groups that take turns on them.
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
   const LogitsArgs& a = p.a;
   uint8_t* const ring = smem;
   uint8_t* const hbuf = ring + p.stages * kBoxBytes;
-  uint8_t* const sring = hbuf + (kStream ? p.hslots : p.units) * kHUnit;  // scale words, by ring stage
+  uint8_t* const sring = hbuf + (kStream ? p.hslots : p.segs) * kHSeg;  // scale words, by ring stage
   TcCtl* const ctl = reinterpret_cast<TcCtl*>(sring + p.stages * kScaleBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = blockIdx.y * NP;
@@ -498,17 +498,17 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
       const bool leader = elect_one();
       asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel that writes the image is done
       const uint32_t rank = cluster_ctarank();
-      const uint8_t* const image = p.image + (int64_t)blockIdx.y * p.units * kHUnit + rank * (kHUnit / 2);
-      uint32_t it = 0, hs = 0, hp = 1;  // units issued; slot, parity of its release
+      const uint8_t* const image = p.image + (int64_t)blockIdx.y * p.segs * kHSeg + rank * (kHSeg / 2);
+      uint32_t it = 0, hs = 0, hp = 1;  // segments issued; slot, parity of its release
       bool ok = true;
       for (int i = 0; ok && i < my_tiles; ++i) {
         const uint8_t* src = image;
-        for (int u = 0; u < p.units; ++u, ++it, src += kHUnit) {
+        for (int seg = 0; seg < p.segs; ++seg, ++it, src += kHSeg) {
           ok = wait_warp<true>(ctl, &ctl->h_empty[hs], hp, a.status);  // both CTAs are done with the slot
           if (!ok) break;
           if (leader) {
-            mbar_arrive_expect_tx(&ctl->h_full[hs], kHUnit);  // this half and the other CTA's
-            bulk_load_pair(src, kHUnit / 2, hbuf + hs * kHUnit + rank * (kHUnit / 2), &ctl->h_full[hs]);
+            mbar_arrive_expect_tx(&ctl->h_full[hs], kHSeg);  // this half and the other CTA's
+            bulk_load_pair(src, kHSeg / 2, hbuf + hs * kHSeg + rank * (kHSeg / 2), &ctl->h_full[hs]);
           }
           if (++hs == (uint32_t)p.hslots) hs = 0, hp ^= 1u;
         }
@@ -536,33 +536,24 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
         // wait for
         bool ready = poll_bar<false>(&ctl->a_full[slot], ap);
         if (j == 0) ready = poll_bar<false>(&ctl->d_empty[db], dp) && ready;
-        if constexpr (kStream) {
-#pragma unroll
-          for (int k = 0; k < kUnits; ++k) { const bool x = poll_bar<false>(&ctl->h_full[hs + k], hp); ready = ready && x; }
-        }
+        if constexpr (kStream) ready = poll_bar<false>(&ctl->h_full[hs], hp) && ready;
         if (!__all_sync(0xffffffffu, ready)) {
-        if (j == 0) ok = wait_warp(ctl, &ctl->d_empty[db], dp, a.status);
-        ok = ok && wait_warp(ctl, &ctl->a_full[slot], ap, a.status);
-        if constexpr (kStream) {
-#pragma unroll
-          for (int k = 0; k < kUnits; ++k) ok = ok && wait_warp(ctl, &ctl->h_full[hs + k], hp, a.status);
-        }
+          if (j == 0) ok = wait_warp(ctl, &ctl->d_empty[db], dp, a.status);
+          ok = ok && wait_warp(ctl, &ctl->a_full[slot], ap, a.status);
+          if constexpr (kStream) ok = ok && wait_warp(ctl, &ctl->h_full[hs], hp, a.status);
         }
         if (!ok) break;
         tc_fence_after();
         const bool last = j == kAccSegs - 1 || seg + 1 == p.segs;
         if (leader) {
-          const uint64_t desc = desc0 + (uint64_t)((kStream ? hs : (uint32_t)seg * kUnits) * (kHUnit >> 4));
+          const uint64_t desc = desc0 + (uint64_t)((kStream ? hs : (uint32_t)seg) * (kHSeg >> 4));
           const uint32_t at = tm + kTmemA + slot * (kSegK / 2), dt = tm + db * NP;
 #pragma unroll
           for (int kk = 0; kk < kSegK / 16; ++kk)
             umma_bf16_ta(dt, at + kk * 8, desc + ((kk >> 2) * (kHUnit / 2) + (kk & 3) * 32) / 16, idesc,
                          (kk | j) != 0 ? 1u : 0u);
           umma_commit(&ctl->a_empty[slot]);
-          if constexpr (kStream) {
-#pragma unroll
-            for (int k = 0; k < kUnits; ++k) umma_commit_pair(&ctl->h_empty[hs + k]);
-          }
+          if constexpr (kStream) umma_commit_pair(&ctl->h_empty[hs]);
           if (last) umma_commit(&ctl->d_full[db]);
         }
         __syncwarp();
@@ -573,10 +564,8 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
           dp ^= db ^ 1u;  // after both sets
         }
         if (++slot == kASlots) slot = 0, ap ^= 1u;
-        if constexpr (kStream) {
-          hs += kUnits;
-          if (hs >= (uint32_t)p.hslots) hs = 0, hp ^= 1u;
-        }
+        if constexpr (kStream)
+          if (++hs == (uint32_t)p.hslots) hs = 0, hp ^= 1u;
       }
     }
     if (leader) {  // every issued MMA has finished before tensor memory is released
@@ -787,8 +776,8 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
   p.wide_scales = repeat == 1 && p.ngroups % p.seg_words == 0 && aligned16(a.scales) && aligned16(a.biases);
   static_assert(kMaxStages % kGroups == 0 && kMinStages % kGroups == 0, "weight ring");
   const int fixed = kCtlBytes, stage = stage_bytes(kBits);
-  p.hslots = kStream ? std::min(kMaxH, (kSmemLimit - fixed - kMinStages * stage) / kHUnit) / kUnits * kUnits : 0;
-  const int h_bytes = (kStream ? p.hslots : p.units) * kHUnit;
+  p.hslots = kStream ? std::min(kMaxH, (kSmemLimit - fixed - kMinStages * stage) / (kUnits * kHUnit)) : 0;
+  const int h_bytes = (kStream ? p.hslots : p.segs) * kUnits * kHUnit;
   p.stages = std::min(kMaxStages, (kSmemLimit - fixed - h_bytes) / stage) / kGroups * kGroups;
   p.image = static_cast<const uint8_t*>(workspace);
   const int smem = p.stages * stage + h_bytes + fixed + 1024;
