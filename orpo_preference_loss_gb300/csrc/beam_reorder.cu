@@ -2,14 +2,18 @@
 //
 //   state[o, b, k, r, t, :] <- state[o, b, parent[b, k], r, t, :]   for t < length[b]
 //
-// One thread owns the same unit of a (slab, entry, row) in all beams of the entry: it reads every
-// moved beam's source before it writes any, and no other thread touches that unit, so the parents
-// may form any map (cycles, many children) without a second buffer.  A unit that several beams take is
-// asked for several times by one thread, of which L1 makes one.  The unit is the widest of 16, 8, 4,
-// 2 or 1 bytes that the address and the two byte strides allow.  Above 16 beams a thread's units would not
-// fit its registers: there a CTA takes kTile units of all moved beams through shared memory.
-// Bound by the bytes moved, so each CTA stays with one (slab, entry, row) for up to kMaxPer units, with 16
-// loads of a thread in flight, and reads the parents once: one unit per thread and CTA cost a
+// Units that start on 4, 8 or 16 bytes, in pieces of as many: one thread owns the same piece of a (slab, entry, row)
+// in all beams of the entry: it reads every moved beam's source before it writes any, and no other thread touches
+// those, so the parents may form any map (cycles, many children) without a second buffer.  A source that several
+// beams take is asked for several times by one thread, of which L1 makes one.  Above 8 beams a thread's sources
+// would leave too few threads their registers: there a CTA takes kTile pieces of all moved beams through shared memory
+// (9 beams, 114 MB: 30 us; with 16 sources in registers 35).
+// Units of any other size: beams start at any byte.  A CTA takes a window of a (slab, entry, row) through shared
+// memory; each source lies there as far from a 16-byte boundary as in memory, and what goes out is put together for
+// the destination's own boundaries by funnel shifts, so that all but the ends moves 16 bytes at a time (bf16 heads of
+// 33, 6 beams, 254 MB: 77 us; in pieces of 2 bytes 91.  Heads of 36 in pieces of 8 bytes: 64, and by bytes 78).
+// Bound by the bytes moved, so each CTA stays with one (slab, entry, row) for up to kMaxPer pieces, with 16
+// loads of a thread in flight, and reads the parents once: one piece per thread and CTA cost a
 // quarter of the rate.
 #include <algorithm>
 
@@ -27,16 +31,27 @@ struct ReorderArgs {
   int64_t outer, batch, rows, capacity, unit;
   int beams;
   int32_t* status;
-  int64_t per;  // units per CTA
+  int64_t per;  // 16-byte pieces (other units: bytes) per CTA
 };
 
 constexpr int kThreads = 256;
 
+// A CTA's (slab, entry, row), of at most 2^30.
+struct Run {
+  uint32_t o, b, row;
+  __device__ __forceinline__ explicit Run(const ReorderArgs& a) {
+    const uint32_t ob = blockIdx.x / (uint32_t)a.rows;
+    row = blockIdx.x - ob * (uint32_t)a.rows;
+    o = ob / (uint32_t)a.batch;
+    b = ob - o * (uint32_t)a.batch;
+  }
+};
+
 template <class T, int KB>
 __global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderArgs a) {
   constexpr int kUnroll = KB <= 8 ? 16 / KB : 1;  // units of a thread in flight per beam
-  const int64_t run = blockIdx.x;                 // (slab, entry, row)
-  const int64_t row = run % a.rows, ob = run / a.rows, b = ob % a.batch, o = ob / a.batch;
+  const Run run(a);
+  const int64_t row = run.row, b = run.b, o = run.o;
   __shared__ int par[KB];
   const int64_t len = a.length ? (int64_t)a.length[b] : a.capacity;
   const int64_t used = len * a.unit / (int64_t)sizeof(T);
@@ -78,86 +93,161 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderArgs a) {
 // Any number of beams: kTile units of every moved beam's source into shared memory, then out.
 constexpr int kTile = 128;
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) reorder_tile_kernel(ReorderArgs a) {
-  extern __shared__ __align__(16) uint8_t tile_raw[];
-  T* const tile = reinterpret_cast<T*>(tile_raw);  // [moved][kTile]
-  const int64_t run = blockIdx.x;
-  const int64_t row = run % a.rows, ob = run / a.rows, b = ob % a.batch, o = ob / a.batch;
-  __shared__ int from[ORPO_MAX_BEAMS], to[ORPO_MAX_BEAMS], moved;
-  const int64_t len = a.length ? (int64_t)a.length[b] : a.capacity;
-  const int64_t used = len * a.unit / (int64_t)sizeof(T);
-  const int64_t begin = (int64_t)blockIdx.y * a.per, end = min(begin + a.per, used);
+// The moved beams of an entry, in any order; false (for the whole CTA) on a bad parent or length.
+struct Moves {
+  int from[ORPO_MAX_BEAMS], to[ORPO_MAX_BEAMS], n;
+};
+__device__ __forceinline__ bool find_moves(const ReorderArgs& a, int64_t b, int64_t len, Moves& m) {
   bool bad = len < 0 || len > a.capacity;
-  if (threadIdx.x == 0) moved = 0;
+  if (threadIdx.x == 0) m.n = 0;
   __syncthreads();
   if (threadIdx.x < a.beams) {
     const int k = threadIdx.x, p = a.parent[b * a.ld_parent + k];
     bad |= p < 0 || p >= a.beams;
     if (p != k) {
-      const int j = atomicAdd(&moved, 1);  // their order does not matter
-      from[j] = p, to[j] = k;
+      const int j = atomicAdd(&m.n, 1);
+      m.from[j] = p, m.to[j] = k;
     }
   }
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) atomicOr(a.status, ORPO_STATUS_PARENT);
-    return;
-  }
+  if (!__syncthreads_or(bad)) return true;
+  if (threadIdx.x == 0) atomicOr(a.status, ORPO_STATUS_PARENT);
+  return false;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) reorder_tile_kernel(ReorderArgs a) {
+  extern __shared__ __align__(16) uint8_t tile_raw[];
+  T* const tile = reinterpret_cast<T*>(tile_raw);  // [moved][kTile]
+  __shared__ Moves moves;
+  const Run run(a);
+  const int64_t row = run.row, b = run.b, o = run.o;
+  const int64_t len = a.length ? (int64_t)a.length[b] : a.capacity;
+  const int64_t used = len * a.unit / (int64_t)sizeof(T);
+  const int64_t begin = (int64_t)blockIdx.y * a.per, end = min(begin + a.per, used);
+  if (!find_moves(a, b, len, moves)) return;
   const int64_t beam_units = a.rows * a.capacity * a.unit / (int64_t)sizeof(T);
   T* base = reinterpret_cast<T*>(a.state) + (o * a.batch + b) * a.beams * beam_units +
             row * (a.capacity * a.unit / (int64_t)sizeof(T));
-  const int n = moved * kTile;
+  const int n = moves.n * kTile;
   for (int64_t i = begin; i < end; i += kTile) {
 #pragma unroll 4
     for (int j = threadIdx.x; j < n; j += kThreads)
-      if (i + j % kTile < end) tile[j] = base[from[j / kTile] * beam_units + i + j % kTile];
+      if (i + j % kTile < end) tile[j] = base[moves.from[j / kTile] * beam_units + i + j % kTile];
     __syncthreads();  // every beam's units are read
 #pragma unroll 4
     for (int j = threadIdx.x; j < n; j += kThreads)
-      if (i + j % kTile < end) base[to[j / kTile] * beam_units + i + j % kTile] = tile[j];
+      if (i + j % kTile < end) base[moves.to[j / kTile] * beam_units + i + j % kTile] = tile[j];
     __syncthreads();
   }
 }
 
-constexpr int64_t kMaxPer = 8192;  // units per CTA at most
-constexpr int64_t kMinPer = 512;   // and at least, where a run has as many
+// Units of any size.  Windows of `window` bytes (a multiple of 16) of every moved beam.
+__global__ void __launch_bounds__(kThreads) reorder_bytes_kernel(ReorderArgs a, int window) {
+  extern __shared__ __align__(16) uint8_t tile_raw[];  // [moved][window + 32]: bytes from the boundary before the source on
+  __shared__ Moves moves;
+  const Run run(a);
+  const int64_t len = a.length ? (int64_t)a.length[run.b] : a.capacity;
+  const int64_t used = len * a.unit;
+  const int64_t begin = (int64_t)blockIdx.y * a.per, end = min(begin + a.per, used);
+  if (!find_moves(a, run.b, len, moves)) return;
+  const int64_t run_bytes = a.capacity * a.unit, beam_bytes = a.rows * run_bytes;
+  uint8_t* const base = a.state + ((int64_t)run.o * a.batch + run.b) * a.beams * beam_bytes + run.row * run_bytes;
+  const uint32_t chunks = (uint32_t)window / 16, n = moves.n * chunks, ends = moves.n * 32;
+  const int pitch = window + 32;
+  for (int64_t w0 = begin; w0 < end; w0 += window) {
+    const int size = (int)min((int64_t)window, end - w0);
+    // of the bytes [p, p + size): those before the first boundary, and whole 16-byte chunks
+    auto head_of = [&](const uint8_t* p) { return min(size, (int)(-reinterpret_cast<uintptr_t>(p) & 15u)); };
+    // byte e (0..31) of a beam's ends: its place in the window, or -1
+    auto end_byte = [&](int head, int e) {
+      const int tail = head + (size - head) / 16 * 16 + e - 16;
+      return e < 16 ? (e < head ? e : -1) : tail < size ? tail : -1;
+    };
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+      const uint32_t j = i / chunks, c = i - j * chunks;
+      const uint8_t* const src = base + moves.from[j] * beam_bytes + w0;
+      const int at = head_of(src) + (int)c * 16;
+      if (at + 16 <= size)
+        *reinterpret_cast<uint4*>(tile_raw + j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u) + at) =
+            *reinterpret_cast<const uint4*>(src + at);
+    }
+    for (uint32_t i = threadIdx.x; i < ends; i += kThreads) {
+      const uint32_t j = i / 32;
+      const uint8_t* const src = base + moves.from[j] * beam_bytes + w0;
+      const int at = end_byte(head_of(src), (int)(i & 31u));
+      if (at >= 0) tile_raw[j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u) + at] = src[at];
+    }
+    __syncthreads();  // every beam's window is read
+#pragma unroll 2
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+      const uint32_t j = i / chunks, c = i - j * chunks;
+      const uint8_t* const src = base + moves.from[j] * beam_bytes + w0;
+      uint8_t* const dst = base + moves.to[j] * beam_bytes + w0;
+      const int at = head_of(dst) + (int)c * 16;
+      if (at + 16 <= size) {
+        const uint32_t off = j * pitch + (uint32_t)(reinterpret_cast<uintptr_t>(src) & 15u) + at, shift = (off & 3u) * 8;
+        const uint32_t* const w = reinterpret_cast<const uint32_t*>(tile_raw) + off / 4;  // 5 words: inside the slot's slack
+        uint32_t x[5];
+#pragma unroll
+        for (int e = 0; e < 5; ++e) x[e] = w[e];
+        *reinterpret_cast<uint4*>(dst + at) = make_uint4(__funnelshift_r(x[0], x[1], shift), __funnelshift_r(x[1], x[2], shift),
+                                                         __funnelshift_r(x[2], x[3], shift), __funnelshift_r(x[3], x[4], shift));
+      }
+    }
+    for (uint32_t i = threadIdx.x; i < ends; i += kThreads) {
+      const uint32_t j = i / 32;
+      const uint8_t* const src = base + moves.from[j] * beam_bytes + w0;
+      uint8_t* const dst = base + moves.to[j] * beam_bytes + w0;
+      const int at = end_byte(head_of(dst), (int)(i & 31u));
+      if (at >= 0) dst[at] = tile_raw[j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u) + at];
+    }
+    __syncthreads();
+  }
+}
 
-template <class T, int KB>  // KB = 0: any number of beams
-cudaError_t launch_kb(const ReorderArgs& a, int sms, cudaStream_t st) {
+constexpr int64_t kMaxPer = 8192;  // pieces per CTA at most
+constexpr int64_t kMinPer = 512;   // and at least, where a run has as many
+constexpr int kBytesSmem = 36 << 10;
+
+// Piece: uint4, uint2, uint32_t, or uint8_t for the kernel of any units (in 16-byte chunks)
+template <class Piece>
+cudaError_t launch(const ReorderArgs& a, int sms, cudaStream_t st) {
+  constexpr bool kBytes = sizeof(Piece) == 1;
+  constexpr int64_t kPiece = kBytes ? 16 : sizeof(Piece);
   // slabs in launches of at most 2^30 runs
   const int64_t runs = a.batch * a.rows;
   const int64_t slabs = std::max<int64_t>(1, (1ll << 30) / runs);
   const int64_t slab_bytes = a.batch * a.beams * a.rows * a.capacity * a.unit;
-  const int64_t units = a.capacity * a.unit / (int64_t)sizeof(T);
+  const int64_t pieces = cdiv(a.capacity * a.unit, kPiece);
+  const int window = std::min(4096, kBytesSmem / a.beams / 16 * 16 - 32);  // at least 544
   for (int64_t o = 0; o < a.outer; o += slabs) {
     ReorderArgs c = a;
     c.state = a.state + o * slab_bytes;
     c.outer = std::min(slabs, a.outer - o);
     // about sixteen CTAs per SM, but at most 65535 per run
-    const int64_t want = cdiv(units * c.outer * runs, (int64_t)sms * 16);
-    const int64_t per = std::max(std::min(kMaxPer, std::max(kMinPer, want)), cdiv(units, 65535));
-    c.per = cdiv(per, kThreads) * kThreads;
-    const dim3 grid((unsigned)(c.outer * runs), (unsigned)cdiv(units, c.per));
+    const int64_t want = cdiv(pieces * c.outer * runs, (int64_t)sms * 16);
+    const int64_t per = std::max(std::min(kMaxPer, std::max(kMinPer, want)), cdiv(pieces, 65535));
+    const int64_t step = kBytes ? window / 16 : kThreads;
+    c.per = cdiv(per, step) * step;
+    const dim3 grid((unsigned)(c.outer * runs), (unsigned)cdiv(pieces, c.per));
     prof_begin(K_REORDER, st);
-    if constexpr (KB != 0) {
-      reorder_kernel<T, KB><<<grid, kThreads, 0, st>>>(c);
+    if constexpr (kBytes) {
+      c.per *= 16;
+      reorder_bytes_kernel<<<grid, kThreads, (size_t)a.beams * (window + 32), st>>>(c, window);
+    } else if (a.beams <= 4) {
+      reorder_kernel<Piece, 4><<<grid, kThreads, 0, st>>>(c);
+    } else if (a.beams <= 8) {
+      reorder_kernel<Piece, 8><<<grid, kThreads, 0, st>>>(c);
     } else {
       static std::atomic<int> done[64];
-      if (cudaError_t e = opt_in_smem(reorder_tile_kernel<T>, ORPO_MAX_BEAMS * kTile * (int)sizeof(T), done)) return e;
-      reorder_tile_kernel<T><<<grid, kThreads, a.beams * kTile * sizeof(T), st>>>(c);
+      if (cudaError_t e = opt_in_smem(reorder_tile_kernel<Piece>, ORPO_MAX_BEAMS * kTile * (int)sizeof(Piece), done)) return e;
+      reorder_tile_kernel<Piece><<<grid, kThreads, a.beams * kTile * sizeof(Piece), st>>>(c);
     }
     prof_end(K_REORDER, st);
     if (cudaError_t e = cudaGetLastError()) return e;
   }
   return cudaSuccess;
-}
-
-template <class T>
-cudaError_t launch(const ReorderArgs& a, int sms, cudaStream_t st) {
-  if (a.beams <= 4) return launch_kb<T, 4>(a, sms, st);
-  if (a.beams <= 8) return launch_kb<T, 8>(a, sms, st);
-  if (a.beams <= 16) return launch_kb<T, 16>(a, sms, st);
-  return launch_kb<T, 0>(a, sms, st);
 }
 
 // product of non-negative sizes, or -1 when it reaches 2^62
@@ -199,7 +289,6 @@ extern "C" int orpo_beam_reorder(void* state, const int32_t* parent, int64_t ld_
   const cudaError_t e = al % 16 == 0  ? launch<uint4>(a, sms, st)
                         : al % 8 == 0 ? launch<uint2>(a, sms, st)
                         : al % 4 == 0 ? launch<uint32_t>(a, sms, st)
-                        : al % 2 == 0 ? launch<uint16_t>(a, sms, st)
                                       : launch<uint8_t>(a, sms, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
 }

@@ -87,7 +87,9 @@ struct TcArgs {
   int stages;             // weight ring
   int hslots;             // streamed h: segments in the ring
   const uint8_t* image;   // streamed h: [m tiles][units] units as shared memory holds them
-  int wide_scales;        // a segment's scales and biases are one aligned word of up to 16 bytes
+  int word_groups;        // a scale word is a group (and its index that of the group)
+  int wide_scales;        // and a segment's scales and biases are one aligned word of up to 16 bytes each
+  int prefetch_scales;    // they start on 16 bytes
 };
 
 // One wait of up to kPollNs in the barrier unit: the polls of eight waiting warps at the default
@@ -252,7 +254,7 @@ __device__ __forceinline__ uint32_t group_of(const TcArgs& p, uint32_t word) {
 __device__ __forceinline__ void prefetch_scales(const TcArgs& p, int64_t tile, int lane) {
   const LogitsArgs& a = p.a;
   const uint32_t bytes = (uint32_t)(p.rows * 2) * p.ngroups;  // a multiple of 16: p.rows is one of 8
-  if (p.wide_scales && (lane == 0 || lane == 1) && (tile + 1) * p.rows <= a.V)
+  if (p.prefetch_scales && (lane == 0 || lane == 1) && (tile + 1) * p.rows <= a.V)
     l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + tile * bytes, bytes);
 }
 
@@ -264,8 +266,9 @@ struct ScaleRole {
   uint32_t sring;
   int my_tiles, row0, lane;
 
-  // W: words per segment, their groups' scales and biases aligned vectors; 0: any number, element by element
-  template <int W>
+  // W: words per segment, a group each, or 0: any number, groups repeated; kWide: loaded as one vector, else element by
+  // element
+  template <int W, bool kWide>
   __device__ __forceinline__ void run() const {
     constexpr int kWords = W ? W : kSegK / 32, kPairs = (kWords + 1) / 2;
     const LogitsArgs& a = p.a;
@@ -289,7 +292,14 @@ struct ScaleRole {
       const int g0 = W ? seg * W : (int)group_of(p, (uint32_t)(seg * p.seg_words));
       const uint16_t *sr = s + g0, *br = b + g0;
       if (row < a.V) {
-        if constexpr (W == 8) {
+        if constexpr (W > 1 && !kWide) {
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+            if (g0 + i < p.ngroups) {
+              x.sc[i / 2] |= (uint32_t)__ldg(sr + i) << (16 * (i & 1));
+              x.bi[i / 2] |= (uint32_t)__ldg(br + i) << (16 * (i & 1));
+            }
+        } else if constexpr (W == 8) {
           const uint4 u = __ldg(reinterpret_cast<const uint4*>(sr)), v = __ldg(reinterpret_cast<const uint4*>(br));
           x.sc[0] = u.x, x.sc[1] = u.y, x.sc[2] = u.z, x.sc[3] = u.w;
           x.bi[0] = v.x, x.bi[1] = v.y, x.bi[2] = v.z, x.bi[3] = v.w;
@@ -577,16 +587,16 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
   } else if (warp < kSumWarp) {
     // ---- scales and biases
     const ScaleRole<kSegK> role{p, ctl, smem_u32(sring), my_tiles, (warp - kScaleWarp) * 32, lane};
-    if (kBits == 4 && p.wide_scales && p.seg_words == 8)
-      role.template run<kSegK / 32>();
-    else if (p.wide_scales && p.seg_words == 4)
-      role.template run<4>();
-    else if (p.wide_scales && p.seg_words == 2)
-      role.template run<2>();
-    else if (p.wide_scales && p.seg_words == 1)
-      role.template run<1>();
+    if (!p.word_groups)
+      role.template run<0, false>();
+    else if (kBits == 4 && p.seg_words == 8)
+      p.wide_scales ? role.template run<kSegK / 32, true>() : role.template run<kSegK / 32, false>();
+    else if (p.seg_words == 4)
+      p.wide_scales ? role.template run<4, true>() : role.template run<4, false>();
+    else if (p.seg_words == 2)
+      p.wide_scales ? role.template run<2, true>() : role.template run<2, false>();
     else
-      role.template run<0>();
+      role.template run<1, true>();
   } else if (warp < kFirstDequantWarp) {
     // ---- sums and output
     const int q = warp & 3, n0 = (warp - kSumWarp) / 4 * kCols;
@@ -773,7 +783,9 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
   p.seg_words = (kSegK / 32) >> p.shift;
   const uint32_t repeat = (uint32_t)(per >> p.shift);  // words per group
   p.gmul = repeat > 1 ? (uint32_t)(((1ull << 32) + repeat - 1) / repeat) : 0u;
-  p.wide_scales = repeat == 1 && p.ngroups % p.seg_words == 0 && aligned16(a.scales) && aligned16(a.biases);
+  p.word_groups = repeat == 1;
+  p.prefetch_scales = aligned16(a.scales) && aligned16(a.biases);
+  p.wide_scales = p.word_groups && p.ngroups % p.seg_words == 0 && p.prefetch_scales;
   static_assert(kMaxStages % kGroups == 0 && kMinStages % kGroups == 0, "weight ring");
   const int fixed = kCtlBytes, stage = stage_bytes(kBits);
   p.hslots = kStream ? std::min(kMaxH, (kSmemLimit - fixed - kMinStages * stage) / (kUnits * kHUnit)) : 0;
