@@ -19,6 +19,7 @@
 
 #include "../../include/orpo_decode.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace orpo {
 namespace {
@@ -49,7 +50,9 @@ struct Run {
 
 template <class T, int KB>
 __global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderArgs a) {
-  constexpr int kUnroll = KB <= 8 ? 16 / KB : 1;  // units of a thread in flight per beam
+  constexpr int kUnroll = 16 / KB;  // pieces of a thread in flight per beam
+  grid_trigger();
+  grid_wait();
   const Run run(a);
   const int64_t row = run.row, b = run.b, o = run.o;
   __shared__ int par[KB];
@@ -118,6 +121,8 @@ template <class T>
 __global__ void __launch_bounds__(kThreads) reorder_tile_kernel(ReorderArgs a) {
   extern __shared__ __align__(16) uint8_t tile_raw[];
   T* const tile = reinterpret_cast<T*>(tile_raw);  // [moved][kTile]
+  grid_trigger();
+  grid_wait();
   __shared__ Moves moves;
   const Run run(a);
   const int64_t row = run.row, b = run.b, o = run.o;
@@ -144,6 +149,8 @@ __global__ void __launch_bounds__(kThreads) reorder_tile_kernel(ReorderArgs a) {
 // Units of any size.  Windows of `window` bytes (a multiple of 16) of every moved beam.
 __global__ void __launch_bounds__(kThreads) reorder_bytes_kernel(ReorderArgs a, int window) {
   extern __shared__ __align__(16) uint8_t tile_raw[];  // [moved][window + 32]: bytes from the boundary before the source on
+  grid_trigger();
+  grid_wait();
   __shared__ Moves moves;
   const Run run(a);
   const int64_t len = a.length ? (int64_t)a.length[run.b] : a.capacity;
@@ -232,20 +239,21 @@ cudaError_t launch(const ReorderArgs& a, int sms, cudaStream_t st) {
     c.per = cdiv(per, step) * step;
     const dim3 grid((unsigned)(c.outer * runs), (unsigned)cdiv(pieces, c.per));
     prof_begin(K_REORDER, st);
+    cudaError_t e;
     if constexpr (kBytes) {
       c.per *= 16;
-      reorder_bytes_kernel<<<grid, kThreads, (size_t)a.beams * (window + 32), st>>>(c, window);
+      e = launch_dependent(reorder_bytes_kernel, grid, kThreads, (size_t)a.beams * (window + 32), st, c, window);
     } else if (a.beams <= 4) {
-      reorder_kernel<Piece, 4><<<grid, kThreads, 0, st>>>(c);
+      e = launch_dependent(reorder_kernel<Piece, 4>, grid, kThreads, 0, st, c);
     } else if (a.beams <= 8) {
-      reorder_kernel<Piece, 8><<<grid, kThreads, 0, st>>>(c);
+      e = launch_dependent(reorder_kernel<Piece, 8>, grid, kThreads, 0, st, c);
     } else {
       static std::atomic<int> done[64];
-      if (cudaError_t e = opt_in_smem(reorder_tile_kernel<Piece>, ORPO_MAX_BEAMS * kTile * (int)sizeof(Piece), done)) return e;
-      reorder_tile_kernel<Piece><<<grid, kThreads, a.beams * kTile * sizeof(Piece), st>>>(c);
+      if ((e = opt_in_smem(reorder_tile_kernel<Piece>, ORPO_MAX_BEAMS * kTile * (int)sizeof(Piece), done)) != cudaSuccess) return e;
+      e = launch_dependent(reorder_tile_kernel<Piece>, grid, kThreads, a.beams * kTile * sizeof(Piece), st, c);
     }
     prof_end(K_REORDER, st);
-    if (cudaError_t e = cudaGetLastError()) return e;
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

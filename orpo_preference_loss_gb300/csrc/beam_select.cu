@@ -173,7 +173,8 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) {
   using E = Elems<kBf16>;
   constexpr int kVec = E::kVec, kSize = E::kSize, kN = E::kN;
-  asm volatile("griddepcontrol.launch_dependents;");  // the merge kernel may be set up meanwhile
+  grid_trigger();  // the merge kernel may be set up meanwhile
+  grid_wait();
   const int64_t r = blockIdx.y;
   if (a.finished != nullptr && a.finished[r]) return;
   __shared__ RowShared sh;
@@ -400,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
 
 __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs a) {
   extern __shared__ uint64_t lists[];  // one per warp: the keys of its beam's parts; then values and tokens
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the row kernel's lists are there
+  grid_trigger();
+  grid_wait();  // the row kernel's lists are there
   const int64_t b = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ uint8_t over[ORPO_MAX_BEAMS];
@@ -546,13 +548,11 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
     c.keys = a.keys + r * plan.parts * n;
     c.stats = a.stats + r * plan.parts;
     const dim3 grid((unsigned)plan.parts, (unsigned)std::min<int64_t>(65535, rows - r));
-    if (logits_bf16)
-      select_rows_kernel<true><<<grid, kThreads, 0, st>>>(c);
-    else
-      select_rows_kernel<false><<<grid, kThreads, 0, st>>>(c);
+    const cudaError_t e = logits_bf16 ? launch_dependent(select_rows_kernel<true>, grid, kThreads, 0, st, c)
+                                      : launch_dependent(select_rows_kernel<false>, grid, kThreads, 0, st, c);
+    if (e != cudaSuccess) return ORPO_ERR_CUDA;
   }
   prof_end(K_BEAM, st);
-  if (cudaGetLastError() != cudaSuccess) return ORPO_ERR_CUDA;
   // a warp per beam, as many as their lists fit shared memory (one list: at most 32 KiB)
   const size_t out_bytes = (size_t)beams * n * 8, list_bytes = (size_t)plan.parts * n * 8;
   const int warps = (int)std::min<size_t>({(size_t)kMergeThreads / 32, (size_t)beams, (kMergeSmem - out_bytes) / list_bytes});
@@ -561,18 +561,8 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
   static std::atomic<int> done[64];
   if (opt_in_smem(select_merge_kernel, kMergeSmem, done) != cudaSuccess) return ORPO_ERR_CUDA;
   prof_begin(K_BEAM, st);
-  // launched while the row kernel runs; it waits for it on the device
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)batch);
-  cfg.blockDim = dim3((unsigned)std::max(warps, 4) * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, select_merge_kernel, a);
+  // it may be set up while the row kernel runs
+  const cudaError_t e = launch_dependent(select_merge_kernel, dim3((unsigned)batch), std::max(warps, 4) * 32, smem, st, a);
   prof_end(K_BEAM, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
 }

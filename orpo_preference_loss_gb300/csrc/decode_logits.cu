@@ -28,6 +28,8 @@ constexpr int kRowsTile = 8;
 
 template <int kBits>
 __global__ void __launch_bounds__(256) logits_generic_kernel(LogitsArgs a) {
+  grid_trigger();
+  grid_wait();
   const int lane = threadIdx.x & 31;
   const int64_t v = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int m0 = blockIdx.y * kRowsTile;
@@ -73,11 +75,7 @@ __global__ void __launch_bounds__(256) logits_generic_kernel(LogitsArgs a) {
 
 cudaError_t launch_generic(const LogitsArgs& a, int bits, cudaStream_t st) {
   const dim3 grid((unsigned)cdiv(a.V, 8), (unsigned)cdiv(a.M, kRowsTile));
-  if (bits == 4)
-    logits_generic_kernel<4><<<grid, 256, 0, st>>>(a);
-  else
-    logits_generic_kernel<8><<<grid, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(bits == 4 ? logits_generic_kernel<4> : logits_generic_kernel<8>, grid, 256, 0, st, a);
 }
 
 }  // namespace

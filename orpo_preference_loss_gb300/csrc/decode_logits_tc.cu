@@ -435,17 +435,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     for (int k = part * 32 + lane; k < per_row; k += split * 32)
       f(smem_u32(hbuf) + (k >> 3) * (NP * 128) + m * 128 + (((k ^ m) & 7) << 4), m, k);
   };
-  if constexpr (!kStream) {
-    if (warp >= kSumWarp)
-      each_piece([&](uint32_t at, int m, int k) {
-        if (8 * k < a.d)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(a.h + (int64_t)(m0 + m) * a.ld_h + 8 * k)
-                       : "memory");
-        else
-          st_shared_v4(at, 0u, 0u, 0u, 0u);
-      });
-  }
-  prefetch_scales(p, blockIdx.x, threadIdx.x - 32);  // the same goes for the first tile's scales
+  grid_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 4), mbar_init(&ctl->w_empty[i], 4);
     for (int i = 0; i < kASlots; ++i) mbar_init(&ctl->a_full[i], 4), mbar_init(&ctl->a_empty[i], 1);
@@ -461,6 +451,18 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     tmem_alloc<1>(&ctl->tmem_base, 512);
     tmem_relinquish<1>();
   }
+  if constexpr (!kStream) {
+    grid_wait();  // set up; from here on memory is read (streamed: h's image waits, and this kernel for that one)
+    if (warp >= kSumWarp)
+      each_piece([&](uint32_t at, int m, int k) {
+        if (8 * k < a.d)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(a.h + (int64_t)(m0 + m) * a.ld_h + 8 * k)
+                       : "memory");
+        else
+          st_shared_v4(at, 0u, 0u, 0u, 0u);
+      });
+  }
+  prefetch_scales(p, blockIdx.x, threadIdx.x - 32);  // the same goes for the first tile's scales
   tc_fence_before();
   __syncthreads();
   if constexpr (kStream) cluster_sync();  // the other CTA's barriers exist
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     // ---- streamed h
     if constexpr (kStream) {
       const bool leader = elect_one();
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // the kernel that writes the image is done
+      grid_wait();  // the kernel that writes the image is done
       const uint32_t rank = cluster_ctarank();
       const uint8_t* const image = p.image + (int64_t)blockIdx.y * p.segs * kHSeg + rank * (kHSeg / 2);
       uint32_t it = 0, hs = 0, hp = 1;  // segments issued; slot, parity of its release
@@ -734,8 +736,8 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
 template <int kBits>
 __global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, int blocks, int64_t pieces, uint4* image) {
   // set up while the kernel before it in the stream ends; the products' kernel may be set up once that one has
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
+  grid_wait();
+  grid_trigger();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= pieces) return;
   const int row = (int)(i / 8 % rows);
@@ -799,34 +801,17 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
   auto kernel = logits_tc_kernel<kBits, NP, kStream>;
   if (cudaError_t e = opt_in_smem(kernel, kSmemLimit + 1024, done)) return e;
   const int mt = (int)cdiv(a.M, NP);
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3((unsigned)tc_threads(NP));
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  cfg.attrs = attr;
   if constexpr (kStream) {
     const int blocks = p.units * 2;
     const int64_t pieces = (int64_t)mt * blocks * NP * 8;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t image = {};
-    image.gridDim = dim3((unsigned)cdiv(pieces, 256));
-    image.blockDim = dim3(256);
-    image.stream = st;
-    image.attrs = attr;
-    image.numAttrs = 1;
-    if (cudaError_t e = cudaLaunchKernelEx(&image, h_image_kernel<kBits>, a, NP, blocks, pieces, static_cast<uint4*>(workspace)))
+    if (cudaError_t e = launch_dependent(h_image_kernel<kBits>, dim3((unsigned)cdiv(pieces, 256)), 256, 0, st, a, NP, blocks,
+                                         pieces, static_cast<uint4*>(workspace)))
       return e;
-    cfg.gridDim = dim3((unsigned)std::min((p.tiles + 1) / 2 * 2, slots), (unsigned)mt);
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {2, 1, 1};
-    cfg.numAttrs = 2;  // its weights may come before the image is there
+    return launch_dependent<2>(kernel, dim3((unsigned)std::min((p.tiles + 1) / 2 * 2, slots), (unsigned)mt), tc_threads(NP),
+                               (size_t)smem, st, mw, p);
   } else {
-    cfg.gridDim = dim3((unsigned)std::min(p.tiles, slots), (unsigned)mt);
-    cfg.numAttrs = 0;
+    return launch_dependent(kernel, dim3((unsigned)std::min(p.tiles, slots), (unsigned)mt), tc_threads(NP), (size_t)smem, st, mw, p);
   }
-  return cudaLaunchKernelEx(&cfg, kernel, mw, p);
 }
 
 template <int kBits>

@@ -299,6 +299,12 @@ __host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, int a_mn, i
 
 // ------------------------------------------------------------------ math helpers
 
+// Programmatic dependent launch.  A kernel launched with launch_dependent (internal.h) may start while the kernel before
+// it in the stream still runs: it touches no global memory before grid_wait, which holds until that one is complete
+// and its writes can be seen.  grid_trigger lets the kernel after it start likewise.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
