@@ -67,8 +67,7 @@ struct SelectArgs {
   uint8_t* out_finished;
   uint64_t* keys;  // [rows, parts, n], descending; 0: none
   float2* stats;   // [rows, parts] max, sum of exp(x - max)
-  int parts, chunks;  // parts of a row, chunks of a row
-  int len;            // grid elements of a chunk, a multiple of 256 (the last may be short, or empty)
+  int parts, chunks;  // parts of a row, chunks of a row (the last may be short, or empty)
   int list_warps;     // merge: warps that merge beams
   int32_t* status;
 };
@@ -172,7 +171,7 @@ __device__ __forceinline__ uint64_t key_of(float x, int token) {
 template <bool kBf16>
 __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) {
   using E = Elems<kBf16>;
-  constexpr int kVec = E::kVec, kSize = E::kSize, kN = E::kN;
+  constexpr int kVec = E::kVec, kSize = E::kSize, kN = E::kN, kLen = chunk_of(kBf16);
   grid_trigger();  // the merge kernel may be set up meanwhile
   grid_wait();
   const int64_t r = blockIdx.y;
@@ -188,29 +187,38 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
   float run_m = -INFINITY, run_s = 0.f;
   int have = 0;  // keys in sh.best
   for (int c = c0; c < c1; ++c) {
-    const int64_t e0 = min((int64_t)c * a.len, grid_len), e1 = min(e0 + a.len, grid_len);
+    const int64_t e0 = min((int64_t)c * kLen, grid_len), e1 = min(e0 + kLen, grid_len);
     const int first = (int)(e0 - off) + tid * kVec;  // logit of this thread's element 0
     auto token_of = [&](int i) { return first + i / kVec * (kThreads * kVec) + i % kVec; };
     // ---- load; -inf where there is no logit
     E x;
     const int last = (int)(e1 - off);  // logits of the chunk end here (at most V)
+    if (e0 >= off && e1 - e0 == kLen) {  // a whole chunk
+      const uint4* src = reinterpret_cast<const uint4*>(row + (e0 - off) * kSize) + tid;
 #pragma unroll
-    for (int i = 0; i < kN / kVec; ++i) {
-      const int v = token_of(i * kVec);
-      uint32_t* w = x.w + i * 4;
-      if (v >= 0 && v <= last - kVec) {
-        const uint4 y = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)v * kSize));
-        w[0] = y.x, w[1] = y.y, w[2] = y.z, w[3] = y.w;
-      } else {
+      for (int i = 0; i < kN / kVec; ++i) {
+        const uint4 y = __ldg(src + i * kThreads);
+        x.w[i * 4] = y.x, x.w[i * 4 + 1] = y.y, x.w[i * 4 + 2] = y.z, x.w[i * 4 + 3] = y.w;
+      }
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = E::kNone;
-          if constexpr (kBf16) {
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + v + 2 * j;
-            if (v + 2 * j >= 0 && v + 2 * j < last) w[j] = (w[j] & 0xffff0000u) | __ldg(p);
-            if (v + 2 * j + 1 >= 0 && v + 2 * j + 1 < last) w[j] = (w[j] & 0xffffu) | ((uint32_t)__ldg(p + 1) << 16);
-          } else if (v + j >= 0 && v + j < last) {
-            w[j] = __ldg(reinterpret_cast<const uint32_t*>(row) + v + j);
+      for (int i = 0; i < kN / kVec; ++i) {
+        const int v = token_of(i * kVec);
+        uint32_t* w = x.w + i * 4;
+        if (v >= 0 && v <= last - kVec) {
+          const uint4 y = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)v * kSize));
+          w[0] = y.x, w[1] = y.y, w[2] = y.z, w[3] = y.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[j] = E::kNone;
+            if constexpr (kBf16) {
+              const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + v + 2 * j;
+              if (v + 2 * j >= 0 && v + 2 * j < last) w[j] = (w[j] & 0xffff0000u) | __ldg(p);
+              if (v + 2 * j + 1 >= 0 && v + 2 * j + 1 < last) w[j] = (w[j] & 0xffffu) | ((uint32_t)__ldg(p + 1) << 16);
+            } else if (v + j >= 0 && v + j < last) {
+              w[j] = __ldg(reinterpret_cast<const uint32_t*>(row) + v + j);
+            }
           }
         }
       }
@@ -490,14 +498,13 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
 
 // Chunks of a row, and the parts (CTAs) they are dealt to.
 struct RowPlan {
-  int chunks, parts, len;
+  int chunks, parts;
 };
 RowPlan row_plan(int64_t V, bool bf16, bool aligned) {
   RowPlan p;
   const int64_t grid = V + (aligned ? 0 : 7);  // up to 7 elements of a row's grid lie before it
   p.chunks = (int)cdiv(grid, chunk_of(bf16));
   p.parts = std::min(p.chunks, kMaxParts);
-  p.len = (int)(cdiv(grid, (int64_t)p.chunks * 256) * 256);
   return p;
 }
 
@@ -537,7 +544,7 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
   const int size = logits_bf16 ? 2 : 4;
   const RowPlan plan = row_plan(V, logits_bf16 != 0, aligned16(logits) && (ld_logits * size) % 16 == 0);
   SelectArgs a{logits, ld_logits, score, finished, eos, beams, (int)V, n, out_score, out_parent, out_token,
-               out_finished, static_cast<uint64_t*>(workspace), nullptr, plan.parts, plan.chunks, plan.len, 0, status};
+               out_finished, static_cast<uint64_t*>(workspace), nullptr, plan.parts, plan.chunks, 0, status};
   a.stats = reinterpret_cast<float2*>(a.keys + rows * plan.parts * n);
   // rows in launches of at most 65535
   prof_begin(K_BEAM, st);
