@@ -237,8 +237,9 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
       top = fmaxf(top, vmax[i]);
     }
     // ---- CTA maximum; threshold
-    // warps that hold an element: the grid is dealt out 32 lanes x kVec at a time
-    const int active = max(1, min(kWarps, (int)(e1 - e0 + 32 * kVec - 1) / (32 * kVec)));
+    // Warps all of whose lanes hold an element (the grid is dealt out 32 lanes x kVec at a time): one with a few would
+    // bring the threshold down to its own few.
+    const int active = max(1, min(kWarps, (int)(e1 - e0) / (32 * kVec)));
     const int need = active == kWarps ? (a.n + kWarps - 1) / kWarps : (a.n + active - 1) / active;
     uint32_t rest = ord_of(top), rth = 0, wmax = 0;
     for (int i = 0; i < min(need, 32); ++i) {

@@ -225,3 +225,21 @@ def test_select_of_a_chain_of_finished_rows():
         orpo.orpo_beam_select(logits, score, finished, 7, beams, *out, ws, st)
         assert torch.equal(out[0], score) and torch.all(out[2] == 7) and torch.all(out[3] == 1)
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("tail", [1, 7, 8, 100, 255, 256, 257, 500, 1000, 1800, 1816, 2040, 2047])
+@pytest.mark.parametrize("n", [1, 5, 64])
+@pytest.mark.parametrize("dtype,chunk", [(torch.float32, 8192), (torch.bfloat16, 16384)])
+def test_select_with_a_short_last_chunk(tail, n, dtype, chunk):
+    V, g = 2 * chunk + tail, torch.Generator("cuda").manual_seed(tail)
+    logits = (torch.randn((2, V), generator=g, device=dev()) * 2.5).to(dtype)
+    score, st = torch.zeros((1, 2), device=dev()), status_tensor()
+    out = [torch.empty((1, n), dtype=d, device=dev()) for d in (torch.float32, torch.int32, torch.int32, torch.uint8)]
+    ws = torch.empty(orpo.orpo_beam_select_workspace_bytes(1, 2, V, n), dtype=torch.uint8, device=dev())
+    orpo.orpo_beam_select(logits, score, None, -1, 2, *out, ws, st)
+    x = logits.double().cpu().numpy()
+    ref = oracle.beam_select(x, np.zeros(2), None, -1, 2, n)
+    assert int(st.item()) == 0 and np.max(np.abs(out[0].cpu().numpy() - ref[0])) < 1e-5
+    # where values of different beams are closer than their rounding, their order may differ
+    if ref[4][0] > 1e-5:
+        assert np.array_equal(out[1].cpu().numpy(), ref[1]) and np.array_equal(out[2].cpu().numpy(), ref[2])
