@@ -16,8 +16,10 @@
 // what reaches it (20 to 140 elements for n = 1 to 64 of well-mixed logits) goes to shared memory, and each
 // finds its rank by counting.  Where more than kCap reach it (long runs of equal or sorted logits), the exact
 // n-th largest is found by bisection on the key.
-// Merge kernel: one CTA per entry; a warp per beam merges its parts' sorted lists and statistics, then
-// the beams' sorted proposals are ranked by value.
+// Merge kernel: one CTA per entry merges the parts' sorted lists of every beam, then the beams' sorted proposals.  Up
+// to 8 lists are merged neighbours by neighbours, more by taking the largest of their heads n times, a warp per beam:
+// its warp-wide maxima share one slow unit, which costs 49 clocks a beam and key.  (15 x 14 rows of 12692, n = 28: 13.7 us
+// by neighbours, 21.9 by heads; 4 x 4 rows of 262144, n = 8, 32 parts: 12.2 and 10.4.)
 // Bound by reading the logits (largev, 32 x 8 rows, bf16: 65.7 MB).
 #include <math.h>
 
@@ -37,6 +39,7 @@ constexpr int chunk_of(bool bf16) { return kThreads * kWords * (bf16 ? 2 : 1); }
 constexpr int kCap = 256;                       // candidates of a chunk, one per thread
 constexpr int kMaxParts = 64;                   // parts of a row: two lists per lane of the merging warp
 constexpr int kMergeThreads = 512;
+constexpr int kFewParts = 8;                    // parts of a row that are merged by neighbours; more: by their heads
 constexpr int kMergeSmem = 160 << 10;
 constexpr uint32_t kNinf = 0x007FFFFFu;         // ord_of(-inf); 0 stands for no element
 
@@ -68,15 +71,9 @@ struct SelectArgs {
   uint64_t* keys;  // [rows, parts, n], descending; 0: none
   float2* stats;   // [rows, parts] max, sum of exp(x - max)
   int parts, chunks;  // parts of a row, chunks of a row (the last may be short, or empty)
-  int list_warps;     // merge: warps that merge beams
+  int group, area;    // merge: beams whose lists are merged at a time, keys of an area of them
   int32_t* status;
 };
-
-__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
-  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
-  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
-  return ((uint64_t)hi << 32) | lo;
-}
 
 constexpr int kVecCap = 256;  // vectors with a candidate
 
@@ -408,35 +405,82 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
   if (tid == 0) a.stats[list] = make_float2(run_m, run_s);
 }
 
+// The n largest of each group's lists of n keys (descending, distinct but for the 0 of no key): neighbours are merged,
+// a key's rank being its place in its own list plus the number of the other's that are greater (binary search), until
+// one list is left.  Lists in `from`, in turns to `to`; returns where they end.  (Four at a time, three searches side
+// by side, took 1 to 2 us longer.)
+__device__ __forceinline__ uint64_t* merge_lists(uint64_t* from, uint64_t* to, int groups, int lists, int n) {
+  while (lists > 1) {
+    const int half = (lists + 1) / 2, total = groups * lists * n;
+    for (int t = threadIdx.x; t < total; t += blockDim.x) {
+      const int list = t / n, j = t - list * n, g = list / lists, l = list - g * lists;
+      const uint64_t key = from[t];
+      int rank = j;
+      if ((l ^ 1) < lists) {
+        const uint64_t* const other = from + (g * lists + (l ^ 1)) * n;
+        int lo = 0, hi = n - j;  // further ones do not matter
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (other[mid] > key)
+            lo = mid + 1;
+          else
+            hi = mid;
+        }
+        rank += lo;
+      }
+      if (rank < n) to[(g * half + l / 2) * n + rank] = key;
+    }
+    __syncthreads();
+    uint64_t* const swap = from;
+    from = to, to = swap, lists = half;
+  }
+  return from;
+}
+
+__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// The same for up to kMaxParts lists by a warp per group: n times the largest of the lists' heads, of which a lane holds
+// those of lists lane and lane + 32.
+__device__ __forceinline__ void merge_heads(const uint64_t* from, uint64_t* to, int groups, int lists, int n) {
+  const int lane = threadIdx.x & 31;
+  for (int g = threadIdx.x / 32; g < groups; g += blockDim.x / 32) {
+    const uint64_t* const mine = from + g * lists * n;
+    int h0 = 0, h1 = 0;
+    uint64_t k0 = lane < lists ? mine[lane * n] : 0, k1 = lane + 32 < lists ? mine[(lane + 32) * n] : 0;
+    for (int i = 0; i < n; ++i) {
+      const uint64_t best = warp_max(k0 > k1 ? k0 : k1);
+      if (lane == 0) to[g * n + i] = best;
+      if (best == k0 && k0 != 0) k0 = ++h0 < n ? mine[lane * n + h0] : 0;
+      if (best == k1 && k1 != 0) k1 = ++h1 < n ? mine[(lane + 32) * n + h1] : 0;
+    }
+  }
+  __syncthreads();
+}
+
 __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs a) {
-  extern __shared__ uint64_t lists[];  // one per warp: the keys of its beam's parts; then values and tokens
+  extern __shared__ uint64_t lists[];  // two areas of `area` keys; then tokens [beams, n]
   grid_trigger();
   grid_wait();  // the row kernel's lists are there
   const int64_t b = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, n = a.n;
   __shared__ uint8_t over[ORPO_MAX_BEAMS];
-  float* const value = reinterpret_cast<float*>(lists + (size_t)a.list_warps * a.parts * a.n);  // [beams, n]
-  int* const token = reinterpret_cast<int*>(value + a.beams * a.n);
-  for (int k = warp; warp < a.list_warps && k < a.beams; k += a.list_warps) {
+  __shared__ float beam_score[ORPO_MAX_BEAMS], beam_lse[ORPO_MAX_BEAMS];
+  uint64_t* const area0 = lists;
+  uint64_t* const area1 = lists + a.area;
+  uint64_t* const best = area1 + a.area;  // [beams, n]: value, then beam and place
+  int* const token = reinterpret_cast<int*>(best + a.beams * n);
+  // log-sum-exp of every beam: a warp takes its parts' statistics, at most two per lane
+  for (int k = warp; k < a.beams; k += warps) {
     const int64_t r = b * a.beams + k;
-    const float score = a.score[r];
     const bool ended = a.finished != nullptr && a.finished[r];
-    if (score != score && lane == 0) atomicOr(a.status, ORPO_STATUS_NONFINITE);
-    if (lane == 0) over[k] = ended;
-    if (ended) {
-      for (int i = lane; i < a.n; i += 32) {
-        value[k * a.n + i] = i == 0 && score == score ? score : -INFINITY;
-        token[k * a.n + i] = a.eos;
-      }
-      continue;
-    }
-    uint64_t* const mine = lists + (size_t)warp * a.parts * a.n;
-    const uint64_t* src = a.keys + r * a.parts * a.n;
-    for (int i = lane; i < a.parts * a.n; i += 32) mine[i] = src[i];
-    // log-sum-exp of the parts, at most two per lane
+    const float score = a.score[r];
     const float2 none = make_float2(-INFINITY, 0.f);
-    const float2 s0 = lane < a.parts ? a.stats[r * a.parts + lane] : none;
-    const float2 s1 = lane + 32 < a.parts ? a.stats[r * a.parts + lane + 32] : none;
+    const float2 s0 = !ended && lane < a.parts ? a.stats[r * a.parts + lane] : none;
+    const float2 s1 = !ended && lane + 32 < a.parts ? a.stats[r * a.parts + lane + 32] : none;
     float m = fmaxf(s0.x, s1.x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -448,52 +492,50 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
       for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
       lse = m + logf(s);
     }
-    __syncwarp();
-    // the n largest of the sorted lists: each lane holds the heads of lists lane and lane + 32 (a threshold
-    // and ranks by counting, as in the row kernel, took 1.6 to 2.4 us longer here)
-    int h0 = 0, h1 = 0;
-    uint64_t k0 = lane < a.parts ? mine[lane * a.n] : 0, k1 = lane + 32 < a.parts ? mine[(lane + 32) * a.n] : 0;
-    for (int i = 0; i < a.n; ++i) {
-      const uint64_t best = warp_max(k0 > k1 ? k0 : k1);
-      if (lane == 0) {
-        const float x = ord_to_float((uint32_t)(best >> 32));
-        float y = -INFINITY;
-        if (x > -INFINITY && fabsf(lse) < INFINITY) y = score + (x - lse);
-        value[k * a.n + i] = y == y ? y : -INFINITY;
-        token[k * a.n + i] = (int)~(uint32_t)best;
-      }
-      if (best == k0 && k0 != 0) k0 = ++h0 < a.n ? mine[lane * a.n + h0] : 0;
-      if (best == k1 && k1 != 0) k1 = ++h1 < a.n ? mine[(lane + 32) * a.n + h1] : 0;
+    if (lane == 0) {
+      if (score != score) atomicOr(a.status, ORPO_STATUS_NONFINITE);
+      over[k] = ended, beam_score[k] = score, beam_lse[k] = lse;
     }
   }
   __syncthreads();
-  // Each beam's proposals are in order, so a proposal's rank is its place in its own beam plus, for every
-  // other beam, the number of that beam's proposals that come before it (a binary search).
-  for (int i = threadIdx.x; i < a.beams * a.n; i += blockDim.x) {
-    const int k = i / a.n, j = i - k * a.n;
-    const float v = value[i];
-    int rank = j;
-    for (int q = 0; q < a.beams && rank < a.n; ++q) {
-      if (q == k) continue;
-      // of beam q those with a greater value, or an equal one if q < k
-      int lo = 0, hi = a.n;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        const float w = value[q * a.n + mid];
-        if (q < k ? w >= v : w > v)
-          lo = mid + 1;
-        else
-          hi = mid;
+  // every beam's n largest keys, as many beams at a time as their parts' lists fit, and their values
+  for (int k0 = 0; k0 < a.beams; k0 += a.group) {
+    const int group = min(a.group, a.beams - k0), per_beam = a.parts * n;
+    const uint64_t* const src = a.keys + (b * a.beams + k0) * per_beam;
+#pragma unroll 4
+    for (int t = tid; t < group * per_beam; t += blockDim.x) area0[t] = over[k0 + t / per_beam] ? 0 : src[t];
+    __syncthreads();
+    const uint64_t* top = area1;
+    if (a.parts <= kFewParts)
+      top = merge_lists(area0, area1, group, a.parts, n);
+    else
+      merge_heads(area0, area1, group, a.parts, n);
+    for (int t = tid; t < group * n; t += blockDim.x) {
+      const int k = k0 + t / n, j = t % n;
+      const float score = beam_score[k], lse = beam_lse[k];
+      float y = -INFINITY;
+      if (over[k]) {
+        if (j == 0) y = score;
+      } else {
+        const float x = ord_to_float((uint32_t)(top[t] >> 32));
+        if (x > -INFINITY && fabsf(lse) < INFINITY) y = score + (x - lse);
       }
-      rank += lo;
+      if (y != y) y = -INFINITY;
+      const int at = k * n + j;
+      token[at] = over[k] ? a.eos : (int)~(uint32_t)top[t];
+      best[at] = key_of(y, at);  // of equal values the lower beam first, and within a beam its own order
     }
-    if (rank < a.n) {
-      const int64_t at = b * a.n + rank;
-      a.out_score[at] = v;
-      a.out_parent[at] = k;
-      a.out_token[at] = token[i];
-      if (a.out_finished) a.out_finished[at] = over[k] || token[i] == a.eos;
-    }
+    __syncthreads();
+  }
+  const uint64_t* const top = a.beams > 1 ? merge_lists(best, area0, 1, a.beams, n) : best;
+  for (int i = tid; i < n; i += blockDim.x) {
+    const uint64_t key = top[i];
+    const int from = (int)~(uint32_t)key, k = from / n;
+    const int64_t at = b * n + i;
+    a.out_score[at] = ord_to_float((uint32_t)(key >> 32));
+    a.out_parent[at] = k;
+    a.out_token[at] = token[from];
+    if (a.out_finished) a.out_finished[at] = over[k] || token[from] == a.eos;
   }
 }
 
@@ -545,7 +587,7 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
   const int size = logits_bf16 ? 2 : 4;
   const RowPlan plan = row_plan(V, logits_bf16 != 0, aligned16(logits) && (ld_logits * size) % 16 == 0);
   SelectArgs a{logits, ld_logits, score, finished, eos, beams, (int)V, n, out_score, out_parent, out_token,
-               out_finished, static_cast<uint64_t*>(workspace), nullptr, plan.parts, plan.chunks, 0, status};
+               out_finished, static_cast<uint64_t*>(workspace), nullptr, plan.parts, plan.chunks, 0, 0, status};
   a.stats = reinterpret_cast<float2*>(a.keys + rows * plan.parts * n);
   // rows in launches of at most 65535
   prof_begin(K_BEAM, st);
@@ -561,16 +603,17 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
     if (e != cudaSuccess) return ORPO_ERR_CUDA;
   }
   prof_end(K_BEAM, st);
-  // a warp per beam, as many as their lists fit shared memory (one list: at most 32 KiB)
-  const size_t out_bytes = (size_t)beams * n * 8, list_bytes = (size_t)plan.parts * n * 8;
-  const int warps = (int)std::min<size_t>({(size_t)kMergeThreads / 32, (size_t)beams, (kMergeSmem - out_bytes) / list_bytes});
-  const size_t smem = warps * list_bytes + out_bytes;
-  a.list_warps = warps;
+  // as many beams' lists at a time as fit shared memory twice, beside every beam's n best and their tokens
+  const int per_beam = plan.parts * n, bests = beams * n;
+  a.group = std::min(beams, (int)((kMergeSmem - bests * 12) / (per_beam * 16)));  // at least 1: 16 * 4096 bytes of 112 KiB
+  a.area = std::max(a.group * per_beam, bests);  // the beams' own lists are merged there too
+  const size_t smem = (size_t)a.area * 16 + (size_t)bests * 12;
   static std::atomic<int> done[64];
   if (opt_in_smem(select_merge_kernel, kMergeSmem, done) != cudaSuccess) return ORPO_ERR_CUDA;
   prof_begin(K_BEAM, st);
   // it may be set up while the row kernel runs
-  const cudaError_t e = launch_dependent(select_merge_kernel, dim3((unsigned)batch), std::max(warps, 4) * 32, smem, st, a);
+  const int threads = std::min(kMergeThreads, std::max(128, (int)cdiv(a.group * per_beam, 32) * 32));
+  const cudaError_t e = launch_dependent(select_merge_kernel, dim3((unsigned)batch), threads, smem, st, a);
   prof_end(K_BEAM, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
 }
