@@ -48,8 +48,8 @@ extern "C" {
  * for bit.
  * Meant for few rows: the quantised weights are read once per 64 rows of h.
  * Workspace: orpo_head_logits_q_workspace_bytes(M, d, bits) bytes, 16-byte aligned; 0 (workspace may be
- * NULL) for up to 16 rows that fit on chip (d <= 3328), else about 2 M d: a copy of h in the order the
- * kernel takes it.
+ * NULL) where h fits on chip (up to 16 rows of d <= 3328, 32 of d <= 1536, 64 or passes of 64 of d <= 768), else
+ * about 2 M d: a copy of h in the order the kernel takes it.
  * Limits: 0 <= M <= 2^31 - 2^16, 1 <= V <= 2^31 - 2^16, 8 <= d < 2^20, d a multiple of 8.
  */
 size_t orpo_head_logits_q_workspace_bytes(int64_t M, int64_t d, int bits);

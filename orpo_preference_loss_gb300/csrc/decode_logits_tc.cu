@@ -32,7 +32,7 @@
 //
 // Order of k: 4-bit dequantisation yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights
 // (8-bit: (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes at a
-// time.  Up to 16 rows of h that fit beside the weights (d up to 3328) are loaded and put in that order by
+// time.  Rows of h that fit beside the weights (16 of d up to 3328, 64 of 768) are loaded and put in that order by
 // each CTA, once.  More are streamed: a small kernel first writes h in that order, and as
 // shared memory holds it, to the workspace, and the CTAs work in pairs (clusters) on neighbouring tiles,
 // each fetching half of every segment of h for both (multicast), since h crosses from L2 once per tile: at 64
@@ -255,6 +255,34 @@ __device__ __forceinline__ uint32_t group_of(const TcArgs& p, uint32_t word) {
   return p.gmul ? __umulhi(word, p.gmul) : word;
 }
 
+// W values from any address: the aligned 8-byte words (W = 2: 4-byte ones) that hold them, and, once they are there, the
+// values put together.  Reads less than a word before and past them.
+template <int W>
+struct Shifted {
+  static constexpr int kWord = W > 2 ? 8 : 4, n = W * 2 / kWord, kWords = (n + 1) * kWord / 4;
+  static __device__ __forceinline__ void load(const uint16_t* p, uint32_t (&w)[kWords]) {
+    const uint32_t s = (uint32_t)reinterpret_cast<uintptr_t>(p) & (kWord - 1);
+    const uint8_t* const q = reinterpret_cast<const uint8_t*>(p) - s;
+#pragma unroll
+    for (int i = 0; i <= n; ++i) {
+      if constexpr (kWord == 8) {
+        uint2 v = make_uint2(0u, 0u);
+        if (i < n || s != 0) v = __ldg(reinterpret_cast<const uint2*>(q) + i);
+        w[2 * i] = v.x, w[2 * i + 1] = v.y;
+      } else {
+        w[i] = i < n || s != 0 ? __ldg(reinterpret_cast<const uint32_t*>(q) + i) : 0u;
+      }
+    }
+  }
+  static __device__ __forceinline__ void take(const uint32_t (&w)[kWords], uint32_t s, uint32_t (&out)[W / 2]) {
+    uint32_t t[W / 2 + 1];
+#pragma unroll
+    for (int i = 0; i <= W / 2; ++i) t[i] = kWord == 8 && (s & 4) ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) out[i] = __funnelshift_r(t[i], t[i + 1], (s & 2) * 8);
+  }
+};
+
 // The rows' scales and biases of a tile, contiguous, to L2, by the two threads with lane 0 and 1.
 __device__ __forceinline__ void prefetch_scales(const TcArgs& p, int64_t tile, int lane) {
   const LogitsArgs& a = p.a;
@@ -271,20 +299,22 @@ struct ScaleRole {
   uint32_t sring;
   int my_tiles, row0, lane;
 
-  // W: words per segment, a group each, or 0: any number, groups repeated; kWide: loaded as one vector, else element by
-  // element
+  // W: words per segment, a group each, or 0: any number, groups repeated; kWide: loaded as one vector, else from any
+  // address (24 rows, d 3232, V 96333, 101 groups a row: 58 us; element by element 69)
   template <int W, bool kWide>
   __device__ __forceinline__ void run() const {
-    constexpr int kWords = W ? W : kSegK / 32, kPairs = (kWords + 1) / 2;
+    constexpr bool kShift = W > 1 && !kWide;
+    constexpr int kWords = W ? W : kSegK / 32, kPairs = (kWords + 1) / 2, kRaw = kShift ? Shifted<W < 2 ? 2 : W>::kWords : kPairs;
     const LogitsArgs& a = p.a;
     struct Set {
-      uint32_t sc[kPairs], bi[kPairs];  // the groups of the segment, in pairs
+      uint32_t sc[kRaw], bi[kRaw];  // the groups of the segment, in pairs, or what holds them
+      uint32_t shift;               // kShift: bytes that they start after their word
     };
     // the next fetch: its segment, its tile's row that is mine, and where the row's scales and biases are
     int seg = 0;
     int64_t row = (int64_t)blockIdx.x * p.rows + row0 + lane, ahead = (int64_t)blockIdx.x + gridDim.x;
     const uint16_t *s, *b;
-    // Scales are fetched two segments ahead, which covers the way from L2 and not from memory.
+    // Scales are fetched two segments ahead, which covers the way from L2 and not from memory.  (Four ahead spilled.)
     auto enter_tile = [&]() {
       s = a.scales + row * p.ngroups;
       b = a.biases + row * p.ngroups;
@@ -293,17 +323,25 @@ struct ScaleRole {
     };
     auto fetch = [&](Set& x) {
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) x.sc[i] = x.bi[i] = 0;
+      for (int i = 0; i < kRaw; ++i) x.sc[i] = x.bi[i] = 0;
+      x.shift = 0;
       const int g0 = W ? seg * W : (int)group_of(p, (uint32_t)(seg * p.seg_words));
       const uint16_t *sr = s + g0, *br = b + g0;
       if (row < a.V) {
-        if constexpr (W > 1 && !kWide) {
+        if constexpr (kShift) {
+          // (the row's first group + g0 + W, and the slack of a shifted load, stay inside the arrays)
+          if (p.prefetch_scales && row * p.ngroups + g0 + W + 4 <= (int64_t)a.V * p.ngroups) {
+            x.shift = (uint32_t)reinterpret_cast<uintptr_t>(sr) & (Shifted<W>::kWord - 1);  // both arrays start on 16 bytes
+            Shifted<W>::load(sr, x.sc);
+            Shifted<W>::load(br, x.bi);
+          } else {
 #pragma unroll
-          for (int i = 0; i < W; ++i)
-            if (g0 + i < p.ngroups) {
-              x.sc[i / 2] |= (uint32_t)__ldg(sr + i) << (16 * (i & 1));
-              x.bi[i / 2] |= (uint32_t)__ldg(br + i) << (16 * (i & 1));
-            }
+            for (int i = 0; i < W; ++i)
+              if (g0 + i < p.ngroups) {
+                x.sc[i / 2] |= (uint32_t)__ldg(sr + i) << (16 * (i & 1));
+                x.bi[i / 2] |= (uint32_t)__ldg(br + i) << (16 * (i & 1));
+              }
+          }
         } else if constexpr (W == 8) {
           const uint4 u = __ldg(reinterpret_cast<const uint4*>(sr)), v = __ldg(reinterpret_cast<const uint4*>(br));
           x.sc[0] = u.x, x.sc[1] = u.y, x.sc[2] = u.z, x.sc[3] = u.w;
@@ -332,22 +370,38 @@ struct ScaleRole {
       }
     };
     uint32_t stage = 0, ph = 0;
+    int at = 0;  // the segment to put
     auto put = [&](const Set& x) {
       if (!wait_warp(ctl, &ctl->w_empty[stage], ph ^ 1u, a.status)) return false;
       const uint32_t out = sring + stage * scale_bytes(1024 / kSegK) + (row0 + lane) * 4;
+      uint32_t sc[kPairs], bi[kPairs];
+      if constexpr (kShift) {
+        Shifted<W>::take(x.sc, x.shift, sc);
+        Shifted<W>::take(x.bi, x.shift, bi);
+        if (++at == p.segs) {
+          const int own = p.ngroups - (p.segs - 1) * W;  // groups of the row's last segment; then come the next row's
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+            if (i >= own) sc[i / 2] &= i & 1 ? 0xffffu : 0u, bi[i / 2] &= i & 1 ? 0xffffu : 0u;
+          at = 0;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) sc[i] = x.sc[i], bi[i] = x.bi[i];
+      }
       uint32_t big[kPairs], odd = 0;  // times 2^133; odd: NaN where one is infinite or NaN, else 0
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        big[i] = bf16x2_mul(bf16x2_mul(x.sc[i], 0x7F007F00u), 0x42804280u);  // 2^127, 2^6
+        big[i] = bf16x2_mul(bf16x2_mul(sc[i], 0x7F007F00u), 0x42804280u);  // 2^127, 2^6
         odd = bf16x2_fma(big[i], 0u, odd);
       }
       const bool plain = __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        const uint32_t v = plain ? x.sc[i] : big[i];
-        if (W || 2 * i < p.seg_words) sts32(out + 2 * i * (kTileRows * 4), __byte_perm(v, x.bi[i], 0x5410));
+        const uint32_t v = plain ? sc[i] : big[i];
+        if (W || 2 * i < p.seg_words) sts32(out + 2 * i * (kTileRows * 4), __byte_perm(v, bi[i], 0x5410));
         if (W > 1 || (W == 0 && 2 * i + 1 < p.seg_words))
-          sts32(out + (2 * i + 1) * (kTileRows * 4), __byte_perm(v, x.bi[i], 0x7632));
+          sts32(out + (2 * i + 1) * (kTileRows * 4), __byte_perm(v, bi[i], 0x7632));
       }
       if (lane == 0) ctl->plain[stage][row0 / 32] = plain;
       __syncwarp();
@@ -435,10 +489,12 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
   // behind them it came 5000 clocks later, and no product starts without it.
   auto each_piece = [&](auto f) {  // f(address in shared memory, row, piece of the row)
     const int live = min(NP, a.M - m0), per_row = p.units * (kUnitK / 8);
-    const int split = kLoadWarps / live, m = (warp - kSumWarp) % live, part = (warp - kSumWarp) / live;
+    const int w = warp - kSumWarp, split = max(1, kLoadWarps / live);  // warps to a row, or rows to a warp
+    const int part = live < kLoadWarps ? w / live : 0;
     if (part >= split) return;
-    for (int k = part * 32 + lane; k < per_row; k += split * 32)
-      f(smem_u32(hbuf) + (k >> 3) * (NP * 128) + m * 128 + (((k ^ m) & 7) << 4), m, k);
+    for (int m = live < kLoadWarps ? w % live : w; m < live; m += kLoadWarps)
+      for (int k = part * 32 + lane; k < per_row; k += split * 32)
+        f(smem_u32(hbuf) + (k >> 3) * (NP * 128) + m * 128 + (((k ^ m) & 7) << 4), m, k);
   };
   grid_trigger();
   if (threadIdx.x == 0) {
@@ -756,12 +812,12 @@ __global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, in
 constexpr int kMinStages = 6;  // of weights, beside resident or streamed h
 constexpr int stage_bytes(int bits) { return kBoxBytes + scale_bytes(bits); }
 int64_t units_of(int64_t d, int bits) { return cdiv(d, seg_k(bits)) * (seg_k(bits) / kUnitK); }
-// Up to 16 rows, beside at least kMinStages of weights.  (With three stages beside them, 13 rows of d 3840 took
-// 36.4 us resident and 34.7 streamed.)
-bool resident(int bits, int64_t M, int64_t d) {
-  return M <= 16 && units_of(d, bits) * (16 * kUnitK * 2) <= kSmemLimit - kCtlBytes - kMinStages * stage_bytes(bits);
-}
 int rows_per_pass(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+// A pass's rows, beside at least kMinStages of weights.  (With three stages beside them, 13 rows of d 3840 took
+// 36.4 us resident and 34.7 streamed; 42 rows of d 768, V 48710, which fit beside six: 13.1 resident, 16.6 streamed.)
+bool resident(int bits, int64_t M, int64_t d) {
+  return units_of(d, bits) * (rows_per_pass(M) * kUnitK * 2) <= kSmemLimit - kCtlBytes - kMinStages * stage_bytes(bits);
+}
 
 template <int kBits, int NP, bool kStream>
 cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_t st) {
@@ -821,10 +877,12 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
 
 template <int kBits>
 cudaError_t launch_bits(const LogitsArgs& a, int sms, void* workspace, cudaStream_t st) {
-  if (resident(kBits, a.M, a.d)) return launch_np<kBits, 16, false>(a, sms, workspace, st);
-  if (a.M <= 16) return launch_np<kBits, 16, true>(a, sms, workspace, st);
-  if (a.M <= 32) return launch_np<kBits, 32, true>(a, sms, workspace, st);
-  return launch_np<kBits, 64, true>(a, sms, workspace, st);
+  const bool whole = resident(kBits, a.M, a.d);
+  switch (rows_per_pass(a.M)) {
+    case 16: return whole ? launch_np<kBits, 16, false>(a, sms, workspace, st) : launch_np<kBits, 16, true>(a, sms, workspace, st);
+    case 32: return whole ? launch_np<kBits, 32, false>(a, sms, workspace, st) : launch_np<kBits, 32, true>(a, sms, workspace, st);
+    default: return whole ? launch_np<kBits, 64, false>(a, sms, workspace, st) : launch_np<kBits, 64, true>(a, sms, workspace, st);
+  }
 }
 
 }  // namespace

@@ -38,18 +38,20 @@ def test_logits_host_checks(lib):
     for bad in (dict(ld_h=68), dict(h=P(0x10008)), dict(wq=P(0x10002)), dict(bits=8, wq=P(0x10004)),
                 dict(out=P(0x10002)), dict(out=P(0x10001), bf16=1), dict(sc=P(0x10001))):
         assert call(**bad) == ERR_ALIGN, bad
-    # more than 16 rows need a workspace
-    need = lib.orpo_head_logits_q_workspace_bytes(17, 64, 4)
-    assert need >= 17 * 64 * 2
-    assert call(M=17) == ERR_NULL
-    assert call(M=17, ws=P(0x10008), ws_bytes=need) == ERR_ALIGN
-    assert call(M=17, ws=FAKE, ws_bytes=need - 1) == ERR_WS
+    # more rows than fit on chip need a workspace
+    big = dict(M=17, d=4096, ld_h=4096)
+    need = lib.orpo_head_logits_q_workspace_bytes(17, 4096, 4)
+    assert need >= 17 * 4096 * 2
+    assert call(**big) == ERR_NULL
+    assert call(**big, ws=P(0x10008), ws_bytes=need) == ERR_ALIGN
+    assert call(**big, ws=FAKE, ws_bytes=need - 1) == ERR_WS
 
 
 def test_logits_workspace(lib):
     q = lib.orpo_head_logits_q_workspace_bytes
-    assert q(1, 2560, 4) == q(16, 3328, 4) == q(16, 3328, 8) == 0
-    for M, d, bits in ((17, 256, 4), (64, 4096, 4), (16, 16384, 4), (1, 8200, 8), (1000, 4096, 4)):
+    for bits in (4, 8):
+        assert q(1, 2560, bits) == q(16, 3328, bits) == q(32, 1536, bits) == q(64, 768, bits) == q(1000, 768, bits) == 0
+    for M, d, bits in ((17, 2048, 4), (64, 4096, 4), (16, 16384, 4), (1, 8200, 8), (1000, 4096, 4)):
         rows, seg = 16 if M <= 16 else 32 if M <= 32 else -(-M // 64) * 64, 1024 // bits
         assert q(M, d, bits) == rows * -(-d // seg) * seg * 2
     assert q(0, 256, 4) == q(4, 256, 5) == q(4, 4, 4) == 0

@@ -113,13 +113,14 @@ def test_scales_of_every_magnitude(bits, group, M):
 
 
 @pytest.mark.parametrize("M,V", [(17, 100), (33, 128), (64, 129), (20, 19457), (64, 38913), (20, 2 * 152 * 128)])
-def test_pairs_of_tiles(M, V):
+@pytest.mark.parametrize("d", [384, 1568])
+def test_pairs_of_tiles(M, V, d):
     """Odd tile counts, single tiles, and vocabularies that just begin another round of tiles."""
-    q, h = random_head(V, 384, 4, 32, seed=V), rows_of(M, 384, seed=M)
+    q, h = random_head(V, d, 4, 32, seed=V), rows_of(M, d, seed=M)
     check(run(h, q, 4, 32)[0], h, q, 4, 32)
 
 
-@pytest.mark.parametrize("M,d,bits", [(17, 512, 4), (3, 5376, 4), (3, 5376, 8), (70, 320, 8)])
+@pytest.mark.parametrize("M,d,bits", [(17, 1600, 4), (3, 5376, 4), (3, 5376, 8), (70, 960, 8)])
 def test_workspace_contents_and_size(M, d, bits):
     q, h = random_head(1000, d, bits, 64, seed=3), rows_of(M, d, seed=5)
     need = orpo.orpo_head_logits_q_workspace_bytes(M, d, bits)
@@ -137,7 +138,7 @@ def test_workspace_contents_and_size(M, d, bits):
         run(h, q, bits, 64, workspace=ws[:need - 1])
 
 
-@pytest.mark.parametrize("M,d", [(4, 512), (20, 512), (4, 5376)])
+@pytest.mark.parametrize("M,d", [(4, 512), (20, 512), (20, 2048), (4, 5376)])
 def test_calls_follow_one_another_without_a_synchronise(M, d):
     """Each step's inputs are written right before it and its outputs read right after it, on one stream: what is set
     up early must wait for both."""
@@ -243,3 +244,17 @@ def test_select_with_a_short_last_chunk(tail, n, dtype, chunk):
     # where values of different beams are closer than their rounding, their order may differ
     if ref[4][0] > 1e-5:
         assert np.array_equal(out[1].cpu().numpy(), ref[1]) and np.array_equal(out[2].cpu().numpy(), ref[2])
+
+
+@pytest.mark.parametrize("d,group", [(832, 64), (1056, 32), (896, 32), (1152, 128), (160, 32)])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("M", [2, 20])
+def test_a_row_does_not_see_the_next_row_s_scales(d, group, bits, M):
+    """Group counts that end inside a segment of columns: infinities and NaN of every third row stay there."""
+    V = 385
+    wq, sc, bi = random_head(V, d, bits, group, seed=d)
+    sc[1::3], bi[1::3] = float("nan"), float("inf")
+    out, st = run(rows_of(M, d, seed=1), (wq, sc, bi), bits, group)
+    good = torch.tensor([v for v in range(V) if v % 3 != 1])
+    check(out, rows_of(M, d, seed=1), (wq, sc, bi), bits, group, good)
+    assert not torch.any(torch.isfinite(out[:, 1::3])) and int(st.item()) == 0
