@@ -26,17 +26,16 @@
 // segments (8-bit: six) beside two sets of accumulators.
 //
 // Measured: one row, d 2560, V 262144, groups of 64, fp32 logits: 65 us, 5.8 TB/s or 86% of the rate of a plain copy;
-// steady state 855 clocks a segment, where that rate would allow 790.  64 rows, d 4096, V 128256: 75 us, 4.1 TB/s
-// and 890 TFLOP/s; without the products 63.  Calls with little work per SM (8 rows, 8 bits, d 2048, V 32000: 17 us for
+// steady state 855 clocks a segment, where that rate would allow 790.  64 rows, d 4096, V 128256: 73 us, 4.3 TB/s
+// and 920 TFLOP/s; without the products 63.  Calls with little work per SM (8 rows, 8 bits, d 2048, V 32000: 17 us for
 // 74 MB) spend 4 us until the first product: memory answers the first requests of all SMs at once.
 //
 // Order of k: 4-bit dequantisation yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights
 // (8-bit: (0,2), (1,3) of 4), which go to tensor memory as they are; h gets the same order, 16 bytes at a
 // time.  Rows of h that fit beside the weights (16 of d up to 3328, 64 of 768) are loaded and put in that order by
 // each CTA, once.  More are streamed: a small kernel first writes h in that order, and as
-// shared memory holds it, to the workspace, and the CTAs work in pairs (clusters) on neighbouring tiles,
-// each fetching half of every segment of h for both (multicast), since h crosses from L2 once per tile: at 64
-// rows that is twice the weights' bytes.
+// shared memory holds it, to the workspace, and each CTA fetches every segment with one plain bulk copy for each
+// of its tiles.  At 64 rows that is twice the weights' bytes from L2, which keeps up (64 rows, d 4096: 73 us).
 // Accuracy: the tensor core truncates as it accumulates (measured: 1e-9 of the result per product, one
 // sign), so an accumulator spans 512 columns and those sums are added in registers, rounding.
 #include <math.h>
@@ -100,34 +99,23 @@ struct TcArgs {
 // One wait of up to kPollNs in the barrier unit: the polls of eight waiting warps at the default
 // interval took as many issue slots as the dequantisation.
 constexpr uint32_t kPollNs = 20000;
-template <bool kCluster>  // acquire at cluster scope: the other CTA of a pair arrives on the barrier too
 __device__ __forceinline__ bool poll_bar(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  if constexpr (kCluster)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
+      : "memory");
   return ok != 0;
 }
 
 // Bounded wait: false on a timeout (reported) or when another role gave up.
-template <bool kCluster = false>
 __device__ __forceinline__ bool wait_bar(TcCtl* ctl, uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (__builtin_expect(poll_bar<kCluster>(bar, parity), 1)) return true;
+  if (__builtin_expect(poll_bar(bar, parity), 1)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!poll_bar<kCluster>(bar, parity)) {
+  while (!poll_bar(bar, parity)) {
     if (ctl->abort_flag) return false;
     if (globaltimer_ns() - t0 > kLimitNs) {
       atomicOr(status, ORPO_STATUS_TIMEOUT);
@@ -139,9 +127,8 @@ __device__ __forceinline__ bool wait_bar(TcCtl* ctl, uint64_t* bar, uint32_t par
 }
 
 // The same for a whole warp: every lane gets the same answer.
-template <bool kCluster = false>
 __device__ __forceinline__ bool wait_warp(TcCtl* ctl, uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, wait_bar<kCluster>(ctl, bar, parity, status));
+  return __all_sync(0xffffffffu, wait_bar(ctl, bar, parity, status));
 }
 
 __device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity) {
@@ -160,23 +147,11 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d, uint32_t a, uint64_t b_
       : "memory");
 }
 
-// `bytes` (a multiple of 16) of global memory to the same shared-memory offset of both CTAs of the pair, counted
-// on the barrier at the same offset of each.
-__device__ __forceinline__ void bulk_load_pair(const void* src, uint32_t bytes, void* dst, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], %4;" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"((uint16_t)3)
-      : "memory");
-}
-
-// Arrive on the barrier at this offset of both CTAs once every MMA issued so far by this thread has completed.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
+// `bytes` (a multiple of 16) of global memory to shared memory, counted on the barrier
+__device__ __forceinline__ void bulk_load(const void* src, uint32_t bytes, void* dst, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // True in one lane of a converged warp.
@@ -481,9 +456,8 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = blockIdx.y * NP;
 
-  // Tiles blockIdx.x, blockIdx.x + gridDim.x, ...; the CTAs of a pair take equally many, the odd one's last
-  // may lie past the vocabulary (zero weights, nothing written).
-  const int my_tiles = (p.tiles - (int)(kStream ? blockIdx.x & ~1u : blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
+  // Tiles blockIdx.x, blockIdx.x + gridDim.x, ...
+  const int my_tiles = (p.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   // Resident h, by the warps that sum and dequantise, a thread always the same 16-byte pieces; rows past M stay as
   // they are, which their own columns of the accumulators get to see and nobody else.  Asked for before any weights:
   // behind them it came 5000 clocks later, and no product starts without it.
@@ -501,8 +475,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     for (int i = 0; i < kMaxStages; ++i) mbar_init(&ctl->w_full[i], 1 + 4), mbar_init(&ctl->w_empty[i], 4);
     for (int i = 0; i < kASlots; ++i) mbar_init(&ctl->a_full[i], 4), mbar_init(&ctl->a_empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&ctl->d_full[i], 1), mbar_init(&ctl->d_empty[i], 4 * kSums);
-    for (int i = 0; i < kMaxH; ++i)
-      mbar_init(&ctl->h_full[i], 1), mbar_init(&ctl->h_empty[i], 2);  // a commit of each CTA of the pair
+    for (int i = 0; i < kMaxH; ++i) mbar_init(&ctl->h_full[i], 1), mbar_init(&ctl->h_empty[i], 1);
     mbar_init(&ctl->h_ready, kLoadWarps);
     mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
@@ -526,7 +499,6 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
   prefetch_scales(p, blockIdx.x, threadIdx.x - 32);  // the same goes for the first tile's scales
   tc_fence_before();
   __syncthreads();
-  if constexpr (kStream) cluster_sync();  // the other CTA's barriers exist
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
 
@@ -570,23 +542,22 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     if constexpr (kStream) {
       const bool leader = elect_one();
       grid_wait();  // the kernel that writes the image is done
-      const uint32_t rank = cluster_ctarank();
-      const uint8_t* const image = p.image + (int64_t)blockIdx.y * p.segs * kHSeg + rank * (kHSeg / 2);
+      const uint8_t* const image = p.image + (int64_t)blockIdx.y * p.segs * kHSeg;
       uint32_t it = 0, hs = 0, hp = 1;  // segments issued; slot, parity of its release
       bool ok = true;
       for (int i = 0; ok && i < my_tiles; ++i) {
         const uint8_t* src = image;
         for (int seg = 0; seg < p.segs; ++seg, ++it, src += kHSeg) {
-          ok = wait_warp<true>(ctl, &ctl->h_empty[hs], hp, a.status);  // both CTAs are done with the slot
+          ok = wait_warp(ctl, &ctl->h_empty[hs], hp, a.status);
           if (!ok) break;
           if (leader) {
-            mbar_arrive_expect_tx(&ctl->h_full[hs], kHSeg);  // this half and the other CTA's
-            bulk_load_pair(src, kHSeg / 2, hbuf + hs * kHSeg + rank * (kHSeg / 2), &ctl->h_full[hs]);
+            mbar_arrive_expect_tx(&ctl->h_full[hs], kHSeg);
+            bulk_load(src, kHSeg, hbuf + hs * kHSeg, &ctl->h_full[hs]);
           }
           if (++hs == (uint32_t)p.hslots) hs = 0, hp ^= 1u;
         }
       }
-      if (!ok && leader) {  // loads in flight, as far as the other CTA's halves came too
+      if (!ok && leader) {  // loads in flight
         const uint32_t k0 = it > (uint32_t)p.hslots ? it - p.hslots : 0;
         for (uint32_t k = k0; k < it; ++k) drain_bar(&ctl->h_full[k % p.hslots], (k / p.hslots) & 1u);
       }
@@ -607,9 +578,9 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
       for (int seg = 0; seg < p.segs; ++seg) {
         // all the waits polled at once: one after the other, each costs its 90 clocks even when there is nothing to
         // wait for
-        bool ready = poll_bar<false>(&ctl->a_full[slot], ap);
-        if (j == 0) ready = poll_bar<false>(&ctl->d_empty[db], dp) && ready;
-        if constexpr (kStream) ready = poll_bar<false>(&ctl->h_full[hs], hp) && ready;
+        bool ready = poll_bar(&ctl->a_full[slot], ap);
+        if (j == 0) ready = poll_bar(&ctl->d_empty[db], dp) && ready;
+        if constexpr (kStream) ready = poll_bar(&ctl->h_full[hs], hp) && ready;
         if (!__all_sync(0xffffffffu, ready)) {
           if (j == 0) ok = wait_warp(ctl, &ctl->d_empty[db], dp, a.status);
           ok = ok && wait_warp(ctl, &ctl->a_full[slot], ap, a.status);
@@ -626,7 +597,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
             umma_bf16_ta(dt, at + kk * 8, desc + ((kk >> 2) * (kHUnit / 2) + (kk & 3) * 32) / 16, idesc,
                          (kk | j) != 0 ? 1u : 0u);
           umma_commit(&ctl->a_empty[slot]);
-          if constexpr (kStream) umma_commit_pair(&ctl->h_empty[hs]);
+          if constexpr (kStream) umma_commit(&ctl->h_empty[hs]);
           if (last) umma_commit(&ctl->d_full[db]);
         }
         __syncwarp();
@@ -784,8 +755,6 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  // pair: the other CTA's loads write here and its commits arrive here, so neither leaves before both are done
-  if constexpr (kStream) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, 512);
@@ -828,9 +797,8 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
   // Tiles of as many rows as deal the vocabulary out evenly in the fewest rounds of 128 rows: with 128 in every
   // one, V = 32000 on 152 SMs takes two rounds of which the second is 64% full.  A multiple of 8, so that a
   // tile's scales start on 16 bytes.
-  const int slots = kStream ? std::max(1, sms / 2) * 2 : sms;
-  const int64_t rounds = cdiv(a.V, (int64_t)kTileRows * slots);
-  p.rows = (int)std::min<int64_t>(kTileRows, cdiv(cdiv(a.V, rounds * slots), 8) * 8);
+  const int64_t rounds = cdiv(a.V, (int64_t)kTileRows * sms);
+  p.rows = (int)std::min<int64_t>(kTileRows, cdiv(cdiv(a.V, rounds * sms), 8) * 8);
   p.tiles = (int)cdiv(a.V, p.rows);
   p.segs = (int)cdiv(a.d, kSegK);
   p.units = p.segs * kUnits;
@@ -868,11 +836,8 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
     if (cudaError_t e = launch_dependent(h_image_kernel<kBits>, dim3((unsigned)cdiv(pieces, 256)), 256, 0, st, a, NP, blocks,
                                          pieces, static_cast<uint4*>(workspace)))
       return e;
-    return launch_dependent<2>(kernel, dim3((unsigned)std::min((p.tiles + 1) / 2 * 2, slots), (unsigned)mt), tc_threads(NP),
-                               (size_t)smem, st, mw, p);
-  } else {
-    return launch_dependent(kernel, dim3((unsigned)std::min(p.tiles, slots), (unsigned)mt), tc_threads(NP), (size_t)smem, st, mw, p);
   }
+  return launch_dependent(kernel, dim3((unsigned)std::min(p.tiles, sms), (unsigned)mt), tc_threads(NP), (size_t)smem, st, mw, p);
 }
 
 template <int kBits>

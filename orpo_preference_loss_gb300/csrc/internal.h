@@ -25,22 +25,19 @@ inline cudaError_t opt_in_smem(Kernel kernel, int bytes, std::atomic<int> (&done
 }
 
 // Launch that may be set up, and its CTAs start, while the kernel before it in the stream ends (programmatic dependent
-// launch; the kernel waits with grid_wait, ptx.cuh).  kCluster: CTAs per cluster.  A call among others then takes 1 to
-// 3 us less.
-template <int kCluster = 1, class... Params, class... Args>
+// launch; the kernel waits with grid_wait, ptx.cuh).  A call among others then takes 1 to 3 us less.
+template <class... Params, class... Args>
 inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {kCluster, 1, 1};
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = kCluster > 1 ? 2 : 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
