@@ -438,7 +438,7 @@ def orpo_head_logits_q(h, wq, scales, biases, bits, group, softcap, logits, stat
 
     h and logits may have any row pitch, e.g. hidden[:, -1] of [M, T, d] hidden states.  workspace: uint8,
     orpo_head_logits_q_workspace_bytes(M, d, bits) of them; None takes what is needed from PyTorch's
-    allocator."""
+    allocator, on the call's stream."""
     M, d = h.shape
     V = wq.shape[0]
     if workspace is not None:
@@ -446,9 +446,10 @@ def orpo_head_logits_q(h, wq, scales, biases, bits, group, softcap, logits, stat
     elif M > 16 or d > 2048:
         need = (_lib or load()).orpo_head_logits_q_workspace_bytes(M, d, bits)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            # from the pool of the stream that the kernels run on: a block of another stream's may have been freed
+            # with work on it still to come there
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
     # A decode step is a few microseconds of GPU work, so the usual, right arguments pass one plain test;
     # whatever fails it is looked at in full for its message.
     hp, hs = h.stride()
