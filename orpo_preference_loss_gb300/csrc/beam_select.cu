@@ -25,6 +25,7 @@
 // sum, candidates, ranks) between six barriers, with 59% of issue slots used; without the sum it took 1.4 us less.
 // 4 x 4 rows of 262144 fp32, n = 8: 10.1 us.
 #include <math.h>
+#include <stddef.h>
 
 #include <algorithm>
 
@@ -81,7 +82,7 @@ struct SelectArgs {
 constexpr int kVecCap = 256;  // vectors with a candidate
 
 struct RowShared {
-  uint32_t words[kWords][kThreads];  // the chunk, in the rare paths; else the vectors with a candidate
+  alignas(16) uint32_t words[kWords][kThreads];  // the chunk, in the rare paths; else the vectors with a candidate
   uint64_t cand[kCap + ORPO_MAX_SELECT];
   uint64_t best[ORPO_MAX_SELECT];
   uint32_t part[kWarps];
@@ -89,6 +90,8 @@ struct RowShared {
   uint32_t thr[kWarps];
   int vecs, count, total;
 };
+static_assert(alignof(RowShared) >= alignof(uint4) && offsetof(RowShared, words) % alignof(uint4) == 0,
+              "candidates' vectors are stored as uint4");
 
 // Sum over the CTA of v; every thread gets it.
 __device__ __forceinline__ int cta_sum(RowShared& sh, int v) {
