@@ -264,10 +264,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
     for (int w = 0; w < kWarps; ++w) cmax = max(cmax, sh.part[w]), thr = min(thr, sh.thr[w]);
     if (have == a.n) thr = max(thr, (uint32_t)(sh.best[a.n - 1] >> 32));  // the n-th best of the chunks before
     const float m = ord_to_float(cmax);
-    // ---- sum of exp(x - m): 2^(x L - c) with c = m L rounded, which is put right after the sum
+    // ---- sum of exp(x - m): 2^(x L - c) with c = m L rounded, which is put right after the sum.  Below 2^24 c is off by
+    // half at most; far above, a term may overflow or vanish before it is put right.
     float s = 0.f;
     const float c2 = m * kLog2e;
-    if (m < INFINITY && fabsf(c2) < INFINITY) {
+    if (fabsf(c2) < 0x1p24f) {
       uint64_t s2 = 0;
       const uint64_t l2 = pack2(kLog2e, kLog2e), mc2 = pack2(-c2, -c2);
 #pragma unroll
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
         s2 = add2(s2, pack2(ex2_approx(lo2(y)), ex2_approx(hi2(y))));
       }
       s = (lo2(s2) + hi2(s2)) * ex2_approx(-fmaf(m, kLog2e, -c2));
-    } else if (m > -INFINITY && m < INFINITY) {  // near the type's lowest value
+    } else if (m > -INFINITY && m < INFINITY) {  // a mask's value, most likely
       s = NAN;                                   // the slow sum below
     }
 #pragma unroll
