@@ -57,11 +57,12 @@ def beam_select(logits, score, finished, eos: int, beams: int, n: int):
                 continue
             row = x[r]
             top = row.max()
-            lse = top + math.log(np.sum(np.exp(row - top))) if math.isfinite(top) else top
+            # lse = top + log_sum, as two numbers: a mask's value of 1e30 leaves nothing of log_sum in one
+            log_sum = math.log(np.sum(np.exp(row - top))) if math.isfinite(top) else 0.0
             order = np.argsort(-row, kind="stable")[:n]
             for j, t in enumerate(order):
-                ok = row[t] > -math.inf and math.isfinite(lse) and not math.isnan(s)
-                props.append((s + (row[t] - lse) if ok else -math.inf, k, j, int(t), False))
+                ok = row[t] > -math.inf and math.isfinite(top) and not math.isnan(s)
+                props.append((s + ((row[t] - top) - log_sum) if ok else -math.inf, k, j, int(t), False))
         props.sort(key=lambda p: (-p[0], p[1], p[2]))
         gap = math.inf
         for p, q in zip(props[:n], props[1:n + 1]):
