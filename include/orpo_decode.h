@@ -62,7 +62,8 @@ int orpo_head_logits_q(const void* h_bf16, int64_t ld_h, const uint8_t* wq, cons
  * The n best continuations of each of `batch` entries with `beams` beams.
  * Row r = b * beams + k of logits (fp32, or bf16 when logits_bf16 = 1; rows ld_logits >= V elements
  * apart) belongs to beam k of entry b, whose score (sum of log-probabilities so far) is score[r].
- *   lse_r = log sum_v exp(x[r, v]);   value(k, v) = score[r] + (x[r, v] - lse_r)   in fp32,
+ *   lse_r = log sum_v exp(x[r, v]);   value(k, v) = score[r] + (x[r, v] - lse_r)   in fp32, with lse_r as m + log s
+ *   (m the row's largest logit, s = sum exp(x - m)) and the value as score + ((x - m) - log s),
  *   and value = -inf where x[r, v] = -inf, where lse_r is not finite (every logit masked, or one
  *   is +inf) or where score[r] is NaN.  A NaN logit counts as -inf.
  * A live beam proposes its n largest logits, the lowest token first among equal ones.  A beam with

@@ -2,6 +2,8 @@
 //
 //   lse_r = log sum_v exp x_rv,  value(k, v) = score_k + (x_kv - lse_k)
 //
+// lse is kept as the row's maximum m and log s, s = sum exp(x - m), and the value is score + ((x - m) - log s): rounded to one
+// number, lse would lose half a unit in the last place of m (5e-4 at 1e4, all of log s at a mask's -1e9).
 // Within a beam the value grows with the logit, so a beam's proposals are its n largest logits and
 // the softmax statistics are needed only for those.  Order inside a beam is a 64-bit key (the
 // logit's bits mapped to an order-preserving integer, then the complement of the token), which is
@@ -475,12 +477,12 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
   const int64_t b = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, n = a.n;
   __shared__ uint8_t over[ORPO_MAX_BEAMS];
-  __shared__ float beam_score[ORPO_MAX_BEAMS], beam_lse[ORPO_MAX_BEAMS];
+  __shared__ float beam_score[ORPO_MAX_BEAMS], beam_max[ORPO_MAX_BEAMS], beam_log[ORPO_MAX_BEAMS];
   uint64_t* const area0 = lists;
   uint64_t* const area1 = lists + a.area;
   uint64_t* const best = area1 + a.area;  // [beams, n]: value, then beam and place
   int* const token = reinterpret_cast<int*>(best + a.beams * n);
-  // log-sum-exp of every beam: a warp takes its parts' statistics, at most two per lane
+  // log-sum-exp of every beam, as maximum and log of the sum: a warp takes its parts' statistics, at most two per lane
   for (int k = warp; k < a.beams; k += warps) {
     const int64_t r = b * a.beams + k;
     const bool ended = a.finished != nullptr && a.finished[r];
@@ -491,17 +493,17 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
     float m = fmaxf(s0.x, s1.x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float lse = m;
+    float log_s = 0.f;
     if (fabsf(m) < INFINITY) {
       float s = (s0.x > -INFINITY ? s0.y * ex2_approx((s0.x - m) * kLog2e) : 0.f) +
                 (s1.x > -INFINITY ? s1.y * ex2_approx((s1.x - m) * kLog2e) : 0.f);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      lse = m + logf(s);
+      log_s = logf(s);
     }
     if (lane == 0) {
       if (score != score) atomicOr(a.status, ORPO_STATUS_NONFINITE);
-      over[k] = ended, beam_score[k] = score, beam_lse[k] = lse;
+      over[k] = ended, beam_score[k] = score, beam_max[k] = m, beam_log[k] = log_s;
     }
   }
   __syncthreads();
@@ -519,13 +521,13 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
       merge_heads(area0, area1, group, a.parts, n);
     for (int t = tid; t < group * n; t += blockDim.x) {
       const int k = k0 + t / n, j = t % n;
-      const float score = beam_score[k], lse = beam_lse[k];
+      const float score = beam_score[k], m = beam_max[k];
       float y = -INFINITY;
       if (over[k]) {
         if (j == 0) y = score;
       } else {
         const float x = ord_to_float((uint32_t)(top[t] >> 32));
-        if (x > -INFINITY && fabsf(lse) < INFINITY) y = score + (x - lse);
+        if (x > -INFINITY && fabsf(m) < INFINITY) y = score + ((x - m) - beam_log[k]);
       }
       if (y != y) y = -INFINITY;
       const int at = k * n + j;

@@ -1,11 +1,15 @@
-"""orpo_beam_select on logits far from zero: masks of any finite value over whole chunks.  Compared with the float64 oracle within the tolerance derived in test_gpu_beam_select.py: logits are
+"""orpo_beam_select on logits far from zero: masks of any finite value over whole chunks or rows, and rows whose
+maximum is large.  Compared with the float64 oracle within the tolerance derived in test_gpu_beam_select.py: logits are
 exact inputs, and their distance to the row's maximum is what is rounded."""
 
+import math
+
+import numpy as np
 import pytest
 import torch
 
 from gpu_helpers import dev
-from test_gpu_beam_select import check, logits
+from test_gpu_beam_select import check, logits, run
 
 pytestmark = pytest.mark.gpu
 
@@ -25,6 +29,36 @@ def test_chunks_masked_by_a_finite_value(fill, dtype, chunk):
     x[4, chunk:] = fill
     x[6, :2 * chunk + 5] = fill
     check(x, score, 4, 6)
+
+
+@pytest.mark.parametrize("fill", FILLS + [torch.finfo(F32).min, 7.0, 1e9, 3e38])
+@pytest.mark.parametrize("V", [100, 20000, 70001])
+def test_rows_of_one_value(fill, V):
+    """Every token of such a beam has probability 1 / V, however large the value: its score minus log V competes with
+    the live beams' continuations."""
+    x, score = logits(8, V, 5)
+    x[1] = fill
+    x[4:] = fill
+    got = check(x, score, 4, 8)
+    alone = run(x[4:].contiguous(), score[4:].contiguous(), 4, 1)
+    best = score[4:].double().max().item() - math.log(V)
+    assert abs(alone[0][0, 0] - best) <= 4e-6 + 2.0 ** -22 * 84
+    assert np.all(np.isfinite(got[0]))
+
+
+def test_rows_of_the_lowest_bf16_value():
+    x, score = logits(8, 40000, 7, dtype=BF16)
+    x[1] = torch.finfo(BF16).min
+    x[6, 3:] = torch.finfo(BF16).min
+    check(x, score, 4, 8)
+
+
+@pytest.mark.parametrize("shift", [1e3, -1e4, 1e4, 1e5, -1e5])
+@pytest.mark.parametrize("V", [1000, 50257])
+def test_rows_far_from_zero(shift, V):
+    x, score = logits(12, V, 9)
+    x += shift
+    check(x, score, 3, 5)
 
 
 def test_one_live_token_among_lowest_values():
