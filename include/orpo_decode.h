@@ -36,7 +36,9 @@ extern "C" {
 
 /*
  * Logits of M rows under the quantised head.
- *   W[v, j] = bf16(scales[v, j/group] * q[v, j] + biases[v, j/group])   (orpo_head_fwd_q's weights)
+ *   W[v, j] = bf16(scales[v, j/group] * q[v, j] + biases[v, j/group]), product and sum rounded once.  (orpo_head_fwd_q
+ *   rounds to fp32 and then to bf16: its weights are these but where the exact value lies within fp32's rounding
+ *   of the middle between two bf16 values, and there one bf16 unit off at most.)
  *   z[m, v] = sum_j h[m, j] W[v, j]       (products of bf16 values, fp32 accumulation)
  *   logits[m, v] = softcap * tanh(z / softcap) if softcap > 0, else z; rounded once when bf16
  * h: bf16 [M, d], rows ld_h elements apart (ld_h >= d, a multiple of 8; e.g. the last positions of

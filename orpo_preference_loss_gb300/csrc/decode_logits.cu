@@ -9,9 +9,9 @@
 // Generic kernel: a warp owns one vocabulary row and a tile of 8 rows of h.  Lane l takes the
 // 8-weight slices l, l + 32, ... of the row (one 4- or 8-byte word of q, one scale and bias: a group
 // is a multiple of 8 columns), so any d that is a multiple of 8 works; the lanes' fp32 sums are
-// added in a fixed shuffle order.  Bound by its instructions, about 20 per weight and row of h (unpack,
-// round, two conversions, a product): 0.76 ms for one row at d 2560, V 262144, 4 bits, where the
-// tensor-core kernel takes 0.065 ms.
+// added in a fixed shuffle order.  Bound by its instructions (dequantisation, loads of h,
+// conversions, products): 0.66 ms for one row at d 2560, V 262144, 4 bits, where the tensor-core kernel takes
+// 0.065 ms.
 #include <math.h>
 
 #include <algorithm>
@@ -44,12 +44,23 @@ __global__ void __launch_bounds__(256) logits_generic_kernel(LogitsArgs a) {
     else
       raw = __ldg(reinterpret_cast<const uint2*>(row) + c);
     const int64_t gi = g0 + (8 * c) / a.group;
-    const float sc = dq_bf16_to_float(__ldg(a.scales + gi)), bi = dq_bf16_to_float(__ldg(a.biases + gi));
+    // (scale, scale) and (bias, bias); product and sum round once, as in the tensor-core kernel
+    const uint32_t s2 = __ldg(a.scales + gi) * 0x10001u, b2 = __ldg(a.biases + gi) * 0x10001u;
     float w[8];
+    if constexpr (kBits == 4) {
+      uint32_t p[4];  // (0, 4), (1, 5), (2, 6), (3, 7)
+      dequant4(raw.x, s2, b2, p);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t q = kBits == 4 ? (raw.x >> (4 * e)) & 15u : ((e < 4 ? raw.x : raw.y) >> (8 * (e & 3))) & 255u;
-      w[e] = __uint_as_float(dq_pack2(0.f, fmaf(sc, (float)q, bi)) & 0xffff0000u);
+      for (int e = 0; e < 4; ++e) w[e] = __uint_as_float(p[e] << 16), w[e + 4] = __uint_as_float(p[e] & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        uint32_t p[2];  // (0, 2), (1, 3)
+        dequant8(o ? raw.y : raw.x, s2, b2, p);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          w[4 * o + e] = __uint_as_float(p[e] << 16), w[4 * o + e + 2] = __uint_as_float(p[e] & 0xffff0000u);
+      }
     }
 #pragma unroll
     for (int m = 0; m < kRowsTile; ++m) {

@@ -5,7 +5,6 @@
 #include <stdint.h>
 
 #include "ptx.cuh"
-#include "quant.cuh"
 
 namespace orpo {
 

@@ -1,0 +1,66 @@
+"""orpo_head_logits_q where the result is known to the last bit.
+
+Weights on a tie: one-hot rows of h read single weights out, which have to be scale q + bias rounded once."""
+
+from fractions import Fraction
+
+import pytest
+import torch
+
+import orpo_preference_loss_gb300 as orpo
+from gpu_helpers import dev, status_tensor
+
+pytestmark = pytest.mark.gpu
+
+
+def run(h, q, bits, group, out=None):
+    st = status_tensor()
+    out = torch.full((h.shape[0], q[0].shape[0]), float("nan"), device=dev()) if out is None else out
+    orpo.orpo_head_logits_q(h, *q, bits, group, 0.0, out, st)
+    assert int(st.item()) == 0
+    return out
+
+
+def bf16_once(x: Fraction) -> float:
+    """x > 0 rounded to 8 significant bits, ties to even."""
+    e = 0
+    while x >= 256:
+        x, e = x / 2, e + 1
+    while x < 128:
+        x, e = x * 2, e - 1
+    n = x.numerator // x.denominator
+    rest = x - n
+    if rest > Fraction(1, 2) or (rest == Fraction(1, 2) and n % 2 == 1):
+        n += 1
+    return float(n) * 2.0 ** e
+
+
+@pytest.mark.parametrize("offset", [0, 4, 8])
+@pytest.mark.parametrize("bits,group", [(4, 32), (4, 8), (8, 32), (8, 16)])
+@pytest.mark.parametrize("magnitude", [0, -12])
+def test_weights_are_rounded_once(bits, group, offset, magnitude):
+    """Products of scale and q that lie halfway between two bf16 values, with biases far below: which way they round is
+    the bias's sign, on every kernel of the entry point (aligned weights and groups of 32 take another than the rest)."""
+    if bits == 8 and offset == 4:
+        pytest.skip("8-bit weights start on 8 bytes")
+    d, ties = 64, [(77, 5), (35, 11), (55, 7), (91, 11), (111, 7), (43, 9)]  # scale (times 2^-7) and q: odd 9-bit products
+    ties = [(s, q) for s, q in ties if 256 < s * q < 512 and s * q % 2 == 1]
+    assert len(ties) >= 4
+    V = 2 * len(ties)
+    raw = torch.zeros((V, d), dtype=torch.uint8)
+    sc = torch.zeros((V, d // group))
+    bi = torch.zeros((V, d // group))
+    want = torch.zeros((d, V))
+    unit, tiny = Fraction(2) ** (magnitude - 7), Fraction(2) ** (magnitude - 40)
+    for i in range(V):
+        s, q = ties[i // 2]
+        sign = 1 if i % 2 == 0 else -1
+        raw[i], sc[i], bi[i] = q, float(s * unit), float(sign * tiny)
+        want[:, i] = bf16_once(s * q * unit + sign * tiny)
+    packed = raw[:, 0::2] | (raw[:, 1::2] << 4) if bits == 4 else raw
+    flat = torch.zeros(packed.numel() + 16, dtype=torch.uint8, device=dev())
+    wq = flat[offset:offset + packed.numel()].view(packed.shape)
+    wq.copy_(packed)
+    h = torch.eye(d, device=dev()).bfloat16()
+    got = run(h, (wq, sc.to(dev()).bfloat16(), bi.to(dev()).bfloat16()), bits, group)
+    assert torch.equal(got.cpu(), want)
