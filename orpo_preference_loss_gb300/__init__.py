@@ -453,6 +453,8 @@ def orpo_head_logits_q(h, wq, scales, biases, bits, group, softcap, logits, stat
     # A decode step is a few microseconds of GPU work, so the usual, right arguments pass one plain test;
     # whatever fails it is looked at in full for its message.
     hp, hs = h.stride()
+    if M <= 1:
+        hp = d  # where a next row would start does not matter
     lp, ls = logits.stride()
     if not (h.is_cuda and h.dtype in BF16 and hs == 1 and hp >= d and wq.is_cuda and wq.dtype is torch.uint8
             and wq.is_contiguous() and wq.shape == (V, d * bits // 8) and scales.is_cuda and scales.dtype in BF16

@@ -1,6 +1,7 @@
 """orpo_head_logits_q where the result is known to the last bit.
 
-Weights on a tie: one-hot rows of h read single weights out, which have to be scale q + bias rounded once."""
+Weights on a tie: one-hot rows of h read single weights out, which have to be scale q + bias rounded once.
+A single row of h out of a wider buffer gives the bits that it gives alone."""
 
 from fractions import Fraction
 
@@ -64,3 +65,15 @@ def test_weights_are_rounded_once(bits, group, offset, magnitude):
     h = torch.eye(d, device=dev()).bfloat16()
     got = run(h, (wq, sc.to(dev()).bfloat16(), bi.to(dev()).bfloat16()), bits, group)
     assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("pitch", [65, 67, 70, 1000])
+def test_the_pitch_of_a_single_row_does_not_matter(pitch):
+    g = torch.Generator("cuda").manual_seed(pitch)
+    wq = torch.randint(0, 256, (300, 32), generator=g, device=dev(), dtype=torch.uint8)
+    sc = torch.ones((300, 2), device=dev()).bfloat16()
+    h = torch.randn((1, 64), generator=g, device=dev()).bfloat16()
+    wide = torch.zeros((1, pitch), device=dev()).bfloat16()
+    wide[:, :64] = h
+    assert wide[:, :64].stride(0) == pitch
+    assert torch.equal(run(wide[:, :64], (wq, sc, sc), 4, 32), run(h, (wq, sc, sc), 4, 32))
