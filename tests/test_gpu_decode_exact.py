@@ -1,7 +1,10 @@
 """orpo_head_logits_q where the result is known to the last bit.
 
-Weights on a tie: one-hot rows of h read single weights out, which have to be scale q + bias rounded once.
-A single row of h out of a wider buffer gives the bits that it gives alone."""
+Weights and rows of h that are small integers: every product and every partial sum is an integer below 2^24, exact in
+fp32 in any order and whether adds round or truncate, so the logits have to be equal to the integers' own product.
+One missing, doubled or misplaced product shows, at any d.  And weights on a tie: one-hot rows of h read single
+weights out, which have to be scale q + bias rounded once.  A single row of h out of a wider buffer gives
+the bits that it gives alone."""
 
 from fractions import Fraction
 
@@ -20,6 +23,34 @@ def run(h, q, bits, group, out=None):
     orpo.orpo_head_logits_q(h, *q, bits, group, 0.0, out, st)
     assert int(st.item()) == 0
     return out
+
+
+@pytest.mark.parametrize("M,d,V,bits,group", [
+    (1, 256, 4096, 4, 64), (1, 2560, 40000, 4, 64), (3, 3840, 20000, 4, 32), (13, 3840, 20000, 4, 32),
+    (16, 16384, 700, 4, 64), (20, 4096, 20000, 4, 128), (24, 3232, 9633, 4, 32), (33, 768, 4871, 4, 96),
+    (64, 4096, 20000, 4, 128), (64, 16384, 333, 4, 64), (130, 1568, 2000, 4, 32), (8, 2048, 32000, 8, 32),
+    (40, 4096, 5000, 8, 64), (3, 5376, 3000, 8, 64), (5, 8200, 500, 4, 8), (11, 4104, 500, 8, 24)])
+def test_integers_are_exact(M, d, V, bits, group):
+    """Weights q - 8 (8 bits: q - 128 of q in 120 .. 135), rows of h in -2 .. 2: sums stay below 16384 * 16 < 2^24."""
+    g = torch.Generator("cuda").manual_seed(d + M)
+    w = torch.randint(-8, 8, (V, d), generator=g, device=dev(), dtype=torch.int16)
+    h = torch.randint(-2, 3, (M, d), generator=g, device=dev(), dtype=torch.int16)
+    if bits == 4:
+        u = (w + 8).to(torch.uint8)
+        wq, bias = u[:, 0::2] | (u[:, 1::2] << 4), -8.0
+    else:
+        wq, bias = (w + 128).to(torch.uint8), -128.0
+    sc = torch.ones((V, d // group), device=dev()).bfloat16()
+    q = (wq.contiguous(), sc, torch.full_like(sc, bias))
+    want = (h.double() @ w.double().T).float()
+    hb = h.bfloat16()
+    first = run(hb, q, bits, group)
+    assert torch.equal(first, want)
+    # small scales take another form of the dequantisation
+    small = (q[0], sc * 2.0 ** -9, q[2] * 2.0 ** -9)
+    assert torch.equal(run(hb, small, bits, group) * 512, want)
+    for _ in range(10):
+        assert torch.equal(run(hb, q, bits, group), want)
 
 
 def bf16_once(x: Fraction) -> float:
