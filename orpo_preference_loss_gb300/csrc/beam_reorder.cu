@@ -250,8 +250,8 @@ cudaError_t launch(const ReorderArgs& a, int sms, cudaStream_t st) {
       e = launch_dependent(reorder_kernel<Piece, 8>, grid, kThreads, 0, st, c);
     } else {
       static std::atomic<int> done[64];
-      if ((e = opt_in_smem(reorder_tile_kernel<Piece>, ORPO_MAX_BEAMS * kTile * (int)sizeof(Piece), done)) != cudaSuccess) return e;
-      e = launch_dependent(reorder_tile_kernel<Piece>, grid, kThreads, a.beams * kTile * sizeof(Piece), st, c);
+      e = opt_in_smem(reorder_tile_kernel<Piece>, ORPO_MAX_BEAMS * kTile * (int)sizeof(Piece), done);
+      if (e == cudaSuccess) e = launch_dependent(reorder_tile_kernel<Piece>, grid, kThreads, a.beams * kTile * sizeof(Piece), st, c);
     }
     prof_end(K_REORDER, st);
     if (e != cudaSuccess) return e;

@@ -600,18 +600,19 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
   a.stats = reinterpret_cast<float2*>(a.keys + rows * plan.parts * n);
   // rows in launches of at most 65535
   prof_begin(K_BEAM, st);
-  for (int64_t r = 0; r < rows; r += 65535) {
+  cudaError_t e = cudaSuccess;
+  for (int64_t r = 0; r < rows && e == cudaSuccess; r += 65535) {
     SelectArgs c = a;
     c.logits = static_cast<const uint8_t*>(logits) + r * ld_logits * size;
     if (finished) c.finished = finished + r;
     c.keys = a.keys + r * plan.parts * n;
     c.stats = a.stats + r * plan.parts;
     const dim3 grid((unsigned)plan.parts, (unsigned)std::min<int64_t>(65535, rows - r));
-    const cudaError_t e = logits_bf16 ? launch_dependent(select_rows_kernel<true>, grid, kThreads, 0, st, c)
-                                      : launch_dependent(select_rows_kernel<false>, grid, kThreads, 0, st, c);
-    if (e != cudaSuccess) return ORPO_ERR_CUDA;
+    e = logits_bf16 ? launch_dependent(select_rows_kernel<true>, grid, kThreads, 0, st, c)
+                    : launch_dependent(select_rows_kernel<false>, grid, kThreads, 0, st, c);
   }
   prof_end(K_BEAM, st);
+  if (e != cudaSuccess) return ORPO_ERR_CUDA;
   // as many beams' lists at a time as fit shared memory twice, beside every beam's n best and their tokens
   const int per_beam = plan.parts * n, bests = beams * n;
   a.group = std::min(beams, (int)((kMergeSmem - bests * 12) / (per_beam * 16)));  // at least 1: 16 * 4096 bytes of 112 KiB
@@ -622,7 +623,7 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
   prof_begin(K_BEAM, st);
   // it may be set up while the row kernel runs
   const int threads = std::min(kMergeThreads, std::max(128, (int)cdiv(a.group * per_beam, 32) * 32));
-  const cudaError_t e = launch_dependent(select_merge_kernel, dim3((unsigned)batch), threads, smem, st, a);
+  e = launch_dependent(select_merge_kernel, dim3((unsigned)batch), threads, smem, st, a);
   prof_end(K_BEAM, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
 }
