@@ -19,6 +19,7 @@
 #include <algorithm>
 
 #include "../../include/orpo_decode.h"
+#include "bounds.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -37,6 +38,12 @@ struct ReorderArgs {
 };
 
 constexpr int kThreads = 256;
+
+// Whether `n` bytes from `p` on are this launch's (bounds-checked build).
+__device__ __forceinline__ bool in_state(const ReorderArgs& a, const void* p, int n) {
+  const int64_t at = static_cast<const uint8_t*>(p) - a.state, size = a.outer * a.batch * a.beams * a.rows * a.capacity * a.unit;
+  return in_bounds(a.status, at, size) && in_bounds(a.status, at + n - 1, size);
+}
 
 // A CTA's (slab, entry, row), of at most 2^30.
 struct Run {
@@ -62,7 +69,8 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderArgs a) {
   const int64_t begin = (int64_t)blockIdx.y * a.per, end = min(begin + a.per, used);
   bool bad = len < 0 || len > a.capacity;
   if (threadIdx.x < KB) {
-    const int k = threadIdx.x, p = k < a.beams ? a.parent[b * a.ld_parent + k] : k;
+    const int k = threadIdx.x;
+    const int p = k < a.beams && in_bounds(a.status, b, a.batch) ? a.parent[b * a.ld_parent + k] : k;
     bad |= k < a.beams && (p < 0 || p >= a.beams);
     par[k] = p;
   }
@@ -81,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderArgs a) {
         const T* src = base + par[k] * beam_units + i;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          if (u == 0 || i + u * kThreads < end) v[u][k] = src[u * kThreads];
+          if ((u == 0 || i + u * kThreads < end) && in_state(a, src + u * kThreads, sizeof(T))) v[u][k] = src[u * kThreads];
       }
 #pragma unroll
     for (int k = 0; k < KB; ++k)
@@ -89,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(ReorderArgs a) {
         T* dst = base + k * beam_units + i;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          if (u == 0 || i + u * kThreads < end) dst[u * kThreads] = v[u][k];
+          if ((u == 0 || i + u * kThreads < end) && in_state(a, dst + u * kThreads, sizeof(T))) dst[u * kThreads] = v[u][k];
       }
   }
 }
@@ -106,11 +114,11 @@ __device__ __forceinline__ bool find_moves(const ReorderArgs& a, int64_t b, int6
   if (threadIdx.x == 0) m.n = 0;
   __syncthreads();
   if (threadIdx.x < a.beams) {
-    const int k = threadIdx.x, p = a.parent[b * a.ld_parent + k];
+    const int k = threadIdx.x, p = in_bounds(a.status, b, a.batch) ? a.parent[b * a.ld_parent + k] : k;
     bad |= p < 0 || p >= a.beams;
     if (p != k) {
       const int j = atomicAdd(&m.n, 1);
-      m.from[j] = p, m.to[j] = k;
+      if (in_bounds(a.status, j, ORPO_MAX_BEAMS)) m.from[j] = p, m.to[j] = k;
     }
   }
   if (!__syncthreads_or(bad)) return true;
@@ -134,15 +142,19 @@ __global__ void __launch_bounds__(kThreads) reorder_tile_kernel(ReorderArgs a) {
   const int64_t beam_units = a.rows * a.capacity * a.unit / (int64_t)sizeof(T);
   T* base = reinterpret_cast<T*>(a.state) + (o * a.batch + b) * a.beams * beam_units +
             row * (a.capacity * a.unit / (int64_t)sizeof(T));
-  const int n = moves.n * kTile;
+  const int n = moves.n * kTile, slots = a.beams * kTile;
   for (int64_t i = begin; i < end; i += kTile) {
 #pragma unroll 4
-    for (int j = threadIdx.x; j < n; j += kThreads)
-      if (i + j % kTile < end) tile[j] = base[moves.from[j / kTile] * beam_units + i + j % kTile];
+    for (int j = threadIdx.x; j < n; j += kThreads) {
+      const T* const src = base + moves.from[j / kTile] * beam_units + i + j % kTile;
+      if (i + j % kTile < end && in_bounds(a.status, j, slots) && in_state(a, src, sizeof(T))) tile[j] = *src;
+    }
     __syncthreads();  // every beam's units are read
 #pragma unroll 4
-    for (int j = threadIdx.x; j < n; j += kThreads)
-      if (i + j % kTile < end) base[moves.to[j / kTile] * beam_units + i + j % kTile] = tile[j];
+    for (int j = threadIdx.x; j < n; j += kThreads) {
+      T* const dst = base + moves.to[j / kTile] * beam_units + i + j % kTile;
+      if (i + j % kTile < end && in_bounds(a.status, j, slots) && in_state(a, dst, sizeof(T))) *dst = tile[j];
+    }
     __syncthreads();
   }
 }
@@ -161,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) reorder_bytes_kernel(ReorderArgs a, 
   const int64_t run_bytes = a.capacity * a.unit, beam_bytes = a.rows * run_bytes;
   uint8_t* const base = a.state + ((int64_t)run.o * a.batch + run.b) * a.beams * beam_bytes + run.row * run_bytes;
   const uint32_t chunks = (uint32_t)window / 16, n = moves.n * chunks, ends = moves.n * 32;
-  const int pitch = window + 32;
+  const int pitch = window + 32, tile_size = a.beams * pitch;
   for (int64_t w0 = begin; w0 < end; w0 += window) {
     const int size = (int)min((int64_t)window, end - w0);
     // of the bytes [p, p + size): those before the first boundary, and whole 16-byte chunks
@@ -176,15 +188,16 @@ __global__ void __launch_bounds__(kThreads) reorder_bytes_kernel(ReorderArgs a, 
       const uint32_t j = i / chunks, c = i - j * chunks;
       const uint8_t* const src = base + moves.from[j] * beam_bytes + w0;
       const int at = head_of(src) + (int)c * 16;
-      if (at + 16 <= size)
-        *reinterpret_cast<uint4*>(tile_raw + j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u) + at) =
-            *reinterpret_cast<const uint4*>(src + at);
+      const int to = (int)(j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u)) + at;
+      if (at + 16 <= size && in_bounds(a.status, to + 15, tile_size) && in_state(a, src + at, 16))
+        *reinterpret_cast<uint4*>(tile_raw + to) = *reinterpret_cast<const uint4*>(src + at);
     }
     for (uint32_t i = threadIdx.x; i < ends; i += kThreads) {
       const uint32_t j = i / 32;
       const uint8_t* const src = base + moves.from[j] * beam_bytes + w0;
       const int at = end_byte(head_of(src), (int)(i & 31u));
-      if (at >= 0) tile_raw[j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u) + at] = src[at];
+      const int to = (int)(j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u)) + at;
+      if (at >= 0 && in_bounds(a.status, to, tile_size) && in_state(a, src + at, 1)) tile_raw[to] = src[at];
     }
     __syncthreads();  // every beam's window is read
 #pragma unroll 2
@@ -196,6 +209,7 @@ __global__ void __launch_bounds__(kThreads) reorder_bytes_kernel(ReorderArgs a, 
       if (at + 16 <= size) {
         const uint32_t off = j * pitch + (uint32_t)(reinterpret_cast<uintptr_t>(src) & 15u) + at, shift = (off & 3u) * 8;
         const uint32_t* const w = reinterpret_cast<const uint32_t*>(tile_raw) + off / 4;  // 5 words: inside the slot's slack
+        if (!in_bounds(a.status, off / 4 * 4 + 19, tile_size) || !in_state(a, dst + at, 16)) continue;
         uint32_t x[5];
 #pragma unroll
         for (int e = 0; e < 5; ++e) x[e] = w[e];
@@ -208,7 +222,8 @@ __global__ void __launch_bounds__(kThreads) reorder_bytes_kernel(ReorderArgs a, 
       const uint8_t* const src = base + moves.from[j] * beam_bytes + w0;
       uint8_t* const dst = base + moves.to[j] * beam_bytes + w0;
       const int at = end_byte(head_of(dst), (int)(i & 31u));
-      if (at >= 0) dst[at] = tile_raw[j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u) + at];
+      const int from = (int)(j * pitch + (reinterpret_cast<uintptr_t>(src) & 15u)) + at;
+      if (at >= 0 && in_bounds(a.status, from, tile_size) && in_state(a, dst + at, 1)) dst[at] = tile_raw[from];
     }
     __syncthreads();
   }

@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "../../include/orpo_decode.h"
+#include "bounds.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -78,14 +79,16 @@ struct SelectArgs {
   float2* stats;   // [rows, parts] max, sum of exp(x - max)
   int parts, chunks;  // parts of a row, chunks of a row (the last may be short, or empty)
   int group, area;    // merge: beams whose lists are merged at a time, keys of an area of them
+  int64_t lists;      // lists of n keys that `keys` holds, and statistics
   int32_t* status;
 };
 
 constexpr int kVecCap = 256;  // vectors with a candidate
+constexpr int kKeys = kCap + ORPO_MAX_SELECT;  // a chunk's candidates and the best of the chunks before
 
 struct RowShared {
   alignas(16) uint32_t words[kWords][kThreads];  // the chunk, in the rare paths; else the vectors with a candidate
-  uint64_t cand[kCap + ORPO_MAX_SELECT];
+  uint64_t cand[kKeys];
   uint64_t best[ORPO_MAX_SELECT];
   uint32_t part[kWarps];
   float sum[kWarps];
@@ -202,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
       const uint4* src = reinterpret_cast<const uint4*>(row + (e0 - off) * kSize) + tid;
 #pragma unroll
       for (int i = 0; i < kN / kVec; ++i) {
+        if (!in_bounds(a.status, token_of(i * kVec), a.V - kVec + 1)) continue;
         const uint4 y = __ldg(src + i * kThreads);
         x.w[i * 4] = y.x, x.w[i * 4 + 1] = y.y, x.w[i * 4 + 2] = y.z, x.w[i * 4 + 3] = y.w;
       }
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
       for (int i = 0; i < kN / kVec; ++i) {
         const int v = token_of(i * kVec);
         uint32_t* w = x.w + i * 4;
-        if (v >= 0 && v <= last - kVec) {
+        if (v >= 0 && v <= last - kVec && in_bounds(a.status, v, a.V - kVec + 1)) {
           const uint4 y = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)v * kSize));
           w[0] = y.x, w[1] = y.y, w[2] = y.z, w[3] = y.w;
         } else {
@@ -219,9 +223,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
             w[j] = E::kNone;
             if constexpr (kBf16) {
               const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + v + 2 * j;
-              if (v + 2 * j >= 0 && v + 2 * j < last) w[j] = (w[j] & 0xffff0000u) | __ldg(p);
-              if (v + 2 * j + 1 >= 0 && v + 2 * j + 1 < last) w[j] = (w[j] & 0xffffu) | ((uint32_t)__ldg(p + 1) << 16);
-            } else if (v + j >= 0 && v + j < last) {
+              if (v + 2 * j >= 0 && v + 2 * j < last && in_bounds(a.status, v + 2 * j, a.V))
+                w[j] = (w[j] & 0xffff0000u) | __ldg(p);
+              if (v + 2 * j + 1 >= 0 && v + 2 * j + 1 < last && in_bounds(a.status, v + 2 * j + 1, a.V))
+                w[j] = (w[j] & 0xffffu) | ((uint32_t)__ldg(p + 1) << 16);
+            } else if (v + j >= 0 && v + j < last && in_bounds(a.status, v + j, a.V)) {
               w[j] = __ldg(reinterpret_cast<const uint32_t*>(row) + v + j);
             }
           }
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
     for (int i = 0; i < kN / kVec; ++i)
       if (vmax[i] >= live) {
         const int at = atomicAdd(&sh.vecs, 1);
-        if (at < kVecCap) {
+        if (at < kVecCap && in_bounds(a.status, at * 8 + 7, kWords * kThreads)) {
           uint32_t* v = &sh.words[0][0] + at * 8;
           v[0] = token_of(i * kVec);
           *reinterpret_cast<uint4*>(v + 4) = make_uint4(x.w[i * 4], x.w[i * 4 + 1], x.w[i * 4 + 2], x.w[i * 4 + 3]);
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
         const float f = __uint_as_float(!kBf16 ? w : j & 1 ? w & 0xffff0000u : w << 16);
         if (f >= live) {
           const int at = atomicAdd(&sh.count, 1);
-          if (at < kCap) sh.cand[at] = key_of(f, (int)v[0] + j);
+          if (at < kCap && in_bounds(a.status, at, kKeys)) sh.cand[at] = key_of(f, (int)v[0] + j);
         }
       }
     }
@@ -365,7 +371,10 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
       for (int i = 0; i < kN; ++i) {
         const float f = ch.at(i);
         const uint32_t o = ord_of(f);
-        if (o > lo || (o == lo && ch.token_of(i) < b0)) sh.cand[atomicAdd(&sh.count, 1)] = key_of(f, ch.token_of(i));
+        if (o > lo || (o == lo && ch.token_of(i) < b0)) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (in_bounds(a.status, at, kKeys)) sh.cand[at] = key_of(f, ch.token_of(i));
+        }
       }
       __syncthreads();
       count = sh.count;
@@ -379,21 +388,24 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
 #pragma unroll 2
       for (int i = 0; i < kN; ++i) {
         const int v = ch.token_of(i);
-        if (v >= from && v < bound && ch.at(i) == -INFINITY) sh.cand[atomicAdd(&sh.count, 1)] = key_of(-INFINITY, v);
+        if (v >= from && v < bound && ch.at(i) == -INFINITY) {
+          const int at = atomicAdd(&sh.count, 1);
+          if (in_bounds(a.status, at, kKeys)) sh.cand[at] = key_of(-INFINITY, v);
+        }
       }
       __syncthreads();
       count = sh.count;
     }
     // ---- with the best so far: rank by counting (keys are distinct)
-    if (tid < have) sh.cand[count + tid] = sh.best[tid];
+    if (tid < have && in_bounds(a.status, count + tid, kKeys)) sh.cand[count + tid] = sh.best[tid];
     __syncthreads();
     count += have;
-    for (int i = tid; i < count; i += kThreads) {
+    for (int i = tid; i < count && in_bounds(a.status, count - 1, kKeys); i += kThreads) {
       const uint64_t key = sh.cand[i];
       int rank = 0;
 #pragma unroll 8
       for (int j = 0; j < count; ++j) rank += sh.cand[j] > key;
-      if (rank < a.n) sh.best[rank] = key;
+      if (rank < a.n && in_bounds(a.status, rank, ORPO_MAX_SELECT)) sh.best[rank] = key;
     }
     have = min(count, a.n);
     // ---- running statistics (every thread keeps them)
@@ -410,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
   }
   __syncthreads();
   const int64_t list = r * a.parts + blockIdx.x;
+  if (!in_bounds(a.status, list, a.lists)) return;
   for (int i = tid; i < a.n; i += kThreads) a.keys[list * a.n + i] = i < have ? sh.best[i] : 0;
   if (tid == 0) a.stats[list] = make_float2(run_m, run_s);
 }
@@ -417,11 +430,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(SelectArgs a) 
 // The n largest of each group's lists of n keys (descending, distinct but for the 0 of no key): neighbours are merged,
 // a key's rank being its place in its own list plus the number of the other's that are greater (binary search), until
 // one list is left.  Lists in `from`, in turns to `to`; returns where they end.  (Four at a time, three searches side
-// by side, took 1 to 2 us longer.)
-__device__ __forceinline__ uint64_t* merge_lists(uint64_t* from, uint64_t* to, int groups, int lists, int n) {
+// by side, took 1 to 2 us longer.)  `size`: keys that both hold at least.
+__device__ __forceinline__ uint64_t* merge_lists(uint64_t* from, uint64_t* to, int groups, int lists, int n, int size, int32_t* status) {
   while (lists > 1) {
     const int half = (lists + 1) / 2, total = groups * lists * n;
-    for (int t = threadIdx.x; t < total; t += blockDim.x) {
+    for (int t = threadIdx.x; t < total && in_bounds(status, total - 1, size); t += blockDim.x) {
       const int list = t / n, j = t - list * n, g = list / lists, l = list - g * lists;
       const uint64_t key = from[t];
       int rank = j;
@@ -430,14 +443,14 @@ __device__ __forceinline__ uint64_t* merge_lists(uint64_t* from, uint64_t* to, i
         int lo = 0, hi = n - j;  // further ones do not matter
         while (lo < hi) {
           const int mid = (lo + hi) / 2;
-          if (other[mid] > key)
+          if (in_bounds(status, (g * lists + (l ^ 1)) * n + mid, total) && other[mid] > key)
             lo = mid + 1;
           else
             hi = mid;
         }
         rank += lo;
       }
-      if (rank < n) to[(g * half + l / 2) * n + rank] = key;
+      if (rank < n && in_bounds(status, (g * half + l / 2) * n + rank, size)) to[(g * half + l / 2) * n + rank] = key;
     }
     __syncthreads();
     uint64_t* const swap = from;
@@ -454,9 +467,10 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
 
 // The same for up to kMaxParts lists by a warp per group: n times the largest of the lists' heads, of which a lane holds
 // those of lists lane and lane + 32.
-__device__ __forceinline__ void merge_heads(const uint64_t* from, uint64_t* to, int groups, int lists, int n) {
+__device__ __forceinline__ void merge_heads(const uint64_t* from, uint64_t* to, int groups, int lists, int n, int size, int32_t* status) {
   const int lane = threadIdx.x & 31;
   for (int g = threadIdx.x / 32; g < groups; g += blockDim.x / 32) {
+    if (!in_bounds(status, (g + 1) * lists * n - 1, size) || !in_bounds(status, lists - 1, kMaxParts)) break;
     const uint64_t* const mine = from + g * lists * n;
     int h0 = 0, h1 = 0;
     uint64_t k0 = lane < lists ? mine[lane * n] : 0, k1 = lane + 32 < lists ? mine[(lane + 32) * n] : 0;
@@ -485,6 +499,7 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
   // log-sum-exp of every beam, as maximum and log of the sum: a warp takes its parts' statistics, at most two per lane
   for (int k = warp; k < a.beams; k += warps) {
     const int64_t r = b * a.beams + k;
+    if (!in_bounds(a.status, (r + 1) * a.parts - 1, a.lists) || !in_bounds(a.status, k, ORPO_MAX_BEAMS)) break;
     const bool ended = a.finished != nullptr && a.finished[r];
     const float score = a.score[r];
     const float2 none = make_float2(-INFINITY, 0.f);
@@ -512,15 +527,18 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
     const int group = min(a.group, a.beams - k0), per_beam = a.parts * n;
     const uint64_t* const src = a.keys + (b * a.beams + k0) * per_beam;
 #pragma unroll 4
-    for (int t = tid; t < group * per_beam; t += blockDim.x) area0[t] = over[k0 + t / per_beam] ? 0 : src[t];
+    for (int t = tid; t < group * per_beam; t += blockDim.x)
+      if (in_bounds(a.status, t, a.area) && in_bounds(a.status, (b * a.beams + k0) * per_beam + t, a.lists * n))
+        area0[t] = over[k0 + t / per_beam] ? 0 : src[t];
     __syncthreads();
     const uint64_t* top = area1;
     if (a.parts <= kFewParts)
-      top = merge_lists(area0, area1, group, a.parts, n);
+      top = merge_lists(area0, area1, group, a.parts, n, a.area, a.status);
     else
-      merge_heads(area0, area1, group, a.parts, n);
+      merge_heads(area0, area1, group, a.parts, n, a.area, a.status);
     for (int t = tid; t < group * n; t += blockDim.x) {
       const int k = k0 + t / n, j = t % n;
+      if (!in_bounds(a.status, k, a.beams)) break;
       const float score = beam_score[k], m = beam_max[k];
       float y = -INFINITY;
       if (over[k]) {
@@ -536,10 +554,11 @@ __global__ void __launch_bounds__(kMergeThreads) select_merge_kernel(SelectArgs 
     }
     __syncthreads();
   }
-  const uint64_t* const top = a.beams > 1 ? merge_lists(best, area0, 1, a.beams, n) : best;
+  const uint64_t* const top = a.beams > 1 ? merge_lists(best, area0, 1, a.beams, n, a.beams * n, a.status) : best;
   for (int i = tid; i < n; i += blockDim.x) {
     const uint64_t key = top[i];
     const int from = (int)~(uint32_t)key, k = from / n;
+    if (!in_bounds(a.status, from, a.beams * n)) continue;
     const int64_t at = b * n + i;
     a.out_score[at] = ord_to_float((uint32_t)(key >> 32));
     a.out_parent[at] = k;
@@ -596,7 +615,7 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
   const int size = logits_bf16 ? 2 : 4;
   const RowPlan plan = row_plan(V, logits_bf16 != 0, aligned16(logits) && (ld_logits * size) % 16 == 0);
   SelectArgs a{logits, ld_logits, score, finished, eos, beams, (int)V, n, out_score, out_parent, out_token,
-               out_finished, static_cast<uint64_t*>(workspace), nullptr, plan.parts, plan.chunks, 0, 0, status};
+               out_finished, static_cast<uint64_t*>(workspace), nullptr, plan.parts, plan.chunks, 0, 0, rows * plan.parts, status};
   a.stats = reinterpret_cast<float2*>(a.keys + rows * plan.parts * n);
   // rows in launches of at most 65535
   prof_begin(K_BEAM, st);
@@ -607,6 +626,7 @@ extern "C" int orpo_beam_select(const void* logits, int64_t ld_logits, int logit
     if (finished) c.finished = finished + r;
     c.keys = a.keys + r * plan.parts * n;
     c.stats = a.stats + r * plan.parts;
+    c.lists = a.lists - r * plan.parts;
     const dim3 grid((unsigned)plan.parts, (unsigned)std::min<int64_t>(65535, rows - r));
     e = logits_bf16 ? launch_dependent(select_rows_kernel<true>, grid, kThreads, 0, st, c)
                     : launch_dependent(select_rows_kernel<false>, grid, kThreads, 0, st, c);

@@ -2,7 +2,7 @@
 //
 // Built with ORPO_DEBUG_BOUNDS, in_bounds(status, i, n) tests 0 <= i < n for an access whose index
 // is computed (partial and block-max slots, skip bitmaps and tile lists, shared-memory tables,
-// quantised weights and scales); a miss ORs ORPO_STATUS_BOUNDS into the status word and the caller
+// quantised weights and scales, the decode step's rows, rings, lists of keys and states); a miss ORs ORPO_STATUS_BOUNDS into the status word and the caller
 // skips the access, so a bad index is reported instead of touching memory.  Without the flag it is
 // the constant true and every check compiles away.
 #pragma once

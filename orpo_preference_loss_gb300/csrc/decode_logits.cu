@@ -38,12 +38,14 @@ __global__ void __launch_bounds__(256) logits_generic_kernel(LogitsArgs a) {
   const int64_t g0 = v * (a.d / a.group);
   float acc[kRowsTile] = {};
   for (int c = lane; c < a.d / 8; c += 32) {
+    if (!in_bounds(a.status, v * (a.d / 8) + c, (int64_t)a.V * (a.d / 8))) break;
     uint2 raw = make_uint2(0u, 0u);
     if constexpr (kBits == 4)
       raw.x = __ldg(reinterpret_cast<const uint32_t*>(row) + c);
     else
       raw = __ldg(reinterpret_cast<const uint2*>(row) + c);
     const int64_t gi = g0 + (8 * c) / a.group;
+    if (!in_bounds(a.status, gi, scales_size(a))) break;
     // (scale, scale) and (bias, bias); product and sum round once, as in the tensor-core kernel
     const uint32_t s2 = __ldg(a.scales + gi) * 0x10001u, b2 = __ldg(a.biases + gi) * 0x10001u;
     float w[8];
@@ -64,7 +66,7 @@ __global__ void __launch_bounds__(256) logits_generic_kernel(LogitsArgs a) {
     }
 #pragma unroll
     for (int m = 0; m < kRowsTile; ++m) {
-      if (m0 + m < a.M) {
+      if (m0 + m < a.M && in_bounds(a.status, (int64_t)(m0 + m) * a.ld_h + 8 * c + 7, h_size(a))) {
         const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.h + (int64_t)(m0 + m) * a.ld_h) + c);
         const uint32_t p[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll

@@ -4,6 +4,7 @@
 
 #include <stdint.h>
 
+#include "bounds.cuh"
 #include "ptx.cuh"
 
 namespace orpo {
@@ -23,6 +24,11 @@ struct LogitsArgs {
   int32_t* status;
 };
 
+// Elements from the first to the last of h, of the logits, and values of scales or biases (for the bounds-checked build).
+__device__ __forceinline__ int64_t h_size(const LogitsArgs& a) { return (int64_t)(a.M - 1) * a.ld_h + a.d; }
+__device__ __forceinline__ int64_t out_size(const LogitsArgs& a) { return (int64_t)(a.M - 1) * a.ld_out + a.V; }
+__device__ __forceinline__ int64_t scales_size(const LogitsArgs& a) { return (int64_t)a.V * (a.d / a.group); }
+
 // cap tanh(z / cap), inv = 1 / cap: the series for small |z / cap| (no cancellation), else by ex2; both are
 // computed and one taken, so that lanes do not part
 __device__ __forceinline__ float softcap_of(float z, float cap, float inv) {
@@ -35,6 +41,7 @@ __device__ __forceinline__ float softcap_of(float z, float cap, float inv) {
 __device__ __forceinline__ void store_logit(const LogitsArgs& a, int m, int v, float z) {
   const float x = a.softcap > 0.f ? softcap_of(z, a.softcap, 1.f / a.softcap) : z;
   const int64_t at = (int64_t)m * a.ld_out + v;
+  if (!in_bounds(a.status, at, out_size(a))) return;
   if (a.out_bf16)
     static_cast<uint16_t*>(a.out)[at] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xffffu);
   else

@@ -91,6 +91,7 @@ struct TcArgs {
   int stages;             // weight ring
   int hslots;             // streamed h: segments in the ring
   const uint8_t* image;   // streamed h: [m tiles][units] units as shared memory holds them
+  int64_t image_bytes;
   int word_groups;        // a scale word is a group (and its index that of the group)
   int wide_scales;        // and a segment's scales and biases are one aligned word of up to 16 bytes each
   int prefetch_scales;    // they start on 16 bytes
@@ -235,6 +236,11 @@ __device__ __forceinline__ uint32_t group_of(const TcArgs& p, uint32_t word) {
 template <int W>
 struct Shifted {
   static constexpr int kWord = W > 2 ? 8 : 4, n = W * 2 / kWord, kWords = (n + 1) * kWord / 4;
+  // whether what load(base + at) reads lies among `size` values from `base` on
+  static __device__ __forceinline__ bool inside(const uint16_t* base, int64_t at, int64_t size, int32_t* status) {
+    const int s = (int)(reinterpret_cast<uintptr_t>(base + at) & (kWord - 1)) / 2;
+    return in_bounds(status, at - s, size) && in_bounds(status, at - s + (s != 0 ? n + 1 : n) * (kWord / 2) - 1, size);
+  }
   static __device__ __forceinline__ void load(const uint16_t* p, uint32_t (&w)[kWords]) {
     const uint32_t s = (uint32_t)reinterpret_cast<uintptr_t>(p) & (kWord - 1);
     const uint8_t* const q = reinterpret_cast<const uint8_t*>(p) - s;
@@ -262,7 +268,8 @@ struct Shifted {
 __device__ __forceinline__ void prefetch_scales(const TcArgs& p, int64_t tile, int lane) {
   const LogitsArgs& a = p.a;
   const uint32_t bytes = (uint32_t)(p.rows * 2) * p.ngroups;  // a multiple of 16: p.rows is one of 8
-  if (p.prefetch_scales && (lane == 0 || lane == 1) && (tile + 1) * p.rows <= a.V)
+  if (p.prefetch_scales && (lane == 0 || lane == 1) && (tile + 1) * p.rows <= a.V &&
+      in_bounds(a.status, tile * bytes + bytes - 1, 2 * scales_size(a)))
     l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + tile * bytes, bytes);
 }
 
@@ -302,21 +309,24 @@ struct ScaleRole {
       x.shift = 0;
       const int g0 = W ? seg * W : (int)group_of(p, (uint32_t)(seg * p.seg_words));
       const uint16_t *sr = s + g0, *br = b + g0;
-      if (row < a.V) {
+      const int64_t at = row * p.ngroups + g0, size = scales_size(a);
+      if (row < a.V && in_bounds(a.status, at, size)) {
         if constexpr (kShift) {
           // (the row's first group + g0 + W, and the slack of a shifted load, stay inside the arrays)
-          if (p.prefetch_scales && row * p.ngroups + g0 + W + 4 <= (int64_t)a.V * p.ngroups) {
+          if (p.prefetch_scales && at + W + 4 <= size && Shifted<W>::inside(a.scales, at, size, a.status) &&
+              Shifted<W>::inside(a.biases, at, size, a.status)) {
             x.shift = (uint32_t)reinterpret_cast<uintptr_t>(sr) & (Shifted<W>::kWord - 1);  // both arrays start on 16 bytes
             Shifted<W>::load(sr, x.sc);
             Shifted<W>::load(br, x.bi);
           } else {
 #pragma unroll
             for (int i = 0; i < W; ++i)
-              if (g0 + i < p.ngroups) {
+              if (g0 + i < p.ngroups && in_bounds(a.status, at + i, size)) {
                 x.sc[i / 2] |= (uint32_t)__ldg(sr + i) << (16 * (i & 1));
                 x.bi[i / 2] |= (uint32_t)__ldg(br + i) << (16 * (i & 1));
               }
           }
+        } else if (W && !in_bounds(a.status, at + W - 1, size)) {
         } else if constexpr (W == 8) {
           const uint4 u = __ldg(reinterpret_cast<const uint4*>(sr)), v = __ldg(reinterpret_cast<const uint4*>(br));
           x.sc[0] = u.x, x.sc[1] = u.y, x.sc[2] = u.z, x.sc[3] = u.w;
@@ -332,7 +342,7 @@ struct ScaleRole {
 #pragma unroll
           for (int i = 0; i < kWords; ++i) {
             const int gi = (int)group_of(p, (uint32_t)(seg * p.seg_words + i)) - g0;
-            if (i < p.seg_words && g0 + gi < p.ngroups) {
+            if (i < p.seg_words && g0 + gi < p.ngroups && in_bounds(a.status, at + gi, size)) {
               x.sc[i / 2] |= (uint32_t)__ldg(sr + gi) << (16 * (i & 1));
               x.bi[i / 2] |= (uint32_t)__ldg(br + gi) << (16 * (i & 1));
             }
@@ -349,6 +359,7 @@ struct ScaleRole {
     auto put = [&](const Set& x) {
       if (!wait_warp(ctl, &ctl->w_empty[stage], ph ^ 1u, a.status)) return false;
       const uint32_t out = sring + stage * scale_bytes(1024 / kSegK) + (row0 + lane) * 4;
+      if (!in_bounds(a.status, stage, p.stages) || !in_bounds(a.status, p.seg_words - 1, kSegK / 32)) return false;
       uint32_t sc[kPairs], bi[kPairs];
       if constexpr (kShift) {
         Shifted<W>::take(x.sc, x.shift, sc);
@@ -489,7 +500,8 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     grid_wait();  // set up; from here on memory is read (streamed: h's image waits, and this kernel for that one)
     if (warp >= kSumWarp)
       each_piece([&](uint32_t at, int m, int k) {
-        if (8 * k < a.d)
+        if (!in_bounds(a.status, at + 15 - smem_u32(hbuf), p.segs * kHSeg)) return;
+        if (8 * k < a.d && in_bounds(a.status, (int64_t)(m0 + m) * a.ld_h + 8 * k + 7, h_size(a)))
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(a.h + (int64_t)(m0 + m) * a.ld_h + 8 * k)
                        : "memory");
         else
@@ -506,6 +518,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     if (warp >= kSumWarp) {  // resident h is here: into the dequantised order
       asm volatile("cp.async.wait_all;" ::: "memory");
       each_piece([&](uint32_t at, int, int) {
+        if (!in_bounds(a.status, at + 15 - smem_u32(hbuf), p.segs * kHSeg)) return;
         const uint4 x = reorder_pairs<kBits>(lds128(at));
         st_shared_v4(at, x.x, x.y, x.z, x.w);
       });
@@ -523,7 +536,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     int row0 = blockIdx.x * p.rows;
     for (int i = 0; ok && i < my_tiles; ++i, row0 += gridDim.x * p.rows) {
       for (int seg = 0; seg < p.segs; ++seg) {
-        ok = wait_warp(ctl, &ctl->w_empty[st], ph, a.status);
+        ok = in_bounds(a.status, st, p.stages) && wait_warp(ctl, &ctl->w_empty[st], ph, a.status);
         if (!ok) break;
         if (leader) {
           mbar_arrive_expect_tx(&ctl->w_full[st], 128 * p.rows);
@@ -548,7 +561,8 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
       for (int i = 0; ok && i < my_tiles; ++i) {
         const uint8_t* src = image;
         for (int seg = 0; seg < p.segs; ++seg, ++it, src += kHSeg) {
-          ok = wait_warp(ctl, &ctl->h_empty[hs], hp, a.status);
+          ok = in_bounds(a.status, hs, p.hslots) && in_bounds(a.status, src + kHSeg - 1 - p.image, p.image_bytes) &&
+               wait_warp(ctl, &ctl->h_empty[hs], hp, a.status);
           if (!ok) break;
           if (leader) {
             mbar_arrive_expect_tx(&ctl->h_full[hs], kHSeg);
@@ -586,6 +600,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
           ok = ok && wait_warp(ctl, &ctl->a_full[slot], ap, a.status);
           if constexpr (kStream) ok = ok && wait_warp(ctl, &ctl->h_full[hs], hp, a.status);
         }
+        ok = ok && in_bounds(a.status, slot, kASlots) && in_bounds(a.status, kStream ? hs : seg, kStream ? p.hslots : p.segs);
         if (!ok) break;
         tc_fence_after();
         const bool last = j == kAccSegs - 1 || seg + 1 == p.segs;
@@ -669,7 +684,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
         const int n_live = a.M - m0 - n0;
 #pragma unroll
         for (int n = 0; n < kCols; ++n) {
-          if (n >= n_live) break;
+          if (n >= n_live || !in_bounds(a.status, at + n * a.ld_out, out_size(a))) break;
           float x = acc[n];
           if (a.softcap > 0.f) x = softcap_of(x, a.softcap, inv_cap);
           if (a.out_bf16) {
@@ -694,7 +709,8 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
     uint32_t slot = wg, aph = 0;   // place in tensor memory
     bool ok = true;
     for (int64_t left = (int64_t)my_tiles * p.segs - wg; left > 0; left -= kGroups) {
-      ok = wait_warp(ctl, &ctl->w_full[stage], wph, a.status);
+      ok = in_bounds(a.status, stage, p.stages) && in_bounds(a.status, slot, kASlots) &&
+           in_bounds(a.status, (kSegK / 32 - 1) >> p.shift, kSegK / 32) && wait_warp(ctl, &ctl->w_full[stage], wph, a.status);
       if (!ok) break;
       const uint32_t wst = wrow + stage * kBoxBytes, sst = srow + stage * kScaleBytes;
       const bool plain = (lds32(smem_u32(ctl->plain[stage])) >> (8 * q) & 1u) != 0;
@@ -764,7 +780,7 @@ __global__ void __launch_bounds__(tc_threads(NP), 1)
 // h for the streamed form: per m tile of `rows` rows and block of 64 columns the block as shared memory holds it
 // (128-byte swizzled rows), 16-byte pieces in the dequantised order, zero where h has no element.
 template <int kBits>
-__global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, int blocks, int64_t pieces, uint4* image) {
+__global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, int blocks, int64_t pieces, uint4* image, int64_t size) {
   // set up while the kernel before it in the stream ends; the products' kernel may be set up once that one has
   grid_wait();
   grid_trigger();
@@ -774,8 +790,8 @@ __global__ void __launch_bounds__(256) h_image_kernel(LogitsArgs a, int rows, in
   const int64_t blk = i / 8 / rows % blocks, m = i / 8 / rows / blocks * rows + row;
   const int64_t k = blk * 64 + (int)((i ^ row) & 7) * 8;
   uint4 x = make_uint4(0u, 0u, 0u, 0u);
-  if (m < a.M && k < a.d) x = reorder_pairs<kBits>(__ldg(reinterpret_cast<const uint4*>(a.h + m * a.ld_h + k)));
-  image[i] = x;
+  if (m < a.M && k < a.d && in_bounds(a.status, m * a.ld_h + k + 7, h_size(a))) x = reorder_pairs<kBits>(__ldg(reinterpret_cast<const uint4*>(a.h + m * a.ld_h + k)));
+  if (in_bounds(a.status, i, size)) image[i] = x;
 }
 
 constexpr int kMinStages = 6;  // of weights, beside resident or streamed h
@@ -823,6 +839,7 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
   const int h_bytes = (kStream ? p.hslots : p.segs) * kUnits * kHUnit;
   p.stages = std::min(kMaxStages, (kSmemLimit - fixed - h_bytes) / stage) / kGroups * kGroups;
   p.image = static_cast<const uint8_t*>(workspace);
+  p.image_bytes = kStream ? (int64_t)logits_tc_workspace(kBits, a.M, a.d) : 0;
   const int smem = p.stages * stage + h_bytes + fixed + 1024;
   CUtensorMap mw;
   if (!encode_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.wq, row_bytes, a.V, row_bytes, 128, p.rows)) return cudaErrorNotSupported;
@@ -834,7 +851,7 @@ cudaError_t launch_np(const LogitsArgs& a, int sms, void* workspace, cudaStream_
     const int blocks = p.units * 2;
     const int64_t pieces = (int64_t)mt * blocks * NP * 8;
     if (cudaError_t e = launch_dependent(h_image_kernel<kBits>, dim3((unsigned)cdiv(pieces, 256)), 256, 0, st, a, NP, blocks,
-                                         pieces, static_cast<uint4*>(workspace)))
+                                         pieces, static_cast<uint4*>(workspace), p.image_bytes / 16))
       return e;
   }
   return launch_dependent(kernel, dim3((unsigned)std::min(p.tiles, sms), (unsigned)mt), tc_threads(NP), (size_t)smem, st, mw, p);
