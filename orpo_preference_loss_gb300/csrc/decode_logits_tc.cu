@@ -269,7 +269,7 @@ __device__ __forceinline__ void prefetch_scales(const TcArgs& p, int64_t tile, i
   const LogitsArgs& a = p.a;
   const uint32_t bytes = (uint32_t)(p.rows * 2) * p.ngroups;  // a multiple of 16: p.rows is one of 8
   if (p.prefetch_scales && (lane == 0 || lane == 1) && (tile + 1) * p.rows <= a.V &&
-      in_bounds(a.status, tile * bytes + bytes - 1, 2 * scales_size(a)))
+      in_bounds(a.status, tile * bytes + bytes - 1, (int64_t)a.V * p.ngroups * 2))
     l2_prefetch(reinterpret_cast<const uint8_t*>(lane == 0 ? a.scales : a.biases) + tile * bytes, bytes);
 }
 
@@ -309,7 +309,7 @@ struct ScaleRole {
       x.shift = 0;
       const int g0 = W ? seg * W : (int)group_of(p, (uint32_t)(seg * p.seg_words));
       const uint16_t *sr = s + g0, *br = b + g0;
-      const int64_t at = row * p.ngroups + g0, size = scales_size(a);
+      const int64_t at = row * p.ngroups + g0, size = (int64_t)a.V * p.ngroups;
       if (row < a.V && in_bounds(a.status, at, size)) {
         if constexpr (kShift) {
           // (the row's first group + g0 + W, and the slack of a shifted load, stay inside the arrays)
