@@ -39,7 +39,8 @@ extern "C" {
  *   W[v, j] = bf16(scales[v, j/group] * q[v, j] + biases[v, j/group]), product and sum rounded once.  (orpo_head_fwd_q
  *   rounds to fp32 and then to bf16: its weights are these but where the exact value lies within fp32's rounding
  *   of the middle between two bf16 values, and there one bf16 unit off at most.)
- *   z[m, v] = sum_j h[m, j] W[v, j]       (products of bf16 values, fp32 accumulation)
+ *   z[m, v] = sum_j h[m, j] W[v, j]       (products of bf16 values, fp32 accumulation: the tensor core's adds truncate
+ *   within 512 columns, and those sums are added with rounding; off by about 3e-7 of the largest logit)
  *   logits[m, v] = softcap * tanh(z / softcap) if softcap > 0, else z; rounded once when bf16
  * h: bf16 [M, d], rows ld_h elements apart (ld_h >= d, a multiple of 8; e.g. the last positions of
  * [M, T, d] hidden states are h + (T-1) d with ld_h = T d), 16-byte aligned.  wq, scales, biases,
@@ -80,7 +81,8 @@ int orpo_head_logits_q(const void* h_bf16, int64_t ld_h, const uint8_t* wq, cons
  * When n == beams, out_score may be score itself and out_finished may be finished itself.
  * eos: a token in [0, V), or -1 for none (finished must then be NULL).
  * Device errors: ORPO_STATUS_NONFINITE (a NaN or +inf logit of a live beam, or a NaN score; masked
- * logits, -inf or the type's lowest value, are no error).
+ * logits, -inf or any finite value, are no error; -inf is the cheap one, a finite value on all but a few tokens costs
+ * about ten times as much).
  * Results do not depend on run-to-run scheduling.
  * Limits: batch >= 0, 1 <= beams <= ORPO_MAX_BEAMS, 1 <= n <= min(ORPO_MAX_SELECT, V),
  * batch * beams <= 2^20, V <= 2^31 - 2^16.  The workspace (16-byte aligned) must hold

@@ -644,7 +644,8 @@ class BeamDecoder:
     A step is the three C entry points of orpo_decode.h in order on the current stream: logits of the
     beams' last hidden rows, selection of each batch entry's `beams` best continuations, and the states
     following their parents.  score, finished, parent and token stay on the device; nothing waits on
-    the host, so a step can be recorded in a CUDA graph."""
+    the host, so a step can be recorded in a CUDA graph.  The constructor and reset fill the buffers on the
+    current stream: a step on another stream has to be ordered behind them."""
 
     def __init__(self, batch: int, beams: int, V: int, d: int, bits: int = 4, group: int = 64, softcap: float = 0.0,
                  eos: int = -1, logits_dtype=torch.float32, device="cuda"):

@@ -7,14 +7,14 @@
 // those, so the parents may form any map (cycles, many children) without a second buffer.  A source that several
 // beams take is asked for several times by one thread, of which L1 makes one.  Above 8 beams a thread's sources
 // would leave too few threads their registers: there a CTA takes kTile pieces of all moved beams through shared memory
-// (9 beams, 114 MB: 30 us; with 16 sources in registers 35).
+// (9 beams, 114 MB: 28 us; with 16 sources in registers 35).
 // Units of any other size: beams start at any byte.  A CTA takes a window of a (slab, entry, row) through shared
 // memory; each source lies there as far from a 16-byte boundary as in memory, and what goes out is put together for
 // the destination's own boundaries by funnel shifts, so that all but the ends moves 16 bytes at a time (bf16 heads of
-// 33, 6 beams, 254 MB: 77 us; in pieces of 2 bytes 91.  Heads of 36 in pieces of 8 bytes: 64, and by bytes 78).
+// 33, 6 beams, 254 MB: 72 us; in pieces of 2 bytes 91.  Heads of 36 in pieces of 8 bytes: 64, and by bytes 78).
 // Bound by the bytes moved, so each CTA stays with one (slab, entry, row) for up to kMaxPer pieces, with 16
 // loads of a thread in flight, and reads the parents once: one piece per thread and CTA cost a
-// quarter of the rate.  Measured: 524 MB (16 slabs, 8 x 4 beams, 3 moved, heads of 128 bf16) 80.5 us, 6.5 TB/s or 96% of
+// quarter of the rate.  Measured: 524 MB (16 slabs, 8 x 4 beams, 3 moved, heads of 128 bf16) 81 us, 6.5 TB/s or 96% of
 // the rate of a plain copy.
 #include <algorithm>
 

@@ -11,21 +11,22 @@
 //
 // Row kernel: a CTA reads a part of one beam's row once, 8192 fp32 or 16384 bf16 logits at a time in
 // registers (32 words per thread, all loads in flight together), and leaves the part's max, sum of exp
-// and n largest keys.  It is bound by instructions before it is by memory, so a logit costs about five
-// (bf16): unpack, half a packed max, and multiply-add, ex2 and add of the sum, two at a time.
+// and n largest keys.  A logit costs 12 to 15 instructions in all, of which about five are its own (bf16: unpack, half a
+// packed max, and multiply-add, ex2 and add of the sum, two at a time); no unit is near its limit.
 // The n largest come without sorting: the r-th largest of a warp's 32 lane maxima, r = ceil(n / warps),
 // has r elements of that warp at or above it, so the least of these over the warps has n of the CTA;
 // what reaches it (20 to 140 elements for n = 1 to 64 of well-mixed logits) goes to shared memory, and each
-// finds its rank by counting.  Where more than kCap reach it (long runs of equal or sorted logits), the exact
-// n-th largest is found by bisection on the key.
+// finds its rank by counting.  Where more than kCap reach it (long runs of equal or sorted logits, masks of a finite value
+// with fewer than n live tokens), the exact n-th largest is found by bisection on the key, which costs 5 to 25 times
+// as much (32 x 8 rows of 128256 bf16, n 16: 370 to 720 us).
 // Merge kernel: one CTA per entry merges the parts' sorted lists of every beam, then the beams' sorted proposals.  Up
 // to 8 lists are merged neighbours by neighbours, more by taking the largest of their heads n times, a warp per beam:
 // its warp-wide maxima share one slow unit, which costs 49 clocks a beam and key.  (15 x 14 rows of 12692, n = 28: 13.7 us
 // by neighbours, 21.9 by heads; 4 x 4 rows of 262144, n = 8, 32 parts: 12.2 and 10.4.)
-// Measured: 32 x 8 rows of 128256 bf16 (65.7 MB), n = 16: 27.6 us, 2.4 TB/s, of which the row kernel 23: a CTA's chunk
+// Measured: 32 x 8 rows of 128256 bf16 (65.7 MB), n = 16: 28 us, 2.3 TB/s, of which the row kernel 23: a CTA's chunk
 // takes 11 to 12 thousand clocks, 3 to 5 of them waiting for its loads and the rest a chain of short steps (threshold,
 // sum, candidates, ranks) between six barriers, with 59% of issue slots used; without the sum it took 1.4 us less.
-// 4 x 4 rows of 262144 fp32, n = 8: 10.1 us.
+// 4 x 4 rows of 262144 fp32, n = 8: 10.4 us, 9.6 out of a graph.
 #include <math.h>
 #include <stddef.h>
 

@@ -25,9 +25,9 @@
 // d 2560, V 262144), and with the plain form of the dequantisation in a loop apart 70.  Tensor memory holds A of three
 // segments (8-bit: six) beside two sets of accumulators.
 //
-// Measured: one row, d 2560, V 262144, groups of 64, fp32 logits: 65 us, 5.8 TB/s or 86% of the rate of a plain copy;
-// steady state 855 clocks a segment, where that rate would allow 790.  64 rows, d 4096, V 128256: 73 us, 4.3 TB/s
-// and 920 TFLOP/s; without the products 63.  Calls with little work per SM (8 rows, 8 bits, d 2048, V 32000: 17 us for
+// Measured: one row, d 2560, V 262144, groups of 64, fp32 logits: 65 to 66 us, 5.8 TB/s or 86% of the rate of a plain copy;
+// steady state 855 clocks a segment, where that rate would allow 790.  64 rows, d 4096, V 128256: 73 to 77 us, 4.2 TB/s
+// and 900 TFLOP/s; without the products 63.  Calls with little work per SM (8 rows, 8 bits, d 2048, V 32000: 17 us for
 // 74 MB) spend 4 us until the first product: memory answers the first requests of all SMs at once.
 //
 // Order of k: 4-bit dequantisation yields the pairs (0,4), (1,5), (2,6), (3,7) of 8 consecutive weights
@@ -35,7 +35,8 @@
 // time.  Rows of h that fit beside the weights (16 of d up to 3328, 64 of 768) are loaded and put in that order by
 // each CTA, once.  More are streamed: a small kernel first writes h in that order, and as
 // shared memory holds it, to the workspace, and each CTA fetches every segment with one plain bulk copy for each
-// of its tiles.  At 64 rows that is twice the weights' bytes from L2, which keeps up (64 rows, d 4096: 73 us).
+// of its tiles.  At 64 rows that is twice the weights' bytes from L2, which keeps up: pairs of CTAs
+// that shared each segment took no less.
 // Accuracy: the tensor core truncates as it accumulates (measured: 1e-9 of the result per product, one
 // sign), so an accumulator spans 512 columns and those sums are added in registers, rounding.
 #include <math.h>
@@ -282,7 +283,7 @@ struct ScaleRole {
   int my_tiles, row0, lane;
 
   // W: words per segment, a group each, or 0: any number, groups repeated; kWide: loaded as one vector, else from any
-  // address (24 rows, d 3232, V 96333, 101 groups a row: 58 us; element by element 69)
+  // address (24 rows, d 3232, V 96333, 101 groups a row: 56 us; element by element 69)
   template <int W, bool kWide>
   __device__ __forceinline__ void run() const {
     constexpr bool kShift = W > 1 && !kWide;
