@@ -3,14 +3,18 @@
  *
  * The pairs the head trains on are responses that were generated; on-policy pairs come from the
  * same head, in the same quantised format.  These entry points are that other direction, one
- * decode step in three calls on one stream:
+ * decode step in a few calls on one stream:
  *
  *   orpo_head_logits_q   logits of a few rows of h (the beams' last positions) out of the
  *                        affine group-quantised head that orpo_head_fwd_q reads
+ *   orpo_logits_adjust   penalties for repeated tokens, biases and grammar masks, in place on
+ *                        those logits (optional)
  *   orpo_beam_select     log-softmax over the vocabulary and the n best continuations over
  *                        beams x vocabulary, per batch entry
  *   orpo_beam_reorder    the beams' states (key/value caches, recurrent states) follow their
- *                        parents, in place
+ *                        parents, in place; states in shared pages: orpo_pages.h
+ *   orpo_beam_history    the beams' token histories, which the penalties read, follow their
+ *                        parents and get the new tokens
  *
  * The mlx-bun documentation pages leave generation out ("Training — design" starts from given
  * chosen / rejected responses); the weight format and the softcap are those of their head (§5.1
@@ -113,6 +117,55 @@ int orpo_beam_select(const void* logits, int64_t ld_logits, int logits_bf16, con
 int orpo_beam_reorder(void* state, const int32_t* parent, int64_t ld_parent, const int32_t* length,
                       int64_t outer, int64_t batch, int beams, int64_t rows, int64_t capacity,
                       int64_t unit_bytes, int32_t* status, void* stream);
+
+/*
+ * Penalties, biases and masks on the logits of `batch` entries with `beams` rows each, in place.  With r = b * beams + k,
+ * H = history[r, 0 .. length[b]-1] and G = history[r, prompt[b] .. length[b]-1] (prompt NULL: 0), for every token v:
+ *   1. v in H:  x > 0 ? x / repetition : x * repetition
+ *   2. v in G, n times:  x - (presence + frequency * n)
+ *   3. x + the sum, in order of j, of bias_value[b, j] over the j with bias_token[b, j] = v
+ *   4. -inf where bit v % 32 of masks[mask_row[r], v / 32] is 0, and where v would complete an n-gram of no_repeat tokens
+ *      that H holds already: H[t] = v for some t >= no_repeat - 1, and the no_repeat - 1 tokens before t are H's last ones
+ *      (no_repeat = 1: every v in H; an n-gram with a token outside [0, V) is none).
+ * in fp32, the result rounded once when bf16; IEEE arithmetic for infinities and NaN, but a token that step 4 bans is -inf
+ * whatever it was.  Logits that no step concerns are neither read nor written, so a call without masks touches few.
+ * History tokens outside [0, V) (padding) count nowhere, nor do bias tokens outside it.
+ *   logits   fp32 or bf16 [batch * beams, V], rows ld_logits >= V elements apart
+ *   history  int32 [batch * beams, capacity], rows ld_history >= capacity apart; length, prompt: int32 [batch].  history may be
+ *            NULL where repetition = 1, presence = frequency = 0 and no_repeat = 0 (it is not read then); prompt may be NULL
+ *   bias_token, bias_value  int32, fp32 [batch, n_bias], rows ld_bias apart: 0 (one list for all) or >= n_bias
+ *   masks    uint32 [n_masks, ceil(V / 32)], rows ld_masks apart, 1 = allowed; mask_row: int32 [batch * beams], -1 for a row
+ *            without a mask.  Both NULL: no masks.
+ * Device errors: ORPO_STATUS_PARENT (a length outside [0, capacity]; that entry's rows are left as they are),
+ * ORPO_STATUS_MASK (a mask_row outside [-1, n_masks); that row is left as it is).
+ * Results do not depend on run-to-run scheduling.  No workspace.
+ * Limits: batch >= 0, 1 <= beams <= 2^20, batch * beams <= 2^20, 1 <= V <= 2^31 - 2^16, 0 <= capacity < 2^28, 0 <= n_bias
+ * <= ORPO_MAX_BIAS, 0 <= no_repeat <= ORPO_MAX_NGRAM, 1 <= n_masks < 2^31 where masks are given; repetition > 0; all
+ * penalties finite.  4-byte alignment (2 for bf16 logits).
+ */
+#define ORPO_MAX_BIAS 65536
+#define ORPO_MAX_NGRAM 32
+int orpo_logits_adjust(void* logits, int64_t ld_logits, int logits_bf16, int64_t batch, int beams, int64_t V,
+                       const int32_t* history, int64_t ld_history, int64_t capacity, const int32_t* length,
+                       const int32_t* prompt, float repetition, float presence, float frequency, int no_repeat,
+                       const int32_t* bias_token, const float* bias_value, int64_t ld_bias, int64_t n_bias,
+                       const uint32_t* masks, int64_t ld_masks, int64_t n_masks, const int32_t* mask_row,
+                       int32_t* status, void* stream);
+
+/*
+ * The beams' token histories follow their parents, in place, and get the selected tokens:
+ *   history[b * beams + k, t] <- history[b * beams + parent[b, k], t],  t < length[b], as if all were read before any is written
+ *   history[b * beams + k, length[b]] <- token[b, k]
+ * history: int32 [batch * beams, capacity], rows ld_history >= capacity apart; parent, token: int32, rows ld_parent, ld_token >=
+ * beams apart (orpo_beam_select's outputs as they are); length: int32 [batch].  Positions from length[b] + 1 on keep what
+ * they hold; length is not changed.
+ * Device errors: ORPO_STATUS_PARENT (a parent outside [0, beams), or a length outside [0, capacity): no place for the token;
+ * that entry is left as it is).
+ * Limits: 1 <= beams <= ORPO_MAX_BEAMS, batch >= 0, batch * beams <= 2^20, 1 <= capacity < 2^28.  4-byte alignment.
+ */
+int orpo_beam_history(int32_t* history, int64_t ld_history, int64_t capacity, const int32_t* parent, int64_t ld_parent,
+                      const int32_t* token, int64_t ld_token, const int32_t* length, int64_t batch, int beams,
+                      int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -72,7 +72,10 @@ enum {
   ORPO_STATUS_TIMEOUT = 1 << 8,    /* a bounded on-chip wait gave up (the kernel returned early) */
   ORPO_STATUS_BOUNDS = 1 << 9,     /* bounds-checked build only (ORPO_DEBUG_BOUNDS): a computed index fell
                                       outside its buffer; the access was skipped */
-  ORPO_STATUS_PARENT = 1 << 10     /* orpo_beam_reorder: a parent or a length out of range */
+  ORPO_STATUS_PARENT = 1 << 10,    /* decode: a parent or a length out of range */
+  ORPO_STATUS_PAGE = 1 << 11,      /* orpo_pages.h: a page number out of range, or a count of holders that is wrong */
+  ORPO_STATUS_FULL = 1 << 12,      /* orpo_pages_advance: fewer free pages than needed */
+  ORPO_STATUS_MASK = 1 << 13       /* orpo_logits_adjust: a mask's number out of range */
 };
 
 /* Largest number of pairs orpo_loss accepts. */
@@ -354,7 +357,7 @@ int orpo_debug_wait_timeout(int32_t* status, int64_t limit_ns, void* stream);
  * orpo_profile_stop() waits for those events and writes, for kernel kinds
  * 0 .. nkinds-1 (names from orpo_profile_kind_name: fwd_logits, fwd_merge,
  * orpo_loss, bwd_recompute, bwd_grad_gemm, debug_gemm, dequant, bwd_skip_plan,
- * logits_q, beam_select, beam_reorder), the summed milliseconds
+ * logits_q, beam_select, beam_reorder, logits_adjust, beam_history, pages_plan, pages_copy), the summed milliseconds
  * into ms[] and the launch count into count[] (host arrays).  Events are
  * host-side objects pooled inside the library; no device memory is used.
  */

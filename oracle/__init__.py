@@ -30,3 +30,12 @@ from .decode_oracle import (  # noqa: F401
     head_logits,
     logits_error_bound,
 )
+from .pages_oracle import (  # noqa: F401
+    beam_history,
+    holders,
+    logits_adjust,
+    pages_advance,
+    pages_compact,
+    pages_copy,
+    pages_release,
+)

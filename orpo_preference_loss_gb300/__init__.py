@@ -22,11 +22,12 @@ __all__ = [
     "orpo_profile_start", "orpo_profile_stop", "orpo_head_fwd_static", "orpo_debug_wait_timeout",
     "orpo_pref_loss", "PREF_KINDS", "orpo_head_q_workspace_bytes", "orpo_head_fwd_q", "orpo_head_bwd_q",
     "use_bounds_checked_library", "orpo_head_logits_q", "orpo_head_logits_q_workspace_bytes", "orpo_beam_select", "orpo_beam_select_workspace_bytes",
-    "orpo_beam_reorder", "BeamDecoder",
+    "orpo_beam_reorder", "BeamDecoder", "orpo_logits_adjust", "orpo_beam_history", "orpo_pages_workspace_bytes",
+    "orpo_pages_advance", "orpo_pages_copy", "orpo_pages_release", "orpo_pages_compact", "PagedStates",
 ]
 
 STATUS_BITS = {"target": 1 << 4, "seqid": 1 << 5, "empty": 1 << 6, "nonfinite": 1 << 7, "timeout": 1 << 8,
-               "bounds": 1 << 9, "parent": 1 << 10}
+               "bounds": 1 << 9, "parent": 1 << 10, "page": 1 << 11, "full": 1 << 12, "mask": 1 << 13}
 MAX_PAIRS = 2048
 MAX_BEAMS = 64
 MAX_SELECT = 64
@@ -119,6 +120,22 @@ def load():
     L.orpo_beam_select.restype = ctypes.c_int
     L.orpo_beam_reorder.argtypes = [vp, vp, i64, vp, i64, i64, ctypes.c_int, i64, i64, i64, vp, vp]
     L.orpo_beam_reorder.restype = ctypes.c_int
+    L.orpo_logits_adjust.argtypes = [vp, i64, ctypes.c_int, i64, ctypes.c_int, i64, vp, i64, i64, vp, vp, f32, f32, f32,
+                                     ctypes.c_int, vp, vp, i64, i64, vp, i64, i64, vp, vp, vp]
+    L.orpo_logits_adjust.restype = ctypes.c_int
+    L.orpo_beam_history.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64, ctypes.c_int, vp, vp]
+    L.orpo_beam_history.restype = ctypes.c_int
+    L.orpo_pages_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.orpo_pages_workspace_bytes.restype = sz
+    L.orpo_pages_advance.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, i64, i64, ctypes.c_int, vp, i64, vp, vp, sz,
+                                     vp, vp]
+    L.orpo_pages_advance.restype = ctypes.c_int
+    L.orpo_pages_copy.argtypes = [vp, i64, i64, i64, i64, i64, vp, i64, vp, vp, vp]
+    L.orpo_pages_copy.restype = ctypes.c_int
+    L.orpo_pages_release.argtypes = [vp, i64, i64, vp, i64, vp, i64, ctypes.c_int, vp, vp]
+    L.orpo_pages_release.restype = ctypes.c_int
+    L.orpo_pages_compact.argtypes = [vp, i64, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp, i64, vp, vp, sz, vp, vp]
+    L.orpo_pages_compact.restype = ctypes.c_int
     L.orpo_profile_start.argtypes = []
     L.orpo_profile_start.restype = ctypes.c_int
     L.orpo_profile_stop.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64), ctypes.c_int]
@@ -427,6 +444,11 @@ def _rows(t, name, dtypes, cols=None, rows=None):
 
 LOGITS = (torch.float32, torch.bfloat16)
 F32, I32, U8, FLAGS = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.uint8, torch.bool)
+MASKS = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def orpo_head_logits_q_workspace_bytes(M: int, d: int, bits: int) -> int:
@@ -550,6 +572,175 @@ def orpo_beam_reorder(state, parent, length, status, stream=None):
         raise OrpoError(code, "orpo_beam_reorder")
 
 
+def _here(first, *others):
+    """The tensors (None: not given) are on the device that is current, where the call's kernels run."""
+    at = first.get_device()
+    if at < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    now = torch.cuda.current_device() if _raw_device is None else _raw_device()
+    if at != now:
+        raise ValueError(f"the tensors are on cuda:{at}, but the current device is cuda:{now}")
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"the tensors are on different devices: {first.device} and {t.device}")
+
+
+def orpo_logits_adjust(logits, beams, status, history=None, length=None, prompt=None, repetition=1.0, presence=0.0, frequency=0.0,
+                       no_repeat=0, bias_token=None, bias_value=None, masks=None, mask_row=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks, in place on logits [batch * beams, V] (fp32 or bf16).
+
+    history: int32 [batch * beams, capacity], of which the first length[b] (int32 [batch]) are tokens of the row, the first
+    prompt[b] of those (None: 0) the prompt's.  bias_token, bias_value: int32, fp32 [batch, n], or [n] for every entry.  masks:
+    int32 or uint32 [n_masks, ceil(V / 32)], bit set = allowed; mask_row: int32 [batch * beams], -1 for a row without a mask."""
+    rows, V = logits.shape
+    if beams < 1 or rows % beams:
+        raise ValueError(f"logits has {rows} rows, expected a multiple of beams = {beams}")
+    batch = rows // beams
+    _here(logits, status, history, length, prompt, bias_token, bias_value, masks, mask_row)
+    pitch = _rows(logits, "logits", LOGITS)
+    if status.dtype is not torch.int32:
+        _dev(status, "status", I32)
+    ld_history = capacity = 0
+    if history is not None:
+        ld_history, capacity = _rows(history, "history", I32, rows=rows), history.shape[1]
+        _dev(length, "length", I32, (batch,))
+        if prompt is not None:
+            _dev(prompt, "prompt", I32, (batch,))
+    ld_bias = n_bias = 0
+    if bias_token is not None or bias_value is not None:
+        if bias_token is None or bias_value is None or bias_token.shape != bias_value.shape:
+            raise ValueError("bias_token and bias_value must be given together, in one shape")
+        if bias_token.dim() == 1:
+            _dev(bias_token, "bias_token", I32)
+            _dev(bias_value, "bias_value", F32)
+        else:
+            ld_bias = _rows(bias_token, "bias_token", I32, rows=batch)
+            if _rows(bias_value, "bias_value", F32) != ld_bias:
+                raise ValueError("bias_token and bias_value must have the same row pitch")
+        n_bias = bias_token.shape[-1]
+    ld_masks = n_masks = 0
+    if masks is not None or mask_row is not None:
+        ld_masks, n_masks = _rows(masks, "masks", MASKS, cols=-(-V // 32)), masks.shape[0]
+        _dev(mask_row, "mask_row", I32, (rows,))
+    code = (_lib or load()).orpo_logits_adjust(
+        logits.data_ptr(), pitch, logits.dtype is torch.bfloat16, batch, beams, V, _at(history), ld_history, capacity,
+        _at(length), _at(prompt), repetition, presence, frequency, no_repeat, _at(bias_token), _at(bias_value), ld_bias, n_bias,
+        _at(masks), ld_masks, n_masks, _at(mask_row), status.data_ptr(), _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_logits_adjust")
+
+
+def orpo_beam_history(history, parent, token, length, status, stream=None):
+    """Token histories [batch * beams, capacity] (int32) follow parent [batch, beams] in place, up to length[b], where
+    token [batch, beams] is then put.  length is not changed."""
+    batch, beams = parent.shape
+    _here(history, parent, token, length, status)
+    ld = _rows(history, "history", I32, rows=batch * beams)
+    ld_parent = _rows(parent, "parent", I32)
+    ld_token = _rows(token, "token", I32, cols=beams, rows=batch)
+    _dev(length, "length", I32, (batch,))
+    _dev(status, "status", I32)
+    code = (_lib or load()).orpo_beam_history(history.data_ptr(), ld, history.shape[1], parent.data_ptr(), ld_parent,
+                                              token.data_ptr(), ld_token, length.data_ptr(), batch, beams, status.data_ptr(),
+                                              _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_beam_history")
+
+
+def orpo_pages_workspace_bytes(table_rows: int, pages: int, page: int, most: int = 1) -> int:
+    return int(load().orpo_pages_workspace_bytes(table_rows, pages, page, most))
+
+
+def _moves(moves, n_moves, workspace, status):
+    _dev(moves, "moves", I32)
+    if moves.dim() != 2 or moves.shape[1] != 3:
+        raise ValueError(f"moves has shape {tuple(moves.shape)}, expected (max_moves, 3)")
+    _dev(n_moves, "n_moves", I32, (1,))
+    if workspace is not None:
+        _dev(workspace, "workspace", U8)
+    _dev(status, "status", I32)
+
+
+def orpo_pages_advance(table, refs, page, parent, length, more, most, moves, n_moves, workspace, status, stream=None):
+    """Page tables [batch * beams, columns] follow parent [batch, beams] (None: they stay), and positions length[b] ..
+    length[b] + more[b] - 1 (more None: `most` of them) of each row become writable.
+
+    Pages are taken and let go of in refs (int32 [pages]); pages to be copied are listed in moves (int32 [max_moves, 3], n_moves
+    int32 [1]) for orpo_pages_copy.  workspace: uint8, orpo_pages_workspace_bytes(batch * beams, pages, page, most)."""
+    rows, columns = table.shape
+    batch = length.shape[0]
+    beams = rows // batch if batch else 1
+    if rows != batch * beams:
+        raise ValueError(f"table has {rows} rows, expected a multiple of the {batch} lengths")
+    _here(table, refs, parent, length, more, moves, n_moves, workspace, status)
+    ld = _rows(table, "table", I32)
+    _dev(refs, "refs", I32, (refs.numel(),))
+    ld_parent = 0 if parent is None else _rows(parent, "parent", I32, cols=beams, rows=batch)
+    _dev(length, "length", I32, (batch,))
+    if more is not None:
+        _dev(more, "more", I32, (batch,))
+    _moves(moves, n_moves, workspace, status)
+    code = (_lib or load()).orpo_pages_advance(
+        table.data_ptr(), ld, columns, refs.data_ptr(), refs.numel(), page, _at(parent), ld_parent, length.data_ptr(), _at(more),
+        most, batch, beams, moves.data_ptr(), moves.shape[0], n_moves.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        status.data_ptr(), _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_pages_advance")
+
+
+def orpo_pages_copy(pool, moves, n_moves, status, stream=None):
+    """Carries out the copies of moves in pool [outer, pages, rows, page, unit] (any dtype)."""
+    _here(pool, moves, n_moves, status)
+    if not pool.is_contiguous() or pool.dim() != 5:
+        raise ValueError("pool must be a contiguous CUDA tensor [outer, pages, rows, page, unit]")
+    _moves(moves, n_moves, None, status)
+    outer, pages, rows, page, unit = pool.shape
+    code = (_lib or load()).orpo_pages_copy(pool.data_ptr(), outer, pages, rows, page, unit * pool.element_size(),
+                                            moves.data_ptr(), moves.shape[0], n_moves.data_ptr(), status.data_ptr(),
+                                            _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_pages_copy")
+
+
+def orpo_pages_release(table, refs, ended, status, stream=None):
+    """The rows of entries with ended[b] != 0 (uint8 or bool [batch]; None: all rows) let go of their pages."""
+    rows, columns = table.shape
+    batch = rows if ended is None else ended.shape[0]
+    beams = rows // batch if batch else 1
+    if rows != batch * beams:
+        raise ValueError(f"table has {rows} rows, expected a multiple of the {batch} entries of ended")
+    _here(table, refs, ended, status)
+    ld = _rows(table, "table", I32)
+    _dev(refs, "refs", I32, (refs.numel(),))
+    if ended is not None:
+        _dev(ended, "ended", FLAGS, (batch,))
+    _dev(status, "status", I32)
+    code = (_lib or load()).orpo_pages_release(table.data_ptr(), ld, columns, refs.data_ptr(), refs.numel(), _at(ended), batch,
+                                               beams, status.data_ptr(), _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_pages_release")
+
+
+def orpo_pages_compact(table, refs, page, new_table, new_refs, live, moves, n_moves, workspace, status, stream=None):
+    """Numbers the pages in use 0 .. live[0] - 1: those at live[0] or above take the free numbers below, in order.
+
+    new_table and new_refs may be table and refs themselves; moves (at least pages / 2 of them) are for orpo_pages_copy."""
+    rows, columns = table.shape
+    _here(table, refs, new_table, new_refs, live, moves, n_moves, workspace, status)
+    ld = _rows(table, "table", I32)
+    ld_new = _rows(new_table, "new_table", I32, cols=columns, rows=rows)
+    _dev(refs, "refs", I32, (refs.numel(),))
+    _dev(new_refs, "new_refs", I32, refs.shape)
+    _dev(live, "live", I32, (1,))
+    _moves(moves, n_moves, workspace, status)
+    code = (_lib or load()).orpo_pages_compact(
+        table.data_ptr(), ld, columns, rows, refs.data_ptr(), refs.numel(), page, new_table.data_ptr(), ld_new,
+        new_refs.data_ptr(), live.data_ptr(), moves.data_ptr(), moves.shape[0], n_moves.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), status.data_ptr(), _stream(stream))
+    if code:
+        raise OrpoError(code, "orpo_pages_compact")
+
+
 def orpo_debug_gemm(A, B, C, M, N, K, a_mn_major, b_mn_major, status, stream=None):
     _dev(A, "A", BF16)
     _dev(B, "B", BF16)
@@ -563,7 +754,7 @@ def orpo_debug_wait_timeout(status, limit_ns, stream=None):
     _check(load().orpo_debug_wait_timeout(_ptr(status), int(limit_ns), _stream(stream)), "orpo_debug_wait_timeout")
 
 
-PROFILE_KINDS = 11
+PROFILE_KINDS = 15
 
 
 def orpo_profile_start():
@@ -638,19 +829,80 @@ class OrpoHead:
         return graph
 
 
+class PagedStates:
+    """Owns the page table of beam states kept in shared pages, and runs the calls of orpo_pages.h on it.
+
+    The pools themselves, [outer, pages, rows, page, unit] of any dtype and any number of them, are the caller's: position
+    t of beam r is position t % page of page table[r, t // page] in every pool.  table [batch * beams, columns], refs [pages],
+    moves and status stay on the device; nothing waits on the host.  The constructor fills them on the current stream.
+    most: the largest number of positions that advance or admit is asked for at once."""
+
+    def __init__(self, batch: int, beams: int, columns: int, pages: int, page: int, most: int = 1, status=None, device="cuda"):
+        self.batch, self.beams, self.columns, self.pages, self.page, self.most = batch, beams, columns, pages, page, most
+        dev = torch.device(device)
+        ws = orpo_pages_workspace_bytes(batch * beams, pages, page, most)
+        if ws == 0:
+            raise ValueError(f"batch {batch}, beams {beams}, pages {pages}, page {page}, most {most} are out of orpo_pages.h's range")
+        self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        self.table = torch.full((batch * beams, columns), -1, dtype=torch.int32, device=dev)
+        self.refs = torch.zeros(pages, dtype=torch.int32, device=dev)
+        self.moves = torch.empty((max(batch * beams, pages // 2), 3), dtype=torch.int32, device=dev)
+        self.n_moves = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.live = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev) if status is None else status
+
+    def _copy(self, pools, stream):
+        for pool in pools:
+            if pool.shape[1] != self.pages or pool.shape[3] != self.page:
+                raise ValueError(f"a pool has shape {tuple(pool.shape)}, expected [outer, {self.pages}, rows, {self.page}, unit]")
+            orpo_pages_copy(pool, self.moves, self.n_moves, self.status, stream)
+
+    def advance(self, length, parent=None, more=None, most=1, pools=(), stream=None):
+        """The beams' tables follow parent [batch, beams] up to length[b], and positions length[b] .. length[b] + more[b] - 1
+        (more None: `most` of them) of every beam can be written in all pools."""
+        orpo_pages_advance(self.table, self.refs, self.page, parent, length, more, most, self.moves, self.n_moves,
+                           self.workspace, self.status, stream)
+        self._copy(pools, stream)
+
+    def admit(self, length, more, most, pools=(), stream=None):
+        """As advance without parents, for beam 0 of each entry alone: a prompt, which the other beams take with their
+        first advance (all parents 0)."""
+        orpo_pages_advance(self.table[::self.beams], self.refs, self.page, None, length, more, most, self.moves, self.n_moves,
+                           self.workspace, self.status, stream)
+        self._copy(pools, stream)
+
+    def release(self, ended=None, stream=None):
+        """Entries with ended[b] != 0 (None: all) let go of their pages."""
+        if ended is not None and ended.shape != (self.batch,):
+            raise ValueError(f"ended has shape {tuple(ended.shape)}, expected ({self.batch},)")
+        orpo_pages_release(self.table, self.refs, ended, self.status, stream)
+
+    def compact(self, pools=(), stream=None):
+        """Pages in use move to the lowest numbers, 0 .. live[0] - 1, in all pools."""
+        orpo_pages_compact(self.table, self.refs, self.page, self.table, self.refs, self.live, self.moves, self.n_moves,
+                           self.workspace, self.status, stream)
+        self._copy(pools, stream)
+
+
 class BeamDecoder:
     """Owns the buffers of beam search on the quantised head and runs one decode step.
 
-    A step is the three C entry points of orpo_decode.h in order on the current stream: logits of the
-    beams' last hidden rows, selection of each batch entry's `beams` best continuations, and the states
-    following their parents.  score, finished, parent and token stay on the device; nothing waits on
-    the host, so a step can be recorded in a CUDA graph.  The constructor and reset fill the buffers on the
-    current stream: a step on another stream has to be ordered behind them."""
+    A step is the C entry points of orpo_decode.h in order on the current stream: logits of the beams' last hidden
+    rows, their penalties, biases and masks where any are given, selection of each batch entry's `beams` best
+    continuations, and the states and histories following their parents.  score, finished, parent and token stay on the
+    device; nothing waits on the host, so a step can be recorded in a CUDA graph.  The constructor and reset fill the buffers
+    on the current stream: a step on another stream has to be ordered behind them.
+
+    repetition, presence, frequency, no_repeat: orpo_logits_adjust's; any of them makes step need a history."""
 
     def __init__(self, batch: int, beams: int, V: int, d: int, bits: int = 4, group: int = 64, softcap: float = 0.0,
-                 eos: int = -1, logits_dtype=torch.float32, device="cuda"):
+                 eos: int = -1, logits_dtype=torch.float32, device="cuda", repetition: float = 1.0, presence: float = 0.0,
+                 frequency: float = 0.0, no_repeat: int = 0):
         self.batch, self.beams, self.V, self.d = batch, beams, V, d
         self.bits, self.group, self.softcap, self.eos = bits, group, float(softcap), int(eos)
+        self.repetition, self.presence, self.frequency = float(repetition), float(presence), float(frequency)
+        self.no_repeat = int(no_repeat)
+        self._penalties = self.repetition != 1.0 or self.presence != 0.0 or self.frequency != 0.0 or self.no_repeat != 0
         dev = torch.device(device)
         ws = orpo_beam_select_workspace_bytes(batch, beams, V, beams)
         if ws == 0:
@@ -673,15 +925,32 @@ class BeamDecoder:
         if self.finished is not None:
             self.finished.zero_()
 
-    def step(self, h, wq, scales, biases, states=(), length=None, stream=None):
+    def step(self, h, wq, scales, biases, states=(), length=None, stream=None, history=None, prompt=None, bias_token=None,
+             bias_value=None, masks=None, mask_row=None, pages=None, pools=()):
         """One step from the hidden rows h [batch * beams, d]; returns (parent, token) [batch, beams].
 
         states: tensors [outer, batch * beams, rows, capacity, unit] that follow their parents, up to
-        position length[b] of each entry."""
+        position length[b] of each entry.  history: int32 [batch * beams, capacity], each beam's length[b] tokens so far (the
+        first prompt[b] of them the prompt's); it follows its parent and gets the new token at length[b].  bias_token,
+        bias_value, masks, mask_row: as for orpo_logits_adjust.  pages, pools: a PagedStates and the pools of it, which follow
+        and in which position length[b] can then be written.  length itself is the caller's to raise."""
+        if length is None and (history is not None or pages is not None):
+            raise ValueError("a history or pages need length")
+        if self._penalties and history is None:
+            raise ValueError("penalties for repeated tokens need a history")
+        if pages is not None and (pages.batch != self.batch or pages.beams != self.beams):
+            raise ValueError(f"pages is for {pages.batch} x {pages.beams} beams, expected {self.batch} x {self.beams}")
         orpo_head_logits_q(h, wq, scales, biases, self.bits, self.group, self.softcap, self.logits, self.status,
                            stream, self.logits_workspace)
+        if self._penalties or bias_token is not None or masks is not None:
+            orpo_logits_adjust(self.logits, self.beams, self.status, history, length, prompt, self.repetition, self.presence,
+                               self.frequency, self.no_repeat, bias_token, bias_value, masks, mask_row, stream)
         orpo_beam_select(self.logits, self.score, self.finished, self.eos, self.beams, self.score, self.parent,
                          self.token, self.finished, self.workspace, self.status, stream)
         for state in states:
             orpo_beam_reorder(state, self.parent, length, self.status, stream)
+        if history is not None:
+            orpo_beam_history(history, self.parent, self.token, length, self.status, stream)
+        if pages is not None:
+            pages.advance(length, self.parent, pools=pools, stream=stream)
         return self.parent, self.token

@@ -794,7 +794,7 @@ const char* orpo_status_string(int code) {
     case ORPO_ERR_TOO_LARGE: return "M exceeds ORPO_FWD_STATIC_MAX_ROWS for orpo_head_fwd_static";
     default: break;
   }
-  static thread_local char buf[160];
+  static thread_local char buf[384];
   if (code < 16) return "unknown code";
   buf[0] = 0;
   const struct {
@@ -806,7 +806,10 @@ const char* orpo_status_string(int code) {
               {ORPO_STATUS_NONFINITE, "non-finite value"},
               {ORPO_STATUS_TIMEOUT, "on-chip wait timed out"},
               {ORPO_STATUS_BOUNDS, "index out of bounds (bounds-checked build)"},
-              {ORPO_STATUS_PARENT, "beam parent or length out of range"}};
+              {ORPO_STATUS_PARENT, "beam parent or length out of range"},
+              {ORPO_STATUS_PAGE, "page number or its count of holders out of range"},
+              {ORPO_STATUS_FULL, "not enough free pages"},
+              {ORPO_STATUS_MASK, "mask number out of range"}};
   for (const auto& b : bits) {
     if (code & b.bit) {
       if (buf[0]) strncat(buf, "; ", sizeof(buf) - strlen(buf) - 1);

@@ -60,7 +60,7 @@ int check_quant(const QuantW* q, int64_t d);
 
 // ---- launch timing (profile.cu); no-ops unless orpo_profile_start() was called
 enum KernelKind { K_FWD = 0, K_MERGE, K_LOSS, K_REC, K_GEMM, K_DEBUG, K_DEQUANT, K_SKIP, K_LOGITS, K_BEAM, K_REORDER,
-                  K_NKINDS };
+                  K_ADJUST, K_HISTORY, K_PAGES, K_PAGECOPY, K_NKINDS };
 void prof_begin(int kind, cudaStream_t st);
 void prof_end(int kind, cudaStream_t st);
 

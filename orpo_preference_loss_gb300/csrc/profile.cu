@@ -35,7 +35,8 @@ cudaEvent_t take_event() {
 
 const char* kNames[K_NKINDS] = {"fwd_logits",    "fwd_merge",    "orpo_loss",   "bwd_recompute",
                                 "bwd_grad_gemm", "debug_gemm",   "dequant",     "bwd_skip_plan",
-                                "logits_q",      "beam_select",  "beam_reorder"};
+                                "logits_q",      "beam_select",  "beam_reorder", "logits_adjust",
+                                "beam_history",  "pages_plan",   "pages_copy"};
 
 }  // namespace
 
