@@ -62,7 +62,7 @@ size_t orpo_pages_workspace_bytes(int64_t table_rows, int64_t pages, int64_t pag
  * page]; that entry is left as it is), ORPO_STATUS_PAGE (a table entry outside [-1, pages); it moves with its row and is
  * otherwise left alone), ORPO_STATUS_FULL (fewer free pages than needed: the reserve part changes nothing, n_moves = 0;
  * make room and call again with parent = NULL).
- * Limits beyond those above: 0 <= most < 2^31, batch * beams * (ceil((most - 1) / page) + 1) < 2^31.
+ * Limits beyond those above: 0 <= most < 2^31, batch * beams * (ceil((most - 1) / page) + 1) <= 2^30.
  */
 int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_t* refs, int64_t pages, int64_t page,
                        const int32_t* parent, int64_t ld_parent, const int32_t* length, const int32_t* more, int64_t most,

@@ -41,6 +41,25 @@ inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int th
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The same for one cluster of `ctas` CTAs (1: a plain CTA), at most the portable 8.
+template <class... Params, class... Args>
+inline cudaError_t launch_cluster_dependent(void (*kernel)(Params...), int ctas, int threads, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- host-side checks shared by the entry points
 // Largest M, V (and debug-GEMM extent): row and column indices, tile counts rounded up to whole tiles,
 // and per-thread row chunks of the loss stay inside int32 with room to spare.

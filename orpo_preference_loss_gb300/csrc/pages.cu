@@ -42,6 +42,32 @@ __device__ __forceinline__ bool wanted(const TableArgs& a, int64_t b, int64_t& b
 // ------------------------------------------------------------------ fork
 // One thread owns a column of all rows of an entry and reads it whole before it writes.  A row that keeps its page number
 // (the shared past) costs no atomics.
+
+// Column c of entry b, whose parents are par.
+template <int KB, class Parents>
+__device__ __forceinline__ void fork_column(const TableArgs& a, int64_t b, int64_t c, const Parents& par) {
+  const int64_t b0 = b * a.beams * a.ld, all = a.batch * a.beams * a.ld;
+  int32_t* const column = a.table + b0 + c;
+  constexpr bool kHold = KB <= 16;  // above, a row's own page is read when it is written: both sets spill
+  int32_t was[KB], now[KB];
+#pragma unroll
+  for (int k = 0; k < KB; ++k)
+    if (par[k] != k && in_bounds(a.status, b0 + c + k * a.ld, all)) {
+      if (kHold) was[k] = column[k * a.ld];
+      now[k] = column[par[k] * a.ld];
+    }
+#pragma unroll
+  for (int k = 0; k < KB; ++k)
+    if (par[k] != k && in_bounds(a.status, b0 + c + k * a.ld, all)) {
+      if (!kHold) was[k] = column[k * a.ld];
+      if (was[k] == now[k]) continue;
+      column[k * a.ld] = now[k];
+      if (is_page(a, now[k])) atomicAdd(a.refs + now[k], 1);
+      if (is_page(a, was[k])) atomicSub(a.refs + was[k], 1);
+      if (now[k] < -1 || now[k] >= a.pages || was[k] < -1 || was[k] >= a.pages) atomicOr(a.status, ORPO_STATUS_PAGE);
+    }
+}
+
 constexpr int kForkThreads = 128;
 
 template <int KB>
@@ -64,33 +90,17 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(TableArgs a, int32_t
     if (bad) atomicOr(a.status, ORPO_STATUS_PARENT);
   }
   if (bad) return;
-  const int64_t used = (begin + a.page - 1) / a.page, b0 = b * a.beams * a.ld, all = a.batch * a.beams * a.ld;
-  for (int64_t c = (int64_t)blockIdx.y * kForkThreads + tid; c < used; c += (int64_t)gridDim.y * kForkThreads) {
-    int32_t* const column = a.table + b0 + c;
-    int32_t was[KB], now[KB];
-#pragma unroll
-    for (int k = 0; k < KB; ++k)
-      if (par[k] != k && in_bounds(a.status, b0 + c + k * a.ld, all)) {
-        was[k] = column[k * a.ld];
-        now[k] = column[par[k] * a.ld];
-      }
-#pragma unroll
-    for (int k = 0; k < KB; ++k)
-      if (par[k] != k && was[k] != now[k] && in_bounds(a.status, b0 + c + k * a.ld, all)) {
-        column[k * a.ld] = now[k];
-        if (is_page(a, now[k])) atomicAdd(a.refs + now[k], 1);
-        if (is_page(a, was[k])) atomicSub(a.refs + was[k], 1);
-        if (now[k] < -1 || now[k] >= a.pages || was[k] < -1 || was[k] >= a.pages) atomicOr(a.status, ORPO_STATUS_PAGE);
-      }
-  }
+  const int64_t used = (begin + a.page - 1) / a.page;
+  for (int64_t c = (int64_t)blockIdx.y * kForkThreads + tid; c < used; c += (int64_t)gridDim.y * kForkThreads) fork_column<KB>(a, b, c, par);
 }
 
-// ------------------------------------------------------------------ scans over one CTA
+// ------------------------------------------------------------------ one CTA, or a cluster of them
 constexpr int kPlanThreads = 1024;
 constexpr int kWarps = kPlanThreads / 32;
+constexpr int kMaxCtas = 8;
 
-// Exclusive sum of x over the CTA's threads, and the total.  `part` is kWarps words of shared memory, free again at the
-// next barrier.
+// Exclusive sum of x over the CTA's threads, and the total.  `part` is kWarps words of shared memory, free again after
+// the call.
 __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* part, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t sum = x;
@@ -114,118 +124,402 @@ __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* part, uint32_t& t
   return before + sum - x;
 }
 
-// ------------------------------------------------------------------ reserve
-// Items are (row, column) pairs of the positions asked for, in order: `width` columns per row, of which those from the
-// end of the row's positions on ask for nothing.
-struct ReserveArgs {
-  TableArgs t;
-  const int32_t* left_alone;  // entries that the fork found wrong; nullptr without a fork
-  int32_t* moves;
-  int32_t* n_moves;
-  int32_t width;
-  int32_t items;
-  int32_t* count;  // [pages] how many items hold a page that others hold too,
-  int32_t* last;   // [pages] and the last of them
-  int32_t* rank;   // [items] number of the item's new page among the new ones, or -1
-  int32_t* fresh;  // [items] the new pages
-};
-
-struct Item {
-  bool inside;
-  int32_t old, fill;
-  int32_t* entry;
-};
-
-__device__ __forceinline__ Item item_at(const ReserveArgs& a, int32_t i) {
-  Item it{false, -1, 0, nullptr};
-  if (i >= a.items) return it;
-  const int32_t row = i / a.width, j = i - row * a.width, b = row / a.t.beams;
-  int64_t begin, end;
-  if ((a.left_alone && a.left_alone[b]) || !wanted(a.t, b, begin, end) || begin == end) return it;
-  const int64_t c = begin / a.t.page + j;
-  if (c * a.t.page >= end || !in_bounds(a.t.status, c, a.t.columns)) return it;
-  it.entry = a.t.table + row * a.t.ld + c;
-  it.old = *it.entry;
-  it.inside = it.old >= -1 && it.old < a.t.pages;
-  it.fill = j == 0 ? (int32_t)(begin % a.t.page) : 0;
-  return it;
+__device__ __forceinline__ void plan_sync(int ctas) {
+  if (ctas > 1) cluster_sync(); else __syncthreads();
 }
 
-__global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
-  __shared__ uint32_t part[kWarps];
+// What each CTA of the cluster tells the others; read between two plan_syncs.
+struct Totals {
+  uint32_t v[4];
+};
+__device__ __forceinline__ uint32_t told(const Totals* mine, int what, int cta, int ctas) {
+  if (ctas == 1) return mine->v[what];
+  uint32_t at, x;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&mine->v[what])), "r"(cta));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+// Sum over the CTAs before this one, and over all.
+__device__ __forceinline__ uint32_t told_before(const Totals* mine, int what, int cta, int ctas, uint32_t& all) {
+  uint32_t before = 0;
+  all = 0;
+  for (int i = 0; i < ctas; ++i) {
+    if (i == cta) before = all;
+    all += told(mine, what, i, ctas);
+  }
+  return before;
+}
+
+// Whether each of the kOwn pages from p on is in use, as bits.
+constexpr int kOwn = 16;
+constexpr int kPageTile = kPlanThreads * kOwn;
+__device__ __forceinline__ uint32_t used_bits(const int32_t* refs, int32_t p, int32_t pages) {
+  uint32_t bits = 0;
+  if (p + kOwn <= pages && (reinterpret_cast<uintptr_t>(refs + p) & 15u) == 0) {
+    int4 v[kOwn / 4];
+#pragma unroll
+    for (int i = 0; i < kOwn / 4; ++i) v[i] = __ldcg(reinterpret_cast<const int4*>(refs + p) + i);
+#pragma unroll
+    for (int i = 0; i < kOwn / 4; ++i)
+      bits |= ((uint32_t)(v[i].x > 0) | (uint32_t)(v[i].y > 0) << 1 | (uint32_t)(v[i].z > 0) << 2 | (uint32_t)(v[i].w > 0) << 3) << (4 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) bits |= (uint32_t)(p + i < pages && __ldcg(refs + p + i) > 0) << i;
+  }
+  return bits;
+}
+// Of those, the ones that exist.
+__device__ __forceinline__ uint32_t page_bits(int32_t p, int32_t pages) {
+  const int n = min(max(pages - p, 0), kOwn);
+  return (1u << n) - 1u;
+}
+
+// ------------------------------------------------------------------ reserve
+// Items are (row, column) pairs of the positions asked for, in order; a row has `width` of them, of which those from the
+// end of its positions on ask for nothing.
+struct ReserveArgs {
+  TableArgs t;
+  int32_t* left_alone;  // [batch] entries that the fork found wrong; nullptr: there was no fork
+  int32_t* moves;
+  int32_t* n_moves;
+  int32_t width;     // items per row, rounded up to a power of two up to 32 or a multiple of kUnit
+  int32_t items;     // so many in all
+  int32_t units_per; // CTA
+  int32_t pages_per; // CTA, a multiple of kPageTile
+  int32_t* count;    // [pages] how many items hold a page that others hold too,
+  int32_t* last;     // [pages] and the last of them
+  uint32_t* needs;   // [units][kUnit / 32] items that need a page, as bits
+  uint32_t* before;  // [units][2] pages and moves that a unit needs; then those of the CTA's units before it
+  int32_t* fresh;    // [items] the new pages, in order
+};
+
+enum { kNone = 0, kNeed = 1, kShared = 2 };
+
+// What row asks for: columns first .. first + n - 1, of which the first holds `fill` positions in use.
+struct Wanted {
+  uint32_t first, n, fill;
+};
+__device__ __forceinline__ Wanted wanted_columns(const TableArgs& a, uint32_t b) {
+  int64_t begin, end;
+  if (!wanted(a, b, begin, end) || begin == end) return {0, 0, 0};
+  const uint32_t page = (uint32_t)a.page, first = (uint32_t)begin / page, last = ((uint32_t)end - 1) / page;
+  return {first, last - first + 1, (uint32_t)begin - first * page};
+}
+
+// ---- a decode step's worth: up to kSmallItems items, and pages whose counts fit shared memory.  One CTA; the counts are
+// read once, with lengths and parents, and the table once: two ways to memory instead of ten.
+// KB: a fork of up to KB beams is done here too; 0: none.
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallItems = kSmallThreads;
+constexpr int kSmallPages = 16384;
+inline size_t small_smem(int64_t pages) { return (size_t)(cdiv(pages, 1024) * 1024) * 12; }
+
+template <int KB>
+__global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArgs a, int32_t padded) {
+  extern __shared__ __align__(16) int32_t refs[];  // [padded] counts, [padded] items of a shared page, [padded] the last of them
+  int32_t* const count = refs + padded;
+  int32_t* const last = count + padded;
+  __shared__ uint32_t part[32];
+  __shared__ int32_t fresh[kSmallItems];
+  __shared__ uint8_t bad[kSmallItems];
+  const TableArgs& t = a.t;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_trigger();
+  bad[tid] = 0;
+  __syncthreads();
   grid_wait();
-  const int tid = threadIdx.x;
-  const int32_t pages = a.t.pages;
-  if (!a.left_alone)
-    for (int64_t b = tid; b < a.t.batch; b += kPlanThreads) {
-      int64_t begin, end;
-      if (!wanted(a.t, b, begin, end)) atomicOr(a.t.status, ORPO_STATUS_PARENT);
+  const int rows = (int)t.batch * t.beams;
+  const uint32_t row = (uint32_t)tid / (uint32_t)a.width, j = (uint32_t)tid - row * (uint32_t)a.width;
+  const uint32_t b = row / (uint32_t)t.beams;
+  // ---- counts, lengths, parents
+  for (int p = tid; p < padded; p += kSmallThreads) refs[p] = p < t.pages ? t.refs[p] : 1;
+  if (tid < rows) {
+    const int e = tid / t.beams;
+    int64_t begin, end;
+    bool wrong = !wanted(t, e, begin, end);
+    if constexpr (KB > 0) {
+      const int p = t.parent[e * t.ld_parent + tid - e * t.beams];
+      wrong |= p < 0 || p >= t.beams;
+    } else if (a.left_alone) {
+      wrong |= a.left_alone[e] != 0;
     }
-  // which of the items that hold a page together is the last: it keeps the page where nothing else holds it
-  for (int32_t i = tid; i < a.items; i += kPlanThreads) {
-    const Item it = item_at(a, i);
-    if (it.inside && it.old >= 0 && a.t.refs[it.old] > 1) a.count[it.old] = 0, a.last[it.old] = -1;
-    if (it.entry && !it.inside) atomicOr(a.t.status, ORPO_STATUS_PAGE);
+    if (wrong) {
+      bad[e] = 1;
+      atomicOr(t.status, ORPO_STATUS_PARENT);
+    }
+  }
+  const bool item = tid < a.items;
+  const Wanted w = item ? wanted_columns(t, b) : Wanted{0, 0, 0};
+  int32_t from = (int32_t)row;
+  if constexpr (KB > 0)
+    if (item && w.fill > 0 && j == 0) from = (int32_t)(b * t.beams) + t.parent[b * t.ld_parent + row - b * t.beams];
+  __syncthreads();
+  // ---- the table: each item's page after the fork, and the first columns to fork
+  const bool asks = item && j < w.n && !bad[b];
+  int32_t* const entry = t.table + row * t.ld + w.first + j;
+  int32_t old = -1;
+  if (asks && in_bounds(t.status, from, rows) && in_bounds(t.status, w.first + j, t.columns)) old = t.table[from * t.ld + w.first + j];
+  if constexpr (KB > 0) {
+    const uint32_t columns = (uint32_t)t.columns, pairs = (uint32_t)t.batch * columns;
+    int par[KB];
+    int32_t was[KB], now[KB];
+    for (uint32_t i = tid; i < (pairs + kSmallThreads - 1) / kSmallThreads * kSmallThreads; i += kSmallThreads) {
+      const uint32_t e = i < pairs ? i / columns : 0, c = i - e * columns;
+      const bool on = i < pairs && !bad[e] && (int64_t)c * t.page < t.length[e];
+      const int64_t b0 = (int64_t)e * t.beams * t.ld, all = t.batch * t.beams * t.ld;
+      int32_t* const column = t.table + b0 + c;
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        par[k] = on && k < t.beams ? t.parent[e * t.ld_parent + k] : k;
+        if (par[k] != k && in_bounds(t.status, b0 + c + k * t.ld, all)) {
+          was[k] = column[k * t.ld];
+          now[k] = column[par[k] * t.ld];
+        }
+      }
+      if (i == tid) __syncthreads();  // the items' pages are read
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+        if (par[k] != k && was[k] != now[k] && in_bounds(t.status, b0 + c + k * t.ld, all)) {
+          column[k * t.ld] = now[k];
+          if (is_page(t, now[k])) atomicAdd(t.refs + now[k], 1), atomicAdd(refs + now[k], 1);
+          if (is_page(t, was[k])) atomicSub(t.refs + was[k], 1), atomicSub(refs + was[k], 1);
+          if (now[k] < -1 || now[k] >= t.pages || was[k] < -1 || was[k] >= t.pages) atomicOr(t.status, ORPO_STATUS_PAGE);
+        }
+    }
   }
   __syncthreads();
-  for (int32_t i = tid; i < a.items; i += kPlanThreads) {
-    const Item it = item_at(a, i);
-    if (it.inside && it.old >= 0 && a.t.refs[it.old] > 1) atomicAdd(a.count + it.old, 1), atomicMax(a.last + it.old, i);
+  // ---- what the item asks for; of the items that hold a page together the last keeps it, where nothing else holds it
+  int what = kNone;
+  if (asks) {
+    if (old < -1 || old >= t.pages) atomicOr(t.status, ORPO_STATUS_PAGE);
+    else if (old < 0) what = kNeed;
+    else if (refs[old] > 1) what = kShared, count[old] = 0, last[old] = -1;
   }
-  __syncthreads();
-  uint32_t needed = 0, moved = 0;
-  for (int32_t i0 = 0; i0 < a.items; i0 += kPlanThreads) {
-    const int32_t i = i0 + tid;
-    const Item it = item_at(a, i);
-    bool need = it.inside;
-    if (need && it.old >= 0) {
-      const int32_t held = a.t.refs[it.old];
-      need = held > 1 && !(__ldcg(a.count + it.old) == held && __ldcg(a.last + it.old) == i);
-    }
-    uint32_t total;
-    const uint32_t at = scan(need, part, total);
-    if (i < a.items && in_bounds(a.t.status, i, a.items)) a.rank[i] = need ? (int32_t)(needed + at) : -1;
-    needed += total;
+  if (__syncthreads_or(what == kShared)) {
+    if (what == kShared) atomicAdd(count + old, 1), atomicMax(last + old, tid);
+    __syncthreads();
+    if (what == kShared && count[old] == refs[old] && last[old] == tid) what = kNone;
   }
-  uint32_t found = 0;
-  for (int32_t p0 = 0; p0 < pages && found < needed; p0 += kPlanThreads) {
-    const int32_t p = p0 + tid;
-    const bool free = p < pages && a.t.refs[p] <= 0;
-    uint32_t total;
-    const uint32_t at = found + scan(free, part, total);
-    if (free && at < needed && in_bounds(a.t.status, at, a.items)) a.fresh[at] = p;
-    found += total;
-  }
+  const bool move = what == kShared && j == 0 && w.fill > 0;
+  uint32_t total;
+  const uint32_t at = scan((uint32_t)(what != kNone) | (uint32_t)move << 16, part, total);
+  const uint32_t needed = total & 0xffff;
+  // ---- free pages, lowest first: a warp's share is a row of ballots
+  uint32_t free = 0;
+  const int share = padded / 32, p0 = warp * share;
+  for (int i = 0; i < share; i += 32) free += __popc(__ballot_sync(~0u, refs[p0 + i + lane] <= 0));
+  uint32_t found;
+  uint32_t rank = scan(lane == 0 ? free : 0, part, found);
+  rank = __shfl_sync(~0u, rank, 0);
   if (found < needed) {
     if (tid == 0) {
-      atomicOr(a.t.status, ORPO_STATUS_FULL);
+      atomicOr(t.status, ORPO_STATUS_FULL);
       *a.n_moves = 0;
     }
     return;
   }
+  for (int i = 0; i < share && rank < needed; i += 32) {
+    const bool is_free = refs[p0 + i + lane] <= 0;
+    const uint32_t bits = __ballot_sync(~0u, is_free), to = rank + __popc(bits & ((1u << lane) - 1u));
+    if (is_free && to < needed && in_bounds(t.status, to, kSmallItems)) fresh[to] = p0 + i + lane;
+    rank += __popc(bits);
+  }
   __syncthreads();
-  for (int32_t i0 = 0; i0 < a.items; i0 += kPlanThreads) {
-    const int32_t i = i0 + tid;
-    const Item it = item_at(a, i);
-    const int32_t rank = i < a.items ? a.rank[i] : -1;
-    const bool move = rank >= 0 && it.old >= 0 && it.fill > 0;
+  if (tid == 0) *a.n_moves = (int32_t)(total >> 16);
+  if (what == kNone) return;
+  const int32_t p = fresh[at & 0xffff];
+  *entry = p;
+  t.refs[p] = 1;
+  if (what == kShared) atomicSub(t.refs + old, 1);
+  const uint32_t m = at >> 16;
+  if (move && in_bounds(t.status, m, rows)) {
+    a.moves[3 * m] = old;
+    a.moves[3 * m + 1] = p;
+    a.moves[3 * m + 2] = (int32_t)w.fill;
+  }
+}
+
+// ---- any number of items and pages, on a cluster of CTAs.  A warp takes a unit of kUnit items, a row's or several rows', at
+// a time.  Each CTA has a stretch of units and one of pages, and tells the others how many pages its units need and how
+// many of its pages are free; then every item's new page is known.
+constexpr int kUnit = 128;
+constexpr int kPer = kUnit / 32;  // items of a lane
+
+struct Items {
+  int32_t row[kPer], old[kPer];
+  Wanted w[kPer];
+  uint32_t j[kPer];
+  bool asks[kPer];
+};
+// The items of a unit: which rows and columns, and the pages that they have.
+__device__ __forceinline__ void load_items(const ReserveArgs& a, int32_t unit, Items& it) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const uint32_t i = (uint32_t)unit * kUnit + u * 32 + lane;
+    const uint32_t row = i / (uint32_t)a.width, b = row / (uint32_t)a.t.beams;
+    it.row[u] = (int32_t)row;
+    it.j[u] = i - row * (uint32_t)a.width;
+    it.asks[u] = i < (uint32_t)a.items && !(a.left_alone && a.left_alone[b]);
+    it.w[u] = it.asks[u] ? wanted_columns(a.t, b) : Wanted{0, 0, 0};
+    it.asks[u] = it.j[u] < it.w[u].n;
+  }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int64_t c = it.w[u].first + it.j[u];
+    it.old[u] = it.asks[u] && in_bounds(a.t.status, c, a.t.columns) ? __ldcg(a.t.table + it.row[u] * a.t.ld + c) : -1;
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
+  __shared__ uint32_t part[kWarps];
+  __shared__ Totals totals;
+  const TableArgs& t = a.t;
+  grid_trigger();
+  grid_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ctas = gridDim.x, cta = blockIdx.x;
+  if (!a.left_alone)
+    for (int64_t b = (int64_t)cta * kPlanThreads + tid; b < t.batch; b += (int64_t)ctas * kPlanThreads) {
+      int64_t begin, end;
+      if (!wanted(t, b, begin, end)) atomicOr(t.status, ORPO_STATUS_PARENT);
+    }
+  if (a.items == 0) {  // a fork alone
+    if (tid == 0 && cta == 0) *a.n_moves = 0;
+    return;
+  }
+  const int32_t units = (int32_t)(((int64_t)a.items + kUnit - 1) / kUnit);
+  const int32_t u_begin = (int32_t)min((int64_t)cta * a.units_per, (int64_t)units), u_end = (int32_t)min((int64_t)u_begin + a.units_per, (int64_t)units);
+  const int32_t p_begin = (int32_t)min((int64_t)cta * a.pages_per, (int64_t)t.pages), p_end = (int32_t)min((int64_t)p_begin + a.pages_per, (int64_t)t.pages);
+  Items it;
+
+  // ---- what each item asks for.  Pages that others hold too are counted below
+  int shared = 0;
+  for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
+    load_items(a, unit, it);
+    uint32_t need = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const bool wrong = it.old[u] < -1 || it.old[u] >= t.pages;
+      if (wrong) atomicOr(t.status, ORPO_STATUS_PAGE);
+      if (it.old[u] >= 0 && !wrong && __ldcg(t.refs + it.old[u]) > 1) a.count[it.old[u]] = 0, a.last[it.old[u]] = -1, shared = 1;
+      const uint32_t bits = __ballot_sync(~0u, it.asks[u] && it.old[u] == -1);
+      if (lane == u) need = bits;
+    }
+    if (lane < kPer && in_bounds(t.status, unit, units)) a.needs[unit * kPer + lane] = need;
+    need = __popc(need);
+#pragma unroll
+    for (int d = 1; d < kPer; d *= 2) need += __shfl_xor_sync(~0u, need, d);
+    if (lane == 0 && in_bounds(t.status, unit, units)) a.before[2 * unit] = need, a.before[2 * unit + 1] = 0;
+  }
+  shared = __syncthreads_or(shared);
+  if (tid == 0) totals.v[0] = shared;
+  plan_sync(ctas);
+  uint32_t any;
+  told_before(&totals, 0, cta, ctas, any);
+  // ---- of the items that hold a page together the last keeps it, where nothing else holds it
+  if (any) {
+    if (shared)
+      for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
+        load_items(a, unit, it);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u)
+          if (it.old[u] >= 0 && it.old[u] < t.pages && __ldcg(t.refs + it.old[u]) > 1) {
+            atomicAdd(a.count + it.old[u], 1);
+            atomicMax(a.last + it.old[u], unit * kUnit + u * 32 + lane);
+          }
+      }
+    plan_sync(ctas);
+    if (shared)
+      for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
+        load_items(a, unit, it);
+        uint32_t moves = 0, need = 0;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          bool copies = false;
+          if (it.old[u] >= 0 && it.old[u] < t.pages) {
+            const int32_t held = __ldcg(t.refs + it.old[u]);
+            copies = held > 1 && !(__ldcg(a.count + it.old[u]) == held && __ldcg(a.last + it.old[u]) == unit * kUnit + u * 32 + lane);
+          }
+          const uint32_t bits = __ballot_sync(~0u, copies || (it.asks[u] && it.old[u] == -1));
+          need += __popc(bits);
+          moves += __popc(__ballot_sync(~0u, copies && it.j[u] == 0 && it.w[u].fill > 0));
+          if (lane == 0 && in_bounds(t.status, unit, units)) a.needs[unit * kPer + u] = bits;
+        }
+        if (lane == 0 && in_bounds(t.status, unit, units)) a.before[2 * unit] = need, a.before[2 * unit + 1] = moves;
+      }
+  }
+  __syncthreads();
+  // ---- sums over the CTA's units, and over its pages
+  uint32_t needed = 0, moved = 0, free = 0, free_bits = 0;
+  for (int32_t u0 = u_begin; u0 < u_end; u0 += kPlanThreads) {
+    const int32_t unit = u0 + tid;
+    const bool mine = unit < u_end && in_bounds(t.status, unit, units);
+    uint32_t all_need, all_moves;
+    const uint32_t need = scan(mine ? a.before[2 * unit] : 0, part, all_need), moves = scan(mine ? a.before[2 * unit + 1] : 0, part, all_moves);
+    if (mine) a.before[2 * unit] = needed + need, a.before[2 * unit + 1] = moved + moves;
+    needed += all_need;
+    moved += all_moves;
+  }
+  for (int32_t p0 = p_begin; p0 < p_end; p0 += kPageTile) {
+    const int32_t p = p0 + tid * kOwn;
+    free_bits = ~used_bits(t.refs, p, p_end) & page_bits(p, p_end);
     uint32_t total;
-    const uint32_t at = moved + scan(move, part, total);
-    if (rank >= 0 && in_bounds(a.t.status, rank, a.items)) {
-      const int32_t p = a.fresh[rank];
-      *it.entry = p;
-      a.t.refs[p] = 1;
-      if (it.old >= 0) atomicSub(a.t.refs + it.old, 1);
-      if (move && in_bounds(a.t.status, at, a.t.batch * a.t.beams)) {
-        a.moves[3 * at] = it.old;
-        a.moves[3 * at + 1] = p;
-        a.moves[3 * at + 2] = it.fill;
+    scan(__popc(free_bits), part, total);
+    free += total;
+  }
+  if (tid == 0) totals.v[1] = needed, totals.v[2] = moved, totals.v[3] = free;
+  plan_sync(ctas);
+  uint32_t all_needed, all_moved, all_free;
+  const uint32_t at_item = told_before(&totals, 1, cta, ctas, all_needed);
+  const uint32_t at_move = told_before(&totals, 2, cta, ctas, all_moved);
+  uint32_t at_free = told_before(&totals, 3, cta, ctas, all_free);
+  const bool full = all_free < all_needed;
+  if (tid == 0 && cta == 0) {
+    *a.n_moves = full ? 0 : (int32_t)all_moved;
+    if (full) atomicOr(t.status, ORPO_STATUS_FULL);
+  }
+  // ---- the new pages, lowest first
+  if (!full)
+    for (int32_t p0 = p_begin; p0 < p_end && at_free < all_needed; p0 += kPageTile) {
+      const int32_t p = p0 + tid * kOwn;
+      if (p_end - p_begin > kPageTile) free_bits = ~used_bits(t.refs, p, p_end) & page_bits(p, p_end);
+      uint32_t total, at = at_free + scan(__popc(free_bits), part, total);
+      for (uint32_t bits = free_bits; bits != 0 && at < all_needed; bits &= bits - 1, ++at)
+        if (in_bounds(t.status, at, a.items)) a.fresh[at] = p + __ffs(bits) - 1;
+      at_free += total;
+    }
+  plan_sync(ctas);  // the last look at another CTA's totals is behind
+  if (full) return;
+  for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
+    uint32_t bits[kPer], any_bits = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) any_bits |= bits[u] = a.needs[unit * kPer + u];
+    if (any_bits == 0) continue;
+    load_items(a, unit, it);
+    uint32_t at = at_item + a.before[2 * unit], to = at_move + a.before[2 * unit + 1];
+    int32_t page[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const uint32_t mine = at + __popc(bits[u] & ((1u << lane) - 1u));
+      page[u] = bits[u] >> lane & 1u && in_bounds(t.status, mine, a.items) ? __ldcg(a.fresh + mine) : -1;
+      at += __popc(bits[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const bool move = page[u] >= 0 && it.old[u] >= 0 && it.j[u] == 0 && it.w[u].fill > 0;
+      const uint32_t moves = __ballot_sync(~0u, move), m = to + __popc(moves & ((1u << lane) - 1u));
+      to += __popc(moves);
+      if (page[u] < 0) continue;
+      t.table[it.row[u] * t.ld + it.w[u].first + it.j[u]] = page[u];
+      t.refs[page[u]] = 1;
+      if (it.old[u] >= 0) atomicSub(t.refs + it.old[u], 1);
+      if (move && in_bounds(t.status, m, t.batch * t.beams)) {
+        a.moves[3 * m] = it.old[u];
+        a.moves[3 * m + 1] = page[u];
+        a.moves[3 * m + 2] = (int32_t)it.w[u].fill;
       }
     }
-    moved += total;
   }
-  if (tid == 0) *a.n_moves = (int32_t)moved;
 }
 
 // ------------------------------------------------------------------ copy
@@ -313,6 +607,8 @@ __global__ void __launch_bounds__(kReleaseThreads) release_kernel(TableArgs a, c
 }
 
 // ------------------------------------------------------------------ compact
+// With u(p) pages in use below page p and n in use in all: a free page p < n is hole number p - u(p), a used page p >= n
+// is mover number u(p) - u(n).  So one count of the pages in use, told between the CTAs, gives every number.
 struct CompactArgs {
   const int32_t* table;
   int64_t ld, columns, rows;
@@ -324,52 +620,100 @@ struct CompactArgs {
   int32_t* live;
   int32_t* moves;
   int32_t* n_moves;
-  int32_t* holes;   // [pages / 2]
-  int32_t* movers;  // [pages / 2]
-  int32_t* to;      // [pages] where a page at or above `live` goes; -1: nowhere
+  int32_t pages_per;  // CTA, a multiple of kPageTile
+  int32_t* holes;   // [pages / 2] free pages below n, by number
+  int32_t* movers;  // [pages] used pages at or above n, by the pages in use below them
+  int32_t* below;   // [pages] for pages at or above n: the pages in use below, or -1 for a free one
   int32_t* status;
 };
 
-__global__ void __launch_bounds__(kPlanThreads) compact_kernel(CompactArgs a) {
+// Entries i, i + step, ... of the table.  first: u(n)
+__device__ __forceinline__ void remap(const CompactArgs& a, int32_t live, int32_t first, int64_t i, int64_t step) {
+  int wrong = 0;
+  for (const int64_t n = a.rows * a.columns; i < n; i += step) {
+    const uint32_t row = (uint32_t)i / (uint32_t)a.columns, c = (uint32_t)i - row * (uint32_t)a.columns;
+    if (!in_bounds(a.status, row * a.ld + c, a.rows * a.ld) || !in_bounds(a.status, row * a.ld_new + c, a.rows * a.ld_new)) continue;
+    int32_t e = a.table[row * a.ld + c];
+    if (e < -1 || e >= a.pages) {
+      wrong = 1;
+    } else if (e >= live) {
+      const int32_t u = a.below[e];
+      if (u < 0) wrong = 1;
+      else if (in_bounds(a.status, u - first, a.pages / 2)) e = a.holes[u - first];
+    }
+    a.new_table[row * a.ld_new + c] = e;
+  }
+  if (wrong) atomicOr(a.status, ORPO_STATUS_PAGE);
+}
+
+// here: 0: the table is done by another kernel; 1: here; 2: here, with the lists in shared memory
+__global__ void __launch_bounds__(kPlanThreads) compact_kernel(CompactArgs a, int here) {
+  extern __shared__ __align__(16) int32_t own[];
+  if (here == 2) {  // one CTA: its arrays fit shared memory
+    a.below = own;
+    a.movers = own + a.pages;
+    a.holes = own + 2 * a.pages;
+  }
   __shared__ uint32_t part[kWarps];
+  __shared__ Totals totals;
   grid_trigger();
   grid_wait();
-  const int tid = threadIdx.x;
-  uint32_t mine = 0, n;
-  for (int32_t p = tid; p < a.pages; p += kPlanThreads) mine += a.refs[p] > 0;
-  scan(mine, part, n);
-  const int32_t live = (int32_t)n;
-  uint32_t holes = 0, movers = 0;
-  for (int32_t p0 = 0; p0 < a.pages; p0 += kPlanThreads) {
-    const int32_t p = p0 + tid;
-    const bool used = p < a.pages && a.refs[p] > 0;
-    const bool hole = p < live && !used, mover = p >= live && used;
+  const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;
+  const int32_t p_begin = (int32_t)min((int64_t)cta * a.pages_per, (int64_t)a.pages), p_end = (int32_t)min((int64_t)p_begin + a.pages_per, (int64_t)a.pages);
+  uint32_t used = 0, bits = 0;
+  for (int32_t p0 = p_begin; p0 < p_end; p0 += kPageTile) {
+    const int32_t p = p0 + tid * kOwn;
+    bits = used_bits(a.refs, p, p_end);
     uint32_t total;
-    const uint32_t at = scan((uint32_t)hole | (uint32_t)mover << 16, part, total);
-    if (hole && in_bounds(a.status, holes + (at & 0xffff), a.pages / 2)) a.holes[holes + (at & 0xffff)] = p;
-    if (mover && in_bounds(a.status, movers + (at >> 16), a.pages / 2)) a.movers[movers + (at >> 16)] = p;
-    if (p < a.pages && p >= live && !used) a.to[p] = -1;
-    holes += total & 0xffff;
-    movers += total >> 16;
+    scan(__popc(bits), part, total);
+    used += total;
   }
-  __syncthreads();
-  if (a.new_refs != a.refs)
-    for (int32_t p = tid; p < a.pages; p += kPlanThreads)
-      if (p >= live || a.refs[p] > 0) a.new_refs[p] = p < live ? a.refs[p] : 0;
-  for (int32_t i = tid; i < (int32_t)movers; i += kPlanThreads) {
+  if (tid == 0) totals.v[0] = used, totals.v[1] = 0;
+  plan_sync(ctas);
+  uint32_t n;
+  uint32_t at = told_before(&totals, 0, cta, ctas, n);
+  const int32_t live = (int32_t)n;
+  for (int32_t p0 = p_begin; p0 < p_end; p0 += kPageTile) {
+    const int32_t p = p0 + tid * kOwn;
+    if (p_end - p_begin > kPageTile) bits = used_bits(a.refs, p, p_end);
+    uint32_t total, u = at + scan(__popc(bits), part, total);
+#pragma unroll 4
+    for (int i = 0; i < kOwn; ++i) {
+      const int32_t q = p + i;
+      if (q >= p_end) break;
+      const bool in_use = bits >> i & 1u;
+      if (q == live) totals.v[1] = u + 1;  // u(n), told with 0 for "not mine"
+      if (q < live) {
+        if (!in_use && in_bounds(a.status, q - (int32_t)u, a.pages / 2)) a.holes[q - (int32_t)u] = q;
+        if (in_use && a.new_refs != a.refs) a.new_refs[q] = __ldcg(a.refs + q);
+      } else {
+        if (in_use && in_bounds(a.status, u, a.pages)) a.movers[u] = q;
+        a.below[q] = in_use ? (int32_t)u : -1;
+        if (a.new_refs != a.refs) a.new_refs[q] = 0;
+      }
+      u += in_use;
+    }
+    at += total;
+  }
+  plan_sync(ctas);
+  uint32_t first;
+  told_before(&totals, 1, cta, ctas, first);
+  first = first ? first - 1 : n;  // every page is in use
+  for (int32_t i = cta * kPlanThreads + tid; i < live - (int32_t)first; i += ctas * kPlanThreads) {
     if (!in_bounds(a.status, i, a.pages / 2)) continue;
-    const int32_t from = a.movers[i], to = a.holes[i];
+    const int32_t from = a.movers[first + i], to = a.holes[i];
     a.moves[3 * i] = from;
     a.moves[3 * i + 1] = to;
     a.moves[3 * i + 2] = a.page;
-    a.to[from] = to;
-    a.new_refs[to] = a.refs[from];
+    a.new_refs[to] = __ldcg(a.refs + from);
     if (a.new_refs == a.refs) a.new_refs[from] = 0;
   }
-  if (tid == 0) {
-    *a.n_moves = (int32_t)movers;
+  if (tid == 0 && cta == 0) {
+    *a.n_moves = live - (int32_t)first;
     *a.live = live;
   }
+  if (here) remap(a, live, (int32_t)first, (int64_t)cta * kPlanThreads + tid, (int64_t)ctas * kPlanThreads);
+  if (ctas > 1) cluster_sync();  // the totals may still be read
 }
 
 constexpr int kRemapThreads = 256;
@@ -378,24 +722,11 @@ __global__ void __launch_bounds__(kRemapThreads) remap_kernel(CompactArgs a) {
   grid_trigger();
   grid_wait();
   const int32_t live = *a.live;
-  const int64_t row = blockIdx.x;
-  int wrong = 0;
-  for (int64_t c = (int64_t)blockIdx.y * kRemapThreads + threadIdx.x; c < a.columns; c += (int64_t)gridDim.y * kRemapThreads) {
-    if (!in_bounds(a.status, row * a.ld + c, a.rows * a.ld) || !in_bounds(a.status, row * a.ld_new + c, a.rows * a.ld_new)) continue;
-    int32_t e = a.table[row * a.ld + c];
-    if (e < -1 || e >= a.pages) {
-      wrong = 1;
-    } else if (e >= live) {
-      const int32_t to = a.to[e];
-      if (to >= 0) e = to; else wrong = 1;
-    }
-    a.new_table[row * a.ld_new + c] = e;
-  }
-  if (wrong) atomicOr(a.status, ORPO_STATUS_PAGE);
+  remap(a, live, live - *a.n_moves, (int64_t)blockIdx.x * kRemapThreads + threadIdx.x, (int64_t)gridDim.x * kRemapThreads);
 }
 
 // ------------------------------------------------------------------ host
-constexpr int64_t kMaxPages = 1ll << 24, kMaxPage = 1ll << 16, kMaxInt = (1ll << 31) - 1;
+constexpr int64_t kMaxPages = 1ll << 24, kMaxPage = 1ll << 16, kMaxInt = (1ll << 31) - 1, kMaxItems = 1ll << 30;
 
 bool table_ok(int64_t table_rows, int64_t ld, int64_t columns, int64_t pages, int64_t page) {
   return table_rows >= 0 && table_rows <= (1ll << 20) && columns >= 0 && columns <= kMaxInt && ld >= columns && pages >= 1 &&
@@ -405,10 +736,33 @@ bool table_ok(int64_t table_rows, int64_t ld, int64_t columns, int64_t pages, in
 int64_t width_of(int64_t most, int64_t page) { return most > 0 ? cdiv(most - 1, page) + 1 : 0; }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
-size_t reserve_bytes(int64_t batch, int64_t pages, int64_t items) {
-  return align16(batch * 4) + 2 * align16(pages * 4) + 2 * align16(items * 4);
+// Items per row with the padding that lets a warp's unit of items start on a row: see ReserveArgs.
+int64_t padded_width(int64_t width) {
+  if (width > 32) return cdiv(width, kUnit) * kUnit;
+  int64_t w = 1;
+  while (w < width) w *= 2;
+  return w;
 }
-size_t compact_bytes(int64_t pages) { return 2 * align16(pages / 2 * 4) + align16(pages * 4); }
+size_t reserve_bytes(int64_t batch, int64_t pages, int64_t rows, int64_t width) {
+  const int64_t units = cdiv(rows * padded_width(width), kUnit);
+  return align16(batch * 4) + 2 * align16(pages * 4) + align16(units * kPer * 4) + align16(units * 8) + align16(std::min(pages, rows * width) * 4);
+}
+size_t compact_bytes(int64_t pages) { return align16(pages / 2 * 4) + 2 * align16(pages * 4); }
+
+// CTAs of a plan over so many units and pages, and a CTA's share of n in whole tiles.
+int plan_ctas(int64_t units, int64_t pages) { return units <= kWarps && pages <= kPageTile ? 1 : kMaxCtas; }
+int32_t share(int64_t n, int ctas, int tile) { return (int32_t)(cdiv(cdiv(n, ctas), tile) * tile); }
+constexpr int64_t kRemapHere = 8192;  // table entries per CTA up to which the compaction's own CTAs rewrite the table
+constexpr int64_t kForkHere = 4096;   // (entry, column) pairs up to which the small step does the fork too
+
+template <int KB>
+cudaError_t launch_small(const ReserveArgs& a, cudaStream_t st) {
+  static std::atomic<int> done[64];
+  const cudaError_t e = opt_in_smem(small_reserve_kernel<KB>, (int)small_smem(kSmallPages), done);
+  if (e != cudaSuccess) return e;
+  const size_t smem = small_smem(a.t.pages);
+  return launch_dependent(small_reserve_kernel<KB>, dim3(1), kSmallThreads, smem, st, a, (int32_t)(smem / 12));
+}
 
 bool misaligned(std::initializer_list<const void*> p) {
   uintptr_t at = 0;
@@ -436,9 +790,9 @@ extern "C" {
 
 size_t orpo_pages_workspace_bytes(int64_t table_rows, int64_t pages, int64_t page, int64_t most) {
   if (!table_ok(table_rows, 0, 0, pages, page) || most < 0 || most > kMaxInt) return 0;
-  const int64_t items = table_rows * width_of(most, page);
-  if (items > kMaxInt) return 0;
-  return std::max(std::max(reserve_bytes(table_rows, pages, items), compact_bytes(pages)), (size_t)16);
+  const int64_t width = width_of(most, page);
+  if (table_rows * padded_width(width) > kMaxItems) return 0;
+  return std::max(std::max(reserve_bytes(table_rows, pages, table_rows, width), compact_bytes(pages)), (size_t)16);
 }
 
 int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_t* refs, int64_t pages, int64_t page,
@@ -449,34 +803,52 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
       !table_ok(batch * beams, ld_table, columns, pages, page) || most < 0 || most > kMaxInt || (parent && ld_parent < beams) ||
       max_moves < batch * beams)
     return ORPO_ERR_SHAPE;
-  const int64_t width = width_of(most, page), items = batch * beams * width;
-  if (items > kMaxInt) return ORPO_ERR_SHAPE;
+  const int64_t rows = batch * beams, width = width_of(most, page);
+  if (rows * padded_width(width) > kMaxItems) return ORPO_ERR_SHAPE;
   if (!n_moves || !status || (batch > 0 && ((columns > 0 && !table) || !refs || !length || !moves || !workspace))) return ORPO_ERR_NULL;
   if (misaligned({table, refs, parent, length, more, moves, n_moves, status}) || !aligned16(workspace)) return ORPO_ERR_ALIGN;
-  if (ws_bytes < (batch > 0 ? reserve_bytes(batch, pages, items) : 0)) return ORPO_ERR_WORKSPACE;
+  if (ws_bytes < (batch > 0 ? reserve_bytes(batch, pages, rows, width) : 0)) return ORPO_ERR_WORKSPACE;
   int sms = 0;
   if (int e = device_check(&sms)) return e;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const TableArgs t{table, ld_table, columns, refs, (int32_t)pages, (int32_t)page, parent, ld_parent, length, more, (int32_t)most,
                     batch, beams, status};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  ReserveArgs a{t, nullptr, moves, n_moves, (int32_t)std::max<int64_t>(width, 1), (int32_t)items, nullptr, nullptr, nullptr, nullptr};
-  int32_t* const left_alone = reinterpret_cast<int32_t*>(ws);
-  a.count = reinterpret_cast<int32_t*>(ws += align16(batch * 4));
-  a.last = reinterpret_cast<int32_t*>(ws += align16(pages * 4));
-  a.rank = reinterpret_cast<int32_t*>(ws += align16(pages * 4));
-  a.fresh = reinterpret_cast<int32_t*>(ws += align16(items * 4));
+  const bool fork = parent && batch > 0;
+  ReserveArgs a{};
+  a.t = t;
+  a.moves = moves;
+  a.n_moves = n_moves;
   cudaError_t e = cudaSuccess;
   prof_begin(K_PAGES, st);
-  if (parent && batch > 0) {
-    a.left_alone = left_alone;
+  const bool small = rows * width > 0 && rows * width <= kSmallItems && pages <= kSmallPages;
+  const bool fork_there = fork && small && beams <= 8 && batch * columns <= kForkHere;
+  if (fork && !fork_there) {
+    a.left_alone = reinterpret_cast<int32_t*>(ws);
     const dim3 grid((unsigned)batch, (unsigned)std::max<int64_t>(1, std::min<int64_t>(65535, cdiv(columns, kForkThreads))));
-    e = beams <= 4    ? launch_dependent(fork_kernel<4>, grid, kForkThreads, 0, st, t, left_alone)
-        : beams <= 8  ? launch_dependent(fork_kernel<8>, grid, kForkThreads, 0, st, t, left_alone)
-        : beams <= 16 ? launch_dependent(fork_kernel<16>, grid, kForkThreads, 0, st, t, left_alone)
-                      : launch_dependent(fork_kernel<64>, grid, kForkThreads, 0, st, t, left_alone);
+    e = beams <= 4    ? launch_dependent(fork_kernel<4>, grid, kForkThreads, 0, st, t, a.left_alone)
+        : beams <= 8  ? launch_dependent(fork_kernel<8>, grid, kForkThreads, 0, st, t, a.left_alone)
+        : beams <= 16 ? launch_dependent(fork_kernel<16>, grid, kForkThreads, 0, st, t, a.left_alone)
+                      : launch_dependent(fork_kernel<64>, grid, kForkThreads, 0, st, t, a.left_alone);
   }
-  if (e == cudaSuccess) e = launch_dependent(reserve_kernel, dim3(1), kPlanThreads, 0, st, a);
+  if (e == cudaSuccess && small) {
+    a.width = (int32_t)width;
+    a.items = (int32_t)(rows * width);
+    e = !fork_there ? launch_small<0>(a, st) : beams <= 4 ? launch_small<4>(a, st) : launch_small<8>(a, st);
+  } else if (e == cudaSuccess) {
+    a.width = (int32_t)padded_width(width);
+    a.items = width > 0 ? (int32_t)(rows * a.width) : 0;
+    const int64_t units = cdiv(a.items, kUnit);
+    const int ctas = a.items > 0 ? plan_ctas(units, pages) : 1;
+    a.units_per = share(units, ctas, 1);
+    a.pages_per = share(pages, ctas, kPageTile);
+    a.count = reinterpret_cast<int32_t*>(ws += align16(batch * 4));
+    a.last = reinterpret_cast<int32_t*>(ws += align16(pages * 4));
+    a.needs = reinterpret_cast<uint32_t*>(ws += align16(pages * 4));
+    a.before = reinterpret_cast<uint32_t*>(ws += align16(units * kPer * 4));
+    a.fresh = reinterpret_cast<int32_t*>(ws += align16(units * 8));
+    e = launch_cluster_dependent(reserve_kernel, ctas, kPlanThreads, 0, st, a);
+  }
   prof_end(K_PAGES, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
 }
@@ -539,16 +911,21 @@ int orpo_pages_compact(const int32_t* table, int64_t ld_table, int64_t columns, 
   int sms = 0;
   if (int e = device_check(&sms)) return e;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int ctas = plan_ctas(0, pages);
   CompactArgs a{table, ld_table, columns, table_rows, refs, (int32_t)pages, (int32_t)page, new_table, ld_new, new_refs, live, moves,
-                n_moves, nullptr, nullptr, nullptr, status};
+                n_moves, share(pages, ctas, kPageTile), nullptr, nullptr, nullptr, status};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.holes = reinterpret_cast<int32_t*>(ws);
   a.movers = reinterpret_cast<int32_t*>(ws += align16(pages / 2 * 4));
-  a.to = reinterpret_cast<int32_t*>(ws += align16(pages / 2 * 4));
+  a.below = reinterpret_cast<int32_t*>(ws += align16(pages * 4));
+  const int here = table_rows * columns > (int64_t)ctas * kRemapHere ? 0 : ctas > 1 ? 1 : 2;
+  static std::atomic<int> done[64];
+  const size_t smem = here == 2 ? (size_t)(2 * pages + pages / 2) * 4 : 0;
+  cudaError_t e = opt_in_smem(compact_kernel, kPageTile * 10, done);
   prof_begin(K_PAGES, st);
-  cudaError_t e = launch_dependent(compact_kernel, dim3(1), kPlanThreads, 0, st, a);
-  if (e == cudaSuccess && entries) {
-    const dim3 grid((unsigned)table_rows, (unsigned)std::min<int64_t>(65535, cdiv(columns, kRemapThreads)));
+  if (e == cudaSuccess) e = launch_cluster_dependent(compact_kernel, ctas, kPlanThreads, smem, st, a, here);
+  if (e == cudaSuccess && !here) {
+    const unsigned grid = (unsigned)std::min<int64_t>((int64_t)sms * 8, cdiv(table_rows * columns, kRemapThreads));
     e = launch_dependent(remap_kernel, grid, kRemapThreads, 0, st, a);
   }
   prof_end(K_PAGES, st);
