@@ -150,29 +150,41 @@ __device__ __forceinline__ uint32_t told_before(const Totals* mine, int what, in
   return before;
 }
 
-// Whether each of the kOwn pages from p on is in use, as bits.
-constexpr int kOwn = 16;
-constexpr int kPageTile = kPlanThreads * kOwn;
-__device__ __forceinline__ uint32_t used_bits(const int32_t* refs, int32_t p, int32_t pages) {
-  uint32_t bits = 0;
-  if (p + kOwn <= pages && (reinterpret_cast<uintptr_t>(refs + p) & 15u) == 0) {
-    int4 v[kOwn / 4];
-#pragma unroll
-    for (int i = 0; i < kOwn / 4; ++i) v[i] = __ldcg(reinterpret_cast<const int4*>(refs + p) + i);
-#pragma unroll
-    for (int i = 0; i < kOwn / 4; ++i)
-      bits |= ((uint32_t)(v[i].x > 0) | (uint32_t)(v[i].y > 0) << 1 | (uint32_t)(v[i].z > 0) << 2 | (uint32_t)(v[i].w > 0) << 3) << (4 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) bits |= (uint32_t)(p + i < pages && __ldcg(refs + p + i) > 0) << i;
+// A CTA's stretch of pages, a run of 32-page words per warp: who is in use, as ballots.  A lane keeps the word of its own
+// number; runs of more than 32 words are looked up again.
+struct PageRun {
+  int32_t begin, words;
+  uint32_t kept;
+  __device__ __forceinline__ PageRun(int32_t p_begin, int32_t p_end) : kept(0) {
+    words = (p_end - p_begin + 32 * kWarps - 1) / (32 * kWarps);
+    begin = p_begin + (int32_t)(threadIdx.x >> 5) * words * 32;
   }
-  return bits;
-}
-// Of those, the ones that exist.
-__device__ __forceinline__ uint32_t page_bits(int32_t p, int32_t pages) {
-  const int n = min(max(pages - p, 0), kOwn);
-  return (1u << n) - 1u;
-}
+  // How many pages of the run, of those below p_end, are in use.
+  __device__ __forceinline__ uint32_t count(const int32_t* refs, int32_t p_end) {
+    const int lane = threadIdx.x & 31;
+    uint32_t n = 0;
+    for (int i = 0; i < words; i += 8) {
+      int32_t v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int32_t p = begin + (i + k) * 32 + lane;
+        v[k] = i + k < words && p < p_end ? __ldcg(refs + p) : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t bits = __ballot_sync(~0u, v[k] > 0);
+        if (lane == i + k) kept = bits;
+        n += __popc(bits);
+      }
+    }
+    return n;
+  }
+  __device__ __forceinline__ uint32_t word(const int32_t* refs, int32_t p_end, int i) const {
+    if (words <= 32) return __shfl_sync(~0u, kept, i);
+    const int32_t p = begin + i * 32 + (int32_t)(threadIdx.x & 31);
+    return __ballot_sync(~0u, p < p_end && __ldcg(refs + p) > 0);
+  }
+};
 
 // ------------------------------------------------------------------ reserve
 // Items are (row, column) pairs of the positions asked for, in order; a row has `width` of them, of which those from the
@@ -185,7 +197,7 @@ struct ReserveArgs {
   int32_t width;     // items per row, rounded up to a power of two up to 32 or a multiple of kUnit
   int32_t items;     // so many in all
   int32_t units_per; // CTA
-  int32_t pages_per; // CTA, a multiple of kPageTile
+  int32_t pages_per; // CTA, a multiple of 32 * kWarps
   int32_t* count;    // [pages] how many items hold a page that others hold too,
   int32_t* last;     // [pages] and the last of them
   uint32_t* needs;   // [units][kUnit / 32] items that need a page, as bits
@@ -354,15 +366,28 @@ struct Items {
 // The items of a unit: which rows and columns, and the pages that they have.
 __device__ __forceinline__ void load_items(const ReserveArgs& a, int32_t unit, Items& it) {
   const int lane = threadIdx.x & 31;
+  if (a.width >= kUnit) {  // of one row
+    const uint32_t i = (uint32_t)unit * kUnit, row = i / (uint32_t)a.width, j = i - row * (uint32_t)a.width, b = row / (uint32_t)a.t.beams;
+    const bool on = i < (uint32_t)a.items && !(a.left_alone && a.left_alone[b]);
+    const Wanted w = on ? wanted_columns(a.t, b) : Wanted{0, 0, 0};
 #pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const uint32_t i = (uint32_t)unit * kUnit + u * 32 + lane;
-    const uint32_t row = i / (uint32_t)a.width, b = row / (uint32_t)a.t.beams;
-    it.row[u] = (int32_t)row;
-    it.j[u] = i - row * (uint32_t)a.width;
-    it.asks[u] = i < (uint32_t)a.items && !(a.left_alone && a.left_alone[b]);
-    it.w[u] = it.asks[u] ? wanted_columns(a.t, b) : Wanted{0, 0, 0};
-    it.asks[u] = it.j[u] < it.w[u].n;
+    for (int u = 0; u < kPer; ++u) {
+      it.row[u] = (int32_t)row;
+      it.j[u] = j + u * 32 + lane;
+      it.w[u] = w;
+      it.asks[u] = it.j[u] < w.n;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const uint32_t i = (uint32_t)unit * kUnit + u * 32 + lane;
+      const uint32_t row = i / (uint32_t)a.width, b = row / (uint32_t)a.t.beams;
+      const bool on = i < (uint32_t)a.items && !(a.left_alone && a.left_alone[b]);
+      it.row[u] = (int32_t)row;
+      it.j[u] = i - row * (uint32_t)a.width;
+      it.w[u] = on ? wanted_columns(a.t, b) : Wanted{0, 0, 0};
+      it.asks[u] = it.j[u] < it.w[u].n;
+    }
   }
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
@@ -391,12 +416,15 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
   const int32_t u_begin = (int32_t)min((int64_t)cta * a.units_per, (int64_t)units), u_end = (int32_t)min((int64_t)u_begin + a.units_per, (int64_t)units);
   const int32_t p_begin = (int32_t)min((int64_t)cta * a.pages_per, (int64_t)t.pages), p_end = (int32_t)min((int64_t)p_begin + a.pages_per, (int64_t)t.pages);
   Items it;
+  PageRun run(p_begin, p_end);
+  const uint32_t used = run.count(t.refs, p_end);
 
   // ---- what each item asks for.  Pages that others hold too are counted below
   int shared = 0;
   for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
     load_items(a, unit, it);
     uint32_t need = 0;
+    if (__any_sync(~0u, it.asks[0] | it.asks[1] | it.asks[2] | it.asks[3])) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const bool wrong = it.old[u] < -1 || it.old[u] >= t.pages;
@@ -404,6 +432,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
       if (it.old[u] >= 0 && !wrong && __ldcg(t.refs + it.old[u]) > 1) a.count[it.old[u]] = 0, a.last[it.old[u]] = -1, shared = 1;
       const uint32_t bits = __ballot_sync(~0u, it.asks[u] && it.old[u] == -1);
       if (lane == u) need = bits;
+    }
     }
     if (lane < kPer && in_bounds(t.status, unit, units)) a.needs[unit * kPer + lane] = need;
     need = __popc(need);
@@ -450,7 +479,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
   }
   __syncthreads();
   // ---- sums over the CTA's units, and over its pages
-  uint32_t needed = 0, moved = 0, free = 0, free_bits = 0;
+  uint32_t needed = 0, moved = 0, free = 0;
   for (int32_t u0 = u_begin; u0 < u_end; u0 += kPlanThreads) {
     const int32_t unit = u0 + tid;
     const bool mine = unit < u_end && in_bounds(t.status, unit, units);
@@ -460,33 +489,28 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
     needed += all_need;
     moved += all_moves;
   }
-  for (int32_t p0 = p_begin; p0 < p_end; p0 += kPageTile) {
-    const int32_t p = p0 + tid * kOwn;
-    free_bits = ~used_bits(t.refs, p, p_end) & page_bits(p, p_end);
-    uint32_t total;
-    scan(__popc(free_bits), part, total);
-    free += total;
-  }
+  const uint32_t run_free = (uint32_t)min(max(p_end - run.begin, 0), run.words * 32) - used;
+  const uint32_t run_before = scan(lane == 0 ? run_free : 0, part, free);
   if (tid == 0) totals.v[1] = needed, totals.v[2] = moved, totals.v[3] = free;
   plan_sync(ctas);
   uint32_t all_needed, all_moved, all_free;
   const uint32_t at_item = told_before(&totals, 1, cta, ctas, all_needed);
   const uint32_t at_move = told_before(&totals, 2, cta, ctas, all_moved);
-  uint32_t at_free = told_before(&totals, 3, cta, ctas, all_free);
+  const uint32_t at_free = told_before(&totals, 3, cta, ctas, all_free);
   const bool full = all_free < all_needed;
   if (tid == 0 && cta == 0) {
     *a.n_moves = full ? 0 : (int32_t)all_moved;
     if (full) atomicOr(t.status, ORPO_STATUS_FULL);
   }
   // ---- the new pages, lowest first
+  uint32_t rank = at_free + __shfl_sync(~0u, run_before, 0);
   if (!full)
-    for (int32_t p0 = p_begin; p0 < p_end && at_free < all_needed; p0 += kPageTile) {
-      const int32_t p = p0 + tid * kOwn;
-      if (p_end - p_begin > kPageTile) free_bits = ~used_bits(t.refs, p, p_end) & page_bits(p, p_end);
-      uint32_t total, at = at_free + scan(__popc(free_bits), part, total);
-      for (uint32_t bits = free_bits; bits != 0 && at < all_needed; bits &= bits - 1, ++at)
-        if (in_bounds(t.status, at, a.items)) a.fresh[at] = p + __ffs(bits) - 1;
-      at_free += total;
+    for (int i = 0; i < run.words && rank < all_needed; ++i) {
+      const int32_t p = run.begin + i * 32 + lane;
+      const bool is_free = !(run.word(t.refs, p_end, i) >> lane & 1u) && p < p_end;
+      const uint32_t bits = __ballot_sync(~0u, is_free), at = rank + __popc(bits & ((1u << lane) - 1u));
+      if (is_free && at < all_needed && in_bounds(t.status, at, a.items)) a.fresh[at] = p;
+      rank += __popc(bits);
     }
   plan_sync(ctas);  // the last look at another CTA's totals is behind
   if (full) return;
@@ -620,7 +644,7 @@ struct CompactArgs {
   int32_t* live;
   int32_t* moves;
   int32_t* n_moves;
-  int32_t pages_per;  // CTA, a multiple of kPageTile
+  int32_t pages_per;  // CTA, a multiple of 32 * kWarps
   int32_t* holes;   // [pages / 2] free pages below n, by number
   int32_t* movers;  // [pages] used pages at or above n, by the pages in use below them
   int32_t* below;   // [pages] for pages at or above n: the pages in use below, or -1 for a free one
@@ -660,40 +684,32 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(CompactArgs a, in
   grid_wait();
   const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;
   const int32_t p_begin = (int32_t)min((int64_t)cta * a.pages_per, (int64_t)a.pages), p_end = (int32_t)min((int64_t)p_begin + a.pages_per, (int64_t)a.pages);
-  uint32_t used = 0, bits = 0;
-  for (int32_t p0 = p_begin; p0 < p_end; p0 += kPageTile) {
-    const int32_t p = p0 + tid * kOwn;
-    bits = used_bits(a.refs, p, p_end);
-    uint32_t total;
-    scan(__popc(bits), part, total);
-    used += total;
-  }
+  const int lane = tid & 31;
+  PageRun run(p_begin, p_end);
+  const uint32_t run_used = run.count(a.refs, p_end);
+  uint32_t used;
+  const uint32_t run_before = scan(lane == 0 ? run_used : 0, part, used);
   if (tid == 0) totals.v[0] = used, totals.v[1] = 0;
   plan_sync(ctas);
   uint32_t n;
-  uint32_t at = told_before(&totals, 0, cta, ctas, n);
+  uint32_t before = told_before(&totals, 0, cta, ctas, n) + __shfl_sync(~0u, run_before, 0);
   const int32_t live = (int32_t)n;
-  for (int32_t p0 = p_begin; p0 < p_end; p0 += kPageTile) {
-    const int32_t p = p0 + tid * kOwn;
-    if (p_end - p_begin > kPageTile) bits = used_bits(a.refs, p, p_end);
-    uint32_t total, u = at + scan(__popc(bits), part, total);
-#pragma unroll 4
-    for (int i = 0; i < kOwn; ++i) {
-      const int32_t q = p + i;
-      if (q >= p_end) break;
-      const bool in_use = bits >> i & 1u;
-      if (q == live) totals.v[1] = u + 1;  // u(n), told with 0 for "not mine"
-      if (q < live) {
-        if (!in_use && in_bounds(a.status, q - (int32_t)u, a.pages / 2)) a.holes[q - (int32_t)u] = q;
-        if (in_use && a.new_refs != a.refs) a.new_refs[q] = __ldcg(a.refs + q);
-      } else {
-        if (in_use && in_bounds(a.status, u, a.pages)) a.movers[u] = q;
-        a.below[q] = in_use ? (int32_t)u : -1;
-        if (a.new_refs != a.refs) a.new_refs[q] = 0;
-      }
-      u += in_use;
+  for (int i = 0; i < run.words; ++i) {  // whole warps: the lanes past p_end take part in the ballots
+    const uint32_t bits = run.word(a.refs, p_end, i);
+    const int32_t p = run.begin + i * 32 + lane;
+    const uint32_t u = before + __popc(bits & ((1u << lane) - 1u));  // pages in use below p
+    const bool in_use = bits >> lane & 1u;
+    before += __popc(bits);
+    if (p >= p_end) continue;
+    if (p == live) totals.v[1] = u + 1;  // u(n), told with 0 for "not mine"
+    if (p < live) {
+      if (!in_use && in_bounds(a.status, p - (int32_t)u, a.pages / 2)) a.holes[p - (int32_t)u] = p;
+      if (in_use && a.new_refs != a.refs) a.new_refs[p] = __ldcg(a.refs + p);
+    } else {
+      if (in_use && in_bounds(a.status, u, a.pages)) a.movers[u] = p;
+      a.below[p] = in_use ? (int32_t)u : -1;
+      if (a.new_refs != a.refs) a.new_refs[p] = 0;
     }
-    at += total;
   }
   plan_sync(ctas);
   uint32_t first;
@@ -750,7 +766,7 @@ size_t reserve_bytes(int64_t batch, int64_t pages, int64_t rows, int64_t width) 
 size_t compact_bytes(int64_t pages) { return align16(pages / 2 * 4) + 2 * align16(pages * 4); }
 
 // CTAs of a plan over so many units and pages, and a CTA's share of n in whole tiles.
-int plan_ctas(int64_t units, int64_t pages) { return units <= kWarps && pages <= kPageTile ? 1 : kMaxCtas; }
+int plan_ctas(int64_t units, int64_t pages) { return units <= kWarps && pages <= kSmallPages ? 1 : kMaxCtas; }
 int32_t share(int64_t n, int ctas, int tile) { return (int32_t)(cdiv(cdiv(n, ctas), tile) * tile); }
 constexpr int64_t kRemapHere = 8192;  // table entries per CTA up to which the compaction's own CTAs rewrite the table
 constexpr int64_t kForkHere = 4096;   // (entry, column) pairs up to which the small step does the fork too
@@ -841,7 +857,7 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
     const int64_t units = cdiv(a.items, kUnit);
     const int ctas = a.items > 0 ? plan_ctas(units, pages) : 1;
     a.units_per = share(units, ctas, 1);
-    a.pages_per = share(pages, ctas, kPageTile);
+    a.pages_per = share(pages, ctas, 32 * kWarps);
     a.count = reinterpret_cast<int32_t*>(ws += align16(batch * 4));
     a.last = reinterpret_cast<int32_t*>(ws += align16(pages * 4));
     a.needs = reinterpret_cast<uint32_t*>(ws += align16(pages * 4));
@@ -913,7 +929,7 @@ int orpo_pages_compact(const int32_t* table, int64_t ld_table, int64_t columns, 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int ctas = plan_ctas(0, pages);
   CompactArgs a{table, ld_table, columns, table_rows, refs, (int32_t)pages, (int32_t)page, new_table, ld_new, new_refs, live, moves,
-                n_moves, share(pages, ctas, kPageTile), nullptr, nullptr, nullptr, status};
+                n_moves, share(pages, ctas, 32 * kWarps), nullptr, nullptr, nullptr, status};
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.holes = reinterpret_cast<int32_t*>(ws);
   a.movers = reinterpret_cast<int32_t*>(ws += align16(pages / 2 * 4));
@@ -921,7 +937,7 @@ int orpo_pages_compact(const int32_t* table, int64_t ld_table, int64_t columns, 
   const int here = table_rows * columns > (int64_t)ctas * kRemapHere ? 0 : ctas > 1 ? 1 : 2;
   static std::atomic<int> done[64];
   const size_t smem = here == 2 ? (size_t)(2 * pages + pages / 2) * 4 : 0;
-  cudaError_t e = opt_in_smem(compact_kernel, kPageTile * 10, done);
+  cudaError_t e = opt_in_smem(compact_kernel, kSmallPages * 10, done);
   prof_begin(K_PAGES, st);
   if (e == cudaSuccess) e = launch_cluster_dependent(compact_kernel, ctas, kPlanThreads, smem, st, a, here);
   if (e == cudaSuccess && !here) {
