@@ -139,8 +139,8 @@ int orpo_beam_reorder(void* state, const int32_t* parent, int64_t ld_parent, con
  * Device errors: ORPO_STATUS_PARENT (a length outside [0, capacity]; that entry's rows are left as they are),
  * ORPO_STATUS_MASK (a mask_row outside [-1, n_masks); that row is left as it is).
  * Results do not depend on run-to-run scheduling.  No workspace.
- * Limits: batch >= 0, 1 <= beams <= 2^20, batch * beams <= 2^20, 1 <= V <= 2^31 - 2^16, 0 <= capacity < 2^28, 0 <= n_bias
- * <= ORPO_MAX_BIAS, 0 <= no_repeat <= ORPO_MAX_NGRAM, 1 <= n_masks < 2^31 where masks are given; repetition > 0; all
+ * Limits: batch >= 0, 1 <= beams <= 2^20, batch * beams <= 2^20, 1 <= V <= 2^31 - 2^16, batch * beams * V < 2^44,
+ * 0 <= capacity < 2^28, 0 <= n_bias <= ORPO_MAX_BIAS, 0 <= no_repeat <= ORPO_MAX_NGRAM, 1 <= n_masks < 2^31 where masks are given; repetition > 0; all
  * penalties finite.  4-byte alignment (2 for bf16 logits).
  */
 #define ORPO_MAX_BIAS 65536

@@ -5,10 +5,17 @@
 //   + the token's biases;  -inf where a mask or an n-gram bans it
 //
 // Only the logits that one of these concerns are read or written, so the work is the history's length and the masked
-// logits, not the vocabulary.  A CTA owns one row's logits of a range of `chunk` tokens.  It counts the history's tokens
-// that fall into its range in a table in shared memory, one word per token, so there is nothing to hash or to overflow
-// and the counts are exact; the first to meet a token lists it.  Then the masked logits are overwritten
-// 16 bytes at a time, and each listed token's logit is read, adjusted and written by one thread.
+// logits, not the vocabulary.  Two kinds of CTAs share a launch; they never write the same logit, so they need no order:
+//   history CTAs   adjust the tokens that the history and the bias list hold, unless a mask bans them.
+//     Without a frequency penalty it is enough to know which tokens there are: one CTA per row, with a bit per token of the
+//     vocabulary in shared memory.  Who sets a token's bit first adjusts its logit at once; the generated part is taken before
+//     the prompt, so that the first to come knows the penalty.
+//     With one, tokens are counted: a CTA per range of the vocabulary, with a counter per token, which no history
+//     can overflow; each CTA reads the whole history.
+//     Neither has anything to probe or to sort, and integer atomics give the same whatever their order.  (A hash table of
+//     a row's tokens took four times as long: its probes follow one another.)
+//   mask CTAs      overwrite the masked logits of a range, 16 bytes per lane where 512 bytes in a row are all masked, else a
+//                  lane per token: nothing is read but the mask.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -42,16 +49,21 @@ struct AdjustArgs {
   int64_t ld_masks, n_masks;
   const int32_t* mask_row;
   int32_t* status;
-  int chunk;       // tokens per CTA, a multiple of 32
-  int list_cap;    // listed tokens at most
+  int parts;       // history CTAs per row
+  int list_cap;    // listed tokens per range at most
+  int bit_words;   // of a map of the vocabulary
+  int clear;       // 16-byte pieces of shared memory to clear
 };
 
-constexpr int kThreads = 256;
-// A token's word in the table: how often the generated part holds it, and
+constexpr int kThreads = 512;
+// What is known of a token: how often the generated part holds it, and flags
 constexpr uint32_t kCount = (1u << 28) - 1;
-constexpr uint32_t kBan = 1u << 28;     // it would end an n-gram for the second time
-constexpr uint32_t kPrompt = 1u << 29;  // the prompt holds it
-constexpr uint32_t kBias = 1u << 30;    // the bias list holds it: the list's thread handles it
+constexpr uint32_t kPrompt = 1u << 28;  // the prompt holds it
+constexpr uint32_t kBan = 1u << 29;     // it would end an n-gram for the second time
+constexpr uint32_t kBias = 1u << 30;    // the bias list holds it: the list's thread adjusts it
+// as 16 bits, for histories of up to kFew tokens
+constexpr int kFew = (1 << 13) - 1;
+constexpr uint32_t kFewPrompt = 1u << 13, kFewBan = 1u << 14, kFewBias = 1u << 15;
 
 template <class T>
 struct Logit;
@@ -68,167 +80,337 @@ struct Logit<uint16_t> {
   static constexpr uint32_t kNinf = 0xff80ff80u;
 };
 
-__host__ __device__ inline int table_bytes(int chunk) { return chunk * 4; }
-__host__ __device__ inline int words_bytes(int chunk) { return (chunk / 32 + 4) * 4; }  // a word of ones before, up to three behind
+// ------------------------------------------------------------------ the history's tokens
+constexpr int kUnroll = 8;
+
+// Calls each(t, token, n) with kUnroll tokens of history positions t[0], ... in [begin, end) (token -1: none), whole warps at
+// a time.
+template <class Each>
+__device__ __forceinline__ void each_tokens(const int32_t* h, int begin, int end, Each each) {
+  const int lane = threadIdx.x & 31;
+  for (int t0 = begin + (int)threadIdx.x - lane; t0 < end; t0 += kUnroll * kThreads) {
+    int t[kUnroll];
+    int32_t v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      t[u] = t0 + u * kThreads + lane;
+      v[u] = t[u] < end ? h[t[u]] : -1;
+    }
+    each(t, v);
+  }
+}
+
+// Whether the tokens before position t are the tail's; all lanes of a warp together, whose v are neighbours.
+__device__ __forceinline__ bool ends_again(const int32_t* h, int t, int32_t v, int len, const int32_t* tail, int n_tail) {
+  if (n_tail <= 0) return n_tail == 0 && t < len;
+  int32_t before = __shfl_up_sync(~0u, v, 1);
+  if (t < n_tail || t >= len) return false;
+  if ((threadIdx.x & 31) == 0) before = h[t - 1];
+  bool same = before == tail[n_tail - 1];
+  for (int i = 2; i <= n_tail && same; ++i) same = h[t - i] == tail[n_tail - i];
+  return same;
+}
 
 template <class T>
+struct Row {
+  T* x;                   // the row's logits
+  const uint32_t* words;  // its mask, or nullptr
+  int64_t at, all;        // where it starts, and all logits (bounds-checked build)
+};
+
+// N tokens (-1: none) with what is known of them and their biases, all their logits on the way at once; masked ones are left
+// to the mask CTAs.
+template <class T, int N>
+__device__ __forceinline__ void adjust(const AdjustArgs& a, const Row<T>& row, const int32_t (&token)[N], const uint32_t (&w)[N],
+                                       float bias) {
+  float y[N];
+  bool on[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    on[i] = token[i] >= 0 && in_bounds(a.status, row.at + token[i], row.all);
+    y[i] = on[i] ? Logit<T>::load(row.x + token[i]) : 0.f;
+    if (row.words && on[i]) on[i] = row.words[token[i] >> 5] >> (token[i] & 31) & 1u;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!on[i]) continue;
+    if (w[i] & (kCount | kPrompt)) y[i] = y[i] > 0.f ? y[i] / a.repetition : y[i] * a.repetition;
+    if (w[i] & kCount) y[i] -= fmaf(a.frequency, (float)(w[i] & kCount), a.presence);
+    y[i] = w[i] & kBan ? -INFINITY : y[i] + bias;
+    row.x[token[i]] = Logit<T>::make(y[i]);
+  }
+}
+
+// The bias list's tokens in [v0, v0 + size): the first of a token's entries adds them all up, in order.
+template <class T, class Known>
+__device__ __forceinline__ void adjust_biased(const AdjustArgs& a, const Row<T>& row, const int32_t* token, const float* value, bool twice,
+                                              int64_t v0, int size, Known known) {
+  for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
+    const int32_t v = token[j];
+    if (v < 0 || (uint32_t)(v - (int32_t)v0) >= (uint32_t)size) continue;
+    float sum = value[j];
+    if (twice) {
+      bool first = true;
+      for (int i = 0; i < j && first; ++i) first = token[i] != v;
+      if (!first) continue;
+      for (int i = j + 1; i < a.n_bias; ++i)
+        if (token[i] == v) sum += value[i];
+    }
+    const int32_t tokens[1] = {v};
+    const uint32_t w[1] = {known(v)};
+    adjust<T, 1>(a, row, tokens, w, sum);
+  }
+}
+
+// ------------------------------------------------------------------ masks
+constexpr int kMaskSets = 2;                              // of 32 words, per warp
+constexpr int kMaskTokens = kThreads * 32 * kMaskSets;    // per CTA
+
+template <class T>
+__device__ __forceinline__ void mask_range(const AdjustArgs& a, const Row<T>& row, int64_t v0) {
+  constexpr int kGroup = 512 / (32 * (int)sizeof(T));  // words whose logits are 512 bytes
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n_words = (a.V + 31) / 32;
+  const bool aligned = (reinterpret_cast<uintptr_t>(row.x) & 15u) == 0;
+  uint32_t word[kMaskSets];
+  int64_t first[kMaskSets];
+#pragma unroll
+  for (int s = 0; s < kMaskSets; ++s) {
+    first[s] = v0 / 32 + (s * (kThreads / 32) + warp) * 32;
+    const int64_t i = first[s] + lane;
+    word[s] = i < n_words ? row.words[i] : ~0u;
+    if (i == n_words - 1 && a.V % 32) word[s] |= ~0u << (a.V % 32);
+  }
+#pragma unroll
+  for (int s = 0; s < kMaskSets; ++s) {
+    const uint32_t none = __ballot_sync(~0u, word[s] == 0), all = __ballot_sync(~0u, word[s] == ~0u);
+    if (all == ~0u) continue;
+    for (int g = 0; g < 32; g += kGroup) {
+      constexpr uint32_t kOnes = (1u << kGroup) - 1u;
+      if ((all >> g & kOnes) == kOnes) continue;
+      T* const x = row.x + (first[s] + g) * 32;
+      if (aligned && (none >> g & kOnes) == kOnes) {
+        if (in_bounds(a.status, row.at + (first[s] + g + kGroup) * 32 - 1, row.all))
+          reinterpret_cast<uint4*>(x)[lane] = make_uint4(Logit<T>::kNinf, Logit<T>::kNinf, Logit<T>::kNinf, Logit<T>::kNinf);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        const uint32_t w = __shfl_sync(~0u, word[s], g + i);
+        if (!(w & 1u << lane) && in_bounds(a.status, row.at + (first[s] + g + i) * 32 + lane, row.all)) x[i * 32 + lane] = Logit<T>::make(-INFINITY);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the kernel
+// How history CTAs know the tokens: bits, or 16- or 32-bit counters of a range.
+enum { kBits = 0, kCount16 = 1, kCount32 = 2 };
+constexpr int kTableBytes = 64 << 10;
+__host__ __device__ constexpr int range_of(int form) { return kTableBytes / (form == kCount16 ? 2 : 4); }
+constexpr int kMostBits = 200 << 10;  // bytes of all bitmaps
+
+// One bit per token of the vocabulary, `stride` words a map: met; banned (n-grams); of the bias list; met in the generated part
+// (kept for the bias list).
+struct Bits {
+  uint32_t *met, *ban, *bias, *gen;
+  __device__ static bool get(const uint32_t* map, int32_t v) { return map[v >> 5] >> (v & 31) & 1u; }
+  __device__ static bool set(uint32_t* map, int32_t v) {  // whether it was set before
+    const uint32_t bit = 1u << (v & 31);
+    return (atomicOr(map + (v >> 5), bit) & bit) != 0;
+  }
+};
+
+template <class T>
+__device__ __forceinline__ void by_bits(const AdjustArgs& a, const Row<T>& row, uint32_t* smem, const int32_t* h, int len, int prompt,
+                                        const int32_t* tail, int n_tail, const int32_t* bias_token, const float* bias_value, int* twice,
+                                        bool penalties) {
+  const int stride = a.bit_words;
+  const bool biased = a.n_bias > 0;
+  const Bits bits{smem, smem + stride, smem + (a.ngram > 0 ? 2 : 1) * stride, smem + (a.ngram > 0 ? 3 : 2) * stride};
+  const int32_t V = (int32_t)a.V;
+  for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
+    const int32_t v = bias_token[j];
+    if (v >= 0 && v < V && Bits::set(bits.bias, v)) *twice = 1;
+  }
+  if (n_tail >= 0)
+    each_tokens(h, 0, len, [&](const int (&t)[kUnroll], const int32_t (&v)[kUnroll]) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (ends_again(h, t[u], v[u], len, tail, n_tail) && v[u] >= 0 && v[u] < V && !Bits::set(bits.ban, v[u]) &&
+            in_bounds(a.status, row.at + v[u], row.all))
+          row.x[v[u]] = Logit<T>::make(-INFINITY);  // as a mask would
+    });
+  prompt = a.presence != 0.f ? min(max(prompt, 0), len) : 0;  // else the prompt's tokens are as the others
+  if (penalties) {
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {  // what was generated, then the prompt
+      if (part == 1 && prompt == 0) break;
+      if (part == 1 || biased || n_tail >= 0) __syncthreads();
+      each_tokens(h, part == 0 ? prompt : 0, part == 0 ? len : prompt, [&](const int (&)[kUnroll], const int32_t (&v)[kUnroll]) {
+        int32_t token[kUnroll];
+        uint32_t w[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          w[u] = part == 0 ? 1u : kPrompt;
+          token[u] = v[u] >= 0 && v[u] < V && !Bits::set(bits.met, v[u]) ? v[u] : -1;
+          if (token[u] >= 0 && n_tail >= 0 && Bits::get(bits.ban, token[u])) token[u] = -1;
+          if (token[u] >= 0 && biased && Bits::get(bits.bias, token[u])) {
+            if (part == 0) Bits::set(bits.gen, token[u]);
+            token[u] = -1;
+          }
+        }
+        adjust<T, kUnroll>(a, row, token, w, 0.f);
+      });
+    }
+  }
+  if (!biased) return;
+  __syncthreads();
+  adjust_biased<T>(a, row, bias_token, bias_value, *twice, 0, V, [&](int32_t v) {
+    return (penalties && Bits::get(bits.gen, v) ? 1u : 0u) | (penalties && Bits::get(bits.met, v) ? kPrompt : 0u) |
+           (n_tail >= 0 && Bits::get(bits.ban, v) ? kBan : 0u);
+  });
+}
+
+// The counters of a range.
+template <int kForm>
+struct Counters {
+  uint32_t* table;
+  // Adds one to, or sets flags of, the token at `at`; what was known before, in the form's own bits.
+  __device__ uint32_t add(uint32_t at) const {
+    if (kForm == kCount32) return atomicAdd(table + at, 1u);
+    return atomicAdd(table + at / 2, 1u << (at & 1u) * 16) >> (at & 1u) * 16 & 0xffffu;
+  }
+  __device__ uint32_t flag(uint32_t at, uint32_t flag32, uint32_t flag16) const {
+    if (kForm == kCount32) return atomicOr(table + at, flag32);
+    return atomicOr(table + at / 2, flag16 << (at & 1u) * 16) >> (at & 1u) * 16 & 0xffffu;
+  }
+  __device__ uint32_t known(uint32_t at) const {
+    if (kForm == kCount32) return table[at];
+    const uint32_t w = table[at / 2] >> (at & 1u) * 16 & 0xffffu;
+    return (w & (uint32_t)kFew) | (w & kFewPrompt ? kPrompt : 0u) | (w & kFewBan ? kBan : 0u) | (w & kFewBias ? kBias : 0u);
+  }
+};
+
+template <class T, int kForm>
+__device__ __forceinline__ void by_counts(const AdjustArgs& a, const Row<T>& row, uint32_t* smem, int64_t v0, const int32_t* h, int len,
+                                          int prompt, const int32_t* tail, int n_tail, const int32_t* bias_token, const float* bias_value,
+                                          int* listed, int* twice, bool penalties) {
+  constexpr int kRange = range_of(kForm);
+  const Counters<kForm> counters{smem};
+  uint16_t* const list = reinterpret_cast<uint16_t*>(smem + kTableBytes / 4);  // tokens met, each once
+  const uint32_t size = (uint32_t)min((int64_t)kRange, a.V - v0);
+  each_tokens(h, 0, len, [&](const int (&t)[kUnroll], const int32_t (&v)[kUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const bool banned = ends_again(h, t[u], v[u], len, tail, n_tail);
+      const uint32_t at = (uint32_t)(v[u] - (int32_t)v0);
+      if (v[u] < 0 || at >= size || !(penalties || banned) || !in_bounds(a.status, at, kRange)) continue;
+      const uint32_t old = t[u] >= prompt ? counters.add(at) : counters.flag(at, kPrompt, kFewPrompt);
+      if (old == 0) {
+        const int j = atomicAdd(listed, 1);
+        if (in_bounds(a.status, j, a.list_cap)) list[j] = (uint16_t)at;
+      }
+      if (banned) counters.flag(at, kBan, kFewBan);
+    }
+  });
+  for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
+    const int32_t v = bias_token[j];
+    const uint32_t at = (uint32_t)(v - (int32_t)v0);
+    if (v < 0 || at >= size || !in_bounds(a.status, at, kRange)) continue;
+    if (counters.flag(at, kBias, kFewBias) & (kForm == kCount32 ? kBias : kFewBias)) *twice = 1;
+  }
+  __syncthreads();
+  adjust_biased<T>(a, row, bias_token, bias_value, *twice, v0, (int)size, [&](int32_t v) { return counters.known(v - (int32_t)v0); });
+  const int n = *listed;
+  for (int j0 = threadIdx.x; j0 < n; j0 += kUnroll * kThreads) {
+    int32_t token[kUnroll];
+    uint32_t w[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + u * kThreads, at = j < n ? list[j] : -1;
+      w[u] = at >= 0 ? counters.known(at) : 0;
+      token[u] = at >= 0 && !(w[u] & kBias) ? (int32_t)v0 + at : -1;
+    }
+    adjust<T, kUnroll>(a, row, token, w, 0.f);
+  }
+}
+
+template <class T, int kForm>
 __global__ void __launch_bounds__(kThreads) adjust_kernel(AdjustArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(16) uint32_t smem[];
   __shared__ int32_t tail[ORPO_MAX_NGRAM];
   __shared__ int listed, twice;
-  const bool counts = a.history != nullptr || a.n_bias > 0;
-  uint32_t* const words = reinterpret_cast<uint32_t*>(smem);
-  uint32_t* const table = reinterpret_cast<uint32_t*>(smem + words_bytes(a.chunk));
-  uint16_t* const list = reinterpret_cast<uint16_t*>(smem + words_bytes(a.chunk) + table_bytes(a.chunk));
   const int tid = threadIdx.x;
   grid_trigger();
-  const int64_t r = blockIdx.x, v0 = (int64_t)blockIdx.y * a.chunk;
-  const int size = (int)min((int64_t)a.chunk, a.V - v0);
-  if (counts)
-    for (int i = tid; i < a.chunk / 4; i += kThreads)
-      if (in_bounds(a.status, i, a.chunk / 4)) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
+  const uint32_t part = blockIdx.x / (uint32_t)a.rows;  // history CTAs, which take longer, come first
+  const int64_t r = blockIdx.x - part * (uint32_t)a.rows;
+  const bool history = part < (uint32_t)a.parts;
+  if (history)
+    for (int i = tid; i < a.clear; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) listed = 0, twice = 0;
   grid_wait();
 
-  const int64_t b = r / a.beams;
+  const int64_t b = (uint32_t)r / (uint32_t)a.beams;
   const int len = a.history ? a.length[b] : 0;
   const int mask = a.masks ? a.mask_row[r] : -1;
+  const int prompt = a.prompt && a.history ? a.prompt[b] : 0;
   const int wrong = (len < 0 || len > a.capacity ? ORPO_STATUS_PARENT : 0) |
                     (mask < -1 || (a.masks && mask >= a.n_masks) ? ORPO_STATUS_MASK : 0);
   if (wrong) {
-    if (tid == 0 && blockIdx.y == 0) atomicOr(a.status, wrong);
+    if (tid == 0 && part == 0) atomicOr(a.status, wrong);
     return;
   }
-  const int n_words = (size + 31) / 32;
-  for (int i = tid; i < a.chunk / 32 + 4; i += kThreads) {
-    uint32_t w = ~0u;
-    if (mask >= 0 && i >= 1 && i <= n_words) {
-      w = a.masks[mask * a.ld_masks + v0 / 32 + i - 1];
-      if (i == n_words && size % 32) w |= ~0u << (size % 32);
-    }
-    words[i] = w;
+  const Row<T> row{static_cast<T*>(a.logits) + r * a.ld, mask >= 0 ? a.masks + mask * a.ld_masks : nullptr, r * a.ld, a.rows * a.ld};
+  if (!history) {
+    if (mask >= 0) mask_range(a, row, (int64_t)(part - a.parts) * kMaskTokens);
+    return;
   }
   const int32_t* const h = a.history + r * a.ld_history;
-  const int n_tail = a.ngram > 0 && len >= a.ngram ? a.ngram - 1 : -1;  // -1: no n-gram to look for
+  const int32_t* const bias_token = a.bias_token + b * a.ld_bias;
+  const float* const bias_value = a.bias_value + b * a.ld_bias;
+  // the n-gram to look for: the last n - 1 tokens, if all of them are tokens
+  int n_tail = a.ngram > 0 && len >= a.ngram ? a.ngram - 1 : -1;
   bool bad_tail = false;
   if (tid < n_tail) {
     const int t = h[len - n_tail + tid];
     tail[tid] = t;
     bad_tail = t < 0 || t >= a.V;
   }
-  const bool bans = !__syncthreads_or(bad_tail) && n_tail >= 0;
-  const int prompt = a.prompt && a.history ? a.prompt[b] : 0;
-
-  // ---- count
-  auto add = [&](int t, int32_t token) {
-    const uint32_t at = (uint32_t)(token - (int32_t)v0);
-    if (token < 0 || at >= (uint32_t)size || !in_bounds(a.status, at, a.chunk)) return;
-    const uint32_t old = t >= prompt ? atomicAdd(&table[at], 1u) : atomicOr(&table[at], kPrompt);
-    if (old == 0) {
-      const int j = atomicAdd(&listed, 1);
-      if (in_bounds(a.status, j, a.list_cap)) list[j] = (uint16_t)at;
-    }
-    if (bans && t >= n_tail) {
-      bool same = true;
-      for (int i = 1; i <= n_tail && same; ++i) same = h[t - i] == tail[n_tail - i];
-      if (same) atomicOr(&table[at], kBan);
-    }
-  };
-  constexpr int kUnroll = 8;
-  int t = tid;
-  for (; t + (kUnroll - 1) * kThreads < len; t += kUnroll * kThreads) {
-    int32_t v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = h[t + u * kThreads];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) add(t + u * kThreads, v[u]);
-  }
-  for (; t < len; t += kThreads) add(t, h[t]);
-  const int32_t* const bias_token = a.bias_token + b * a.ld_bias;
-  const float* const bias_value = a.bias_value + b * a.ld_bias;
-  for (int j = tid; j < a.n_bias; j += kThreads) {
-    const int32_t token = bias_token[j];
-    const uint32_t at = (uint32_t)(token - (int32_t)v0);
-    if (token < 0 || at >= (uint32_t)size || !in_bounds(a.status, at, a.chunk)) continue;
-    if (atomicOr(&table[at], kBias) & kBias) twice = 1;
-  }
-  __syncthreads();
-
-  // ---- adjust: one thread per token; masked tokens are left to the masks
-  T* const x = static_cast<T*>(a.logits) + r * a.ld + v0;
+  if (__syncthreads_or(bad_tail)) n_tail = -1;
   const bool penalties = a.repetition != 1.f || a.presence != 0.f || a.frequency != 0.f;
-  auto adjust = [&](uint32_t at, uint32_t w, float bias) {
-    if (!(words[1 + at / 32] >> (at % 32) & 1u)) return;
-    if (!in_bounds(a.status, r * a.ld + v0 + at, a.rows * a.ld)) return;
-    if (w & kBan) {
-      x[at] = Logit<T>::make(-INFINITY);
-      return;
-    }
-    float y = Logit<T>::load(x + at);
-    if (w & (kCount | kPrompt)) y = y > 0.f ? y / a.repetition : y * a.repetition;
-    if (w & kCount) y -= fmaf(a.frequency, (float)(w & kCount), a.presence);
-    x[at] = Logit<T>::make(y + bias);
-  };
-  for (int j = tid; j < a.n_bias; j += kThreads) {
-    const int32_t token = bias_token[j];
-    const uint32_t at = (uint32_t)(token - (int32_t)v0);
-    if (token < 0 || at >= (uint32_t)size || !in_bounds(a.status, at, a.chunk)) continue;
-    float sum = bias_value[j];
-    if (twice) {  // the first of a token's entries adds them all up, in order
-      bool first = true;
-      for (int i = 0; i < j && first; ++i) first = bias_token[i] != token;
-      if (!first) continue;
-      for (int i = j + 1; i < a.n_bias; ++i)
-        if (bias_token[i] == token) sum += bias_value[i];
-    }
-    adjust(at, table[at], sum);
-  }
-  if (penalties || bans)
-    for (int j = tid; j < listed; j += kThreads) {
-      const uint32_t at = list[j], w = table[at];
-      if (w & kBias || (!penalties && !(w & kBan))) continue;
-      adjust(at, w, 0.f);
-    }
-
-  // ---- masks: pieces of 16 bytes from the boundary before the range on
-  if (mask < 0) return;
-  constexpr int E = 16 / (int)sizeof(T);
-  const int before = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
-  for (int p = tid; p * E < size + before; p += kThreads) {
-    const int at = p * E - before;  // first token of the piece
-    const uint32_t bit = (uint32_t)(at + 32);
-    const uint32_t ok = __funnelshift_r(words[bit / 32], words[bit / 32 + 1], bit % 32) & ((1u << E) - 1);
-    if (ok == (1u << E) - 1) continue;
-    if (ok == 0) {
-      if (in_bounds(a.status, r * a.ld + v0 + at, a.rows * a.ld) && in_bounds(a.status, r * a.ld + v0 + at + E - 1, a.rows * a.ld))
-        *reinterpret_cast<uint4*>(x + at) = make_uint4(Logit<T>::kNinf, Logit<T>::kNinf, Logit<T>::kNinf, Logit<T>::kNinf);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        if (!(ok >> i & 1u) && in_bounds(a.status, r * a.ld + v0 + at + i, a.rows * a.ld)) x[at + i] = Logit<T>::make(-INFINITY);
-    }
-  }
+  if constexpr (kForm == kBits)
+    by_bits<T>(a, row, smem, h, len, prompt, tail, n_tail, bias_token, bias_value, &twice, penalties);
+  else
+    by_counts<T, kForm>(a, row, smem, (int64_t)part * range_of(kForm), h, len, prompt, tail, n_tail, bias_token, bias_value, &listed, &twice,
+                        penalties);
 }
 
-constexpr int kMaxChunk = 32768;  // list entries are 16 bits, and the table has to fit beside it
+template <class T, int kForm>
+cudaError_t launch_form(const AdjustArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
+  static std::atomic<int> done[64];
+  cudaError_t e = opt_in_smem(adjust_kernel<T, kForm>, kForm == kBits ? kMostBits : kTableBytes + range_of(kForm) * 2, done);
+  if (e != cudaSuccess) return e;
+  prof_begin(K_ADJUST, st);
+  e = launch_dependent(adjust_kernel<T, kForm>, grid, kThreads, smem, st, a);
+  prof_end(K_ADJUST, st);
+  return e;
+}
 
 template <class T>
 cudaError_t launch(AdjustArgs a, cudaStream_t st) {
-  a.chunk = a.V > (int64_t)65535 * 8192 ? kMaxChunk : 8192;
-  a.chunk = (int)std::min<int64_t>(a.chunk, cdiv(a.V, 128) * 128);
-  const bool counts = a.history != nullptr || a.n_bias > 0;
-  a.list_cap = (int)std::min<int64_t>(a.chunk, a.history ? a.capacity : 0);
-  const int smem = words_bytes(a.chunk) + (counts ? table_bytes(a.chunk) + cdiv(a.list_cap * 2, 16) * 16 : 0);
-  static std::atomic<int> done[64];
-  constexpr int kMost = kMaxChunk * 6 + kMaxChunk / 8 + 16;
-  static_assert(kMost <= 227 << 10, "a CTA's shared memory");
-  cudaError_t e = opt_in_smem(adjust_kernel<T>, kMost, done);
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)a.rows, (unsigned)cdiv(a.V, a.chunk));
-  prof_begin(K_ADJUST, st);
-  e = launch_dependent(adjust_kernel<T>, grid, kThreads, (size_t)smem, st, a);
-  prof_end(K_ADJUST, st);
-  return e;
+  const bool history = a.history != nullptr || a.n_bias > 0;
+  a.bit_words = (int)(cdiv(a.V, 128) * 4);
+  const int64_t bits = (int64_t)a.bit_words * 4 * (1 + (a.ngram > 0) + 2 * (a.n_bias > 0));
+  const int form = a.frequency == 0.f && bits <= kMostBits ? kBits : a.capacity <= kFew ? kCount16 : kCount32;
+  a.parts = !history ? 0 : form == kBits ? 1 : (int)cdiv(a.V, range_of(form));
+  a.list_cap = std::min(range_of(form), a.history ? a.capacity : 0);
+  const int64_t smem = !history ? 0 : form == kBits ? bits : kTableBytes + cdiv(a.list_cap * 2, 16) * 16;
+  a.clear = (int)((form == kBits ? bits : kTableBytes) / 16);
+  const dim3 grid((unsigned)(a.rows * (a.parts + (a.masks ? cdiv(a.V, kMaskTokens) : 0))));
+  return form == kBits      ? launch_form<T, kBits>(a, grid, (size_t)smem, st)
+         : form == kCount16 ? launch_form<T, kCount16>(a, grid, (size_t)smem, st)
+                            : launch_form<T, kCount32>(a, grid, (size_t)smem, st);
 }
 
 }  // namespace
@@ -243,7 +425,7 @@ extern "C" int orpo_logits_adjust(void* logits, int64_t ld_logits, int logits_bf
                                   const uint32_t* masks, int64_t ld_masks, int64_t n_masks, const int32_t* mask_row,
                                   int32_t* status, void* stream) {
   if (batch < 0 || batch > (1ll << 20) || beams < 1 || beams > (1 << 20) || batch * beams > (1ll << 20) || V < 1 ||
-      V > kMaxRows || ld_logits < V || capacity < 0 || capacity >= (1ll << 28) || n_bias < 0 || n_bias > ORPO_MAX_BIAS)
+      V > kMaxRows || batch * beams * V >= (1ll << 44) || ld_logits < V || capacity < 0 || capacity >= (1ll << 28) || n_bias < 0 || n_bias > ORPO_MAX_BIAS)
     return ORPO_ERR_SHAPE;
   if (!std::isfinite(repetition) || repetition <= 0.f || !std::isfinite(presence) || !std::isfinite(frequency) ||
       no_repeat < 0 || no_repeat > ORPO_MAX_NGRAM)
@@ -265,7 +447,7 @@ extern "C" int orpo_logits_adjust(void* logits, int64_t ld_logits, int logits_bf
   if (int e = device_check(&sms)) return e;
   const AdjustArgs a{logits, ld_logits, batch * beams, V, beams, reads ? history : nullptr, ld_history, (int)capacity,
                      length, prompt, repetition, presence, frequency, no_repeat, bias_token, bias_value, ld_bias, (int)n_bias,
-                     masks, ld_masks, n_masks, mask_row, status, 0, 0};
+                     masks, ld_masks, n_masks, mask_row, status, 0, 0, 0, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = logits_bf16 ? launch<uint16_t>(a, st) : launch<float>(a, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;

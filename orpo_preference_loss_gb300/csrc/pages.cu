@@ -363,38 +363,69 @@ struct Items {
   uint32_t j[kPer];
   bool asks[kPer];
 };
-// The items of a unit: which rows and columns, and the pages that they have.
-__device__ __forceinline__ void load_items(const ReserveArgs& a, int32_t unit, Items& it) {
-  const int lane = threadIdx.x & 31;
-  if (a.width >= kUnit) {  // of one row
-    const uint32_t i = (uint32_t)unit * kUnit, row = i / (uint32_t)a.width, j = i - row * (uint32_t)a.width, b = row / (uint32_t)a.t.beams;
-    const bool on = i < (uint32_t)a.items && !(a.left_alone && a.left_alone[b]);
-    const Wanted w = on ? wanted_columns(a.t, b) : Wanted{0, 0, 0};
+
+// The units of a warp, one after the other: next() gives their items and the pages that those have.  What the rows of up to
+// 32 units ask for is looked up at once, a unit per lane, where a unit is of one row.
+struct Units {
+  const ReserveArgs& a;
+  int32_t unit, end;
+  int32_t row;  // of this lane's unit
+  uint32_t j;
+  Wanted w;
+  int at = 32;
+  __device__ Units(const ReserveArgs& args, int32_t begin, int32_t end_)
+      : a(args), unit(begin + (int32_t)(threadIdx.x >> 5) - kWarps), end(end_), row(0), j(0), w{0, 0, 0} {}
+
+  __device__ __forceinline__ Wanted of_row(uint32_t r) const {
+    const uint32_t b = r / (uint32_t)a.t.beams;
+    return (int64_t)r < a.t.batch * a.t.beams && !(a.left_alone && a.left_alone[b]) ? wanted_columns(a.t, b) : Wanted{0, 0, 0};
+  }
+  // false: there is no other unit.  any: whether the unit's items ask for anything; else `it` is not filled.
+  __device__ __forceinline__ bool next(Items& it, bool& any) {
+    unit += kWarps;
+    if (unit >= end) return false;
+    const int lane = threadIdx.x & 31;
+    if (a.width >= kUnit) {
+      if (at == 32) {
+        const int64_t mine = (int64_t)unit + lane * kWarps;
+        const uint32_t i = mine < end ? (uint32_t)mine * kUnit : 0;
+        row = (int32_t)(i / (uint32_t)a.width);
+        j = i - (uint32_t)row * (uint32_t)a.width;
+        w = mine < end ? of_row((uint32_t)row) : Wanted{0, 0, 0};
+        at = 0;
+      }
+      const int32_t r = __shfl_sync(~0u, row, at);
+      const uint32_t j0 = __shfl_sync(~0u, j, at);
+      const Wanted x{__shfl_sync(~0u, w.first, at), __shfl_sync(~0u, w.n, at), __shfl_sync(~0u, w.fill, at)};
+      ++at;
+      any = j0 < x.n;
+      if (!any) return true;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        it.row[u] = r;
+        it.j[u] = j0 + u * 32 + lane;
+        it.w[u] = x;
+        it.asks[u] = it.j[u] < x.n;
+      }
+    } else {
+      any = true;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const uint32_t i = (uint32_t)unit * kUnit + u * 32 + lane, r = i / (uint32_t)a.width;
+        it.row[u] = (int32_t)r;
+        it.j[u] = i - r * (uint32_t)a.width;
+        it.w[u] = of_row(r);
+        it.asks[u] = it.j[u] < it.w[u].n;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
-      it.row[u] = (int32_t)row;
-      it.j[u] = j + u * 32 + lane;
-      it.w[u] = w;
-      it.asks[u] = it.j[u] < w.n;
+      const int64_t c = (int64_t)it.w[u].first + it.j[u];
+      it.old[u] = it.asks[u] && in_bounds(a.t.status, c, a.t.columns) ? __ldcg(a.t.table + it.row[u] * a.t.ld + c) : -1;
     }
-  } else {
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const uint32_t i = (uint32_t)unit * kUnit + u * 32 + lane;
-      const uint32_t row = i / (uint32_t)a.width, b = row / (uint32_t)a.t.beams;
-      const bool on = i < (uint32_t)a.items && !(a.left_alone && a.left_alone[b]);
-      it.row[u] = (int32_t)row;
-      it.j[u] = i - row * (uint32_t)a.width;
-      it.w[u] = on ? wanted_columns(a.t, b) : Wanted{0, 0, 0};
-      it.asks[u] = it.j[u] < it.w[u].n;
-    }
+    return true;
   }
-#pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const int64_t c = it.w[u].first + it.j[u];
-    it.old[u] = it.asks[u] && in_bounds(a.t.status, c, a.t.columns) ? __ldcg(a.t.table + it.row[u] * a.t.ld + c) : -1;
-  }
-}
+};
 
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
   __shared__ uint32_t part[kWarps];
@@ -402,7 +433,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
   const TableArgs& t = a.t;
   grid_trigger();
   grid_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ctas = gridDim.x, cta = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, ctas = gridDim.x, cta = blockIdx.x;
   if (!a.left_alone)
     for (int64_t b = (int64_t)cta * kPlanThreads + tid; b < t.batch; b += (int64_t)ctas * kPlanThreads) {
       int64_t begin, end;
@@ -421,10 +452,11 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
 
   // ---- what each item asks for.  Pages that others hold too are counted below
   int shared = 0;
-  for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
-    load_items(a, unit, it);
+  bool asked;
+  for (Units list(a, u_begin, u_end); list.next(it, asked);) {
+    const int32_t unit = list.unit;
     uint32_t need = 0;
-    if (__any_sync(~0u, it.asks[0] | it.asks[1] | it.asks[2] | it.asks[3])) {
+    if (asked) {
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const bool wrong = it.old[u] < -1 || it.old[u] >= t.pages;
@@ -448,19 +480,20 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
   // ---- of the items that hold a page together the last keeps it, where nothing else holds it
   if (any) {
     if (shared)
-      for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
-        load_items(a, unit, it);
+      for (Units list(a, u_begin, u_end); list.next(it, asked);) {
+        if (!asked) continue;
 #pragma unroll
         for (int u = 0; u < kPer; ++u)
           if (it.old[u] >= 0 && it.old[u] < t.pages && __ldcg(t.refs + it.old[u]) > 1) {
             atomicAdd(a.count + it.old[u], 1);
-            atomicMax(a.last + it.old[u], unit * kUnit + u * 32 + lane);
+            atomicMax(a.last + it.old[u], list.unit * kUnit + u * 32 + lane);
           }
       }
     plan_sync(ctas);
     if (shared)
-      for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
-        load_items(a, unit, it);
+      for (Units list(a, u_begin, u_end); list.next(it, asked);) {
+        if (!asked) continue;
+        const int32_t unit = list.unit;
         uint32_t moves = 0, need = 0;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
@@ -514,12 +547,12 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
     }
   plan_sync(ctas);  // the last look at another CTA's totals is behind
   if (full) return;
-  for (int32_t unit = u_begin + warp; unit < u_end; unit += kWarps) {
-    uint32_t bits[kPer], any_bits = 0;
+  for (Units list(a, u_begin, u_end); list.next(it, asked);) {
+    if (!asked) continue;
+    const int32_t unit = list.unit;
+    uint32_t bits[kPer];
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) any_bits |= bits[u] = a.needs[unit * kPer + u];
-    if (any_bits == 0) continue;
-    load_items(a, unit, it);
+    for (int u = 0; u < kPer; ++u) bits[u] = a.needs[unit * kPer + u];
     uint32_t at = at_item + a.before[2 * unit], to = at_move + a.before[2 * unit + 1];
     int32_t page[kPer];
 #pragma unroll
@@ -555,16 +588,18 @@ struct CopyArgs {
   int32_t max_moves;
   const int32_t* n_moves;
   int32_t* status;
-  int64_t stretches;  // of one (slab, page, row)
+  int64_t stretches;  // of one (slab, page), at most
+  int64_t stretch;    // pieces of one, a multiple of 32
 };
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;  // pieces of a lane in flight
 
-// A warp takes a stretch of kCopyUnroll * 32 pieces of one (move, slab, row).
+// A warp takes a stretch of at most kCopyUnroll * 32 pieces of one (move, slab): of the page's bytes there, all rows one after
+// the other, those whose positions move.
 template <class Piece>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
-  constexpr int kStretch = kCopyUnroll * 32;
+  constexpr int kSize = (int)sizeof(Piece);
   grid_trigger();
   grid_wait();
   const int32_t n = *a.n_moves;
@@ -574,34 +609,50 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(CopyArgs a) {
     if (warp == 0 && lane == 0) atomicOr(a.status, ORPO_STATUS_PAGE);
     return;
   }
-  const int64_t run = (int64_t)a.page * a.unit, stretches = a.stretches, per_move = a.outer * a.rows * stretches;
-  const int64_t all = a.outer * a.pages * a.page_bytes;
+  const uint32_t row_pieces = (uint32_t)((int64_t)a.page * a.unit / kSize);
+  const int64_t pieces = a.rows * row_pieces, per_move = a.outer * a.stretches, all = a.outer * a.pages * a.page_bytes;
   for (int64_t w = warp; w < n * per_move; w += warps) {
-    const int64_t m = w / per_move, left = w - m * per_move, run_at = left / stretches, s = left - run_at * stretches;
-    const int64_t o = run_at / a.rows, r = run_at - o * a.rows;
+    const int64_t m = w / per_move, left = w - m * per_move, o = left / a.stretches, s = left - o * a.stretches;
     const int32_t from = a.moves[3 * m], to = a.moves[3 * m + 1], positions = a.moves[3 * m + 2];
     if (from < 0 || from >= a.pages || to < 0 || to >= a.pages || from == to || positions < 0 || positions > a.page) {
       if (left == 0 && lane == 0) atomicOr(a.status, ORPO_STATUS_PAGE);
       continue;
     }
-    const int64_t bytes = (int64_t)positions * a.unit, pieces = bytes / (int64_t)sizeof(Piece);
-    const int64_t src = (o * a.pages + from) * a.page_bytes + r * run, dst = (o * a.pages + to) * a.page_bytes + r * run;
+    const int64_t first = s * a.stretch, begin = first + lane, end = min(pieces, first + a.stretch);
+    uint32_t moves = 0, cut = 0;  // which of the lane's pieces move, and which in part
+    const uint32_t bytes = (uint32_t)positions * (uint32_t)a.unit;  // of a row
+    if (positions == a.page) {
+#pragma unroll
+      for (int u = 0; u < kCopyUnroll; ++u) moves |= (uint32_t)(begin + u * 32 < end) << u;
+    } else {
+      const uint32_t in_row = (uint32_t)(first - first / row_pieces * row_pieces) + lane;  // counted from the row that `first` is in
+#pragma unroll
+      for (int u = 0; u < kCopyUnroll; ++u) {
+        uint32_t i = in_row + u * 32;
+        if (row_pieces >= kCopyUnroll * 32) i -= i >= row_pieces ? row_pieces : 0;  // at most one row on
+        else i %= row_pieces;
+        const int64_t byte = (int64_t)i * kSize;
+        const bool mine = begin + u * 32 < end && byte < bytes, part = byte + kSize > bytes;
+        moves |= (uint32_t)(mine && !part) << u;
+        cut |= (uint32_t)(mine && part) << u;
+      }
+    }
+    const int64_t src_at = (o * a.pages + from) * a.page_bytes + begin * kSize, dst_at = (o * a.pages + to) * a.page_bytes + begin * kSize;
+    const Piece* const src = reinterpret_cast<const Piece*>(a.pool + src_at);
+    Piece* const dst = reinterpret_cast<Piece*>(a.pool + dst_at);
     Piece v[kCopyUnroll];
 #pragma unroll
-    for (int u = 0; u < kCopyUnroll; ++u) {
-      const int64_t i = s * kStretch + u * 32 + lane;
-      if (i < pieces && in_bounds(a.status, src + (i + 1) * (int64_t)sizeof(Piece) - 1, all))
-        v[u] = reinterpret_cast<const Piece*>(a.pool + src)[i];
-    }
+    for (int u = 0; u < kCopyUnroll; ++u)
+      if (moves >> u & 1u && in_bounds(a.status, src_at + (u * 32 + 1) * kSize - 1, all)) v[u] = src[u * 32];
 #pragma unroll
-    for (int u = 0; u < kCopyUnroll; ++u) {
-      const int64_t i = s * kStretch + u * 32 + lane;
-      if (i < pieces && in_bounds(a.status, dst + (i + 1) * (int64_t)sizeof(Piece) - 1, all))
-        reinterpret_cast<Piece*>(a.pool + dst)[i] = v[u];
+    for (int u = 0; u < kCopyUnroll; ++u)
+      if (moves >> u & 1u && in_bounds(a.status, dst_at + (u * 32 + 1) * kSize - 1, all)) dst[u * 32] = v[u];
+    for (; cut != 0; cut &= cut - 1) {  // positions that end inside a piece
+      const int u = __ffs(cut) - 1;
+      for (uint32_t i = 0; i < bytes % kSize; ++i)
+        if (in_bounds(a.status, src_at + u * 32 * kSize + i, all) && in_bounds(a.status, dst_at + u * 32 * kSize + i, all))
+          a.pool[dst_at + u * 32 * kSize + i] = a.pool[src_at + u * 32 * kSize + i];
     }
-    // what is left of a run whose positions do not fill whole pieces
-    const int64_t i = pieces * (int64_t)sizeof(Piece) + lane;
-    if (s == 0 && i < bytes && in_bounds(a.status, dst + i, all) && in_bounds(a.status, src + i, all)) a.pool[dst + i] = a.pool[src + i];
   }
 }
 
@@ -788,8 +839,10 @@ bool misaligned(std::initializer_list<const void*> p) {
 
 template <class Piece>
 cudaError_t launch_copy(CopyArgs a, int sms, cudaStream_t st) {
-  a.stretches = cdiv((int64_t)a.page * a.unit, (int64_t)sizeof(Piece) * kCopyUnroll * 32);
-  const int64_t warps = (int64_t)a.max_moves * a.outer * a.rows * a.stretches;  // at most
+  const int64_t pieces = cdiv(a.page_bytes, (int64_t)sizeof(Piece));
+  a.stretches = cdiv(pieces, kCopyUnroll * 32);
+  a.stretch = cdiv(cdiv(pieces, a.stretches), 32) * 32;
+  const int64_t warps = (int64_t)a.max_moves * a.outer * a.stretches;  // at most
   const int grid = (int)std::min<int64_t>((int64_t)sms * 8, cdiv(warps, kCopyThreads / 32));
   prof_begin(K_PAGECOPY, st);
   const cudaError_t e = launch_dependent(copy_kernel<Piece>, grid, kCopyThreads, 0, st, a);
@@ -883,7 +936,7 @@ int orpo_pages_copy(void* pool, int64_t outer, int64_t pages, int64_t rows, int6
   int sms = 0;
   if (int e = device_check(&sms)) return e;
   const CopyArgs a{static_cast<uint8_t*>(pool), outer, rows, rows * run, (int32_t)pages, (int32_t)page, (int32_t)unit_bytes, moves,
-                   (int32_t)max_moves, n_moves, status, 0};
+                   (int32_t)max_moves, n_moves, status, 0, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const uint64_t at = (uint64_t)reinterpret_cast<uintptr_t>(pool) | (uint64_t)run;
   const cudaError_t e = at % 16 == 0  ? launch_copy<uint4>(a, sms, st)

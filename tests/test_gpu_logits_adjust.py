@@ -245,6 +245,29 @@ def test_long_histories(cap):
     check(c, 1.2, 0.1, 0.01, 3)
 
 
+@pytest.mark.parametrize("frequency", [0.0, 0.25])
+@pytest.mark.parametrize("V,cap", [(409600, 500), (409601, 500), (600000, 9000), (1638400, 300), (1638401, 300), (3000000, 200)])
+def test_large_vocabularies(V, cap, frequency):
+    """On both sides of what fits a CTA's maps of the vocabulary: one, two, three or four of them."""
+    for n_bias, ngram in ((0, 0), (20, 0), (0, 2), (20, 2)):
+        c = case(1, 2, V, cap, seed=V + n_bias, n_bias=n_bias, spread=0.001 if ngram else 1.0)
+        check(c, 1.2, 0.5, frequency, ngram)
+    c = case(1, 2, V, cap, seed=V, spread=1e-5)
+    check(c, no_repeat=2)
+
+
+@pytest.mark.parametrize("cap", [8191, 8192])
+def test_one_token_all_along(cap):
+    """The largest count that 16 bits hold beside their flags, next to counts and flags of its neighbours."""
+    for token in (0, 1, 32767, 32768):
+        h = np.full((2, cap), token, dtype=np.int32)
+        h[1, ::2] = token ^ 1
+        c = case(2, 1, 40000, cap, seed=token, n_bias=2)
+        c["history"], c["length"], c["prompt"] = h, np.full(2, cap, dtype=np.int32), np.array([0, 5], dtype=np.int32)
+        c["bias_token"][:] = [[token ^ 1, 9], [token, token]]
+        check(c, 1.5, 0.1, 0.01)
+
+
 def test_rows_past_2_31_elements():
     """The last rows of 4.4 GB of bf16 logits lie past 2^31 elements."""
     V, rows = 262144, 8300
