@@ -3,9 +3,10 @@
 The body is a stand-in that needs no checkpoint: hidden state t is a decayed sum of the embeddings of the
 tokens so far, kept per beam, so it has to follow its beam's parent like a key/value cache does.  The
 beam score of a finished response is then the sum of the per-token log-probabilities that
-orpo_head_fwd_q gives for it: both read the same quantised weights.
+orpo_head_fwd_q gives for it: both read the same quantised weights (penalties change what is scored, so the two differ
+where there are any).  --paged keeps the hidden rows in pages that the beams share.
 
-    python examples/beam_decode.py [--steps 24] [--beams 4]
+    python examples/beam_decode.py [--steps 24] [--beams 4] [--paged] [--repetition 1.2] [--no-repeat 3]
 """
 
 import argparse
@@ -25,7 +26,10 @@ def hidden(state):
     return (state / state.norm(dim=-1, keepdim=True).clamp_min(1e-6) * state.shape[-1] ** 0.5).bfloat16()
 
 
-def generate(batch, beams, steps, d=256, V=4096, bits=4, group=64, softcap=30.0, seed=0):
+PAGE = 4  # positions per page
+
+
+def generate(batch, beams, steps, d=256, V=4096, bits=4, group=64, softcap=30.0, seed=0, paged=False, repetition=1.0, no_repeat=0):
     """Returns (head, quantised weights, responses [batch, beams, steps], their hidden rows)."""
     dev = torch.device("cuda")
     w = workloads.make("tiny", seed=seed, d=d, V=V)
@@ -36,21 +40,36 @@ def generate(batch, beams, steps, d=256, V=4096, bits=4, group=64, softcap=30.0,
     embedding = torch.randn((V, d), generator=g, device=dev)
     prompt = torch.randint(0, V, (batch,), generator=g, device=dev)
 
-    dec = orpo.BeamDecoder(batch, beams, V, d, bits, group, softcap, eos=1, device=dev)
-    # per-beam states: the running sum, and what was generated (tokens, hidden rows) up to length[b]
+    dec = orpo.BeamDecoder(batch, beams, V, d, bits, group, softcap, eos=1, device=dev, repetition=repetition, no_repeat=no_repeat)
+    # per-beam states: the running sum, and what was generated (tokens behind the prompt's, hidden rows) up to length[b]
     running = embedding[prompt].repeat_interleave(beams, 0).view(1, batch * beams, 1, 1, d)
-    tokens = torch.full((1, batch * beams, 1, steps, 1), 1, dtype=torch.int32, device=dev)
-    rows = torch.zeros((1, batch * beams, 1, steps, d), dtype=torch.bfloat16, device=dev)
+    history = torch.full((batch * beams, steps + 1), 1, dtype=torch.int32, device=dev)
+    history[:, 0] = prompt.repeat_interleave(beams)
     length = torch.zeros(batch, dtype=torch.int32, device=dev)
+    states, pages, pools = (), None, ()
+    if paged:
+        columns = steps // PAGE + 1
+        pages = orpo.PagedStates(batch, beams, columns, batch * beams * columns, PAGE, status=dec.status, device=dev)
+        pool = torch.zeros((1, pages.pages, 1, PAGE, d), dtype=torch.bfloat16, device=dev)
+        pools = (pool,)
+        pages.advance(length)  # room for the first position
+    else:
+        rows = torch.zeros((1, batch * beams, 1, steps, d), dtype=torch.bfloat16, device=dev)
+        states = (rows,)
     for t in range(steps):
         h = hidden(running.view(-1, d))
-        rows[0, :, 0, t] = h
+        if paged:
+            pool[0, pages.table[:, t // PAGE].long(), 0, t % PAGE] = h
+        else:
+            rows[0, :, 0, t] = h
         length.fill_(t + 1)
-        parent, token = dec.step(h, *weights, states=(tokens, rows), length=length)
+        parent, token = dec.step(h, *weights, states=states, length=length, history=history, pages=pages, pools=pools)
         orpo.orpo_beam_reorder(running, parent, None, dec.status)
-        tokens[0, :, 0, t, 0] = token.view(-1)
         running.mul_(DECAY).add_(embedding[token.view(-1).long()].view_as(running))
-    return dec, weights, tokens.view(batch, beams, steps), rows.view(batch * beams * steps, d)
+    if paged:
+        at = torch.arange(steps, device=dev)
+        rows = pool[0, pages.table[:, at // PAGE].long(), 0, at % PAGE]
+    return dec, weights, history[:, 1:].reshape(batch, beams, steps), rows.reshape(batch * beams * steps, d)
 
 
 def rescore(dec, weights, tokens, rows):
@@ -71,8 +90,11 @@ def main():
     ap.add_argument("--batch", type=int, default=2)
     ap.add_argument("--beams", type=int, default=4)
     ap.add_argument("--steps", type=int, default=24)
+    ap.add_argument("--paged", action="store_true")
+    ap.add_argument("--repetition", type=float, default=1.0)
+    ap.add_argument("--no-repeat", type=int, default=0)
     a = ap.parse_args()
-    dec, weights, tokens, rows = generate(a.batch, a.beams, a.steps)
+    dec, weights, tokens, rows = generate(a.batch, a.beams, a.steps, paged=a.paged, repetition=a.repetition, no_repeat=a.no_repeat)
     again = rescore(dec, weights, tokens, rows)
     status = int(dec.status.item())
     if status:

@@ -143,7 +143,7 @@ int orpo_beam_reorder(void* state, const int32_t* parent, int64_t ld_parent, con
  * 0 <= capacity < 2^28, 0 <= n_bias <= ORPO_MAX_BIAS, 0 <= no_repeat <= ORPO_MAX_NGRAM, 1 <= n_masks < 2^31 where masks are given; repetition > 0; all
  * penalties finite.  4-byte alignment (2 for bf16 logits).
  */
-#define ORPO_MAX_BIAS 65536
+#define ORPO_MAX_BIAS 4096
 #define ORPO_MAX_NGRAM 32
 int orpo_logits_adjust(void* logits, int64_t ld_logits, int logits_bf16, int64_t batch, int beams, int64_t V,
                        const int32_t* history, int64_t ld_history, int64_t capacity, const int32_t* length,

@@ -34,7 +34,7 @@ def test_adjust_host_checks(lib):
     assert call(rep=1.0, h=None, length=None) == OK  # nothing to do
     for bad in (dict(batch=-1), dict(batch=(1 << 20) + 1), dict(beams=0), dict(beams=(1 << 20) + 1), dict(batch=1 << 18, beams=8), dict(V=0),
                 dict(V=MAX_ROWS + 1, ld=MAX_ROWS + 1), dict(ld=999), dict(cap=-1), dict(cap=1 << 28, ld_h=1 << 28), dict(ld_h=63),
-                {**bias, "nb": -1}, {**bias, "nb": 65537}, {**bias, "ld_b": 4}, {**mask, "nm": 0}, {**mask, "nm": 1 << 31},
+                {**bias, "nb": -1}, {**bias, "nb": 4097}, {**bias, "ld_b": 4}, {**mask, "nm": 0}, {**mask, "nm": 1 << 31},
                 {**mask, "ld_m": 31}):
         assert call(**bad) == ERR_SHAPE, bad
     for bad in (dict(rep=0.0), dict(rep=-1.0), dict(rep=math.nan), dict(rep=math.inf), dict(pres=math.nan), dict(freq=-math.inf),
