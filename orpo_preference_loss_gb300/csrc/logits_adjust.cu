@@ -51,6 +51,7 @@ struct AdjustArgs {
   int32_t* status;
   int parts;       // history CTAs per row
   int list_cap;    // listed tokens per range at most
+  int list_words;  // 32-bit words of that list
   int bit_words;   // of a map of the vocabulary
   int clear;       // 16-byte pieces of shared memory to clear
 };
@@ -118,8 +119,7 @@ struct Row {
   int64_t at, all;        // where it starts, and all logits (bounds-checked build)
 };
 
-// N tokens (-1: none) with what is known of them and their biases, all their logits on the way at once; masked ones are left
-// to the mask CTAs.
+// N tokens (-1: none) that no mask bans, with what is known of them and their bias, all their logits on the way at once.
 template <class T, int N>
 __device__ __forceinline__ void adjust(const AdjustArgs& a, const Row<T>& row, const int32_t (&token)[N], const uint32_t (&w)[N],
                                        float bias) {
@@ -129,7 +129,6 @@ __device__ __forceinline__ void adjust(const AdjustArgs& a, const Row<T>& row, c
   for (int i = 0; i < N; ++i) {
     on[i] = token[i] >= 0 && in_bounds(a.status, row.at + token[i], row.all);
     y[i] = on[i] ? Logit<T>::load(row.x + token[i]) : 0.f;
-    if (row.words && on[i]) on[i] = row.words[token[i] >> 5] >> (token[i] & 31) & 1u;
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -148,6 +147,7 @@ __device__ __forceinline__ void adjust_biased(const AdjustArgs& a, const Row<T>&
   for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
     const int32_t v = token[j];
     if (v < 0 || (uint32_t)(v - (int32_t)v0) >= (uint32_t)size) continue;
+    if (row.words && !(row.words[v >> 5] >> (v & 31) & 1u)) continue;  // left to the masks
     float sum = value[j];
     if (twice) {
       bool first = true;
@@ -227,6 +227,9 @@ __device__ __forceinline__ void by_bits(const AdjustArgs& a, const Row<T>& row, 
                                         bool penalties) {
   const int stride = a.bit_words;
   const bool biased = a.n_bias > 0;
+  // tokens that the mask bans count as met from the start, so that nobody adjusts them
+  if (row.words)
+    for (int i = threadIdx.x; i < (int)((a.V + 31) / 32); i += kThreads) smem[i] = ~row.words[i];
   const Bits bits{smem, smem + stride, smem + (a.ngram > 0 ? 2 : 1) * stride, smem + (a.ngram > 0 ? 3 : 2) * stride};
   const int32_t V = (int32_t)a.V;
   for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
@@ -246,7 +249,7 @@ __device__ __forceinline__ void by_bits(const AdjustArgs& a, const Row<T>& row, 
 #pragma unroll 1
     for (int part = 0; part < 2; ++part) {  // what was generated, then the prompt
       if (part == 1 && prompt == 0) break;
-      if (part == 1 || biased || n_tail >= 0) __syncthreads();
+      if (part == 1 || biased || n_tail >= 0 || row.words) __syncthreads();
       each_tokens(h, part == 0 ? prompt : 0, part == 0 ? len : prompt, [&](const int (&)[kUnroll], const int32_t (&v)[kUnroll]) {
         int32_t token[kUnroll];
         uint32_t w[kUnroll];
@@ -300,12 +303,18 @@ __device__ __forceinline__ void by_counts(const AdjustArgs& a, const Row<T>& row
   const Counters<kForm> counters{smem};
   uint16_t* const list = reinterpret_cast<uint16_t*>(smem + kTableBytes / 4);  // tokens met, each once
   const uint32_t size = (uint32_t)min((int64_t)kRange, a.V - v0);
+  uint32_t* const allowed = smem + kTableBytes / 4 + a.list_words;  // the mask's part
+  if (row.words) {
+    for (int i = threadIdx.x; i < (int)((size + 31) / 32); i += kThreads) allowed[i] = row.words[v0 / 32 + i];
+    __syncthreads();
+  }
   each_tokens(h, 0, len, [&](const int (&t)[kUnroll], const int32_t (&v)[kUnroll]) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const bool banned = ends_again(h, t[u], v[u], len, tail, n_tail);
       const uint32_t at = (uint32_t)(v[u] - (int32_t)v0);
       if (v[u] < 0 || at >= size || !(penalties || banned) || !in_bounds(a.status, at, kRange)) continue;
+      if (row.words && !(allowed[at / 32] >> (at % 32) & 1u)) continue;  // left to the masks
       const uint32_t old = t[u] >= prompt ? counters.add(at) : counters.flag(at, kPrompt, kFewPrompt);
       if (old == 0) {
         const int j = atomicAdd(listed, 1);
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(AdjustArgs a) {
 template <class T, int kForm>
 cudaError_t launch_form(const AdjustArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
   static std::atomic<int> done[64];
-  cudaError_t e = opt_in_smem(adjust_kernel<T, kForm>, kForm == kBits ? kMostBits : kTableBytes + range_of(kForm) * 2, done);
+  cudaError_t e = opt_in_smem(adjust_kernel<T, kForm>, kForm == kBits ? kMostBits : kTableBytes + range_of(kForm) * 2 + range_of(kForm) / 8, done);
   if (e != cudaSuccess) return e;
   prof_begin(K_ADJUST, st);
   e = launch_dependent(adjust_kernel<T, kForm>, grid, kThreads, smem, st, a);
@@ -405,7 +414,8 @@ cudaError_t launch(AdjustArgs a, cudaStream_t st) {
   const int form = a.frequency == 0.f && bits <= kMostBits ? kBits : a.capacity <= kFew ? kCount16 : kCount32;
   a.parts = !history ? 0 : form == kBits ? 1 : (int)cdiv(a.V, range_of(form));
   a.list_cap = std::min(range_of(form), a.history ? a.capacity : 0);
-  const int64_t smem = !history ? 0 : form == kBits ? bits : kTableBytes + cdiv(a.list_cap * 2, 16) * 16;
+  a.list_words = (int)cdiv(a.list_cap, 8) * 4;
+  const int64_t smem = !history ? 0 : form == kBits ? bits : kTableBytes + a.list_words * 4 + (a.masks ? range_of(form) / 8 : 0);
   a.clear = (int)((form == kBits ? bits : kTableBytes) / 16);
   const dim3 grid((unsigned)(a.rows * (a.parts + (a.masks ? cdiv(a.V, kMaskTokens) : 0))));
   return form == kBits      ? launch_form<T, kBits>(a, grid, (size_t)smem, st)
@@ -447,7 +457,7 @@ extern "C" int orpo_logits_adjust(void* logits, int64_t ld_logits, int logits_bf
   if (int e = device_check(&sms)) return e;
   const AdjustArgs a{logits, ld_logits, batch * beams, V, beams, reads ? history : nullptr, ld_history, (int)capacity,
                      length, prompt, repetition, presence, frequency, no_repeat, bias_token, bias_value, ld_bias, (int)n_bias,
-                     masks, ld_masks, n_masks, mask_row, status, 0, 0, 0, 0};
+                     masks, ld_masks, n_masks, mask_row, status, 0, 0, 0, 0, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = logits_bf16 ? launch<uint16_t>(a, st) : launch<float>(a, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
