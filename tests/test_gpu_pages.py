@@ -68,9 +68,10 @@ def beams_table(rng, batch, beams, columns, pages, page, lengths, shared=0.5):
 
 
 @pytest.mark.parametrize("batch,beams,page,longest", [(1, 1, 1, 9), (1, 4, 16, 100), (3, 4, 5, 60), (2, 8, 16, 2500), (4, 9, 7, 80), (1, 17, 3, 40),
-                                                      (1, 64, 4, 50), (70, 16, 8, 30)])
-def test_decode_steps_against_the_oracle(batch, beams, page, longest):
-    """Several steps in a row, with new parents each and one more position each."""
+                                                      (1, 64, 4, 50), (70, 16, 8, 30), (1, 4, 1, 5000), (2, 6, 1, 2200)])
+@pytest.mark.parametrize("more_pages", [0, 20000])
+def test_decode_steps_against_the_oracle(batch, beams, page, longest, more_pages):
+    """Several steps in a row, with new parents each and one more position each, in small and in large pools."""
     rng = np.random.default_rng(batch + beams + page)
     steps = 4
     lengths = rng.integers(0, longest, batch)
@@ -78,7 +79,7 @@ def test_decode_steps_against_the_oracle(batch, beams, page, longest):
     if batch > 1:
         lengths[1] = page * 2  # a border
     columns = -(-(longest + steps) // page)
-    pages = batch * beams * (columns + 1) + 7
+    pages = batch * beams * (columns + 1) + 7 + more_pages
     table = beams_table(rng, batch, beams, columns, pages, page, lengths)
     p = Pages(table, pages, page, pad=3)
     want = table, oracle.holders(table, pages)
@@ -144,6 +145,39 @@ def test_too_few_pages_change_nothing_but_the_fork():
     p.status.zero_()
     got = p.advance(None, [8])
     assert got[0].tolist() == [[0, 2, 3], [0, 1, 4]] and int(p.status.item()) == 0
+
+
+@pytest.mark.parametrize("rows,columns", [(3, 5461), (1200, 25), (1200, 4), (1000, 6)])
+def test_too_few_pages_of_a_large_pool(rows, columns):
+    """One page fewer than rows is free; it is enough for all but one."""
+    held = rows * columns
+    pages = held + rows - 1
+    table = np.full((rows, columns + 1), -1, dtype=np.int32)
+    table[:, :-1] = np.random.default_rng(rows).permutation(pages)[:held].reshape(rows, columns)
+    refs = oracle.holders(table, pages)
+    length = np.full(rows, 2 * columns)
+    p = Pages(table, pages, 2, refs=refs)
+    got = p.advance(None, length)
+    assert int(p.status.item()) == FULL and int(p.n.item()) == 0
+    assert np.array_equal(got[0], table) and np.array_equal(got[1], refs)
+    p.status.zero_()
+    more = np.ones(rows, dtype=np.int32)
+    more[1] = 0
+    want = oracle.pages_advance(table, refs, 2, None, length, more, 1)
+    same(p.advance(None, length, more), want[:3])
+    assert int(p.status.item()) == 0 and not want[3]
+
+
+@pytest.mark.parametrize("columns,pages", [(5000, 6000), (3, 20000), (5000, 20000)])
+def test_wrong_entries_beside_right_ones_in_every_form(columns, pages):
+    table = np.full((8, columns), -1, dtype=np.int32)
+    table[:, :2] = np.arange(16).reshape(8, 2)
+    p = Pages(table, pages, 4)
+    got = p.advance([[1, 0], [1, 2], [0, 0], [1, 1]], [8, 8, 4 * columns, 6])
+    want = oracle.pages_advance(table, oracle.holders(table, pages), 4, np.array([[1, 0], [0, 1], [0, 1], [1, 1]]), [8, 7, 7, 6], None, 1)
+    assert int(p.status.item()) == PARENT
+    same(got, want[:3])
+    assert got[2] == [(15, 16, 2)]
 
 
 def test_wrong_entries_are_left_as_they_are():
