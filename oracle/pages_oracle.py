@@ -72,10 +72,10 @@ def logits_adjust(logits, beams, history=None, length=None, prompt=None, repetit
             if 0 <= t < V:
                 x[r, t], bound[r, t] = -math.inf, 0.0
         if masks is not None and mask_row[r] >= 0:
-            words = [int(w) & 0xffffffff for w in masks[mask_row[r]]]
-            for v in range(V):
-                if not words[v // 32] >> (v % 32) & 1:
-                    x[r, v], bound[r, v] = -math.inf, 0.0
+            words = np.array([int(w) & 0xffffffff for w in masks[mask_row[r]]], dtype=np.int64)
+            v = np.arange(V)
+            masked = (words[v // 32] >> (v % 32)) % 2 == 0
+            x[r, masked], bound[r, masked] = -math.inf, 0.0
     return x, bound
 
 

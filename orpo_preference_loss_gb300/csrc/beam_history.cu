@@ -104,6 +104,7 @@ extern "C" int orpo_beam_history(int32_t* history, int64_t ld_history, int64_t c
   const cudaError_t e = beams <= 4    ? (wide ? launch<int4, 4>(a, st) : launch<int, 4>(a, st))
                         : beams <= 8  ? (wide ? launch<int4, 8>(a, st) : launch<int, 8>(a, st))
                         : beams <= 16 ? launch<int, 16>(a, st)
+                        : beams <= 32 ? launch<int, 32>(a, st)
                                       : launch<int, 64>(a, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;
 }

@@ -218,33 +218,43 @@ __device__ __forceinline__ Wanted wanted_columns(const TableArgs& a, uint32_t b)
   return {first, last - first + 1, (uint32_t)begin - first * page};
 }
 
-// ---- a decode step's worth: up to kSmallItems items, and pages whose counts fit shared memory.  One CTA; the counts are
-// read once, with lengths and parents, and the table once: two ways to memory instead of ten.
-// KB: a fork of up to KB beams is done here too; 0: none.
+// ---- a decode step's worth: up to kSmallItems items, in one CTA.
+// KB: a fork of up to KB beams is done here too, for (entry, column) pairs of at most one per thread; the counts of holders are
+// then in shared memory, where what the fork changes can be looked up at once.  0: no fork here, and the counts stay
+// where they are.
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallItems = kSmallThreads;
-constexpr int kSmallPages = 16384;
-inline size_t small_smem(int64_t pages) { return (size_t)(cdiv(pages, 1024) * 1024) * 12; }
+constexpr int kForkHere = kSmallThreads;    // pairs
+constexpr int kForkPages = 32768;           // 128 KB of counts
+constexpr int kSlots = 2 * kSmallItems;     // of the table of pages that several items hold
+inline int32_t padded_pages(int64_t pages) { return (int32_t)(cdiv(pages, 32 * kWarps) * 32 * kWarps); }
 
 template <int KB>
 __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArgs a, int32_t padded) {
-  extern __shared__ __align__(16) int32_t refs[];  // [padded] counts, [padded] items of a shared page, [padded] the last of them
-  int32_t* const count = refs + padded;
-  int32_t* const last = count + padded;
-  __shared__ uint32_t part[32];
+  extern __shared__ __align__(16) int32_t refs[];  // KB > 0: [padded] counts of holders
+  __shared__ int32_t keys[kSlots], count[kSlots], last[kSlots];  // pages that several items hold: how many, and the last
+  __shared__ uint32_t part[kWarps];
   __shared__ int32_t fresh[kSmallItems];
   __shared__ uint8_t bad[kSmallItems];
   const TableArgs& t = a.t;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   grid_trigger();
   bad[tid] = 0;
+  for (int i = tid; i < kSlots; i += kSmallThreads) keys[i] = -1, count[i] = 0, last[i] = -1;
   __syncthreads();
   grid_wait();
   const int rows = (int)t.batch * t.beams;
   const uint32_t row = (uint32_t)tid / (uint32_t)a.width, j = (uint32_t)tid - row * (uint32_t)a.width;
   const uint32_t b = row / (uint32_t)t.beams;
   // ---- counts, lengths, parents
-  for (int p = tid; p < padded; p += kSmallThreads) refs[p] = p < t.pages ? t.refs[p] : 1;
+  PageRun run(0, KB > 0 ? padded : t.pages);
+  uint32_t used = 0;
+  if constexpr (KB > 0) {
+#pragma unroll 4
+    for (int p = tid; p < padded; p += kSmallThreads) refs[p] = p < t.pages ? t.refs[p] : 1;
+  } else {
+    used = run.count(t.refs, t.pages);
+  }
   if (tid < rows) {
     const int e = tid / t.beams;
     int64_t begin, end;
@@ -266,62 +276,74 @@ __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArg
   if constexpr (KB > 0)
     if (item && w.fill > 0 && j == 0) from = (int32_t)(b * t.beams) + t.parent[b * t.ld_parent + row - b * t.beams];
   __syncthreads();
-  // ---- the table: each item's page after the fork, and the first columns to fork
+  // ---- the table: each item's page after the fork, and the columns to fork
   const bool asks = item && j < w.n && !bad[b];
   int32_t* const entry = t.table + row * t.ld + w.first + j;
-  int32_t old = -1;
+  int32_t old = -1, held = 0;
   if (asks && in_bounds(t.status, from, rows) && in_bounds(t.status, w.first + j, t.columns)) old = t.table[from * t.ld + w.first + j];
   if constexpr (KB > 0) {
-    const uint32_t columns = (uint32_t)t.columns, pairs = (uint32_t)t.batch * columns;
+    const uint32_t columns = (uint32_t)t.columns, e = columns > 0 ? (uint32_t)tid / columns : 0, c = (uint32_t)tid - e * columns;
+    const bool on = e < (uint32_t)t.batch && columns > 0 && !bad[e] && (int64_t)c * t.page < t.length[e];
+    const int64_t b0 = (int64_t)e * t.beams * t.ld, all = t.batch * t.beams * t.ld;
+    int32_t* const column = t.table + b0 + c;
     int par[KB];
     int32_t was[KB], now[KB];
-    for (uint32_t i = tid; i < (pairs + kSmallThreads - 1) / kSmallThreads * kSmallThreads; i += kSmallThreads) {
-      const uint32_t e = i < pairs ? i / columns : 0, c = i - e * columns;
-      const bool on = i < pairs && !bad[e] && (int64_t)c * t.page < t.length[e];
-      const int64_t b0 = (int64_t)e * t.beams * t.ld, all = t.batch * t.beams * t.ld;
-      int32_t* const column = t.table + b0 + c;
 #pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        par[k] = on && k < t.beams ? t.parent[e * t.ld_parent + k] : k;
-        if (par[k] != k && in_bounds(t.status, b0 + c + k * t.ld, all)) {
-          was[k] = column[k * t.ld];
-          now[k] = column[par[k] * t.ld];
-        }
+    for (int k = 0; k < KB; ++k) {
+      par[k] = on && k < t.beams ? t.parent[e * t.ld_parent + k] : k;
+      if (par[k] != k && in_bounds(t.status, b0 + c + k * t.ld, all)) {
+        was[k] = column[k * t.ld];
+        now[k] = column[par[k] * t.ld];
       }
-      if (i == tid) __syncthreads();  // the items' pages are read
-#pragma unroll
-      for (int k = 0; k < KB; ++k)
-        if (par[k] != k && was[k] != now[k] && in_bounds(t.status, b0 + c + k * t.ld, all)) {
-          column[k * t.ld] = now[k];
-          if (is_page(t, now[k])) atomicAdd(t.refs + now[k], 1), atomicAdd(refs + now[k], 1);
-          if (is_page(t, was[k])) atomicSub(t.refs + was[k], 1), atomicSub(refs + was[k], 1);
-          if (now[k] < -1 || now[k] >= t.pages || was[k] < -1 || was[k] >= t.pages) atomicOr(t.status, ORPO_STATUS_PAGE);
-        }
     }
+    __syncthreads();  // all that the fork overwrites is read
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+      if (par[k] != k && was[k] != now[k] && in_bounds(t.status, b0 + c + k * t.ld, all)) {
+        column[k * t.ld] = now[k];
+        if (is_page(t, now[k])) atomicAdd(t.refs + now[k], 1), atomicAdd(refs + now[k], 1);
+        if (is_page(t, was[k])) atomicSub(t.refs + was[k], 1), atomicSub(refs + was[k], 1);
+        if (now[k] < -1 || now[k] >= t.pages || was[k] < -1 || was[k] >= t.pages) atomicOr(t.status, ORPO_STATUS_PAGE);
+      }
+    __syncthreads();
   }
-  __syncthreads();
   // ---- what the item asks for; of the items that hold a page together the last keeps it, where nothing else holds it
   int what = kNone;
   if (asks) {
-    if (old < -1 || old >= t.pages) atomicOr(t.status, ORPO_STATUS_PAGE);
-    else if (old < 0) what = kNeed;
-    else if (refs[old] > 1) what = kShared, count[old] = 0, last[old] = -1;
+    if (old < -1 || old >= t.pages) {
+      atomicOr(t.status, ORPO_STATUS_PAGE);
+    } else if (old < 0) {
+      what = kNeed;
+    } else {
+      held = KB > 0 ? refs[old] : __ldcg(t.refs + old);
+      if (held > 1) what = kShared;
+    }
   }
   if (__syncthreads_or(what == kShared)) {
-    if (what == kShared) atomicAdd(count + old, 1), atomicMax(last + old, tid);
+    uint32_t s = 0;
+    if (what == kShared) {
+      s = (uint32_t)old * 2654435769u / (0xffffffffu / kSlots + 1u);
+      for (;;) {  // twice as many slots as items: an empty one is always met
+        const int32_t key = atomicCAS(keys + s, -1, old);
+        if (key == -1 || key == old) break;
+        s = (s + 1) % kSlots;
+      }
+      atomicAdd(count + s, 1);
+      atomicMax(last + s, tid);
+    }
     __syncthreads();
-    if (what == kShared && count[old] == refs[old] && last[old] == tid) what = kNone;
+    if (what == kShared && count[s] == held && last[s] == tid) what = kNone;
   }
   const bool move = what == kShared && j == 0 && w.fill > 0;
   uint32_t total;
   const uint32_t at = scan((uint32_t)(what != kNone) | (uint32_t)move << 16, part, total);
   const uint32_t needed = total & 0xffff;
-  // ---- free pages, lowest first: a warp's share is a row of ballots
-  uint32_t free = 0;
-  const int share = padded / 32, p0 = warp * share;
-  for (int i = 0; i < share; i += 32) free += __popc(__ballot_sync(~0u, refs[p0 + i + lane] <= 0));
+  // ---- free pages, lowest first
+  if constexpr (KB > 0)
+    for (int i = 0; i < run.words; ++i) used += __popc(__ballot_sync(~0u, refs[run.begin + i * 32 + lane] > 0));
+  const int run_pages = min(max((KB > 0 ? padded : t.pages) - run.begin, 0), run.words * 32);
   uint32_t found;
-  uint32_t rank = scan(lane == 0 ? free : 0, part, found);
+  uint32_t rank = scan(lane == 0 ? (uint32_t)run_pages - used : 0, part, found);
   rank = __shfl_sync(~0u, rank, 0);
   if (found < needed) {
     if (tid == 0) {
@@ -330,10 +352,11 @@ __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArg
     }
     return;
   }
-  for (int i = 0; i < share && rank < needed; i += 32) {
-    const bool is_free = refs[p0 + i + lane] <= 0;
-    const uint32_t bits = __ballot_sync(~0u, is_free), to = rank + __popc(bits & ((1u << lane) - 1u));
-    if (is_free && to < needed && in_bounds(t.status, to, kSmallItems)) fresh[to] = p0 + i + lane;
+  for (int i = 0; i < run.words && rank < needed; ++i) {
+    const int32_t p = run.begin + i * 32 + lane;
+    const uint32_t taken = KB > 0 ? __ballot_sync(~0u, refs[p] > 0) : run.word(t.refs, t.pages, i);
+    const uint32_t bits = __ballot_sync(~0u, !(taken >> lane & 1u) && p < t.pages), to = rank + __popc(bits & ((1u << lane) - 1u));
+    if (bits >> lane & 1u && to < needed && in_bounds(t.status, to, kSmallItems)) fresh[to] = p;
     rank += __popc(bits);
   }
   __syncthreads();
@@ -817,18 +840,19 @@ size_t reserve_bytes(int64_t batch, int64_t pages, int64_t rows, int64_t width) 
 size_t compact_bytes(int64_t pages) { return align16(pages / 2 * 4) + 2 * align16(pages * 4); }
 
 // CTAs of a plan over so many units and pages, and a CTA's share of n in whole tiles.
-int plan_ctas(int64_t units, int64_t pages) { return units <= kWarps && pages <= kSmallPages ? 1 : kMaxCtas; }
+constexpr int64_t kOneCta = 4096;  // pages
+int plan_ctas(int64_t units, int64_t pages) { return units <= kWarps && pages <= kOneCta ? 1 : kMaxCtas; }
 int32_t share(int64_t n, int ctas, int tile) { return (int32_t)(cdiv(cdiv(n, ctas), tile) * tile); }
 constexpr int64_t kRemapHere = 8192;  // table entries per CTA up to which the compaction's own CTAs rewrite the table
-constexpr int64_t kForkHere = 4096;   // (entry, column) pairs up to which the small step does the fork too
+constexpr int64_t kSmallPages = 262144;  // pages whose counts one CTA looks through
 
 template <int KB>
 cudaError_t launch_small(const ReserveArgs& a, cudaStream_t st) {
   static std::atomic<int> done[64];
-  const cudaError_t e = opt_in_smem(small_reserve_kernel<KB>, (int)small_smem(kSmallPages), done);
+  const cudaError_t e = opt_in_smem(small_reserve_kernel<KB>, kForkPages * 4, done);
   if (e != cudaSuccess) return e;
-  const size_t smem = small_smem(a.t.pages);
-  return launch_dependent(small_reserve_kernel<KB>, dim3(1), kSmallThreads, smem, st, a, (int32_t)(smem / 12));
+  const int32_t padded = KB > 0 ? padded_pages(a.t.pages) : 0;
+  return launch_dependent(small_reserve_kernel<KB>, dim3(1), kSmallThreads, (size_t)padded * 4, st, a, padded);
 }
 
 bool misaligned(std::initializer_list<const void*> p) {
@@ -891,13 +915,14 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
   cudaError_t e = cudaSuccess;
   prof_begin(K_PAGES, st);
   const bool small = rows * width > 0 && rows * width <= kSmallItems && pages <= kSmallPages;
-  const bool fork_there = fork && small && beams <= 8 && batch * columns <= kForkHere;
+  const bool fork_there = fork && small && beams <= 8 && batch * columns <= kForkHere && pages <= kForkPages;
   if (fork && !fork_there) {
     a.left_alone = reinterpret_cast<int32_t*>(ws);
     const dim3 grid((unsigned)batch, (unsigned)std::max<int64_t>(1, std::min<int64_t>(65535, cdiv(columns, kForkThreads))));
     e = beams <= 4    ? launch_dependent(fork_kernel<4>, grid, kForkThreads, 0, st, t, a.left_alone)
         : beams <= 8  ? launch_dependent(fork_kernel<8>, grid, kForkThreads, 0, st, t, a.left_alone)
         : beams <= 16 ? launch_dependent(fork_kernel<16>, grid, kForkThreads, 0, st, t, a.left_alone)
+        : beams <= 32 ? launch_dependent(fork_kernel<32>, grid, kForkThreads, 0, st, t, a.left_alone)
                       : launch_dependent(fork_kernel<64>, grid, kForkThreads, 0, st, t, a.left_alone);
   }
   if (e == cudaSuccess && small) {
@@ -990,7 +1015,7 @@ int orpo_pages_compact(const int32_t* table, int64_t ld_table, int64_t columns, 
   const int here = table_rows * columns > (int64_t)ctas * kRemapHere ? 0 : ctas > 1 ? 1 : 2;
   static std::atomic<int> done[64];
   const size_t smem = here == 2 ? (size_t)(2 * pages + pages / 2) * 4 : 0;
-  cudaError_t e = opt_in_smem(compact_kernel, kSmallPages * 10, done);
+  cudaError_t e = opt_in_smem(compact_kernel, (int)kOneCta * 10, done);
   prof_begin(K_PAGES, st);
   if (e == cudaSuccess) e = launch_cluster_dependent(compact_kernel, ctas, kPlanThreads, smem, st, a, here);
   if (e == cudaSuccess && !here) {

@@ -69,7 +69,8 @@ def check(c, repetition=1.0, presence=0.0, frequency=0.0, no_repeat=0, use_promp
     return got
 
 
-SIZES = [(1, 1, 1, 1), (1, 4, 31, 5), (2, 3, 33, 40), (3, 2, 1000, 300), (1, 1, 8192, 4096), (2, 2, 8193, 1000), (1, 3, 20011, 5000)]
+# few rows take counters, many (more than two CTAs per SM would hold) a bit per token
+SIZES = [(160, 2, 33, 40), (310, 1, 2500, 300), (1, 400, 700, 5000), (1, 1, 1, 1), (1, 4, 31, 5), (2, 3, 33, 40), (3, 2, 1000, 300), (1, 1, 8192, 4096), (2, 2, 8193, 1000), (1, 3, 20011, 5000)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
@@ -95,10 +96,11 @@ def test_n_grams(n):
                   rng.integers(0, 3, cap), rng.integers(V, V + 5, cap)]).astype(np.int32)
     h = np.concatenate([h] * 5)
     length = np.repeat([cap, n - 1, n, n + 1, 97], 6).astype(np.int32)
-    x = torch.zeros((30, V), device=dev())
-    c = dict(x=x, beams=1, history=h, length=length, prompt=None)
-    got = check(c, no_repeat=n, use_prompt=False)
-    assert np.isinf(got[0]).sum() >= 1
+    for times in (1, 12):  # counters, and a bit per token
+        x = torch.zeros((30 * times, V), device=dev())
+        c = dict(x=x, beams=1, history=np.tile(h, (times, 1)), length=np.tile(length, times), prompt=None)
+        got = check(c, no_repeat=n, use_prompt=False)
+        assert np.isinf(got[0]).sum() >= 1
 
 
 def test_history_tokens_outside_the_vocabulary_count_nowhere():
@@ -127,11 +129,12 @@ def test_infinities_nan_and_the_type_s_lowest_value(dtype):
     low = torch.finfo(dtype).min
     vals = [math.inf, -math.inf, math.nan, low, -low, 0.0, -0.0, 1e-42, -1e-42, 2.0]
     V = len(vals)
-    x = torch.tensor([vals] * 4, device=dev()).to(dtype)
     masks = np.array([[0], [(1 << V) - 1]], dtype=np.int32)
-    c = dict(x=x, beams=4, history=np.tile(np.arange(V, dtype=np.int32), (4, 1)), length=np.array([V]), prompt=np.array([0]),
-             masks=masks, mask_row=np.array([0, 1, -1, 1], dtype=np.int32))
-    got = check(c, repetition=1.5, presence=0.25)
+    for times in (100, 1):
+        x = torch.tensor([vals] * 4 * times, device=dev()).to(dtype)
+        c = dict(x=x, beams=4 * times, history=np.tile(np.arange(V, dtype=np.int32), (4 * times, 1)), length=np.array([V]), prompt=np.array([0]),
+                 masks=masks, mask_row=np.tile(np.array([0, 1, -1, 1], dtype=np.int32), times))
+        got = check(c, repetition=1.5, presence=0.25)
     assert np.all(got[0] == -math.inf)  # whatever was there
     assert got[1][0] == math.inf and got[1][1] == -math.inf and math.isnan(got[1][2]) and got[1][3] == -math.inf
 
@@ -139,9 +142,10 @@ def test_infinities_nan_and_the_type_s_lowest_value(dtype):
 def test_bias_lists():
     """The same token twice and more, in the list and in the history; a list for all entries; infinite values; long lists."""
     rng = np.random.default_rng(0)
-    c = case(2, 2, 500, 50, n_bias=300, seed=1)
-    c["bias_token"][:, ::3] = 7
-    check(c, 1.2, 0.3, 0.1)
+    for batch, frequency in ((2, 0.1), (2, 0.0), (200, 0.0)):
+        c = case(batch, 2, 500, 50, n_bias=300, seed=1)
+        c["bias_token"][:, ::3] = 7
+        check(c, 1.2, 0.3, frequency)
     c = case(3, 2, 20000, 50, n_bias=64, seed=2, shared=True)
     check(c, 1.2)
     c = case(1, 1, 40, 5, seed=3)
@@ -248,10 +252,11 @@ def test_long_histories(cap):
 @pytest.mark.parametrize("frequency", [0.0, 0.25])
 @pytest.mark.parametrize("V,cap", [(409600, 500), (409601, 500), (600000, 9000), (1638400, 300), (1638401, 300), (3000000, 200)])
 def test_large_vocabularies(V, cap, frequency):
-    """On both sides of what fits a CTA's maps of the vocabulary: one, two, three or four of them."""
+    """On both sides of what fits a CTA's maps of the vocabulary: one, two, three or four of them, for few rows and many."""
     for n_bias, ngram in ((0, 0), (20, 0), (0, 2), (20, 2)):
-        c = case(1, 2, V, cap, seed=V + n_bias, n_bias=n_bias, spread=0.001 if ngram else 1.0)
-        check(c, 1.2, 0.5, frequency, ngram)
+        for batch in (1, 305 // (2 * -(-V // 32768)) + 1):
+            c = case(batch, 2, V, cap, seed=V + n_bias, n_bias=n_bias, spread=0.001 if ngram else 1.0)
+            check(c, 1.2, 0.5, frequency, ngram)
     c = case(1, 2, V, cap, seed=V, spread=1e-5)
     check(c, no_repeat=2)
 
