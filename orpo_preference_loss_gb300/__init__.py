@@ -10,6 +10,8 @@ is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -33,6 +35,7 @@ MAX_BEAMS = 64
 MAX_SELECT = 64
 
 _lib = None
+_fast = None
 
 
 class OrpoError(RuntimeError):
@@ -61,7 +64,7 @@ def use_bounds_checked_library() -> None:
 
 def load():
     """Load the library (built in-tree); raises if it is missing."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     path = lib_path()
@@ -142,8 +145,22 @@ def load():
     L.orpo_profile_stop.restype = ctypes.c_int
     L.orpo_profile_kind_name.argtypes = [ctypes.c_int]
     L.orpo_profile_kind_name.restype = ctypes.c_char_p
+    _fast = _load_binding(L)
     _lib = L
     return L
+
+
+def _load_binding(L):
+    """The module of csrc/binding.cpp, bound to the library's entry points."""
+    path = _build.binding_path(_variant == "debug")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with orpo_preference_loss_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("orpo_binding", path)
+    module = importlib.util.module_from_spec(importlib.machinery.ModuleSpec("orpo_binding", loader, origin=path))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.orpo_logits_adjust, L.orpo_beam_history, L.orpo_pages_advance,
+                                                                  L.orpo_pages_copy, L.orpo_pages_release, L.orpo_pages_compact)))
+    return module
 
 
 def _ptr(t):
@@ -447,10 +464,6 @@ F32, I32, U8, FLAGS = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.u
 MASKS = (torch.int32, torch.uint32) if hasattr(torch, "uint32") else (torch.int32,)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
 def orpo_head_logits_q_workspace_bytes(M: int, d: int, bits: int) -> int:
     return int(load().orpo_head_logits_q_workspace_bytes(M, d, bits))
 
@@ -577,6 +590,14 @@ def _now():
     return torch.cuda.current_device() if _raw_device is None else _raw_device()
 
 
+def _where(stream):
+    """(the current device's number, the stream's handle), as csrc/binding.cpp takes them."""
+    if _raw_device is None or _raw_stream is None or stream is not None:
+        return _now(), (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    now = _raw_device()
+    return now, _raw_stream(now)
+
+
 def _here(first, *others):
     """The tensors (None: not given) are on the device that is current, where the call's kernels run."""
     at = first.get_device()
@@ -590,8 +611,32 @@ def _here(first, *others):
             raise ValueError(f"the tensors are on different devices: {first.device} and {t.device}")
 
 
-def _adjust_args(logits, beams, status, history, length, prompt, bias_token, bias_value, masks, mask_row):
-    """Looks at every argument, for its message; returns the pitches and sizes."""
+# Each of the calls below goes through csrc/binding.cpp, which looks at the tensors in a fraction of the time.  Where that
+# finds one that is not of the usual kind (-1), the arguments are looked at here one by one, for the message.
+
+
+def orpo_logits_adjust(logits, beams, status, history=None, length=None, prompt=None, repetition=1.0, presence=0.0, frequency=0.0,
+                       no_repeat=0, bias_token=None, bias_value=None, masks=None, mask_row=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks, in place on logits [batch * beams, V] (fp32 or bf16).
+
+    history: int32 [batch * beams, capacity], of which the first length[b] (int32 [batch]) are tokens of the row, the first
+    prompt[b] of those (None: 0) the prompt's.  bias_token, bias_value: int32, fp32 [batch, n], or [n] for every entry.  masks:
+    int32 or uint32 [n_masks, ceil(V / 32)], bit set = allowed; mask_row: int32 [batch * beams], -1 for a row without a mask."""
+    code = -1
+    if logits.is_cuda:
+        if _fast is None:
+            load()
+        code = _fast.adjust(*_where(stream), logits, beams, status, history, length, prompt, repetition, presence, frequency, no_repeat,
+                            bias_token, bias_value, masks, mask_row)
+    if code < 0:
+        code = _adjust(logits, beams, status, history, length, prompt, repetition, presence, frequency, no_repeat, bias_token,
+                       bias_value, masks, mask_row, stream)
+    if code:
+        raise OrpoError(code, "orpo_logits_adjust")
+
+
+def _adjust(logits, beams, status, history, length, prompt, repetition, presence, frequency, no_repeat, bias_token, bias_value,
+            masks, mask_row, stream):
     rows, V = logits.shape
     if beams < 1 or rows % beams:
         raise ValueError(f"logits has {rows} rows, expected a multiple of beams = {beams}")
@@ -621,80 +666,30 @@ def _adjust_args(logits, beams, status, history, length, prompt, bias_token, bia
     if masks is not None or mask_row is not None:
         ld_masks, n_masks = _rows(masks, "masks", MASKS, cols=-(-V // 32)), masks.shape[0]
         _dev(mask_row, "mask_row", I32, (rows,))
-    return pitch, ld_history, capacity, ld_bias, n_bias, ld_masks, n_masks
-
-
-def orpo_logits_adjust(logits, beams, status, history=None, length=None, prompt=None, repetition=1.0, presence=0.0, frequency=0.0,
-                       no_repeat=0, bias_token=None, bias_value=None, masks=None, mask_row=None, stream=None):
-    """Penalties for repeated tokens, biases and grammar masks, in place on logits [batch * beams, V] (fp32 or bf16).
-
-    history: int32 [batch * beams, capacity], of which the first length[b] (int32 [batch]) are tokens of the row, the first
-    prompt[b] of those (None: 0) the prompt's.  bias_token, bias_value: int32, fp32 [batch, n], or [n] for every entry.  masks:
-    int32 or uint32 [n_masks, ceil(V / 32)], bit set = allowed; mask_row: int32 [batch * beams], -1 for a row without a mask."""
-    rows, V = logits.shape
-    pitch, step = logits.stride()
-    at, i32 = logits.get_device(), torch.int32
-    ld_history = capacity = ld_bias = n_bias = ld_masks = n_masks = 0
-    # the usual, right arguments pass plain tests; whatever fails them is looked at in full for its message
-    fine = (beams > 0 and rows % beams == 0 and step == 1 and pitch >= V and rows > 1 and logits.dtype in LOGITS and at >= 0 and at == _now()
-            and status.get_device() == at and status.dtype is i32)
-    if fine and history is not None:
-        held, capacity = history.shape
-        ld_history, step = history.stride()
-        fine = (held == rows and step == 1 and ld_history >= capacity and history.dtype is i32 and history.get_device() == at
-                and length is not None and length.shape == (rows // beams,) and length.dtype is i32 and length.is_contiguous()
-                and length.get_device() == at
-                and (prompt is None or (prompt.shape == length.shape and prompt.dtype is i32 and prompt.is_contiguous()
-                                        and prompt.get_device() == at)))
-    if fine and (bias_token is not None or bias_value is not None):
-        fine = (bias_token is not None and bias_value is not None and bias_token.dim() == 2 and rows > beams)
-        if fine:
-            lists, n_bias = bias_token.shape
-            ld_bias, step = bias_token.stride()
-            fine = (lists == rows // beams and step == 1 and ld_bias >= n_bias and bias_token.dtype is i32
-                    and bias_token.get_device() == at and bias_value.shape == bias_token.shape
-                    and bias_value.stride() == (ld_bias, 1) and bias_value.dtype is torch.float32 and bias_value.get_device() == at)
-    if fine and (masks is not None or mask_row is not None):
-        fine = masks is not None and mask_row is not None and masks.dim() == 2
-        if fine:
-            n_masks, words = masks.shape
-            ld_masks, step = masks.stride()
-            fine = (words == (V + 31) // 32 and n_masks > 1 and step == 1 and ld_masks >= words and masks.dtype in MASKS
-                    and masks.get_device() == at and mask_row.shape == (rows,) and mask_row.dtype is i32
-                    and mask_row.is_contiguous() and mask_row.get_device() == at)
-    if not fine:
-        pitch, ld_history, capacity, ld_bias, n_bias, ld_masks, n_masks = _adjust_args(
-            logits, beams, status, history, length, prompt, bias_token, bias_value, masks, mask_row)
-    code = (_lib or load()).orpo_logits_adjust(
-        logits.data_ptr(), pitch, logits.dtype is torch.bfloat16, rows // beams, beams, V, _at(history), ld_history, capacity,
-        _at(length), _at(prompt), repetition, presence, frequency, no_repeat, _at(bias_token), _at(bias_value), ld_bias, n_bias,
-        _at(masks), ld_masks, n_masks, _at(mask_row), status.data_ptr(), _stream(stream))
-    if code:
-        raise OrpoError(code, "orpo_logits_adjust")
+    return load().orpo_logits_adjust(
+        _ptr(logits), pitch, logits.dtype is torch.bfloat16, batch, beams, V, _ptr(history), ld_history, capacity, _ptr(length),
+        _ptr(prompt), repetition, presence, frequency, no_repeat, _ptr(bias_token), _ptr(bias_value), ld_bias, n_bias, _ptr(masks),
+        ld_masks, n_masks, _ptr(mask_row), _ptr(status), _stream(stream))
 
 
 def orpo_beam_history(history, parent, token, length, status, stream=None):
     """Token histories [batch * beams, capacity] (int32) follow parent [batch, beams] in place, up to length[b], where
     token [batch, beams] is then put.  length is not changed."""
-    batch, beams = parent.shape
-    rows, capacity = history.shape
-    ld, step = history.stride()
-    at, i32 = history.get_device(), torch.int32
-    ld_parent, step_p = parent.stride()
-    ld_token, step_t = token.stride()
-    if not (rows == batch * beams and rows > 1 and step == 1 and ld >= capacity and history.dtype is i32 and at >= 0 and at == _now()
-            and step_p == 1 and ld_parent >= beams and parent.dtype is i32 and parent.get_device() == at
-            and token.shape == parent.shape and step_t == 1 and ld_token >= beams and token.dtype is i32
-            and token.get_device() == at and length.shape == (batch,) and length.dtype is i32 and length.is_contiguous()
-            and length.get_device() == at and status.dtype is i32 and status.get_device() == at):
+    code = -1
+    if history.is_cuda:
+        if _fast is None:
+            load()
+        code = _fast.history(*_where(stream), history, parent, token, length, status)
+    if code < 0:
+        batch, beams = parent.shape
         _here(history, parent, token, length, status)
         ld = _rows(history, "history", I32, rows=batch * beams)
         ld_parent = _rows(parent, "parent", I32)
         ld_token = _rows(token, "token", I32, cols=beams, rows=batch)
         _dev(length, "length", I32, (batch,))
         _dev(status, "status", I32)
-    code = (_lib or load()).orpo_beam_history(history.data_ptr(), ld, capacity, parent.data_ptr(), ld_parent, token.data_ptr(),
-                                              ld_token, length.data_ptr(), batch, beams, status.data_ptr(), _stream(stream))
+        code = load().orpo_beam_history(_ptr(history), ld, history.shape[1], _ptr(parent), ld_parent, _ptr(token), ld_token,
+                                        _ptr(length), batch, beams, _ptr(status), _stream(stream))
     if code:
         raise OrpoError(code, "orpo_beam_history")
 
@@ -713,96 +708,78 @@ def _moves(moves, n_moves, workspace, status):
     _dev(status, "status", I32)
 
 
-def _moves_fine(moves, n_moves, status, at):
-    shape, i32 = moves.shape, torch.int32
-    return (len(shape) == 2 and shape[1] == 3 and moves.is_contiguous() and moves.dtype is i32 and moves.get_device() == at
-            and n_moves.shape == (1,) and n_moves.dtype is i32 and n_moves.get_device() == at and status.dtype is i32
-            and status.get_device() == at)
-
-
-def _workspace_fine(workspace, at):
-    return workspace.dtype is torch.uint8 and workspace.is_contiguous() and workspace.get_device() == at
-
-
 def orpo_pages_advance(table, refs, page, parent, length, more, most, moves, n_moves, workspace, status, stream=None):
     """Page tables [batch * beams, columns] follow parent [batch, beams] (None: they stay), and positions length[b] ..
     length[b] + more[b] - 1 (more None: `most` of them) of each row become writable.
 
     Pages are taken and let go of in refs (int32 [pages]); pages to be copied are listed in moves (int32 [max_moves, 3], n_moves
     int32 [1]) for orpo_pages_copy.  workspace: uint8, orpo_pages_workspace_bytes(batch * beams, pages, page, most)."""
-    rows, columns = table.shape
-    batch = length.shape[0]
-    beams = rows // batch if batch else 1
-    if rows != batch * beams:
-        raise ValueError(f"table has {rows} rows, expected a multiple of the {batch} lengths")
-    ld, step = table.stride()
-    at, i32 = table.get_device(), torch.int32
-    pages = refs.numel()
-    ld_parent = 0
-    fine = (rows > 1 and step == 1 and ld >= columns and table.dtype is i32 and at >= 0 and at == _now() and refs.dim() == 1
-            and refs.is_contiguous() and refs.dtype is i32 and refs.get_device() == at and length.shape == (batch,)
-            and length.dtype is i32 and length.is_contiguous() and length.get_device() == at
-            and (more is None or (more.shape == (batch,) and more.dtype is i32 and more.is_contiguous() and more.get_device() == at))
-            and _moves_fine(moves, n_moves, status, at) and _workspace_fine(workspace, at))
-    if fine and parent is not None:
-        ld_parent, step = parent.stride()
-        fine = (parent.shape == (batch, beams) and step == 1 and ld_parent >= beams and parent.dtype is i32
-                and parent.get_device() == at)
-    if not fine:
+    code = -1
+    if table.is_cuda:
+        if _fast is None:
+            load()
+        code = _fast.advance(*_where(stream), table, refs, page, parent, length, more, most, moves, n_moves, workspace, status)
+    if code < 0:
+        rows, columns = table.shape
+        batch = length.shape[0]
+        beams = rows // batch if batch else 1
+        if rows != batch * beams:
+            raise ValueError(f"table has {rows} rows, expected a multiple of the {batch} lengths")
         _here(table, refs, parent, length, more, moves, n_moves, workspace, status)
         ld = _rows(table, "table", I32)
-        _dev(refs, "refs", I32, (pages,))
+        _dev(refs, "refs", I32, (refs.numel(),))
         ld_parent = 0 if parent is None else _rows(parent, "parent", I32, cols=beams, rows=batch)
         _dev(length, "length", I32, (batch,))
         if more is not None:
             _dev(more, "more", I32, (batch,))
         _moves(moves, n_moves, workspace, status)
-    code = (_lib or load()).orpo_pages_advance(
-        table.data_ptr(), ld, columns, refs.data_ptr(), pages, page, _at(parent), ld_parent, length.data_ptr(), _at(more),
-        most, batch, beams, moves.data_ptr(), moves.shape[0], n_moves.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        status.data_ptr(), _stream(stream))
+        code = load().orpo_pages_advance(
+            _ptr(table), ld, columns, _ptr(refs), refs.numel(), page, _ptr(parent), ld_parent, _ptr(length), _ptr(more), most, batch,
+            beams, _ptr(moves), moves.shape[0], _ptr(n_moves), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
     if code:
         raise OrpoError(code, "orpo_pages_advance")
 
 
 def orpo_pages_copy(pool, moves, n_moves, status, stream=None):
     """Carries out the copies of moves in pool [outer, pages, rows, page, unit] (any dtype)."""
-    at = pool.get_device()
-    if not (at >= 0 and at == _now() and pool.is_contiguous() and pool.dim() == 5 and _moves_fine(moves, n_moves, status, at)):
+    code = -1
+    if pool.is_cuda:
+        if _fast is None:
+            load()
+        code = _fast.copy(*_where(stream), pool, moves, n_moves, status)
+    if code < 0:
         _here(pool, moves, n_moves, status)
         if not pool.is_contiguous() or pool.dim() != 5:
             raise ValueError("pool must be a contiguous CUDA tensor [outer, pages, rows, page, unit]")
         _moves(moves, n_moves, None, status)
-    outer, pages, rows, page, unit = pool.shape
-    code = (_lib or load()).orpo_pages_copy(pool.data_ptr(), outer, pages, rows, page, unit * pool.element_size(),
-                                            moves.data_ptr(), moves.shape[0], n_moves.data_ptr(), status.data_ptr(),
-                                            _stream(stream))
+        outer, pages, rows, page, unit = pool.shape
+        code = load().orpo_pages_copy(_ptr(pool), outer, pages, rows, page, unit * pool.element_size(), _ptr(moves), moves.shape[0],
+                                      _ptr(n_moves), _ptr(status), _stream(stream))
     if code:
         raise OrpoError(code, "orpo_pages_copy")
 
 
 def orpo_pages_release(table, refs, ended, status, stream=None):
     """The rows of entries with ended[b] != 0 (uint8 or bool [batch]; None: all rows) let go of their pages."""
-    rows, columns = table.shape
-    batch = rows if ended is None else ended.shape[0]
-    beams = rows // batch if batch else 1
-    if rows != batch * beams:
-        raise ValueError(f"table has {rows} rows, expected a multiple of the {batch} entries of ended")
-    ld, step = table.stride()
-    at, i32 = table.get_device(), torch.int32
-    pages = refs.numel()
-    if not (rows > 1 and step == 1 and ld >= columns and table.dtype is i32 and at >= 0 and at == _now() and refs.dim() == 1
-            and refs.is_contiguous() and refs.dtype is i32 and refs.get_device() == at and status.dtype is i32
-            and status.get_device() == at
-            and (ended is None or (ended.dim() == 1 and ended.dtype in FLAGS and ended.is_contiguous() and ended.get_device() == at))):
+    code = -1
+    if table.is_cuda:
+        if _fast is None:
+            load()
+        code = _fast.release(*_where(stream), table, refs, ended, status)
+    if code < 0:
+        rows, columns = table.shape
+        batch = rows if ended is None else ended.shape[0]
+        beams = rows // batch if batch else 1
+        if rows != batch * beams:
+            raise ValueError(f"table has {rows} rows, expected a multiple of the {batch} entries of ended")
         _here(table, refs, ended, status)
         ld = _rows(table, "table", I32)
-        _dev(refs, "refs", I32, (pages,))
+        _dev(refs, "refs", I32, (refs.numel(),))
         if ended is not None:
             _dev(ended, "ended", FLAGS, (batch,))
         _dev(status, "status", I32)
-    code = (_lib or load()).orpo_pages_release(table.data_ptr(), ld, columns, refs.data_ptr(), pages, _at(ended), batch, beams,
-                                               status.data_ptr(), _stream(stream))
+        code = load().orpo_pages_release(_ptr(table), ld, columns, _ptr(refs), refs.numel(), _ptr(ended), batch, beams, _ptr(status),
+                                         _stream(stream))
     if code:
         raise OrpoError(code, "orpo_pages_release")
 
@@ -811,28 +788,23 @@ def orpo_pages_compact(table, refs, page, new_table, new_refs, live, moves, n_mo
     """Numbers the pages in use 0 .. live[0] - 1: those at live[0] or above take the free numbers below, in order.
 
     new_table and new_refs may be table and refs themselves; moves (at least pages / 2 of them) are for orpo_pages_copy."""
-    rows, columns = table.shape
-    ld, step = table.stride()
-    ld_new, step_new = new_table.stride()
-    at, i32 = table.get_device(), torch.int32
-    pages = refs.numel()
-    if not (rows > 1 and step == 1 and ld >= columns and table.dtype is i32 and at >= 0 and at == _now() and new_table.shape == table.shape
-            and step_new == 1 and ld_new >= columns and new_table.dtype is i32 and new_table.get_device() == at and refs.dim() == 1
-            and refs.is_contiguous() and refs.dtype is i32 and refs.get_device() == at and new_refs.shape == refs.shape
-            and new_refs.is_contiguous() and new_refs.dtype is i32 and new_refs.get_device() == at and live.shape == (1,)
-            and live.dtype is i32 and live.get_device() == at and _moves_fine(moves, n_moves, status, at)
-            and _workspace_fine(workspace, at)):
+    code = -1
+    if table.is_cuda:
+        if _fast is None:
+            load()
+        code = _fast.compact(*_where(stream), table, refs, page, new_table, new_refs, live, moves, n_moves, workspace, status)
+    if code < 0:
+        rows, columns = table.shape
         _here(table, refs, new_table, new_refs, live, moves, n_moves, workspace, status)
         ld = _rows(table, "table", I32)
         ld_new = _rows(new_table, "new_table", I32, cols=columns, rows=rows)
-        _dev(refs, "refs", I32, (pages,))
-        _dev(new_refs, "new_refs", I32, (pages,))
+        _dev(refs, "refs", I32, (refs.numel(),))
+        _dev(new_refs, "new_refs", I32, (refs.numel(),))
         _dev(live, "live", I32, (1,))
         _moves(moves, n_moves, workspace, status)
-    code = (_lib or load()).orpo_pages_compact(
-        table.data_ptr(), ld, columns, rows, refs.data_ptr(), pages, page, new_table.data_ptr(), ld_new, new_refs.data_ptr(),
-        live.data_ptr(), moves.data_ptr(), moves.shape[0], n_moves.data_ptr(), workspace.data_ptr(), workspace.numel(),
-        status.data_ptr(), _stream(stream))
+        code = load().orpo_pages_compact(
+            _ptr(table), ld, columns, rows, _ptr(refs), refs.numel(), page, _ptr(new_table), ld_new, _ptr(new_refs), _ptr(live),
+            _ptr(moves), moves.shape[0], _ptr(n_moves), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
     if code:
         raise OrpoError(code, "orpo_pages_compact")
 

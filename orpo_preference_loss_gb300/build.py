@@ -2,8 +2,9 @@
 
 Each .cu file is compiled in parallel into an object, then linked into a shared
 library against the shared CUDA runtime (the one PyTorch also loads).  The
-result lives in ``orpo_preference_loss_gb300/_build/`` (git-ignored).  A build
-is skipped when the library is newer than every source and header.
+result lives in ``orpo_preference_loss_gb300/_build/`` (git-ignored).  The Python
+module of csrc/binding.cpp is compiled beside it with the host compiler, against
+PyTorch's headers.  A build is skipped when both are newer than every source and header.
 
 ``build(debug=True)`` makes the bounds-checked variant ``liborpo_head_debug.so``
 in ``_build_debug/``: the same sources with ORPO_DEBUG_BOUNDS, where every
@@ -19,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -29,6 +31,8 @@ LIB_NAME = "liborpo_head.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 DEBUG_OUT_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(DEBUG_OUT_DIR, "liborpo_head_debug.so")
+
+BINDING_NAME = "orpo_binding.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -42,20 +46,35 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found; the CUDA toolkit is required to build liborpo_head")
 
 
+def binding_path(debug: bool = False) -> str:
+    return os.path.join(DEBUG_OUT_DIR if debug else OUT_DIR, BINDING_NAME)
+
+
+def _binding_command(out: str):
+    """The host compiler's command for the Python module (its library is handed to it when it is loaded)."""
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
+            "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "binding.cpp"), "-o", out,
+            "-L", os.path.join(home, "lib"), f"-Wl,-rpath,{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date(debug: bool = False) -> bool:
     lib = DEBUG_LIB_PATH if debug else LIB_PATH
-    if not os.path.exists(lib):
+    if not os.path.exists(lib) or not os.path.exists(binding_path(debug)):
         return False
-    t = os.path.getmtime(lib)
+    t = min(os.path.getmtime(lib), os.path.getmtime(binding_path(debug)))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -85,19 +104,24 @@ def _build_locked(verbose: bool, debug: bool) -> str:
     flags = NVCC_FLAGS + (["-DORPO_DEBUG_BOUNDS"] if debug else [])
     objs = [os.path.join(out, os.path.basename(s)[:-3] + ".o") for s in srcs]
 
+    binding = binding_path(debug)
+
     def compile_one(pair):
         src, obj = pair
+        if src.endswith(".cpp"):
+            return src, subprocess.run(_binding_command(obj), capture_output=True, text=True)
         cmd = [nvcc, *ARCH, *flags, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, r
 
-    with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
-        results = list(ex.map(compile_one, zip(srcs, objs)))
+    jobs = [*zip(srcs, objs), (os.path.join(CSRC, "binding.cpp"), binding + ".tmp")]
+    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+        results = list(ex.map(compile_one, jobs))
     failed = False
     for src, r in results:
         if r.returncode != 0:
             failed = True
-            sys.stderr.write(f"--- nvcc failed on {src}\n{r.stdout}\n{r.stderr}\n")
+            sys.stderr.write(f"--- the compiler failed on {src}\n{r.stdout}\n{r.stderr}\n")
         elif verbose:
             sys.stderr.write(f"--- {os.path.basename(src)}\n{r.stderr}")
     if failed:
@@ -108,6 +132,7 @@ def _build_locked(verbose: bool, debug: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"liborpo_head link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    os.replace(binding + ".tmp", binding)
     return lib
 
 
