@@ -57,6 +57,7 @@ struct AdjustArgs {
   int list_cap;    // listed tokens per range at most
   int list_words;  // 32-bit words of that list
   int bit_words;   // of a map of the vocabulary
+  int sets;        // of words per mask CTA
   int clear;       // 16-byte pieces of shared memory to clear
 };
 
@@ -88,18 +89,33 @@ struct Logit<uint16_t> {
 // ------------------------------------------------------------------ the history's tokens
 constexpr int kUnroll = 6;  // tokens of a thread in flight; with 4 and three CTAs per SM the wide case takes 25 us instead of 21, with 8 as many
 
-// Calls each(t, token, n) with kUnroll tokens of history positions t[0], ... in [begin, end) (token -1: none), whole warps at
+// A thread's first kUnroll tokens of history positions [begin, end) (-1: none), asked for before they are needed.
+struct First {
+  int begin = -1;
+  int32_t v[kUnroll];
+  __device__ __forceinline__ void load(const int32_t* h, int from, int end) {
+    begin = from;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int t = from + u * kThreads + (int)threadIdx.x;
+      v[u] = t < end ? h[t] : -1;
+    }
+  }
+};
+
+// Calls each(t, token) with kUnroll tokens of history positions t[0], ... in [begin, end) (token -1: none), whole warps at
 // a time.
 template <class Each>
-__device__ __forceinline__ void each_tokens(const int32_t* h, int begin, int end, Each each) {
+__device__ __forceinline__ void each_tokens(const int32_t* h, int begin, int end, const First& first, Each each) {
   const int lane = threadIdx.x & 31;
   for (int t0 = begin + (int)threadIdx.x - lane; t0 < end; t0 += kUnroll * kThreads) {
     int t[kUnroll];
     int32_t v[kUnroll];
+    const bool ready = begin == first.begin && t0 < begin + kThreads;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       t[u] = t0 + u * kThreads + lane;
-      v[u] = t[u] < end ? h[t[u]] : -1;
+      v[u] = ready ? first.v[u] : t[u] < end ? h[t[u]] : -1;
     }
     each(t, v);
   }
@@ -148,7 +164,7 @@ __device__ __forceinline__ void adjust(const AdjustArgs& a, const Row<T>& row, c
 template <class T, class Known>
 __device__ __forceinline__ void adjust_biased(const AdjustArgs& a, const Row<T>& row, const int32_t* token, const float* value, bool twice,
                                               int64_t v0, int size, Known known) {
-  for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
+  for (int j = kThreads - 1 - (int)threadIdx.x; j < a.n_bias; j += kThreads) {  // from the last thread on: the first have the history's
     const int32_t v = token[j];
     if (v < 0 || (uint32_t)(v - (int32_t)v0) >= (uint32_t)size) continue;
     if (row.words && !(row.words[v >> 5] >> (v & 31) & 1u)) continue;  // left to the masks
@@ -167,11 +183,11 @@ __device__ __forceinline__ void adjust_biased(const AdjustArgs& a, const Row<T>&
 }
 
 // ------------------------------------------------------------------ masks
-constexpr int kMaskSets = 2;                              // of 32 words, per warp
-constexpr int kMaskTokens = kThreads * 32 * kMaskSets;    // per CTA
+constexpr int kSetTokens = kThreads * 32;  // a word per thread
+constexpr int kMaskSets = 2;               // of those per CTA, or one where so many CTAs are resident at once
 
 template <class T>
-__device__ __forceinline__ void mask_range(const AdjustArgs& a, const Row<T>& row, int64_t v0) {
+__device__ __forceinline__ void mask_range(const AdjustArgs& a, const Row<T>& row, int64_t v0, int sets) {
   constexpr int kGroup = 512 / (32 * (int)sizeof(T));  // words whose logits are 512 bytes
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t n_words = (a.V + 31) / 32;
@@ -182,7 +198,7 @@ __device__ __forceinline__ void mask_range(const AdjustArgs& a, const Row<T>& ro
   for (int s = 0; s < kMaskSets; ++s) {
     first[s] = v0 / 32 + (s * (kThreads / 32) + warp) * 32;
     const int64_t i = first[s] + lane;
-    word[s] = i < n_words ? row.words[i] : ~0u;
+    word[s] = s < sets && i < n_words ? row.words[i] : ~0u;
     if (i == n_words - 1 && a.V % 32) word[s] |= ~0u << (a.V % 32);
   }
 #pragma unroll
@@ -226,35 +242,31 @@ struct Bits {
 };
 
 template <class T>
-__device__ __forceinline__ void by_bits(const AdjustArgs& a, const Row<T>& row, uint32_t* smem, const int32_t* h, int len, int prompt,
+__device__ __forceinline__ void by_bits(const AdjustArgs& a, const Row<T>& row, uint32_t* smem, const First& first, const int32_t* h, int len, int prompt,
                                         const int32_t* tail, int n_tail, const int32_t* bias_token, const float* bias_value, int* twice,
                                         bool penalties) {
   const int stride = a.bit_words;
   const bool biased = a.n_bias > 0;
-  // tokens that the mask bans count as met from the start, so that nobody adjusts them
-  if (row.words)
-    for (int i = threadIdx.x; i < (int)((a.V + 31) / 32); i += kThreads) smem[i] = ~row.words[i];
   const Bits bits{smem, smem + stride, smem + (a.ngram > 0 ? 2 : 1) * stride, smem + (a.ngram > 0 ? 3 : 2) * stride};
   const int32_t V = (int32_t)a.V;
-  for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
+  for (int j = kThreads - 1 - (int)threadIdx.x; j < a.n_bias; j += kThreads) {  // from the last thread on: the first have the history's
     const int32_t v = bias_token[j];
     if (v >= 0 && v < V && Bits::set(bits.bias, v)) *twice = 1;
   }
   if (n_tail >= 0)
-    each_tokens(h, 0, len, [&](const int (&t)[kUnroll], const int32_t (&v)[kUnroll]) {
+    each_tokens(h, 0, len, first, [&](const int (&t)[kUnroll], const int32_t (&v)[kUnroll]) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
         if (ends_again(h, t[u], v[u], len, tail, n_tail) && v[u] >= 0 && v[u] < V && !Bits::set(bits.ban, v[u]) &&
             in_bounds(a.status, row.at + v[u], row.all))
           row.x[v[u]] = Logit<T>::make(-INFINITY);  // as a mask would
     });
-  prompt = a.presence != 0.f ? min(max(prompt, 0), len) : 0;  // else the prompt's tokens are as the others
   if (penalties) {
 #pragma unroll 1
     for (int part = 0; part < 2; ++part) {  // what was generated, then the prompt
       if (part == 1 && prompt == 0) break;
-      if (part == 1 || biased || n_tail >= 0 || row.words) __syncthreads();
-      each_tokens(h, part == 0 ? prompt : 0, part == 0 ? len : prompt, [&](const int (&)[kUnroll], const int32_t (&v)[kUnroll]) {
+      if (part == 1 || biased || n_tail >= 0) __syncthreads();
+      each_tokens(h, part == 0 ? prompt : 0, part == 0 ? len : prompt, part == 0 ? first : First(), [&](const int (&)[kUnroll], const int32_t (&v)[kUnroll]) {
         int32_t token[kUnroll];
         uint32_t w[kUnroll];
 #pragma unroll
@@ -300,19 +312,15 @@ struct Counters {
 };
 
 template <class T, int kForm>
-__device__ __forceinline__ void by_counts(const AdjustArgs& a, const Row<T>& row, uint32_t* smem, int64_t v0, const int32_t* h, int len,
+__device__ __forceinline__ void by_counts(const AdjustArgs& a, const Row<T>& row, uint32_t* smem, const First& first, int64_t v0, const int32_t* h, int len,
                                           int prompt, const int32_t* tail, int n_tail, const int32_t* bias_token, const float* bias_value,
                                           int* listed, int* twice, bool penalties) {
   constexpr int kRange = range_of(kForm);
   const Counters<kForm> counters{smem};
   uint16_t* const list = reinterpret_cast<uint16_t*>(smem + kTableBytes / 4);  // tokens met, each once
   const uint32_t size = (uint32_t)min((int64_t)kRange, a.V - v0);
-  uint32_t* const allowed = smem + kTableBytes / 4 + a.list_words;  // the mask's part
-  if (row.words) {
-    for (int i = threadIdx.x; i < (int)((size + 31) / 32); i += kThreads) allowed[i] = row.words[v0 / 32 + i];
-    __syncthreads();
-  }
-  each_tokens(h, 0, len, [&](const int (&t)[kUnroll], const int32_t (&v)[kUnroll]) {
+  const uint32_t* const allowed = smem + kTableBytes / 4 + a.list_words;  // the mask's part
+  each_tokens(h, 0, len, first, [&](const int (&t)[kUnroll], const int32_t (&v)[kUnroll]) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const bool banned = ends_again(h, t[u], v[u], len, tail, n_tail);
@@ -327,7 +335,7 @@ __device__ __forceinline__ void by_counts(const AdjustArgs& a, const Row<T>& row
       if (banned) counters.flag(at, kBan, kFewBan);
     }
   });
-  for (int j = threadIdx.x; j < a.n_bias; j += kThreads) {
+  for (int j = kThreads - 1 - (int)threadIdx.x; j < a.n_bias; j += kThreads) {  // from the last thread on: the first have the history's
     const int32_t v = bias_token[j];
     const uint32_t at = (uint32_t)(v - (int32_t)v0);
     if (v < 0 || at >= size || !in_bounds(a.status, at, kRange)) continue;
@@ -362,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_kernel(AdjustArgs a) {
   if (history)
     for (int i = tid; i < a.clear; i += kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) listed = 0, twice = 0;
+  __syncthreads();
   grid_wait();
 
   const int64_t b = (uint32_t)r / (uint32_t)a.beams;
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_kernel(AdjustArgs a) {
   }
   const Row<T> row{static_cast<T*>(a.logits) + r * a.ld, mask >= 0 ? a.masks + mask * a.ld_masks : nullptr, r * a.ld, a.rows * a.ld};
   if (!history) {
-    if (mask >= 0) mask_range(a, row, (int64_t)(part - a.parts) * kMaskTokens);
+    if (mask >= 0) mask_range(a, row, (int64_t)(part - a.parts) * a.sets * kSetTokens, a.sets);
     return;
   }
   const int32_t* const h = a.history + r * a.ld_history;
@@ -390,12 +399,24 @@ __global__ void __launch_bounds__(kThreads, 2) adjust_kernel(AdjustArgs a) {
     tail[tid] = t;
     bad_tail = t < 0 || t >= a.V;
   }
+  // its mask: for bits, masked tokens count as met from the start, so that nobody adjusts them
+  if (row.words) {
+    constexpr int kRange = kForm == kBits ? 0 : range_of(kForm);
+    const int64_t w0 = kForm == kBits ? 0 : (int64_t)part * (kRange / 32), words = (a.V + 31) / 32;
+    uint32_t* const to = kForm == kBits ? smem : smem + kTableBytes / 4 + a.list_words;
+    const int n = (int)(kForm == kBits ? words : min(words - w0, (int64_t)kRange / 32));
+    for (int i = tid; i < n; i += kThreads) to[i] = kForm == kBits ? ~row.words[i] : row.words[w0 + i];
+  }
+  // the tokens that are looked at first: for bits the generated part's, where it has a penalty of its own
+  const int generated = kForm == kBits && a.presence != 0.f ? min(max(prompt, 0), len) : 0;
+  First first;
+  first.load(h, n_tail >= 0 ? 0 : generated, len);
   if (__syncthreads_or(bad_tail)) n_tail = -1;
   const bool penalties = a.repetition != 1.f || a.presence != 0.f || a.frequency != 0.f;
   if constexpr (kForm == kBits)
-    by_bits<T>(a, row, smem, h, len, prompt, tail, n_tail, bias_token, bias_value, &twice, penalties);
+    by_bits<T>(a, row, smem, first, h, len, generated, tail, n_tail, bias_token, bias_value, &twice, penalties);
   else
-    by_counts<T, kForm>(a, row, smem, (int64_t)part * range_of(kForm), h, len, prompt, tail, n_tail, bias_token, bias_value, &listed, &twice,
+    by_counts<T, kForm>(a, row, smem, first, (int64_t)part * range_of(kForm), h, len, prompt, tail, n_tail, bias_token, bias_value, &listed, &twice,
                         penalties);
 }
 
@@ -426,7 +447,8 @@ cudaError_t launch(AdjustArgs a, int sms, cudaStream_t st) {
   a.list_words = (int)cdiv(a.list_cap, 8) * 4;
   const int64_t smem = !history ? 0 : form == kBits ? bits : kTableBytes + a.list_words * 4 + (a.masks ? range_of(form) / 8 : 0);
   a.clear = (int)((form == kBits ? bits : kTableBytes) / 16);
-  const dim3 grid((unsigned)(a.rows * (a.parts + (a.masks ? cdiv(a.V, kMaskTokens) : 0))));
+  a.sets = a.rows * cdiv(a.V, kSetTokens) <= (int64_t)sms * 2 ? 1 : kMaskSets;
+  const dim3 grid((unsigned)(a.rows * (a.parts + (a.masks ? cdiv(a.V, a.sets * kSetTokens) : 0))));
   return form == kBits      ? launch_form<T, kBits>(a, grid, (size_t)smem, st)
          : form == kCount16 ? launch_form<T, kCount16>(a, grid, (size_t)smem, st)
                             : launch_form<T, kCount32>(a, grid, (size_t)smem, st);
@@ -466,7 +488,7 @@ extern "C" int orpo_logits_adjust(void* logits, int64_t ld_logits, int logits_bf
   if (int e = device_check(&sms)) return e;
   const AdjustArgs a{logits, ld_logits, batch * beams, V, beams, reads ? history : nullptr, ld_history, (int)capacity,
                      length, prompt, repetition, presence, frequency, no_repeat, bias_token, bias_value, ld_bias, (int)n_bias,
-                     masks, ld_masks, n_masks, mask_row, status, 0, 0, 0, 0, 0};
+                     masks, ld_masks, n_masks, mask_row, status, 0, 0, 0, 0, 0, 0};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = logits_bf16 ? launch<uint16_t>(a, sms, st) : launch<float>(a, sms, st);
   return e == cudaSuccess ? ORPO_OK : ORPO_ERR_CUDA;

@@ -70,7 +70,7 @@ def check(c, repetition=1.0, presence=0.0, frequency=0.0, no_repeat=0, use_promp
 
 
 # few rows take counters, many (more than two CTAs per SM would hold) a bit per token
-SIZES = [(160, 2, 33, 40), (310, 1, 2500, 300), (1, 400, 700, 5000), (1, 1, 1, 1), (1, 4, 31, 5), (2, 3, 33, 40), (3, 2, 1000, 300), (1, 1, 8192, 4096), (2, 2, 8193, 1000), (1, 3, 20011, 5000)]
+SIZES = [(160, 2, 33, 40), (310, 1, 2500, 300), (1, 1, 1, 1), (1, 4, 31, 5), (2, 3, 33, 40), (3, 2, 1000, 300), (1, 1, 8192, 4096), (2, 2, 8193, 1000), (1, 3, 20011, 5000)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
@@ -84,6 +84,13 @@ def test_against_the_oracle(batch, beams, V, cap, dtype, what):
         check(c, repetition=1.3 if what in ("repetition", "all") or every else 1.0, presence=0.4 if what in ("presence", "all") or every else 0.0,
               frequency=0.25 if what in ("frequency", "all") or every else 0.0, no_repeat=2 if what == "ngram" or every else 0,
               use_prompt=pad != 1)
+
+
+@pytest.mark.parametrize("no_repeat,presence,n_bias", [(0, 0.0, 0), (0, 0.4, 5), (2, 0.0, 0), (2, 0.4, 5)])
+def test_many_rows_of_long_histories(no_repeat, presence, n_bias):
+    """More tokens than a CTA takes at a time, in the form with a bit per token."""
+    c = case(1, 310, 700, 3500, seed=no_repeat, masks=3, n_bias=n_bias)
+    check(c, 1.2, presence, 0.0, no_repeat)
 
 
 @pytest.mark.parametrize("n", [1, 2, 3, 5, 32])
