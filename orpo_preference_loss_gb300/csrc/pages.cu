@@ -8,7 +8,7 @@
 // The plans (which page goes where) touch a few kilobytes: they are bound by the way to memory and back, which each step of
 // "length, parent, table entry, count of holders, free page" takes once, and by barriers.  So a decode step's plan is one CTA that
 // takes those ways twice (captured in a graph: 4 beams, 100 pages 4.5 us; 16 x 8 beams, 3000 pages about 8), larger ones a cluster of 8
-// CTAs that tell each other sums through shared memory (64 prompts of up to 512 pages into 164k pages: 17).  The copies are
+// CTAs that tell each other sums through shared memory (64 prompts of up to 512 pages into 164k pages: 16).  The copies are
 // bound by the bytes moved: 1.06 GB in 161 us, 97% of the rate of a plain copy.
 #include <algorithm>
 
@@ -203,11 +203,12 @@ struct ReserveArgs {
   int32_t width;     // items per row, rounded up to a power of two up to 32 or a multiple of kUnit
   int32_t items;     // so many in all
   int32_t units_per; // CTA
-  int32_t pages_per; // CTA, a multiple of 32 * kWarps
   int32_t* count;    // [pages] how many items hold a page that others hold too,
   int32_t* last;     // [pages] and the last of them
   uint32_t* needs;   // [units][kUnit / 32] items that need a page, as bits
-  uint32_t* before;  // [units][2] pages and moves that a unit needs; then those of the CTA's units before it
+  uint32_t* copies;  // [units] moves of a unit
+  uint32_t* before;  // [units][2] pages needed and moves of the CTA's units before
+  uint32_t* free;    // [pages / kTile] free pages
   int32_t* fresh;    // [items] the new pages, in order
 };
 
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArg
   PageRun run(0, KB > 0 ? padded : t.pages);
   uint32_t used = 0;
   if constexpr (KB > 0) {
-#pragma unroll 4
+#pragma unroll 8
     for (int p = tid; p < padded; p += kSmallThreads) refs[p] = p < t.pages ? t.refs[p] : 1;
   } else {
     used = run.count(t.refs, t.pages);
@@ -383,8 +384,10 @@ __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArg
 }
 
 // ---- any number of items and pages, on a cluster of CTAs.  A warp takes a unit of kUnit items, a row's or several rows', at
-// a time.  Each CTA has a stretch of units and one of pages, and tells the others how many pages its units need and how
-// many of its pages are free; then every item's new page is known.
+// a time, and a tile of kTile pages.  Each CTA has a stretch of units, and every ctas-th tile, so that the lowest free pages, which
+// are the ones that are taken, are everybody's; the CTAs tell each other how many pages their units need and how many of each
+// tile's are free, and then every item's new page is known.
+constexpr int kTile = 1024;
 constexpr int kUnit = 128;
 constexpr int kPer = kUnit / 32;  // items of a lane
 
@@ -458,6 +461,27 @@ struct Units {
   }
 };
 
+// A tile's free pages: a lane has the word of its own number.
+__device__ __forceinline__ uint32_t free_word(const int32_t* refs, int32_t tile, int32_t pages) {
+  const int lane = threadIdx.x & 31;
+  uint32_t kept = 0;
+#pragma unroll 1
+  for (int i = 0; i < 32; i += 8) {
+    int32_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int32_t p = tile * kTile + (i + k) * 32 + lane;
+      v[k] = p < pages ? __ldcg(refs + p) : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t bits = __ballot_sync(~0u, v[k] <= 0);
+      if (lane == i + k) kept = bits;
+    }
+  }
+  return kept;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
   __shared__ uint32_t part[kWarps];
   __shared__ Totals totals;
@@ -476,34 +500,53 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
   }
   const int32_t units = (int32_t)(((int64_t)a.items + kUnit - 1) / kUnit);
   const int32_t u_begin = (int32_t)min((int64_t)cta * a.units_per, (int64_t)units), u_end = (int32_t)min((int64_t)u_begin + a.units_per, (int64_t)units);
-  const int32_t p_begin = (int32_t)min((int64_t)cta * a.pages_per, (int64_t)t.pages), p_end = (int32_t)min((int64_t)p_begin + a.pages_per, (int64_t)t.pages);
+  const int32_t tiles = (t.pages + kTile - 1) / kTile, first_tile = (tid >> 5) * ctas + cta, tile_step = kWarps * ctas;
   Items it;
-  PageRun run(p_begin, p_end);
-  const uint32_t used = run.count(t.refs, p_end);
+  bool asked;
 
+  // ---- how many pages of each tile are free
+  uint32_t first_word = 0;  // of the warp's first tile
+  for (int32_t tile = first_tile; tile < tiles; tile += tile_step) {
+    const uint32_t word = free_word(t.refs, tile, t.pages), n = __reduce_add_sync(~0u, (uint32_t)__popc(word));
+    if (tile == first_tile) first_word = word;
+    if (lane == 0) a.free[tile] = n;
+  }
   // ---- what each item asks for.  Pages that others hold too are counted below
   int shared = 0;
-  bool asked;
   for (Units list(a, u_begin, u_end); list.next(it, asked);) {
     const int32_t unit = list.unit;
     uint32_t need = 0;
     if (asked) {
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const bool wrong = it.old[u] < -1 || it.old[u] >= t.pages;
-      if (wrong) atomicOr(t.status, ORPO_STATUS_PAGE);
-      if (it.old[u] >= 0 && !wrong && __ldcg(t.refs + it.old[u]) > 1) a.count[it.old[u]] = 0, a.last[it.old[u]] = -1, shared = 1;
-      const uint32_t bits = __ballot_sync(~0u, it.asks[u] && it.old[u] == -1);
-      if (lane == u) need = bits;
-    }
+      for (int u = 0; u < kPer; ++u) {
+        const bool wrong = it.old[u] < -1 || it.old[u] >= t.pages;
+        if (wrong) atomicOr(t.status, ORPO_STATUS_PAGE);
+        if (it.old[u] >= 0 && !wrong && __ldcg(t.refs + it.old[u]) > 1) a.count[it.old[u]] = 0, a.last[it.old[u]] = -1, shared = 1;
+        const uint32_t bits = __ballot_sync(~0u, it.asks[u] && it.old[u] == -1);
+        if (lane == u) need = bits;
+      }
     }
     if (lane < kPer && in_bounds(t.status, unit, units)) a.needs[unit * kPer + lane] = need;
-    need = __popc(need);
-#pragma unroll
-    for (int d = 1; d < kPer; d *= 2) need += __shfl_xor_sync(~0u, need, d);
-    if (lane == 0 && in_bounds(t.status, unit, units)) a.before[2 * unit] = need, a.before[2 * unit + 1] = 0;
+    if (lane == kPer && in_bounds(t.status, unit, units)) a.copies[unit] = 0;
   }
   shared = __syncthreads_or(shared);
+  // ---- sums over the CTA's units, told to the others
+  const auto sum_up = [&] {
+    uint32_t needed = 0, moved = 0;
+    for (int32_t u0 = u_begin; u0 < u_end; u0 += kPlanThreads) {
+      const int32_t unit = u0 + tid;
+      const bool mine = unit < u_end && in_bounds(t.status, unit, units);
+      uint32_t need = 0, all_need, all_moves;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) need += mine ? __popc(a.needs[unit * kPer + u]) : 0;
+      const uint32_t at_need = scan(need, part, all_need), at_move = scan(mine ? a.copies[unit] : 0, part, all_moves);
+      if (mine) a.before[2 * unit] = needed + at_need, a.before[2 * unit + 1] = moved + at_move;
+      needed += all_need;
+      moved += all_moves;
+    }
+    if (tid == 0) totals.v[1] = needed, totals.v[2] = moved;
+  };
+  sum_up();
   if (tid == 0) totals.v[0] = shared;
   plan_sync(ctas);
   uint32_t any;
@@ -525,7 +568,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
       for (Units list(a, u_begin, u_end); list.next(it, asked);) {
         if (!asked) continue;
         const int32_t unit = list.unit;
-        uint32_t moves = 0, need = 0;
+        uint32_t moves = 0;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
           bool copies = false;
@@ -534,48 +577,50 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(ReserveArgs a) {
             copies = held > 1 && !(__ldcg(a.count + it.old[u]) == held && __ldcg(a.last + it.old[u]) == unit * kUnit + u * 32 + lane);
           }
           const uint32_t bits = __ballot_sync(~0u, copies || (it.asks[u] && it.old[u] == -1));
-          need += __popc(bits);
           moves += __popc(__ballot_sync(~0u, copies && it.j[u] == 0 && it.w[u].fill > 0));
           if (lane == 0 && in_bounds(t.status, unit, units)) a.needs[unit * kPer + u] = bits;
         }
-        if (lane == 0 && in_bounds(t.status, unit, units)) a.before[2 * unit] = need, a.before[2 * unit + 1] = moves;
+        if (lane == 0 && in_bounds(t.status, unit, units)) a.copies[unit] = moves;
       }
+    __syncthreads();
+    sum_up();
+    plan_sync(ctas);
   }
-  __syncthreads();
-  // ---- sums over the CTA's units, and over its pages
-  uint32_t needed = 0, moved = 0, free = 0;
-  for (int32_t u0 = u_begin; u0 < u_end; u0 += kPlanThreads) {
-    const int32_t unit = u0 + tid;
-    const bool mine = unit < u_end && in_bounds(t.status, unit, units);
-    uint32_t all_need, all_moves;
-    const uint32_t need = scan(mine ? a.before[2 * unit] : 0, part, all_need), moves = scan(mine ? a.before[2 * unit + 1] : 0, part, all_moves);
-    if (mine) a.before[2 * unit] = needed + need, a.before[2 * unit + 1] = moved + moves;
-    needed += all_need;
-    moved += all_moves;
-  }
-  const uint32_t run_free = (uint32_t)min(max(p_end - run.begin, 0), run.words * 32) - used;
-  const uint32_t run_before = scan(lane == 0 ? run_free : 0, part, free);
-  if (tid == 0) totals.v[1] = needed, totals.v[2] = moved, totals.v[3] = free;
-  plan_sync(ctas);
-  uint32_t all_needed, all_moved, all_free;
+  uint32_t all_needed, all_moved;
   const uint32_t at_item = told_before(&totals, 1, cta, ctas, all_needed);
   const uint32_t at_move = told_before(&totals, 2, cta, ctas, all_moved);
-  const uint32_t at_free = told_before(&totals, 3, cta, ctas, all_free);
-  const bool full = all_free < all_needed;
+  // ---- the new pages, lowest first.  rank: free pages before the tile; then all of them
+  uint32_t rank = 0;
+  int32_t seen = 0;  // tiles counted in rank
+  const auto count_to = [&](int32_t tile) {
+    uint32_t mine = 0;
+    for (int32_t i = seen + lane; i < tile; i += 32) mine += __ldcg(a.free + i);
+    rank += __reduce_add_sync(~0u, mine);
+    seen = tile;
+  };
+  for (int32_t tile = first_tile; tile < tiles; tile += tile_step) {
+    count_to(tile);
+    if (rank >= all_needed) break;
+    const uint32_t word = tile == first_tile ? first_word : free_word(t.refs, tile, t.pages);
+    uint32_t start = __popc(word);  // free pages of the tile before the lane's word
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const uint32_t y = __shfl_up_sync(~0u, start, d);
+      if (lane >= d) start += y;
+    }
+    start -= __popc(word);
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t bits = __shfl_sync(~0u, word, i), at = rank + __shfl_sync(~0u, start, i) + __popc(bits & ((1u << lane) - 1u));
+      if (bits >> lane & 1u && at < all_needed && in_bounds(t.status, at, a.items)) a.fresh[at] = tile * kTile + i * 32 + lane;
+    }
+  }
+  if (rank < all_needed) count_to(tiles);
+  const bool full = rank < all_needed;  // the same for everybody: all tiles are counted, or enough of them
   if (tid == 0 && cta == 0) {
     *a.n_moves = full ? 0 : (int32_t)all_moved;
     if (full) atomicOr(t.status, ORPO_STATUS_FULL);
   }
-  // ---- the new pages, lowest first
-  uint32_t rank = at_free + __shfl_sync(~0u, run_before, 0);
-  if (!full)
-    for (int i = 0; i < run.words && rank < all_needed; ++i) {
-      const int32_t p = run.begin + i * 32 + lane;
-      const bool is_free = !(run.word(t.refs, p_end, i) >> lane & 1u) && p < p_end;
-      const uint32_t bits = __ballot_sync(~0u, is_free), at = rank + __popc(bits & ((1u << lane) - 1u));
-      if (is_free && at < all_needed && in_bounds(t.status, at, a.items)) a.fresh[at] = p;
-      rank += __popc(bits);
-    }
   plan_sync(ctas);  // the last look at another CTA's totals is behind
   if (full) return;
   for (Units list(a, u_begin, u_end); list.next(it, asked);) {
@@ -843,7 +888,8 @@ int64_t padded_width(int64_t width) {
 }
 size_t reserve_bytes(int64_t batch, int64_t pages, int64_t rows, int64_t width) {
   const int64_t units = cdiv(rows * padded_width(width), kUnit);
-  return align16(batch * 4) + 2 * align16(pages * 4) + align16(units * kPer * 4) + align16(units * 8) + align16(std::min(pages, rows * width) * 4);
+  return align16(batch * 4) + 2 * align16(pages * 4) + align16(units * kPer * 4) + align16(units * 4) + align16(units * 8) +
+         align16(cdiv(pages, kTile) * 4) + align16(std::min(pages, rows * width) * 4);
 }
 size_t compact_bytes(int64_t pages) { return align16(pages / 2 * 4) + 2 * align16(pages * 4); }
 
@@ -948,12 +994,13 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
     const int64_t units = cdiv(a.items, kUnit);
     const int ctas = a.items > 0 ? plan_ctas(units, pages) : 1;
     a.units_per = share(units, ctas, 1);
-    a.pages_per = share(pages, ctas, 32 * kWarps);
     a.count = reinterpret_cast<int32_t*>(ws += align16(batch * 4));
     a.last = reinterpret_cast<int32_t*>(ws += align16(pages * 4));
     a.needs = reinterpret_cast<uint32_t*>(ws += align16(pages * 4));
-    a.before = reinterpret_cast<uint32_t*>(ws += align16(units * kPer * 4));
-    a.fresh = reinterpret_cast<int32_t*>(ws += align16(units * 8));
+    a.copies = reinterpret_cast<uint32_t*>(ws += align16(units * kPer * 4));
+    a.before = reinterpret_cast<uint32_t*>(ws += align16(units * 4));
+    a.free = reinterpret_cast<uint32_t*>(ws += align16(units * 8));
+    a.fresh = reinterpret_cast<int32_t*>(ws += align16(cdiv(pages, kTile) * 4));
     e = launch_cluster_dependent(reserve_kernel, ctas, kPlanThreads, 0, st, a);
   }
   prof_end(K_PAGES, st);
