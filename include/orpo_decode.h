@@ -132,7 +132,8 @@ int orpo_beam_reorder(void* state, const int32_t* parent, int64_t ld_parent, con
  * History tokens outside [0, V) (padding) count nowhere, nor do bias tokens outside it.
  *   logits   fp32 or bf16 [batch * beams, V], rows ld_logits >= V elements apart
  *   history  int32 [batch * beams, capacity], rows ld_history >= capacity apart; length, prompt: int32 [batch].  history may be
- *            NULL where repetition = 1, presence = frequency = 0 and no_repeat = 0 (it is not read then); prompt may be NULL
+ *            NULL where repetition = 1, presence = frequency = 0 and no_repeat = 0, or capacity = 0 (it is not read then);
+ *            prompt may be NULL
  *   bias_token, bias_value  int32, fp32 [batch, n_bias], rows ld_bias apart: 0 (one list for all) or >= n_bias
  *   masks    uint32 [n_masks, ceil(V / 32)], rows ld_masks apart, 1 = allowed; mask_row: int32 [batch * beams], -1 for a row
  *            without a mask.  Both NULL: no masks.

@@ -921,7 +921,7 @@ class PagedStates:
 
     def _copy(self, pools, stream):
         for pool in pools:
-            if pool.shape[1] != self.pages or pool.shape[3] != self.page:
+            if pool.dim() != 5 or pool.shape[1] != self.pages or pool.shape[3] != self.page:
                 raise ValueError(f"a pool has shape {tuple(pool.shape)}, expected [outer, {self.pages}, rows, {self.page}, unit]")
             orpo_pages_copy(pool, self.moves, self.n_moves, self.status, stream)
 

@@ -471,7 +471,7 @@ extern "C" int orpo_logits_adjust(void* logits, int64_t ld_logits, int logits_bf
   if (!std::isfinite(repetition) || repetition <= 0.f || !std::isfinite(presence) || !std::isfinite(frequency) ||
       no_repeat < 0 || no_repeat > ORPO_MAX_NGRAM)
     return ORPO_ERR_ARG;
-  const bool reads = repetition != 1.f || presence != 0.f || frequency != 0.f || no_repeat > 0;
+  const bool reads = capacity > 0 && (repetition != 1.f || presence != 0.f || frequency != 0.f || no_repeat > 0);
   if (reads && history && ld_history < capacity) return ORPO_ERR_SHAPE;
   if (n_bias > 0 && ld_bias != 0 && ld_bias < n_bias) return ORPO_ERR_SHAPE;
   if (masks && (n_masks < 1 || n_masks >= (1ll << 31) || ld_masks < cdiv(V, 32))) return ORPO_ERR_SHAPE;

@@ -297,3 +297,14 @@ def test_rows_past_2_31_elements():
     want[:, [0, 5, 262143, 9]] = 1.0
     want[1:, 96:128] = -math.inf
     assert int(st.item()) == 0 and torch.equal(x[-3:], want) and not bool(x[:-3].any())
+
+
+def test_empty_histories_lists_and_batches():
+    st, x = status_tensor(), torch.ones((2, 40), device=dev())
+    none = torch.empty((2, 0), dtype=torch.int32, device=dev())
+    orpo.orpo_logits_adjust(x, 1, st, none, t32([0, 0]), repetition=2.0, no_repeat=2)
+    orpo.orpo_logits_adjust(x, 2, st, torch.zeros((2, 5), dtype=torch.int32, device=dev()), t32([0]), repetition=2.0, no_repeat=1)
+    orpo.orpo_logits_adjust(x, 1, st, bias_token=none, bias_value=none.float())
+    orpo.orpo_logits_adjust(x[:0], 3, st, none[:0], t32([]), repetition=2.0)
+    orpo.orpo_logits_adjust(x, 2, st)
+    assert bool((x == 1).all()) and int(st.item()) == 0

@@ -195,6 +195,8 @@ def test_what_a_step_needs_is_asked_for(weights):
     pages = orpo.PagedStates(1, 2, 4, 10, 4, device=dev())
     with pytest.raises(ValueError, match="pool"):
         pages.compact((torch.zeros((1, 9, 1, 4, 8), device=dev()),))
+    with pytest.raises(ValueError, match="pool"):
+        pages.advance(t32([0]), pools=(torch.zeros((10, 4, 8), device=dev()),))
     with pytest.raises(ValueError, match="ended"):
         pages.release(torch.zeros(2, dtype=torch.uint8, device=dev()))
     with pytest.raises(ValueError, match="range"):

@@ -32,6 +32,7 @@ def test_adjust_host_checks(lib):
     bias = dict(bt=FAKE, bv=FAKE, nb=5)
     assert call(batch=0) == OK
     assert call(rep=1.0, h=None, length=None) == OK  # nothing to do
+    assert call(h=None, length=None, cap=0) == OK
     for bad in (dict(batch=-1), dict(batch=(1 << 20) + 1), dict(beams=0), dict(beams=(1 << 20) + 1), dict(batch=1 << 18, beams=8), dict(V=0),
                 dict(V=MAX_ROWS + 1, ld=MAX_ROWS + 1), dict(ld=999), dict(cap=-1), dict(cap=1 << 28, ld_h=1 << 28), dict(ld_h=63),
                 {**bias, "nb": -1}, {**bias, "nb": 4097}, {**bias, "ld_b": 4}, {**mask, "nm": 0}, {**mask, "nm": 1 << 31},
