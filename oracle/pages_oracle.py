@@ -5,6 +5,7 @@ Written from the definitions alone, one token, row and page at a time; shares no
 
 from __future__ import annotations
 
+import collections
 import math
 
 import numpy as np
@@ -117,7 +118,7 @@ def pages_advance(table, refs, page, parent, length, more, most):
                         refs[now] += 1
                     if was >= 0:
                         refs[was] -= 1
-    free = [p for p in range(len(refs)) if refs[p] == 0]
+    free = collections.deque(p for p in range(len(refs)) if refs[p] == 0)
     before = table.copy(), refs.copy()
     moves = []
     for r in range(table.shape[0]):
@@ -129,7 +130,7 @@ def pages_advance(table, refs, page, parent, length, more, most):
                 continue
             if not free:
                 return (*before, [], True)
-            p = free.pop(0)
+            p = free.popleft()
             if e >= 0:
                 refs[e] -= 1
                 if c * page < n:

@@ -228,33 +228,40 @@ __device__ __forceinline__ Wanted wanted_columns(const TableArgs& a, uint32_t b)
 // ---- a decode step's worth: up to kSmallItems items, in one CTA.
 // KB: a fork of up to KB beams is done here too, for (entry, column) pairs of at most one per thread; the counts of holders are
 // then in shared memory, where what the fork changes can be looked up at once.  0: no fork here, and the counts stay
-// where they are.
+// where they are.  kQ: items per thread, one after the other.
 constexpr int kSmallThreads = 1024;
-constexpr int kSmallItems = kSmallThreads;
+constexpr int kSmallMost = 4;               // items per thread at most
+constexpr int kSmallItems = kSmallMost * kSmallThreads;
 // In turns, 128 x 256 pairs took 14.5 us here, by a kernel of their own and a plan without a fork 8.3.  Up to one turn it is a
-// launch less: with the copy 14.0 us to enqueue, else 15.9.
+// launch less: with the copy 6.0 us to enqueue, else 7.6.
 constexpr int kForkHere = kSmallThreads;    // pairs
 constexpr int kForkPages = 32768;           // 128 KB of counts
-constexpr int kSlots = 2 * kSmallItems;     // of the table of pages that several items hold
 inline int32_t padded_pages(int64_t pages) { return (int32_t)(cdiv(pages, 32 * kWarps) * 32 * kWarps); }
 
-template <int KB>
+// Pages that several items hold, in shared memory: twice as many slots as items.
+template <int kItems>
+struct SmallTables {
+  int32_t keys[2 * kItems], count[2 * kItems], last[2 * kItems];  // page, how many items, and the last of them
+  int32_t fresh[kItems];                                           // the new pages
+  uint8_t bad[kItems];                                             // entries
+};
+
+template <int KB, int kQ>
 __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArgs a, int32_t padded) {
-  extern __shared__ __align__(16) int32_t refs[];  // KB > 0: [padded] counts of holders
-  __shared__ int32_t keys[kSlots], count[kSlots], last[kSlots];  // pages that several items hold: how many, and the last
+  constexpr int kItems = kQ * kSmallThreads;
+  constexpr uint32_t kSlots = 2 * kItems;
+  extern __shared__ __align__(16) uint8_t small_raw[];
+  SmallTables<kItems>& s = *reinterpret_cast<SmallTables<kItems>*>(small_raw);
+  int32_t* const refs = reinterpret_cast<int32_t*>(small_raw + sizeof(SmallTables<kItems>));  // KB > 0: [padded] counts of holders
   __shared__ uint32_t part[kWarps];
-  __shared__ int32_t fresh[kSmallItems];
-  __shared__ uint8_t bad[kSmallItems];
   const TableArgs& t = a.t;
   const int tid = threadIdx.x, lane = tid & 31;
   grid_trigger();
-  bad[tid] = 0;
-  for (int i = tid; i < kSlots; i += kSmallThreads) keys[i] = -1, count[i] = 0, last[i] = -1;
+  for (int i = tid; i < kItems; i += kSmallThreads) s.bad[i] = 0;
+  for (int i = tid; i < (int)kSlots; i += kSmallThreads) s.keys[i] = -1, s.count[i] = 0, s.last[i] = -1;
   __syncthreads();
   grid_wait();
   const int rows = (int)t.batch * t.beams;
-  const uint32_t row = (uint32_t)tid / (uint32_t)a.width, j = (uint32_t)tid - row * (uint32_t)a.width;
-  const uint32_t b = row / (uint32_t)t.beams;
   // ---- counts, lengths, parents
   PageRun run(0, KB > 0 ? padded : t.pages);
   uint32_t used = 0;
@@ -264,35 +271,50 @@ __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArg
   } else {
     used = run.count(t.refs, t.pages);
   }
-  if (tid < rows) {
-    const int e = tid / t.beams;
+  for (int r = tid; r < rows; r += kSmallThreads) {
+    const int e = r / t.beams;
     int64_t begin, end;
     bool wrong = !wanted(t, e, begin, end);
     if constexpr (KB > 0) {
-      const int p = t.parent[e * t.ld_parent + tid - e * t.beams];
+      const int p = t.parent[e * t.ld_parent + r - e * t.beams];
       wrong |= p < 0 || p >= t.beams;
     } else if (a.left_alone) {
       wrong |= a.left_alone[e] != 0;
     }
     if (wrong) {
-      bad[e] = 1;
+      if (in_bounds(t.status, e, kItems)) s.bad[e] = 1;
       atomicOr(t.status, ORPO_STATUS_PARENT);
     }
   }
-  const bool item = tid < a.items;
-  const Wanted w = item ? wanted_columns(t, b) : Wanted{0, 0, 0};
-  int32_t from = (int32_t)row;
-  if constexpr (KB > 0)
-    if (item && w.fill > 0 && j == 0) from = (int32_t)(b * t.beams) + t.parent[b * t.ld_parent + row - b * t.beams];
+  Wanted w[kQ];
+  uint32_t row[kQ], j[kQ];
+  int32_t from[kQ];
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    const uint32_t i = (uint32_t)tid * kQ + q;
+    row[q] = i / (uint32_t)a.width;
+    j[q] = i - row[q] * (uint32_t)a.width;
+    w[q] = i < (uint32_t)a.items ? wanted_columns(t, row[q] / (uint32_t)t.beams) : Wanted{0, 0, 0};
+    from[q] = (int32_t)row[q];
+    if constexpr (KB > 0) {
+      const uint32_t b = row[q] / (uint32_t)t.beams;
+      if (w[q].fill > 0 && j[q] == 0) from[q] = (int32_t)(b * t.beams) + t.parent[b * t.ld_parent + row[q] - b * t.beams];
+    }
+  }
   __syncthreads();
   // ---- the table: each item's page after the fork, and the columns to fork
-  const bool asks = item && j < w.n && !bad[b];
-  int32_t* const entry = t.table + row * t.ld + w.first + j;
-  int32_t old = -1, held = 0;
-  if (asks && in_bounds(t.status, from, rows) && in_bounds(t.status, w.first + j, t.columns)) old = t.table[from * t.ld + w.first + j];
+  int32_t old[kQ];
+  bool asks[kQ];
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    asks[q] = j[q] < w[q].n && !s.bad[row[q] / (uint32_t)t.beams];
+    old[q] = -1;
+    if (asks[q] && in_bounds(t.status, from[q], rows) && in_bounds(t.status, w[q].first + j[q], t.columns))
+      old[q] = t.table[from[q] * t.ld + w[q].first + j[q]];
+  }
   if constexpr (KB > 0) {
     const uint32_t columns = (uint32_t)t.columns, e = columns > 0 ? (uint32_t)tid / columns : 0, c = (uint32_t)tid - e * columns;
-    const bool on = e < (uint32_t)t.batch && columns > 0 && !bad[e] && (int64_t)c * t.page < t.length[e];
+    const bool on = e < (uint32_t)t.batch && columns > 0 && !s.bad[e] && (int64_t)c * t.page < t.length[e];
     const int64_t b0 = (int64_t)e * t.beams * t.ld, all = t.batch * t.beams * t.ld;
     int32_t* const column = t.table + b0 + c;
     int par[KB];
@@ -316,37 +338,41 @@ __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArg
       }
     __syncthreads();
   }
-  // ---- what the item asks for; of the items that hold a page together the last keeps it, where nothing else holds it
-  int what = kNone;
-  if (asks) {
-    if (old < -1 || old >= t.pages) {
-      atomicOr(t.status, ORPO_STATUS_PAGE);
-    } else if (old < 0) {
-      what = kNeed;
-    } else {
-      held = KB > 0 ? refs[old] : __ldcg(t.refs + old);
-      if (held > 1) what = kShared;
-    }
+  // ---- what the items ask for; of the items that hold a page together the last keeps it, where nothing else holds it
+  int what[kQ];
+  int32_t held[kQ];
+  bool shared = false;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    const bool is = asks[q] && is_page(t, old[q]);
+    if (asks[q] && (old[q] < -1 || old[q] >= t.pages)) atomicOr(t.status, ORPO_STATUS_PAGE);
+    held[q] = is ? (KB > 0 ? refs[old[q]] : __ldcg(t.refs + old[q])) : 0;
+    what[q] = asks[q] && old[q] == -1 ? kNeed : held[q] > 1 ? kShared : kNone;
+    shared |= what[q] == kShared;
   }
-  if (__syncthreads_or(what == kShared)) {
-    uint32_t s = 0;
-    if (what == kShared) {
-      s = (uint32_t)old * 2654435769u / (0xffffffffu / kSlots + 1u);
-      for (;;) {  // twice as many slots as items: an empty one is always met
-        const int32_t key = atomicCAS(keys + s, -1, old);
-        if (key == -1 || key == old) break;
-        s = (s + 1) % kSlots;
+  if (__syncthreads_or(shared)) {
+    uint32_t slot[kQ];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      if (what[q] != kShared) continue;
+      slot[q] = (uint32_t)old[q] * 2654435769u / (0xffffffffu / kSlots + 1u);
+      for (;;) {  // an empty slot is always met
+        const int32_t key = atomicCAS(s.keys + slot[q], -1, old[q]);
+        if (key == -1 || key == old[q]) break;
+        slot[q] = (slot[q] + 1) % kSlots;
       }
-      atomicAdd(count + s, 1);
-      atomicMax(last + s, tid);
+      atomicAdd(s.count + slot[q], 1);
+      atomicMax(s.last + slot[q], tid * kQ + q);
     }
     __syncthreads();
-    if (what == kShared && count[s] == held && last[s] == tid) what = kNone;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+      if (what[q] == kShared && s.count[slot[q]] == held[q] && s.last[slot[q]] == tid * kQ + q) what[q] = kNone;
   }
-  const bool move = what == kShared && j == 0 && w.fill > 0;
-  uint32_t total;
-  const uint32_t at = scan((uint32_t)(what != kNone) | (uint32_t)move << 16, part, total);
-  const uint32_t needed = total & 0xffff;
+  uint32_t mine = 0, total;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) mine += (uint32_t)(what[q] != kNone) | (uint32_t)(what[q] == kShared && j[q] == 0 && w[q].fill > 0) << 16;
+  const uint32_t before = scan(mine, part, total), needed = total & 0xffff;
   // ---- free pages, lowest first
   if constexpr (KB > 0)
     for (int i = 0; i < run.words; ++i) used += __popc(__ballot_sync(~0u, refs[run.begin + i * 32 + lane] > 0));
@@ -365,21 +391,24 @@ __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArg
     const int32_t p = run.begin + i * 32 + lane;
     const uint32_t taken = KB > 0 ? __ballot_sync(~0u, refs[p] > 0) : run.word(t.refs, t.pages, i);
     const uint32_t bits = __ballot_sync(~0u, !(taken >> lane & 1u) && p < t.pages), to = rank + __popc(bits & ((1u << lane) - 1u));
-    if (bits >> lane & 1u && to < needed && in_bounds(t.status, to, kSmallItems)) fresh[to] = p;
+    if (bits >> lane & 1u && to < needed && in_bounds(t.status, to, kItems)) s.fresh[to] = p;
     rank += __popc(bits);
   }
   __syncthreads();
   if (tid == 0) *a.n_moves = (int32_t)(total >> 16);
-  if (what == kNone) return;
-  const int32_t p = fresh[at & 0xffff];
-  *entry = p;
-  t.refs[p] = 1;
-  if (what == kShared) atomicSub(t.refs + old, 1);
-  const uint32_t m = at >> 16;
-  if (move && in_bounds(t.status, m, rows)) {
-    a.moves[3 * m] = old;
+  uint32_t at = before & 0xffff, m = before >> 16;
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) {
+    if (what[q] == kNone) continue;
+    const int32_t p = s.fresh[at++];
+    t.table[row[q] * t.ld + w[q].first + j[q]] = p;
+    t.refs[p] = 1;
+    if (what[q] != kShared) continue;
+    atomicSub(t.refs + old[q], 1);
+    if (j[q] != 0 || w[q].fill == 0 || !in_bounds(t.status, m, rows)) continue;
+    a.moves[3 * m] = old[q];
     a.moves[3 * m + 1] = p;
-    a.moves[3 * m + 2] = (int32_t)w.fill;
+    a.moves[3 * m++ + 2] = (int32_t)w[q].fill;
   }
 }
 
@@ -902,16 +931,19 @@ int32_t share(int64_t n, int ctas, int tile) { return (int32_t)(cdiv(cdiv(n, cta
 // kernel of their own 14.0, but that one is 2 us more to enqueue; at 33024 7.5 here.
 constexpr int64_t kRemapHere = 8192;
 // Pages whose counts one CTA looks through for a decode step: 512 rows in 16385 pages take 7 us in one CTA and 15 on a cluster, in
-// 100000 14 and 17; one CTA takes 0.09 us per 1000 pages more, the cluster 0.01.
+// 100000 13 and 17; one CTA takes 0.08 us per 1000 pages more, the cluster 0.01.  (Items: 1025 take 12 us in one CTA and 27 on a
+// cluster, 4096 19 and 27.)
 constexpr int64_t kSmallPages = 131072;
 
-template <int KB>
+template <int KB, int kQ>
 cudaError_t launch_small(const ReserveArgs& a, cudaStream_t st) {
   static std::atomic<int> done[64];
-  const cudaError_t e = opt_in_smem(small_reserve_kernel<KB>, kForkPages * 4, done);
+  constexpr int kTables = (int)sizeof(SmallTables<kQ * kSmallThreads>);
+  static_assert(kTables % 16 == 0 && kTables + kForkPages * 4 <= 227 << 10 || KB == 0, "a CTA's shared memory");
+  const cudaError_t e = opt_in_smem(small_reserve_kernel<KB, kQ>, kTables + (KB > 0 ? kForkPages * 4 : 0), done);
   if (e != cudaSuccess) return e;
   const int32_t padded = KB > 0 ? padded_pages(a.t.pages) : 0;
-  return launch_dependent(small_reserve_kernel<KB>, dim3(1), kSmallThreads, (size_t)padded * 4, st, a, padded);
+  return launch_dependent(small_reserve_kernel<KB, kQ>, dim3(1), kSmallThreads, (size_t)kTables + (size_t)padded * 4, st, a, padded);
 }
 
 bool misaligned(std::initializer_list<const void*> p) {
@@ -974,7 +1006,7 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
   cudaError_t e = cudaSuccess;
   prof_begin(K_PAGES, st);
   const bool small = rows * width > 0 && rows * width <= kSmallItems && pages <= kSmallPages;
-  const bool fork_there = fork && small && beams <= 8 && batch * columns <= kForkHere && pages <= kForkPages;
+  const bool fork_there = fork && small && beams <= 8 && rows * width <= kSmallThreads && batch * columns <= kForkHere && pages <= kForkPages;
   if (fork && !fork_there) {
     a.left_alone = reinterpret_cast<int32_t*>(ws);
     const dim3 grid((unsigned)batch, (unsigned)std::max<int64_t>(1, std::min<int64_t>(65535, cdiv(columns, kForkThreads))));
@@ -987,7 +1019,10 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
   if (e == cudaSuccess && small) {
     a.width = (int32_t)width;
     a.items = (int32_t)(rows * width);
-    e = !fork_there ? launch_small<0>(a, st) : beams <= 4 ? launch_small<4>(a, st) : launch_small<8>(a, st);
+    e = a.items > kSmallThreads ? launch_small<0, kSmallMost>(a, st)
+        : !fork_there           ? launch_small<0, 1>(a, st)
+        : beams <= 4            ? launch_small<4, 1>(a, st)
+                                : launch_small<8, 1>(a, st);
   } else if (e == cudaSuccess) {
     a.width = (int32_t)padded_width(width);
     a.items = width > 0 ? (int32_t)(rows * a.width) : 0;

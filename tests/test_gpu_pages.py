@@ -69,7 +69,7 @@ def beams_table(rng, batch, beams, columns, pages, page, lengths, shared=0.5):
 
 @pytest.mark.parametrize("batch,beams,page,longest", [(1, 1, 1, 9), (1, 4, 16, 100), (3, 4, 5, 60), (2, 8, 16, 2500), (4, 9, 7, 80), (1, 17, 3, 40),
                                                       (1, 64, 4, 50), (70, 16, 8, 30), (1, 4, 1, 5000), (2, 6, 1, 2200)])
-@pytest.mark.parametrize("more_pages", [0, 20000])
+@pytest.mark.parametrize("more_pages", [0, 33000, 140000])
 def test_decode_steps_against_the_oracle(batch, beams, page, longest, more_pages):
     """Several steps in a row, with new parents each and one more position each, in small and in large pools."""
     rng = np.random.default_rng(batch + beams + page)
@@ -92,7 +92,7 @@ def test_decode_steps_against_the_oracle(batch, beams, page, longest, more_pages
         lengths = lengths + 1
 
 
-@pytest.mark.parametrize("batch,beams,page,most", [(1, 1, 16, 100), (5, 1, 4, 33), (3, 4, 7, 20), (40, 1, 3, 200), (1, 1, 1, 5000), (300, 2, 16, 90)])
+@pytest.mark.parametrize("batch,beams,page,most", [(1, 1, 16, 100), (5, 1, 4, 33), (3, 4, 7, 20), (40, 1, 3, 200), (1, 1, 1, 5000), (300, 2, 16, 90), (150, 2, 16, 90), (4096, 1, 8, 1), (4097, 1, 8, 1)])
 def test_prompts_against_the_oracle(batch, beams, page, most):
     """Different numbers of new positions, none among them, on rows that have pages or none, and pages asked for before."""
     rng = np.random.default_rng(most)
@@ -112,13 +112,15 @@ def test_prompts_against_the_oracle(batch, beams, page, most):
         assert not full and int(p.status.item()) == 0
 
 
-def test_pages_shared_between_entries_and_within_the_written_range():
+@pytest.mark.parametrize("times,pages", [(1, 40), (1, 140000), (300, 40000), (1100, 40000)])
+def test_pages_shared_between_entries_and_within_the_written_range(times, pages):
     """Rows of different entries that hold the same pages: all but the last, and all where something else holds it too, copy."""
-    table = np.array([[0, 1, 2, -1], [0, 1, 2, -1], [0, 1, 2, -1], [3, 2, 1, -1], [2, 2, 2, -1]], dtype=np.int32)
+    table = np.array([[0, 1, 2, -1], [0, 1, 2, -1], [0, 1, 2, -1], [3, 2, 1, -1], [2, 2, 2, -1]] * times, dtype=np.int32)
     for lengths, more in (([5, 6, 9, 4, 12], None), ([2, 2, 2, 0, 12], [10, 10, 10, 12, 1]), ([12] * 5, [4] * 5), ([0] * 5, [12] * 5)):
-        p = Pages(table, 40, 4, most=12)
-        want = oracle.pages_advance(table, oracle.holders(table, 40), 4, None, lengths, more, 12 if more else 1)
-        same(p.advance(None, lengths, more, 12 if more else 1), want[:3])
+        lengths, more, most = lengths * times, more and more * times, 12 if more else 1
+        p = Pages(table, pages, 4, most=most)
+        want = oracle.pages_advance(table, oracle.holders(table, pages), 4, None, lengths, more, most)
+        same(p.advance(None, lengths, more, most), want[:3])
         assert not want[3] and int(p.status.item()) == 0
 
 
@@ -147,7 +149,7 @@ def test_too_few_pages_change_nothing_but_the_fork():
     assert got[0].tolist() == [[0, 2, 3], [0, 1, 4]] and int(p.status.item()) == 0
 
 
-@pytest.mark.parametrize("rows,columns", [(3, 5461), (1200, 25), (1200, 4), (1000, 6)])
+@pytest.mark.parametrize("rows,columns", [(3, 5461), (1200, 25), (1200, 4), (1000, 6), (5000, 2), (5, 30000)])
 def test_too_few_pages_of_a_large_pool(rows, columns):
     """One page fewer than rows is free; it is enough for all but one."""
     held = rows * columns
@@ -168,7 +170,7 @@ def test_too_few_pages_of_a_large_pool(rows, columns):
     assert int(p.status.item()) == 0 and not want[3]
 
 
-@pytest.mark.parametrize("columns,pages", [(5000, 6000), (3, 20000), (5000, 20000)])
+@pytest.mark.parametrize("columns,pages", [(5000, 6000), (3, 20000), (3, 140000), (5000, 140000)])
 def test_wrong_entries_beside_right_ones_in_every_form(columns, pages):
     table = np.full((8, columns), -1, dtype=np.int32)
     table[:, :2] = np.arange(16).reshape(8, 2)
