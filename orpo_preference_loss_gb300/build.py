@@ -32,8 +32,6 @@ LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 DEBUG_OUT_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(DEBUG_OUT_DIR, "liborpo_head_debug.so")
 
-BINDING_NAME = "orpo_binding.so"
-
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-O2", "-Xptxas", "-v"]
@@ -47,7 +45,10 @@ def nvcc_path() -> str:
 
 
 def binding_path(debug: bool = False) -> str:
-    return os.path.join(DEBUG_OUT_DIR if debug else OUT_DIR, BINDING_NAME)
+    """The Python module, named for the PyTorch and Python that it is compiled against: it fits no other."""
+    import torch
+
+    return os.path.join(DEBUG_OUT_DIR if debug else OUT_DIR, f"orpo_binding-{torch.__version__}-{sys.implementation.cache_tag}.so")
 
 
 def _binding_command(out: str):
