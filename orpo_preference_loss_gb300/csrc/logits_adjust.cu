@@ -5,7 +5,8 @@
 //   + the token's biases;  -inf where a mask or an n-gram bans it
 //
 // Only the logits that one of these concerns are read or written, so the work is the history's length and the masked
-// logits, not the vocabulary.  Two kinds of CTAs share a launch; they never write the same logit, so they need no order:
+// logits, not the vocabulary.  Two kinds of CTAs share a launch; they never write the same logit, but for the -inf of a token that
+// a mask and an n-gram both ban, so they need no order:
 //   history CTAs   adjust the tokens that the history and the bias list hold, unless a mask bans them.
 //     By bits: without a frequency penalty it is enough to know which tokens there are: one CTA per row, with a bit per token
 //     of the vocabulary in shared memory, where masked tokens are set from the start.  Who sets a token's bit adjusts its
