@@ -590,12 +590,10 @@ def _now():
     return torch.cuda.current_device() if _raw_device is None else _raw_device()
 
 
-def _where(stream):
-    """(the current device's number, the stream's handle), as csrc/binding.cpp takes them."""
-    if _raw_device is None or _raw_stream is None or stream is not None:
-        return _now(), (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-    now = _raw_device()
-    return now, _raw_stream(now)
+def _bound():
+    """The module of csrc/binding.cpp, once the library is loaded."""
+    load()
+    return _fast
 
 
 def _here(first, *others):
@@ -622,12 +620,8 @@ def orpo_logits_adjust(logits, beams, status, history=None, length=None, prompt=
     history: int32 [batch * beams, capacity], of which the first length[b] (int32 [batch]) are tokens of the row, the first
     prompt[b] of those (None: 0) the prompt's.  bias_token, bias_value: int32, fp32 [batch, n], or [n] for every entry.  masks:
     int32 or uint32 [n_masks, ceil(V / 32)], bit set = allowed; mask_row: int32 [batch * beams], -1 for a row without a mask."""
-    code = -1
-    if logits.is_cuda:
-        if _fast is None:
-            load()
-        code = _fast.adjust(*_where(stream), logits, beams, status, history, length, prompt, repetition, presence, frequency, no_repeat,
-                            bias_token, bias_value, masks, mask_row)
+    code = (_fast or _bound()).adjust(stream, logits, beams, status, history, length, prompt, repetition, presence, frequency, no_repeat,
+                                      bias_token, bias_value, masks, mask_row)
     if code < 0:
         code = _adjust(logits, beams, status, history, length, prompt, repetition, presence, frequency, no_repeat, bias_token,
                        bias_value, masks, mask_row, stream)
@@ -675,11 +669,7 @@ def _adjust(logits, beams, status, history, length, prompt, repetition, presence
 def orpo_beam_history(history, parent, token, length, status, stream=None):
     """Token histories [batch * beams, capacity] (int32) follow parent [batch, beams] in place, up to length[b], where
     token [batch, beams] is then put.  length is not changed."""
-    code = -1
-    if history.is_cuda:
-        if _fast is None:
-            load()
-        code = _fast.history(*_where(stream), history, parent, token, length, status)
+    code = (_fast or _bound()).history(stream, history, parent, token, length, status)
     if code < 0:
         batch, beams = parent.shape
         _here(history, parent, token, length, status)
@@ -714,11 +704,7 @@ def orpo_pages_advance(table, refs, page, parent, length, more, most, moves, n_m
 
     Pages are taken and let go of in refs (int32 [pages]); pages to be copied are listed in moves (int32 [max_moves, 3], n_moves
     int32 [1]) for orpo_pages_copy.  workspace: uint8, orpo_pages_workspace_bytes(batch * beams, pages, page, most)."""
-    code = -1
-    if table.is_cuda:
-        if _fast is None:
-            load()
-        code = _fast.advance(*_where(stream), table, refs, page, parent, length, more, most, moves, n_moves, workspace, status)
+    code = (_fast or _bound()).advance(stream, table, refs, page, parent, length, more, most, moves, n_moves, workspace, status)
     if code < 0:
         rows, columns = table.shape
         batch = length.shape[0]
@@ -742,11 +728,7 @@ def orpo_pages_advance(table, refs, page, parent, length, more, most, moves, n_m
 
 def orpo_pages_copy(pool, moves, n_moves, status, stream=None):
     """Carries out the copies of moves in pool [outer, pages, rows, page, unit] (any dtype)."""
-    code = -1
-    if pool.is_cuda:
-        if _fast is None:
-            load()
-        code = _fast.copy(*_where(stream), pool, moves, n_moves, status)
+    code = (_fast or _bound()).copy(stream, pool, moves, n_moves, status)
     if code < 0:
         _here(pool, moves, n_moves, status)
         if not pool.is_contiguous() or pool.dim() != 5:
@@ -761,11 +743,7 @@ def orpo_pages_copy(pool, moves, n_moves, status, stream=None):
 
 def orpo_pages_release(table, refs, ended, status, stream=None):
     """The rows of entries with ended[b] != 0 (uint8 or bool [batch]; None: all rows) let go of their pages."""
-    code = -1
-    if table.is_cuda:
-        if _fast is None:
-            load()
-        code = _fast.release(*_where(stream), table, refs, ended, status)
+    code = (_fast or _bound()).release(stream, table, refs, ended, status)
     if code < 0:
         rows, columns = table.shape
         batch = rows if ended is None else ended.shape[0]
@@ -788,11 +766,7 @@ def orpo_pages_compact(table, refs, page, new_table, new_refs, live, moves, n_mo
     """Numbers the pages in use 0 .. live[0] - 1: those at live[0] or above take the free numbers below, in order.
 
     new_table and new_refs may be table and refs themselves; moves (at least pages / 2 of them) are for orpo_pages_copy."""
-    code = -1
-    if table.is_cuda:
-        if _fast is None:
-            load()
-        code = _fast.compact(*_where(stream), table, refs, page, new_table, new_refs, live, moves, n_moves, workspace, status)
+    code = (_fast or _bound()).compact(stream, table, refs, page, new_table, new_refs, live, moves, n_moves, workspace, status)
     if code < 0:
         rows, columns = table.shape
         _here(table, refs, new_table, new_refs, live, moves, n_moves, workspace, status)

@@ -57,9 +57,9 @@ def _binding_command(out: str):
 
     home = os.path.dirname(torch.__file__)
     return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"],
-            "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-I", os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"), "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", os.path.join(CSRC, "binding.cpp"), "-o", out,
-            "-L", os.path.join(home, "lib"), f"-Wl,-rpath,{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            "-L", os.path.join(home, "lib"), f"-Wl,-rpath,{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def _sources():

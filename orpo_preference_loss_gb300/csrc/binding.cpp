@@ -6,6 +6,8 @@
 // one for a message (or, where they are right all the same, calls through ctypes).  The entry points' addresses are
 // handed in by bind(), so this module belongs to whichever library is loaded.
 #include <Python.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -43,7 +45,17 @@ struct Args {
     if (v == -1.0 && PyErr_Occurred()) PyErr_Clear(), ok = false;
     return (float)v;
   }
-  void* handle() { return reinterpret_cast<void*>((uintptr_t)whole()); }
+  // A torch.cuda.Stream, or None for the current one; and which device is current.
+  void* stream() {
+    PyObject* const o = next();
+    device = c10::cuda::current_device();
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
+    PyObject* const handle = PyObject_GetAttrString(o, "cuda_stream");
+    void* const s = handle ? PyLong_AsVoidPtr(handle) : nullptr;
+    Py_XDECREF(handle);
+    if (PyErr_Occurred()) PyErr_Clear(), ok = false;
+    return s;
+  }
   // A CUDA tensor on the call's device; nullptr for None where that is allowed.
   const at::Tensor* tensor(bool none = false) {
     PyObject* const o = next();
@@ -87,11 +99,10 @@ PyObject* called(Call call) {
 
 PyObject* unusual() { return PyLong_FromLong(kUnusual); }
 
-// now, stream, logits, beams, status, history, length, prompt, repetition, presence, frequency, no_repeat, bias_token, bias_value,
+// stream, logits, beams, status, history, length, prompt, repetition, presence, frequency, no_repeat, bias_token, bias_value,
 // masks, mask_row
 PyObject* adjust(Args a) {
-  a.device = a.whole();
-  void* const stream = a.handle();
+  void* const stream = a.stream();
   const at::Tensor* const x = a.tensor();
   const int64_t beams = a.whole();
   const at::Tensor *const status = a.ints(), *const history = a.ints(true), *const length = a.ints(true), *const prompt = a.ints(true);
@@ -123,10 +134,9 @@ PyObject* adjust(Args a) {
   });
 }
 
-// now, stream, history, parent, token, length, status
+// stream, history, parent, token, length, status
 PyObject* history(Args a) {
-  a.device = a.whole();
-  void* const stream = a.handle();
+  void* const stream = a.stream();
   const at::Tensor *const h = a.ints(), *const parent = a.ints(), *const token = a.ints(), *const length = a.ints(), *const status = a.ints();
   int64_t ld = 0, ld_parent = 0, ld_token = 0;
   if (!a.ok || !matrix_of(parent, -1, -1, ld_parent)) return unusual();
@@ -143,10 +153,9 @@ bool moves_of(const at::Tensor* moves, const at::Tensor* n_moves) {
   return moves->dim() == 2 && moves->size(1) == 3 && moves->is_contiguous() && vector_of(n_moves, 1);
 }
 
-// now, stream, table, refs, page, parent, length, more, most, moves, n_moves, workspace, status
+// stream, table, refs, page, parent, length, more, most, moves, n_moves, workspace, status
 PyObject* advance(Args a) {
-  a.device = a.whole();
-  void* const stream = a.handle();
+  void* const stream = a.stream();
   const at::Tensor *const table = a.ints(), *const refs = a.ints();
   const int64_t page = a.whole();
   const at::Tensor *const parent = a.ints(true), *const length = a.ints(), *const more = a.ints(true);
@@ -165,10 +174,9 @@ PyObject* advance(Args a) {
   });
 }
 
-// now, stream, pool, moves, n_moves, status
+// stream, pool, moves, n_moves, status
 PyObject* copy(Args a) {
-  a.device = a.whole();
-  void* const stream = a.handle();
+  void* const stream = a.stream();
   const at::Tensor *const pool = a.tensor(), *const moves = a.ints(), *const n_moves = a.ints(), *const status = a.ints();
   if (!a.ok || pool->dim() != 5 || !pool->is_contiguous() || !moves_of(moves, n_moves)) return unusual();
   return called([&] {
@@ -177,10 +185,9 @@ PyObject* copy(Args a) {
   });
 }
 
-// now, stream, table, refs, ended, status
+// stream, table, refs, ended, status
 PyObject* release(Args a) {
-  a.device = a.whole();
-  void* const stream = a.handle();
+  void* const stream = a.stream();
   const at::Tensor *const table = a.ints(), *const refs = a.ints(), *const ended = a.tensor(true), *const status = a.ints();
   int64_t ld = 0;
   if (!a.ok || !matrix_of(table, -1, -1, ld) || !vector_of(refs, refs->numel())) return unusual();
@@ -194,10 +201,9 @@ PyObject* release(Args a) {
   });
 }
 
-// now, stream, table, refs, page, new_table, new_refs, live, moves, n_moves, workspace, status
+// stream, table, refs, page, new_table, new_refs, live, moves, n_moves, workspace, status
 PyObject* compact(Args a) {
-  a.device = a.whole();
-  void* const stream = a.handle();
+  void* const stream = a.stream();
   const at::Tensor *const table = a.ints(), *const refs = a.ints();
   const int64_t page = a.whole();
   const at::Tensor *const new_table = a.ints(), *const new_refs = a.ints(), *const live = a.ints(), *const moves = a.ints(),
@@ -249,12 +255,12 @@ constexpr PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<bind>("bind"),
-                           method<guarded<adjust, 16>>("adjust"),
-                           method<guarded<history, 7>>("history"),
-                           method<guarded<advance, 13>>("advance"),
-                           method<guarded<copy, 6>>("copy"),
-                           method<guarded<release, 6>>("release"),
-                           method<guarded<compact, 12>>("compact"),
+                           method<guarded<adjust, 15>>("adjust"),
+                           method<guarded<history, 6>>("history"),
+                           method<guarded<advance, 12>>("advance"),
+                           method<guarded<copy, 5>>("copy"),
+                           method<guarded<release, 5>>("release"),
+                           method<guarded<compact, 11>>("compact"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "orpo_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
