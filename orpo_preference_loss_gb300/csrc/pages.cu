@@ -7,7 +7,7 @@
 //
 // The plans (which page goes where) touch a few kilobytes: they are bound by the way to memory and back, which each step of
 // "length, parent, table entry, count of holders, free page" takes once, and by barriers.  So a decode step's plan is one CTA that
-// takes those ways twice (captured in a graph: 4 beams, 100 pages 4.5 us; 16 x 8 beams, 3000 pages about 8), larger ones a cluster of 8
+// takes those ways twice (captured in a graph: 4 beams, 100 pages 3.8 us; 16 x 8 beams, 3000 pages about 8), larger ones a cluster of 8
 // CTAs that tell each other sums through shared memory (64 prompts of up to 512 pages into 164k pages: 16).  The copies are
 // bound by the bytes moved: 1.06 GB in 161 us, 97% of the rate of a plain copy.
 #include <algorithm>
@@ -105,8 +105,9 @@ constexpr int kPlanThreads = 1024;
 constexpr int kWarps = kPlanThreads / 32;
 constexpr int kMaxCtas = 8;
 
-// Exclusive sum of x over the CTA's threads, and the total.  `part` is kWarps words of shared memory, free again after
+// Exclusive sum of x over the threads of a CTA of kW warps, and the total.  `part` is kW words of shared memory, free again after
 // the call.
+template <int kW = kWarps>
 __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* part, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t sum = x;
@@ -117,7 +118,7 @@ __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t* part, uint32_t& t
   }
   if (lane == 31) part[warp] = sum;
   __syncthreads();
-  const uint32_t w = part[lane];
+  const uint32_t w = lane < kW ? part[lane] : 0;
   uint32_t before = w;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
@@ -156,11 +157,12 @@ __device__ __forceinline__ uint32_t told_before(const Totals* mine, int what, in
 
 // A CTA's stretch of pages, a run of 32-page words per warp: who is in use, as ballots.  A lane keeps the word of its own
 // number; runs of more than 32 words are looked up again.
+template <int kW = kWarps>
 struct PageRun {
   int32_t begin, words;
   uint32_t kept;
   __device__ __forceinline__ PageRun(int32_t p_begin, int32_t p_end) : kept(0) {
-    words = (p_end - p_begin + 32 * kWarps - 1) / (32 * kWarps);
+    words = (p_end - p_begin + 32 * kW - 1) / (32 * kW);
     begin = p_begin + (int32_t)(threadIdx.x >> 5) * words * 32;
   }
   // How many pages of the run, of those below p_end, are in use.
@@ -228,15 +230,19 @@ __device__ __forceinline__ Wanted wanted_columns(const TableArgs& a, uint32_t b)
 // ---- a decode step's worth: up to kSmallItems items, in one CTA.
 // KB: a fork of up to KB beams is done here too, for (entry, column) pairs of at most one per thread; the counts of holders are
 // then in shared memory, where what the fork changes can be looked up at once.  0: no fork here, and the counts stay
-// where they are.  kQ: items per thread, one after the other.
+// where they are.  kQ: items per thread, one after the other.  kT: threads.
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallMost = 4;               // items per thread at most
 constexpr int kSmallItems = kSmallMost * kSmallThreads;
+// Where items, pairs and pages are few, so are the threads: the barriers of a step of 4 beams in 27 pages, copy included, are
+// then shorter (6.3 us captured; with 1024 threads 6.9).
+constexpr int kFewThreads = 256;
+constexpr int kFewPages = 8192;
 // In turns, 128 x 256 pairs took 14.5 us here, by a kernel of their own and a plan without a fork 8.3.  Up to one turn it is a
-// launch less: with the copy 6.0 us to enqueue, else 7.6.
+// launch less: with the copy 5.1 us to enqueue, else 6.4.
 constexpr int kForkHere = kSmallThreads;    // pairs
 constexpr int kForkPages = 32768;           // 128 KB of counts
-inline int32_t padded_pages(int64_t pages) { return (int32_t)(cdiv(pages, 32 * kWarps) * 32 * kWarps); }
+inline int32_t padded_pages(int64_t pages, int threads) { return (int32_t)(cdiv(pages, threads) * threads); }
 
 // Pages that several items hold, in shared memory: twice as many slots as items.
 template <int kItems>
@@ -246,32 +252,32 @@ struct SmallTables {
   uint8_t bad[kItems];                                             // entries
 };
 
-template <int KB, int kQ>
-__global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArgs a, int32_t padded) {
-  constexpr int kItems = kQ * kSmallThreads;
+template <int KB, int kQ, int kT>
+__global__ void __launch_bounds__(kT) small_reserve_kernel(ReserveArgs a, int32_t padded) {
+  constexpr int kItems = kQ * kT, kW = kT / 32;
   constexpr uint32_t kSlots = 2 * kItems;
   extern __shared__ __align__(16) uint8_t small_raw[];
   SmallTables<kItems>& s = *reinterpret_cast<SmallTables<kItems>*>(small_raw);
   int32_t* const refs = reinterpret_cast<int32_t*>(small_raw + sizeof(SmallTables<kItems>));  // KB > 0: [padded] counts of holders
-  __shared__ uint32_t part[kWarps];
+  __shared__ uint32_t part[kW];
   const TableArgs& t = a.t;
   const int tid = threadIdx.x, lane = tid & 31;
   grid_trigger();
-  for (int i = tid; i < kItems; i += kSmallThreads) s.bad[i] = 0;
-  for (int i = tid; i < (int)kSlots; i += kSmallThreads) s.keys[i] = -1, s.count[i] = 0, s.last[i] = -1;
+  for (int i = tid; i < kItems; i += kT) s.bad[i] = 0;
+  for (int i = tid; i < (int)kSlots; i += kT) s.keys[i] = -1, s.count[i] = 0, s.last[i] = -1;
   __syncthreads();
   grid_wait();
   const int rows = (int)t.batch * t.beams;
   // ---- counts, lengths, parents
-  PageRun run(0, KB > 0 ? padded : t.pages);
+  PageRun<kW> run(0, KB > 0 ? padded : t.pages);
   uint32_t used = 0;
   if constexpr (KB > 0) {
 #pragma unroll 8
-    for (int p = tid; p < padded; p += kSmallThreads) refs[p] = p < t.pages ? t.refs[p] : 1;
+    for (int p = tid; p < padded; p += kT) refs[p] = p < t.pages ? t.refs[p] : 1;
   } else {
     used = run.count(t.refs, t.pages);
   }
-  for (int r = tid; r < rows; r += kSmallThreads) {
+  for (int r = tid; r < rows; r += kT) {
     const int e = r / t.beams;
     int64_t begin, end;
     bool wrong = !wanted(t, e, begin, end);
@@ -372,13 +378,13 @@ __global__ void __launch_bounds__(kSmallThreads) small_reserve_kernel(ReserveArg
   uint32_t mine = 0, total;
 #pragma unroll
   for (int q = 0; q < kQ; ++q) mine += (uint32_t)(what[q] != kNone) | (uint32_t)(what[q] == kShared && j[q] == 0 && w[q].fill > 0) << 16;
-  const uint32_t before = scan(mine, part, total), needed = total & 0xffff;
+  const uint32_t before = scan<kW>(mine, part, total), needed = total & 0xffff;
   // ---- free pages, lowest first
   if constexpr (KB > 0)
     for (int i = 0; i < run.words; ++i) used += __popc(__ballot_sync(~0u, refs[run.begin + i * 32 + lane] > 0));
   const int run_pages = min(max((KB > 0 ? padded : t.pages) - run.begin, 0), run.words * 32);
   uint32_t found;
-  uint32_t rank = scan(lane == 0 ? (uint32_t)run_pages - used : 0, part, found);
+  uint32_t rank = scan<kW>(lane == 0 ? (uint32_t)run_pages - used : 0, part, found);
   rank = __shfl_sync(~0u, rank, 0);
   if (found < needed) {
     if (tid == 0) {
@@ -841,7 +847,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(CompactArgs a, in
   const int tid = threadIdx.x, ctas = gridDim.x, cta = blockIdx.x;
   const int32_t p_begin = (int32_t)min((int64_t)cta * a.pages_per, (int64_t)a.pages), p_end = (int32_t)min((int64_t)p_begin + a.pages_per, (int64_t)a.pages);
   const int lane = tid & 31;
-  PageRun run(p_begin, p_end);
+  PageRun<> run(p_begin, p_end);
   const uint32_t run_used = run.count(a.refs, p_end);
   uint32_t used;
   const uint32_t run_before = scan(lane == 0 ? run_used : 0, part, used);
@@ -928,22 +934,26 @@ constexpr int64_t kOneCta = 4096;  // pages
 int plan_ctas(int64_t units, int64_t pages) { return units <= kWarps && pages <= kOneCta ? 1 : kMaxCtas; }
 int32_t share(int64_t n, int ctas, int tile) { return (int32_t)(cdiv(cdiv(n, ctas), tile) * tile); }
 // Table entries per CTA up to which the compaction's own CTAs rewrite the table.  At 65536 entries that takes 16.1 us, by a
-// kernel of their own 14.0, but that one is 2 us more to enqueue; at 33024 7.5 here.
+// kernel of their own 14.0, but that one is 1.4 us more to enqueue; at 33024 7.5 here.
 constexpr int64_t kRemapHere = 8192;
 // Pages whose counts one CTA looks through for a decode step: 512 rows in 16385 pages take 7 us in one CTA and 15 on a cluster, in
 // 100000 13 and 17; one CTA takes 0.08 us per 1000 pages more, the cluster 0.01.  (Items: 1025 take 12 us in one CTA and 27 on a
 // cluster, 4096 19 and 27.)
 constexpr int64_t kSmallPages = 131072;
 
-template <int KB, int kQ>
+template <int KB, int kQ, int kT>
 cudaError_t launch_small(const ReserveArgs& a, cudaStream_t st) {
   static std::atomic<int> done[64];
-  constexpr int kTables = (int)sizeof(SmallTables<kQ * kSmallThreads>);
-  static_assert(kTables % 16 == 0 && kTables + kForkPages * 4 <= 227 << 10 || KB == 0, "a CTA's shared memory");
-  const cudaError_t e = opt_in_smem(small_reserve_kernel<KB, kQ>, kTables + (KB > 0 ? kForkPages * 4 : 0), done);
+  constexpr int kTables = (int)sizeof(SmallTables<kQ * kT>), kMost = kTables + (KB > 0 ? kForkPages * 4 : 0);
+  static_assert(kTables % 16 == 0 && kMost <= 227 << 10, "a CTA's shared memory");
+  const cudaError_t e = opt_in_smem(small_reserve_kernel<KB, kQ, kT>, kMost, done);
   if (e != cudaSuccess) return e;
-  const int32_t padded = KB > 0 ? padded_pages(a.t.pages) : 0;
-  return launch_dependent(small_reserve_kernel<KB, kQ>, dim3(1), kSmallThreads, (size_t)kTables + (size_t)padded * 4, st, a, padded);
+  const int32_t padded = KB > 0 ? padded_pages(a.t.pages, kT) : 0;
+  return launch_dependent(small_reserve_kernel<KB, kQ, kT>, dim3(1), kT, (size_t)kTables + (size_t)padded * 4, st, a, padded);
+}
+template <int KB>
+cudaError_t launch_small(const ReserveArgs& a, bool few, cudaStream_t st) {
+  return few ? launch_small<KB, 1, kFewThreads>(a, st) : launch_small<KB, 1, kSmallThreads>(a, st);
 }
 
 bool misaligned(std::initializer_list<const void*> p) {
@@ -1019,10 +1029,11 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
   if (e == cudaSuccess && small) {
     a.width = (int32_t)width;
     a.items = (int32_t)(rows * width);
-    e = a.items > kSmallThreads ? launch_small<0, kSmallMost>(a, st)
-        : !fork_there           ? launch_small<0, 1>(a, st)
-        : beams <= 4            ? launch_small<4, 1>(a, st)
-                                : launch_small<8, 1>(a, st);
+    const bool few = a.items <= kFewThreads && pages <= kFewPages && (!fork_there || batch * columns <= kFewThreads);
+    e = a.items > kSmallThreads ? launch_small<0, kSmallMost, kSmallThreads>(a, st)
+        : !fork_there           ? launch_small<0>(a, few, st)
+        : beams <= 4            ? launch_small<4>(a, few, st)
+                                : launch_small<8>(a, few, st);
   } else if (e == cudaSuccess) {
     a.width = (int32_t)padded_width(width);
     a.items = width > 0 ? (int32_t)(rows * a.width) : 0;
