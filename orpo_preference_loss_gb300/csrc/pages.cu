@@ -809,7 +809,7 @@ struct CompactArgs {
   int32_t pages_per;  // CTA, a multiple of 32 * kWarps
   int32_t* holes;   // [pages / 2] free pages below n, by number
   int32_t* movers;  // [pages] used pages at or above n, by the pages in use below them
-  int32_t* below;   // [pages] for pages at or above n: the pages in use below, or -1 for a free one
+  int32_t* below;   // [pages] the pages in use below, or -1 for a free page
   int32_t* status;
 };
 
@@ -822,10 +822,10 @@ __device__ __forceinline__ void remap(const CompactArgs& a, int32_t live, int32_
     int32_t e = a.table[row * a.ld + c];
     if (e < -1 || e >= a.pages) {
       wrong = 1;
-    } else if (e >= live) {
-      const int32_t u = a.below[e];
+    } else if (e >= 0) {
+      const int32_t u = a.below[e];  // by now the counts of the holes may be those of the pages that move there
       if (u < 0) wrong = 1;
-      else if (in_bounds(a.status, u - first, a.pages / 2)) e = a.holes[u - first];
+      else if (e >= live && in_bounds(a.status, u - first, a.pages / 2)) e = a.holes[u - first];
     }
     a.new_table[row * a.ld_new + c] = e;
   }
@@ -864,12 +864,12 @@ __global__ void __launch_bounds__(kPlanThreads) compact_kernel(CompactArgs a, in
     before += __popc(bits);
     if (p >= p_end) continue;
     if (p == live) totals.v[1] = u + 1;  // u(n), told with 0 for "not mine"
+    a.below[p] = in_use ? (int32_t)u : -1;
     if (p < live) {
       if (!in_use && in_bounds(a.status, p - (int32_t)u, a.pages / 2)) a.holes[p - (int32_t)u] = p;
       if (in_use && a.new_refs != a.refs) a.new_refs[p] = __ldcg(a.refs + p);
     } else {
       if (in_use && in_bounds(a.status, u, a.pages)) a.movers[u] = p;
-      a.below[p] = in_use ? (int32_t)u : -1;
       if (a.new_refs != a.refs) a.new_refs[p] = 0;
     }
   }
