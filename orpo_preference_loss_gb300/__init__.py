@@ -877,7 +877,8 @@ class PagedStates:
     The pools themselves, [outer, pages, rows, page, unit] of any dtype and any number of them, are the caller's: position
     t of beam r is position t % page of page table[r, t // page] in every pool.  table [batch * beams, columns], refs [pages],
     moves and status stay on the device; nothing waits on the host.  The constructor fills them on the current stream.
-    most: the largest number of positions that advance or admit is asked for at once."""
+    A call that raises for its arguments has changed nothing.  most: the largest number of positions that advance or admit is
+    asked for at once."""
 
     def __init__(self, batch: int, beams: int, columns: int, pages: int, page: int, most: int = 1, status=None, device="cuda"):
         self.batch, self.beams, self.columns, self.pages, self.page, self.most = batch, beams, columns, pages, page, most
@@ -893,15 +894,27 @@ class PagedStates:
         self.live = torch.zeros(1, dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev) if status is None else status
 
+    def _check_pools(self, pools):
+        """The pools as a tuple.  Raises where one does not fit the table: a plan changes the table in place, so by the time a
+        copy is refused it would be too late."""
+        pools, at = tuple(pools), self.table.get_device()
+        for pool in pools:
+            if (pool.dim() != 5 or pool.shape[1] != self.pages or pool.shape[3] != self.page or not pool.is_contiguous()
+                    or pool.get_device() != at):
+                raise ValueError(f"a pool has shape {tuple(pool.shape)} on {pool.device}, expected a contiguous tensor [outer, {self.pages}, rows, "
+                                 f"{self.page}, unit] on {self.table.device}")
+            if self.page * pool.shape[4] * pool.element_size() >= 1 << 31:
+                raise ValueError(f"a pool has pages of {self.page} x {pool.shape[4] * pool.element_size()} bytes, expected less than 2^31")
+        return pools
+
     def _copy(self, pools, stream):
         for pool in pools:
-            if pool.dim() != 5 or pool.shape[1] != self.pages or pool.shape[3] != self.page:
-                raise ValueError(f"a pool has shape {tuple(pool.shape)}, expected [outer, {self.pages}, rows, {self.page}, unit]")
             orpo_pages_copy(pool, self.moves, self.n_moves, self.status, stream)
 
     def advance(self, length, parent=None, more=None, most=1, pools=(), stream=None):
         """The beams' tables follow parent [batch, beams] up to length[b], and positions length[b] .. length[b] + more[b] - 1
         (more None: `most` of them) of every beam can be written in all pools."""
+        pools = self._check_pools(pools)
         orpo_pages_advance(self.table, self.refs, self.page, parent, length, more, most, self.moves, self.n_moves,
                            self.workspace, self.status, stream)
         self._copy(pools, stream)
@@ -909,6 +922,7 @@ class PagedStates:
     def admit(self, length, more, most, pools=(), stream=None):
         """As advance without parents, for beam 0 of each entry alone: a prompt, which the other beams take with their
         first advance (all parents 0)."""
+        pools = self._check_pools(pools)
         orpo_pages_advance(self.table[::self.beams], self.refs, self.page, None, length, more, most, self.moves, self.n_moves,
                            self.workspace, self.status, stream)
         self._copy(pools, stream)
@@ -921,6 +935,7 @@ class PagedStates:
 
     def compact(self, pools=(), stream=None):
         """Pages in use move to the lowest numbers, 0 .. live[0] - 1, in all pools."""
+        pools = self._check_pools(pools)
         orpo_pages_compact(self.table, self.refs, self.page, self.table, self.refs, self.live, self.moves, self.n_moves,
                            self.workspace, self.status, stream)
         self._copy(pools, stream)
@@ -982,6 +997,8 @@ class BeamDecoder:
             raise ValueError("penalties for repeated tokens need a history")
         if pages is not None and (pages.batch != self.batch or pages.beams != self.beams):
             raise ValueError(f"pages is for {pages.batch} x {pages.beams} beams, expected {self.batch} x {self.beams}")
+        if pages is not None:
+            pools = pages._check_pools(pools)
         orpo_head_logits_q(h, wq, scales, biases, self.bits, self.group, self.softcap, self.logits, self.status,
                            stream, self.logits_workspace)
         if self._penalties or bias_token is not None or masks is not None:
