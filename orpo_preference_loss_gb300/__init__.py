@@ -983,20 +983,26 @@ class BeamDecoder:
             self.finished.zero_()
 
     def step(self, h, wq, scales, biases, states=(), length=None, stream=None, history=None, prompt=None, bias_token=None,
-             bias_value=None, masks=None, mask_row=None, pages=None, pools=()):
+             bias_value=None, masks=None, mask_row=None, pages=None, pools=(), more=None):
         """One step from the hidden rows h [batch * beams, d]; returns (parent, token) [batch, beams].
 
         states: tensors [outer, batch * beams, rows, capacity, unit] that follow their parents, up to
         position length[b] of each entry.  history: int32 [batch * beams, capacity], each beam's length[b] tokens so far (the
         first prompt[b] of them the prompt's); it follows its parent and gets the new token at length[b].  bias_token,
         bias_value, masks, mask_row: as for orpo_logits_adjust.  pages, pools: a PagedStates and the pools of it, which follow
-        and in which position length[b] can then be written.  length itself is the caller's to raise."""
+        and in which position length[b] can then be written.  more: int32 [batch], 0 for entries that get no such position (they
+        ended and were released, or all their positions are in use), else 1; None: 1 for all.  length itself is the caller's to
+        raise."""
         if length is None and (history is not None or pages is not None):
             raise ValueError("a history or pages need length")
         if self._penalties and history is None:
             raise ValueError("penalties for repeated tokens need a history")
         if pages is not None and (pages.batch != self.batch or pages.beams != self.beams):
             raise ValueError(f"pages is for {pages.batch} x {pages.beams} beams, expected {self.batch} x {self.beams}")
+        if more is not None:
+            if pages is None:
+                raise ValueError("more is for pages")
+            _dev(more, "more", I32, (self.batch,))
         if pages is not None:
             pools = pages._check_pools(pools)
         orpo_head_logits_q(h, wq, scales, biases, self.bits, self.group, self.softcap, self.logits, self.status,
@@ -1011,5 +1017,5 @@ class BeamDecoder:
         if history is not None:
             orpo_beam_history(history, self.parent, self.token, length, self.status, stream)
         if pages is not None:
-            pages.advance(length, self.parent, pools=pools, stream=stream)
+            pages.advance(length, self.parent, more, pools=pools, stream=stream)
         return self.parent, self.token

@@ -82,7 +82,7 @@ def weights():
     return torch.from_numpy(wq).to(dev()), t16(s), t16(b)
 
 
-STEP = ("pool", "second pool", "host pool")
+STEP = ("pool", "second pool", "host pool", "more without pages", "more of another type", "more of another size")
 
 
 @pytest.mark.parametrize("kind", STEP)
