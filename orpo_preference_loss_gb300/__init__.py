@@ -999,9 +999,12 @@ class BeamDecoder:
             raise ValueError("penalties for repeated tokens need a history")
         if pages is not None and (pages.batch != self.batch or pages.beams != self.beams):
             raise ValueError(f"pages is for {pages.batch} x {pages.beams} beams, expected {self.batch} x {self.beams}")
+        if (bias_token is None) != (bias_value is None) or (masks is None) != (mask_row is None):
+            raise ValueError("bias_token and bias_value, and masks and mask_row, must be given together")
+        pools = tuple(pools)
+        if pages is None and (pools or more is not None):
+            raise ValueError("pools and more need pages")
         if more is not None:
-            if pages is None:
-                raise ValueError("more is for pages")
             _dev(more, "more", I32, (self.batch,))
         if pages is not None:
             pools = pages._check_pools(pools)

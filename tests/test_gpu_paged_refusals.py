@@ -82,7 +82,8 @@ def weights():
     return torch.from_numpy(wq).to(dev()), t16(s), t16(b)
 
 
-STEP = ("pool", "second pool", "host pool", "more without pages", "more of another type", "more of another size")
+STEP = ("pool", "second pool", "host pool", "more without pages", "more of another type", "more of another size",
+        "pools without pages", "bias values alone", "bias tokens alone", "mask rows alone", "masks alone", "masks of another size")
 
 
 @pytest.mark.parametrize("kind", STEP)
