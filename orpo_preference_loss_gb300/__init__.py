@@ -899,12 +899,11 @@ class PagedStates:
         copy is refused it would be too late."""
         pools, at = tuple(pools), self.table.get_device()
         for pool in pools:
-            if (pool.dim() != 5 or pool.shape[1] != self.pages or pool.shape[3] != self.page or not pool.is_contiguous()
-                    or pool.get_device() != at):
-                raise ValueError(f"a pool has shape {tuple(pool.shape)} on {pool.device}, expected a contiguous tensor [outer, {self.pages}, rows, "
-                                 f"{self.page}, unit] on {self.table.device}")
-            if self.page * pool.shape[4] * pool.element_size() >= 1 << 31:
-                raise ValueError(f"a pool has pages of {self.page} x {pool.shape[4] * pool.element_size()} bytes, expected less than 2^31")
+            shape = pool.shape
+            if (len(shape) != 5 or shape[1] != self.pages or shape[3] != self.page or not pool.is_contiguous() or pool.get_device() != at
+                    or self.page * shape[4] * pool.element_size() >= 1 << 31):
+                raise ValueError(f"a pool has shape {tuple(shape)} of {pool.dtype} on {pool.device}, expected a contiguous tensor [outer, {self.pages}, "
+                                 f"rows, {self.page}, unit] on {self.table.device} with less than 2^31 bytes per page and row")
         return pools
 
     def _copy(self, pools, stream):
@@ -914,7 +913,9 @@ class PagedStates:
     def advance(self, length, parent=None, more=None, most=1, pools=(), stream=None):
         """The beams' tables follow parent [batch, beams] up to length[b], and positions length[b] .. length[b] + more[b] - 1
         (more None: `most` of them) of every beam can be written in all pools."""
-        pools = self._check_pools(pools)
+        self._advance(length, parent, more, most, self._check_pools(pools), stream)
+
+    def _advance(self, length, parent, more, most, pools, stream):
         orpo_pages_advance(self.table, self.refs, self.page, parent, length, more, most, self.moves, self.n_moves,
                            self.workspace, self.status, stream)
         self._copy(pools, stream)
@@ -1004,10 +1005,30 @@ class BeamDecoder:
         pools = tuple(pools)
         if pages is None and (pools or more is not None):
             raise ValueError("pools and more need pages")
+        # The selection replaces the scores, so whatever the calls behind it would refuse is looked at before the first.
+        rows, at = self.batch * self.beams, self.score.get_device()
+        states = tuple(states)
+        if length is not None and (states or history is not None or pages is not None):
+            if not (length.dtype is torch.int32 and length.shape == (self.batch,) and length.is_contiguous() and length.get_device() == at):
+                _dev(length, "length", I32, (self.batch,))
+                raise ValueError(f"length is on {length.device}, expected {self.score.device}")
+        for state in states:
+            shape = state.shape
+            if (len(shape) != 5 or shape[1] != rows or not state.is_contiguous() or state.get_device() != at
+                    or (self.batch * shape[2] > 1 << 30 and state.numel() > 0)):
+                raise ValueError(f"a state has shape {tuple(shape)} on {state.device}, expected a contiguous tensor [outer, {rows}, rows, "
+                                 f"capacity, unit] on {self.score.device}")
+        if history is not None:
+            _rows(history, "history", I32, rows=rows)
+            if not 1 <= history.shape[1] < 1 << 28 or history.get_device() != at:
+                raise ValueError(f"history has room for {history.shape[1]} tokens on {history.device}, expected at least 1 and less than 2^28 on "
+                                 f"{self.score.device}")
         if more is not None:
             _dev(more, "more", I32, (self.batch,))
         if pages is not None:
             pools = pages._check_pools(pools)
+            if pages.table.get_device() != at:
+                raise ValueError(f"pages is on {pages.table.device}, expected {self.score.device}")
         orpo_head_logits_q(h, wq, scales, biases, self.bits, self.group, self.softcap, self.logits, self.status,
                            stream, self.logits_workspace)
         if self._penalties or bias_token is not None or masks is not None:
@@ -1020,5 +1041,5 @@ class BeamDecoder:
         if history is not None:
             orpo_beam_history(history, self.parent, self.token, length, self.status, stream)
         if pages is not None:
-            pages.advance(length, self.parent, more, pools=pools, stream=stream)
+            pages._advance(length, self.parent, more, 1, pools, stream)
         return self.parent, self.token

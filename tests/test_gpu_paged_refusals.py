@@ -82,8 +82,9 @@ def weights():
     return torch.from_numpy(wq).to(dev()), t16(s), t16(b)
 
 
-STEP = ("pool", "second pool", "host pool", "more without pages", "more of another type", "more of another size",
-        "pools without pages", "bias values alone", "bias tokens alone", "mask rows alone", "masks alone", "masks of another size")
+STEP = ("pool", "second pool", "host pool", "pools without pages", "more without pages", "more of another type", "more of another size", "history of another type",
+        "history of other rows", "empty history", "length of another type", "length of another size", "length on the host", "state", "second state",
+        "state of other beams", "bias values alone", "bias tokens alone", "mask rows alone", "masks alone", "masks of another size")
 
 
 @pytest.mark.parametrize("kind", STEP)
