@@ -202,7 +202,7 @@ struct ReserveArgs {
   int32_t* left_alone;  // [batch] entries that the fork found wrong; nullptr: there was no fork
   int32_t* moves;
   int32_t* n_moves;
-  int32_t width;     // items per row, rounded up to a power of two up to 32 or a multiple of kUnit
+  int32_t width;     // items per row, with padding: see padded_width
   int32_t items;     // so many in all
   int32_t units_per; // CTA
   int32_t* count;    // [pages] how many items hold a page that others hold too,
@@ -434,7 +434,7 @@ struct Items {
 };
 
 // The units of a warp, one after the other: next() gives their items and the pages that those have.  What the rows of up to
-// 32 units ask for is looked up at once, a unit per lane, where a unit is of one row.
+// 32 units ask for is looked up at once, a unit per lane, where every unit is of one row.
 struct Units {
   const ReserveArgs& a;
   int32_t unit, end;
@@ -454,7 +454,7 @@ struct Units {
     unit += kWarps;
     if (unit >= end) return false;
     const int lane = threadIdx.x & 31;
-    if (a.width >= kUnit) {
+    if (a.width % kUnit == 0) {
       if (at == 32) {
         const int64_t mine = (int64_t)unit + lane * kWarps;
         const uint32_t i = mine < end ? (uint32_t)mine * kUnit : 0;
@@ -914,15 +914,21 @@ bool table_ok(int64_t table_rows, int64_t ld, int64_t columns, int64_t pages, in
 int64_t width_of(int64_t most, int64_t page) { return most > 0 ? cdiv(most - 1, page) + 1 : 0; }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
-// Items per row with the padding that lets a warp's unit of items start on a row: see ReserveArgs.
-int64_t padded_width(int64_t width) {
+// Items per row, rounded up to a power of two up to 32 or a multiple of kUnit, so that a warp's unit of items starts on a row.
+int64_t rounded_width(int64_t width) {
   if (width > 32) return cdiv(width, kUnit) * kUnit;
   int64_t w = 1;
   while (w < width) w *= 2;
   return w;
 }
+// The same where that stays within kMaxItems; else no padding, and units hold the ends of rows.
+int64_t padded_width(int64_t rows, int64_t width) {
+  const int64_t w = rounded_width(width);
+  return rows * w <= kMaxItems ? w : width;
+}
+// Never less for more rows or a larger width, so a workspace for the largest call serves all of them.
 size_t reserve_bytes(int64_t batch, int64_t pages, int64_t rows, int64_t width) {
-  const int64_t units = cdiv(rows * padded_width(width), kUnit);
+  const int64_t units = cdiv(std::min(rows * rounded_width(width), kMaxItems), kUnit);
   return align16(batch * 4) + 2 * align16(pages * 4) + align16(units * kPer * 4) + align16(units * 4) + align16(units * 8) +
          align16(cdiv(pages, kTile) * 4) + align16(std::min(pages, rows * width) * 4);
 }
@@ -985,7 +991,7 @@ extern "C" {
 size_t orpo_pages_workspace_bytes(int64_t table_rows, int64_t pages, int64_t page, int64_t most) {
   if (!table_ok(table_rows, 0, 0, pages, page) || most < 0 || most > kMaxInt) return 0;
   const int64_t width = width_of(most, page);
-  if (table_rows * padded_width(width) > kMaxItems) return 0;
+  if (table_rows * width > kMaxItems) return 0;
   return std::max(std::max(reserve_bytes(table_rows, pages, table_rows, width), compact_bytes(pages)), (size_t)16);
 }
 
@@ -998,7 +1004,7 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
       max_moves < batch * beams)
     return ORPO_ERR_SHAPE;
   const int64_t rows = batch * beams, width = width_of(most, page);
-  if (rows * padded_width(width) > kMaxItems) return ORPO_ERR_SHAPE;
+  if (rows * width > kMaxItems) return ORPO_ERR_SHAPE;
   if (!n_moves || !status || (batch > 0 && ((columns > 0 && !table) || !refs || !length || !moves || !workspace))) return ORPO_ERR_NULL;
   if (misaligned({table, refs, parent, length, more, moves, n_moves, status}) || !aligned16(workspace)) return ORPO_ERR_ALIGN;
   if (ws_bytes < (batch > 0 ? reserve_bytes(batch, pages, rows, width) : 0)) return ORPO_ERR_WORKSPACE;
@@ -1035,7 +1041,7 @@ int orpo_pages_advance(int32_t* table, int64_t ld_table, int64_t columns, int32_
         : beams <= 4            ? launch_small<4>(a, few, st)
                                 : launch_small<8>(a, few, st);
   } else if (e == cudaSuccess) {
-    a.width = (int32_t)padded_width(width);
+    a.width = (int32_t)padded_width(rows, width);
     a.items = width > 0 ? (int32_t)(rows * a.width) : 0;
     const int64_t units = cdiv(a.items, kUnit);
     const int ctas = a.items > 0 ? plan_ctas(units, pages) : 1;
