@@ -13,6 +13,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -150,14 +151,24 @@ def load():
     return L
 
 
+class _NoBinding:
+    """Where csrc/binding.cpp's module is not there: answers as that does to arguments it does not take, so all go through ctypes."""
+
+    adjust = history = advance = copy = release = compact = staticmethod(lambda *args: -1)
+
+
 def _load_binding(L):
-    """The module of csrc/binding.cpp, bound to the library's entry points."""
+    """The module of csrc/binding.cpp, bound to the library's entry points.  It saves time and nothing else, so the library does
+    without one: another PyTorch than it was built for, or none of PyTorch's headers."""
     path = _build.binding_path(_variant == "debug")
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with orpo_preference_loss_gb300.build.build()")
-    loader = importlib.machinery.ExtensionFileLoader("orpo_binding", path)
-    module = importlib.util.module_from_spec(importlib.machinery.ModuleSpec("orpo_binding", loader, origin=path))
-    loader.exec_module(module)
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("orpo_binding", path)
+        module = importlib.util.module_from_spec(importlib.machinery.ModuleSpec("orpo_binding", loader, origin=path))
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"the binding {path} cannot be loaded ({e}): calls take some microseconds more; "
+                      "orpo_preference_loss_gb300.build.build() makes it", RuntimeWarning, stacklevel=3)
+        return _NoBinding()
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.orpo_logits_adjust, L.orpo_beam_history, L.orpo_pages_advance,
                                                                   L.orpo_pages_copy, L.orpo_pages_release, L.orpo_pages_compact)))
     return module

@@ -4,7 +4,8 @@ Each .cu file is compiled in parallel into an object, then linked into a shared
 library against the shared CUDA runtime (the one PyTorch also loads).  The
 result lives in ``orpo_preference_loss_gb300/_build/`` (git-ignored).  The Python
 module of csrc/binding.cpp is compiled beside it with the host compiler, against
-PyTorch's headers.  A build is skipped when both are newer than every source and header.
+PyTorch's headers; where that fails there is a warning, and the calls it is for go through
+ctypes.  Either is skipped when it is newer than its sources and headers.
 
 ``build(debug=True)`` makes the bounds-checked variant ``liborpo_head_debug.so``
 in ``_build_debug/``: the same sources with ORPO_DEBUG_BOUNDS, where every
@@ -21,6 +22,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -66,17 +68,23 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
+def _newer(path: str, sources) -> bool:
+    """Whether path is there and no older than its sources, the C ABI's headers and this file."""
+    deps = [*sources, *glob.glob(os.path.join(ROOT, "include", "*.h")), os.path.abspath(__file__)]
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps)
+
+
+def _library_up_to_date(debug: bool) -> bool:
+    return _newer(DEBUG_LIB_PATH if debug else LIB_PATH,
+                  [*_sources(), *glob.glob(os.path.join(CSRC, "*.cuh")), *glob.glob(os.path.join(CSRC, "*.h"))])
+
+
+def _binding_up_to_date(debug: bool) -> bool:
+    return _newer(binding_path(debug), [os.path.join(CSRC, "binding.cpp")])
 
 
 def up_to_date(debug: bool = False) -> bool:
-    lib = DEBUG_LIB_PATH if debug else LIB_PATH
-    if not os.path.exists(lib) or not os.path.exists(binding_path(debug)):
-        return False
-    t = min(os.path.getmtime(lib), os.path.getmtime(binding_path(debug)))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _library_up_to_date(debug) and _binding_up_to_date(debug)
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
@@ -93,9 +101,38 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         try:
             if not force and up_to_date(debug):
                 return lib
-            return _build_locked(verbose, debug)
+            with ThreadPoolExecutor(max_workers=1) as ex:
+                binding = None if not force and _binding_up_to_date(debug) else ex.submit(_build_binding, verbose, debug)
+                if force or not _library_up_to_date(debug):
+                    _build_locked(verbose, debug)
+                failed = binding is not None and binding.result()
+            if failed:
+                sys.stderr.write(f"--- the compiler failed on binding.cpp\n{failed}\n")
+                warnings.warn(f"{os.path.basename(binding_path(debug))} could not be built: the calls that it is for go through ctypes, "
+                              "which takes some microseconds more each", RuntimeWarning, stacklevel=2)
+            return lib
         finally:
             fcntl.flock(lock, fcntl.LOCK_UN)
+
+
+def _build_binding(verbose: bool, debug: bool) -> str | None:
+    """Returns what the compiler said where it failed."""
+    path = binding_path(debug)
+    tmp = path + ".tmp"
+    try:
+        r = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
+        failed, said = r.returncode != 0, f"{r.stdout}\n{r.stderr}"
+    except OSError as e:  # no compiler
+        failed, said = True, str(e)
+    if failed:
+        for old in (path, tmp):  # one of an earlier build may not fit the library any more
+            if os.path.exists(old):
+                os.remove(old)
+        return said
+    if verbose:
+        sys.stderr.write(f"--- binding.cpp\n{said}\n")
+    os.replace(tmp, path)
+    return None
 
 
 def _build_locked(verbose: bool, debug: bool) -> str:
@@ -105,24 +142,19 @@ def _build_locked(verbose: bool, debug: bool) -> str:
     flags = NVCC_FLAGS + (["-DORPO_DEBUG_BOUNDS"] if debug else [])
     objs = [os.path.join(out, os.path.basename(s)[:-3] + ".o") for s in srcs]
 
-    binding = binding_path(debug)
-
     def compile_one(pair):
         src, obj = pair
-        if src.endswith(".cpp"):
-            return src, subprocess.run(_binding_command(obj), capture_output=True, text=True)
         cmd = [nvcc, *ARCH, *flags, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, r
 
-    jobs = [*zip(srcs, objs), (os.path.join(CSRC, "binding.cpp"), binding + ".tmp")]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-        results = list(ex.map(compile_one, jobs))
+    with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+        results = list(ex.map(compile_one, zip(srcs, objs)))
     failed = False
     for src, r in results:
         if r.returncode != 0:
             failed = True
-            sys.stderr.write(f"--- the compiler failed on {src}\n{r.stdout}\n{r.stderr}\n")
+            sys.stderr.write(f"--- nvcc failed on {src}\n{r.stdout}\n{r.stderr}\n")
         elif verbose:
             sys.stderr.write(f"--- {os.path.basename(src)}\n{r.stderr}")
     if failed:
@@ -133,7 +165,6 @@ def _build_locked(verbose: bool, debug: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"liborpo_head link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    os.replace(binding + ".tmp", binding)
     return lib
 
 
