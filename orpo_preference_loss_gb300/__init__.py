@@ -620,6 +620,13 @@ def _here(first, *others):
             raise ValueError(f"the tensors are on different devices: {first.device} and {t.device}")
 
 
+def _fits(bits, **numbers):
+    """ctypes cuts a whole number to its C type without a word: 2^32 + 2 would pass for 2."""
+    for name, n in numbers.items():
+        if isinstance(n, int) and not -(1 << bits - 1) <= n < 1 << bits - 1:
+            raise ValueError(f"{name} = {n} is out of range")
+
+
 # Each of the calls below goes through csrc/binding.cpp, which looks at the tensors in a fraction of the time.  Where that
 # finds one that is not of the usual kind (-1), the arguments are looked at here one by one, for the message.
 
@@ -646,6 +653,7 @@ def _adjust(logits, beams, status, history, length, prompt, repetition, presence
     if beams < 1 or rows % beams:
         raise ValueError(f"logits has {rows} rows, expected a multiple of beams = {beams}")
     batch = rows // beams
+    _fits(32, beams=beams, no_repeat=no_repeat)
     _here(logits, status, history, length, prompt, bias_token, bias_value, masks, mask_row)
     pitch = _rows(logits, "logits", LOGITS)
     _dev(status, "status", I32)
@@ -696,6 +704,7 @@ def orpo_beam_history(history, parent, token, length, status, stream=None):
 
 
 def orpo_pages_workspace_bytes(table_rows: int, pages: int, page: int, most: int = 1) -> int:
+    _fits(64, table_rows=table_rows, pages=pages, page=page, most=most)
     return int(load().orpo_pages_workspace_bytes(table_rows, pages, page, most))
 
 
@@ -722,6 +731,7 @@ def orpo_pages_advance(table, refs, page, parent, length, more, most, moves, n_m
         beams = rows // batch if batch else 1
         if rows != batch * beams:
             raise ValueError(f"table has {rows} rows, expected a multiple of the {batch} lengths")
+        _fits(64, page=page, most=most)
         _here(table, refs, parent, length, more, moves, n_moves, workspace, status)
         ld = _rows(table, "table", I32)
         _dev(refs, "refs", I32, (refs.numel(),))
@@ -780,6 +790,7 @@ def orpo_pages_compact(table, refs, page, new_table, new_refs, live, moves, n_mo
     code = (_fast or _bound()).compact(stream, table, refs, page, new_table, new_refs, live, moves, n_moves, workspace, status)
     if code < 0:
         rows, columns = table.shape
+        _fits(64, page=page)
         _here(table, refs, new_table, new_refs, live, moves, n_moves, workspace, status)
         ld = _rows(table, "table", I32)
         ld_new = _rows(new_table, "new_table", I32, cols=columns, rows=rows)

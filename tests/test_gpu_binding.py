@@ -74,3 +74,27 @@ def test_both_ways_give_the_same(monkeypatch):
     monkeypatch.setattr(orpo, "_fast", NoBinding())
     for a, b in zip(fast, all_calls()):
         assert torch.equal(a, b)
+
+
+def test_whole_numbers_are_not_cut_to_their_c_types(monkeypatch):
+    """2^32 + 2 is not 2, nor is 2^64 + 4 a page of 4 positions."""
+    st, x = status_tensor(), torch.ones((2, 64), device=dev())
+    history, length = torch.zeros((2, 8), dtype=torch.int32, device=dev()), t32([3])
+    table, refs, moves, n = t32([[-1] * 3] * 2), t32([0] * 9), t32([[0] * 3] * 4), t32([0])
+    ws = torch.zeros(4096, dtype=torch.uint8, device=dev())
+    for fast in (orpo._bound(), NoBinding()):
+        monkeypatch.setattr(orpo, "_fast", fast)
+        for kw in (dict(no_repeat=2**32 + 2), dict(no_repeat=2**64), dict(no_repeat=-2**32 + 2), dict(beams=2**32 + 2)):
+            with pytest.raises((ValueError, orpo.OrpoError)):
+                orpo.orpo_logits_adjust(**{**dict(logits=x, beams=2, status=st, history=history, length=length), **kw})
+        for kw in (dict(page=2**64 + 4), dict(most=2**64 + 1), dict(most=-2**64 + 1)):
+            with pytest.raises((ValueError, orpo.OrpoError)):
+                orpo.orpo_pages_advance(**{**dict(table=table, refs=refs, page=4, parent=None, length=length, more=None, most=1, moves=moves, n_moves=n,
+                                                  workspace=ws, status=st), **kw})
+        with pytest.raises((ValueError, orpo.OrpoError)):
+            orpo.orpo_pages_compact(table, refs, 2**64 + 4, table.clone(), refs.clone(), t32([0]), moves, n, ws, st)
+    for bad in ((2**64 + 2, 9, 4, 1), (2, 2**64 + 9, 4, 1), (2, 9, 2**64 + 4, 1), (2, 9, 4, 2**64 + 1)):
+        with pytest.raises(ValueError):
+            orpo.orpo_pages_workspace_bytes(*bad)
+    torch.cuda.synchronize()
+    assert bool((x == 1).all()) and bool((table == -1).all()) and int(st) == 0
