@@ -4,7 +4,8 @@
 //
 // One thread owns the same piece of all beams of an entry: it reads every moved beam's source before it writes any, and
 // no other thread touches those.  Pieces are 16 bytes for up to 8 beams (their sources are 32 registers), 4 above.  Bound by
-// the launch and two ways to memory: 4 beams of 100 tokens 1.5 us captured in a graph, 32 x 8 of 8191 (9.5 MB) 3.3.
+// the launch and two ways to memory: 4 beams of 100 tokens 1.5 us captured in a graph, 32 x 8 of 8191 (9.5 MB) 3.3, 28 x 9 of
+// them 5.4, 16 x 16 4.4, 4 x 64 5.9.
 #include <algorithm>
 
 #include "../../include/orpo_decode.h"

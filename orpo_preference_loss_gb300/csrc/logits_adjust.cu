@@ -14,13 +14,14 @@
 //     By counters: a CTA per range of the vocabulary, with a counter per token, which no history can overflow; each CTA reads
 //     the whole history.
 //     Neither has anything to probe or to sort, and integer atomics give the same whatever their order.  (With a hash table of
-//     a row's tokens 16 rows of 262144 took 15.9 us; with counters 6.5: probes follow one another.)
+//     a row's tokens 16 rows of 262144 took 15.9 us; with counters 6.2: probes follow one another.)
 //   mask CTAs      overwrite the masked logits of a range, 16 bytes per lane where 512 bytes in a row are all masked, else a
 //                  lane per token: nothing is read but the mask.
-// Bound, for few rows, by three ways to memory (length, tokens, logits) and the launch: 4 rows of 4096 2.8 us captured in a
-// graph, 16 rows of 262144 with everything on 6.5.  For many, by the logits' lookups, which are 32 different sectors a warp
-// (32 x 8 rows of 128256 bf16, histories of 4096, a grammar's masks: 21 us, of which the masks alone take 11, the
-// history alone 16).
+// Bound, for few rows, by three ways to memory (length, tokens, logits) and the launch: 4 rows of 4096 2.9 us captured in a
+// graph, 16 rows of 262144 with everything on 6.2.  For many rows (32 x 8 of 128256 bf16, histories of 4096, a grammar's masks:
+// 20.4 us; the masks alone 11.4, the history alone 16.2) the logits' lookups are the largest known part: 32 different sectors a
+// warp, read and written, for two rows on the busiest SM 2 x 3600 x 2 requests, about 7.6 us at one per clock.  With a frequency penalty
+// every CTA of a row reads its whole history: 30.7 us, 22.6 without masks, 34 there with 32-bit counters.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -161,7 +162,8 @@ __device__ __forceinline__ void adjust(const AdjustArgs& a, const Row<T>& row, c
   }
 }
 
-// The bias list's tokens in [v0, v0 + size): the first of a token's entries adds them all up, in order.
+// The bias list's tokens in [v0, v0 + size): the first of a token's entries adds them all up, in order.  Where any token comes
+// twice every entry searches the list: 4 rows of 128256 with 4096 entries take 6.7 us, with one of them repeated 790.
 template <class T, class Known>
 __device__ __forceinline__ void adjust_biased(const AdjustArgs& a, const Row<T>& row, const int32_t* token, const float* value, bool twice,
                                               int64_t v0, int size, Known known) {
@@ -438,8 +440,8 @@ cudaError_t launch(AdjustArgs a, int sms, cudaStream_t st) {
   a.bit_words = (int)(cdiv(a.V, 128) * 4);
   const int64_t bits = (int64_t)a.bit_words * 4 * (1 + (a.ngram > 0) + 2 * (a.n_bias > 0));
   // Bits take one CTA per row, counters several, which is better while all of them are resident at once: 35 rows of 50257
-  // 5.5 us by counters and 6.7 by bits, 16 of 262144 6.5 and 7.8, but 256 of 128256 27 and 18.  16-bit counters have twice
-  // the range of 32-bit ones: those last two take 6.5 and 27 us with them and 8.3 and 39 with 32 bits.
+  // 5.0 us by counters and 7.2 by bits, 16 of 262144 6.1 and 7.9, but 256 of 128256 31.0 and 20.5.  16-bit counters have twice
+  // the range of 32-bit ones, so half the CTAs read the history: with 32 bits the three take 4.5, 7.0 and 44.0 us.
   const int counted = a.capacity <= kFew ? kCount16 : kCount32;
   const bool spread = a.rows * cdiv(a.V, range_of(counted)) <= (int64_t)sms * 2;
   const int form = a.frequency == 0.f && bits <= kMostBits && !spread ? kBits : counted;

@@ -234,12 +234,13 @@ __device__ __forceinline__ Wanted wanted_columns(const TableArgs& a, uint32_t b)
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallMost = 4;               // items per thread at most
 constexpr int kSmallItems = kSmallMost * kSmallThreads;
-// Where items, pairs and pages are few, so are the threads: the barriers of a step of 4 beams in 27 pages, copy included, are
-// then shorter (6.3 us captured; with 1024 threads 6.9).
+// Where items, pairs and pages are few, so are the threads: the barriers are then shorter (a step of 4 beams in 27 pages with its
+// copy 6.3 us captured, with 1024 threads 6.9; the plan alone, fork included, in 27 pages 4.1 and 4.5, in 4000 4.5 and
+// 5.3), but each looks through more pages (in 8192 5.2 and 4.9).
 constexpr int kFewThreads = 256;
 constexpr int kFewPages = 8192;
-// In turns, 128 x 256 pairs took 14.5 us here, by a kernel of their own and a plan without a fork 8.3.  Up to one turn it is a
-// launch less: with the copy 5.1 us to enqueue, else 6.4.
+// In turns, 128 x 256 pairs took 14.5 us here, by a kernel of their own and a plan without a fork 8.3; two to some thirty turns were
+// not measured.  Up to one turn it is a launch less: with the copy 5.1 us to enqueue, else 6.4.
 constexpr int kForkHere = kSmallThreads;    // pairs
 constexpr int kForkPages = 32768;           // 128 KB of counts
 inline int32_t padded_pages(int64_t pages, int threads) { return (int32_t)(cdiv(pages, threads) * threads); }
@@ -939,8 +940,8 @@ size_t compact_bytes(int64_t pages) { return align16(pages / 2 * 4) + 2 * align1
 constexpr int64_t kOneCta = 4096;  // pages
 int plan_ctas(int64_t units, int64_t pages) { return units <= kWarps && pages <= kOneCta ? 1 : kMaxCtas; }
 int32_t share(int64_t n, int ctas, int tile) { return (int32_t)(cdiv(cdiv(n, ctas), tile) * tile); }
-// Table entries per CTA up to which the compaction's own CTAs rewrite the table.  At 65536 entries that takes 16.1 us, by a
-// kernel of their own 14.0, but that one is 1.4 us more to enqueue; at 33024 7.5 here.
+// Table entries per CTA up to which the compaction's own CTAs rewrite the table.  At 65536 entries that takes 15.4 to 16.1 us in 70000
+// pages and 10 in 9000, by a kernel of their own 12.3 and 8, but that one is 1.4 us more to enqueue; at 33024 7.8 here.
 constexpr int64_t kRemapHere = 8192;
 // Pages whose counts one CTA looks through for a decode step: 512 rows in 16385 pages take 7 us in one CTA and 15 on a cluster, in
 // 100000 13 and 17; one CTA takes 0.08 us per 1000 pages more, the cluster 0.01.  (Items: 1025 take 12 us in one CTA and 27 on a
