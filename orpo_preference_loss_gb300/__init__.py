@@ -1024,7 +1024,7 @@ class BeamDecoder:
             raise ValueError(f"pages is for {pages.batch} x {pages.beams} beams, expected {self.batch} x {self.beams}")
         if (bias_token is None) != (bias_value is None) or (masks is None) != (mask_row is None):
             raise ValueError("bias_token and bias_value, and masks and mask_row, must be given together")
-        pools = tuple(pools)
+        pools = () if pools is None else tuple(pools)
         if pages is None and (pools or more is not None):
             raise ValueError("pools and more need pages")
         # The selection replaces the scores, so whatever the calls behind it would refuse is looked at before the first.

@@ -73,6 +73,14 @@ def test_no_page_goes_to_an_entry_that_was_released(weights, captured, raised):
         length += t32([1, 1 if raised else 0, 1])
 
 
+def test_no_pools_by_either_name(weights):
+    for kw in (dict(pools=None), dict(pools=()), {}):
+        dec, pages = decoder(1, 3, 4, 20, 4, t32([5]))
+        dec.step(hidden(1, 3, 0), *weights, **kw)
+        dec.step(hidden(1, 3, 1), *weights, length=t32([5]), pages=pages, **kw)
+        assert int(dec.status) == 0
+
+
 def test_the_last_step_of_a_full_table(weights):
     """All positions are in use: the beams still follow their parents, and nothing is asked for."""
     batch, beams, page, columns = 2, 3, 4, 5
